@@ -13,6 +13,7 @@
 #include <string>
 
 #include "kda.h"
+#include "kda_attn.h"
 #include "kda_internal.h"
 #include "kda_ops.h"
 
@@ -864,6 +865,205 @@ int kda_conv_halo(int32_t io_dtype, int32_t channels, int32_t width, const void 
     a.win = dst->states; a.n_slots = dst->n_slots; a.write_idx = dst->write_idx;
     return launched(kda::launch_conv_halo(io_dtype == KDA_DTYPE_BF16, width, a, (hipStream_t)stream),
                     "conv halo");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Softmax-attention layers
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_attn_config(const kda_attn_config *cfg) {
+    if (!cfg) return fail(KDA_ERR_ARG, "cfg is NULL");
+    if (cfg->num_q_heads <= 0 || cfg->num_kv_heads <= 0)
+        return fail(KDA_ERR_ARG, "num_q_heads and num_kv_heads must be positive (got %d, %d)",
+                    cfg->num_q_heads, cfg->num_kv_heads);
+    if (cfg->num_q_heads % cfg->num_kv_heads != 0)
+        return fail(KDA_ERR_ARG, "num_q_heads must be a multiple of num_kv_heads (got %d, %d)",
+                    cfg->num_q_heads, cfg->num_kv_heads);
+    if (cfg->io_dtype != KDA_DTYPE_F32 && cfg->io_dtype != KDA_DTYPE_BF16)
+        return fail(KDA_ERR_ARG, "io_dtype must be KDA_DTYPE_F32 or KDA_DTYPE_BF16 (got %d)", cfg->io_dtype);
+    if (cfg->head_dim != 64 && cfg->head_dim != 128)
+        return fail(KDA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", cfg->head_dim);
+    if (cfg->num_q_heads > 65535)
+        return fail(KDA_ERR_UNSUPPORTED, "num_q_heads must be at most 65535 (got %d)", cfg->num_q_heads);
+    return KDA_OK;
+}
+
+// The distance between the tokens of a tensor of `heads` heads.
+int check_row(const kda_attn_config *cfg, int64_t row, int heads, const char *name) {
+    const int64_t el = cfg->io_dtype == KDA_DTYPE_BF16 ? 2 : 4;
+    if (row < (int64_t)heads * cfg->head_dim)
+        return fail(KDA_ERR_ARG, "%s must be at least %lld elements (got %lld)", name,
+                    (long long)heads * cfg->head_dim, (long long)row);
+    if (row * el % 16 != 0)
+        return fail(KDA_ERR_ALIGN, "%s must be a multiple of 16 bytes (got %lld elements)", name,
+                    (long long)row);
+    return KDA_OK;
+}
+
+int check_rows(const kda_attn_config *cfg, int32_t N, int64_t T) {
+    if (N < 0) return fail(KDA_ERR_ARG, "N must be non-negative (got %d)", N);
+    if (T < 0) return fail(KDA_ERR_ARG, "T must be non-negative (got %lld)", (long long)T);
+    if (T > INT32_MAX / cfg->num_q_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "T * num_q_heads must fit in 31 bits (got T = %lld)", (long long)T);
+    if (T > 0 && N == 0) return fail(KDA_ERR_ARG, "T > 0 needs at least one sequence");
+    return KDA_OK;
+}
+
+int check_cache(const kda_attn_config *cfg, const kda_kv_cache *c) {
+    (void)cfg;
+    if (!c) return fail(KDA_ERR_ARG, "cache is NULL");
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
+        return fail(KDA_ERR_UNSUPPORTED, "cache->page must be 16, 32, 64 or 128 (got %d)", c->page);
+    if (c->n_pages <= 0)
+        return fail(KDA_ERR_ARG, "cache->n_pages must be positive (got %lld)", (long long)c->n_pages);
+    if (c->table_width <= 0)
+        return fail(KDA_ERR_ARG, "cache->table_width must be positive (got %d)", c->table_width);
+    if (c->table_width > INT32_MAX / c->page)
+        return fail(KDA_ERR_UNSUPPORTED, "cache->table_width * cache->page must fit in 31 bits (got %d, %d)",
+                    c->table_width, c->page);
+    KDA_TRY(check_tensor(c->k, "cache->k", true));
+    KDA_TRY(check_tensor(c->v, "cache->v", true));
+    KDA_TRY(check_tensor(c->k_scale, "cache->k_scale", true, 4));
+    KDA_TRY(check_tensor(c->v_scale, "cache->v_scale", true, 4));
+    KDA_TRY(check_tensor(c->table, "cache->table", true, 4));
+    return KDA_OK;
+}
+
+kda::KvArgs kv_args(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N, int64_t T,
+                    const int64_t *cu, const int64_t *kv_len) {
+    kda::KvArgs a{};
+    a.k_codes = (uint8_t *)c->k; a.v_codes = (uint8_t *)c->v;
+    a.k_scale = c->k_scale; a.v_scale = c->v_scale;
+    a.table = c->table; a.n_pages = c->n_pages; a.page = c->page; a.width = c->table_width;
+    a.cu = cu; a.kv_len = kv_len; a.N = N; a.Hk = cfg->num_kv_heads; a.T = T;
+    return a;
+}
+
+int attn_plan(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N, int64_t T) {
+    return kda::attn_workers(device_cus(), N, T, cfg->num_q_heads / cfg->num_kv_heads,
+                             cfg->num_kv_heads, (int64_t)c->table_width * c->page);
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_qk_norm_rope(const kda_attn_config *cfg, int64_t T, const void *q, int64_t q_row,
+                     const void *k, int64_t k_row, const float *q_weight, const float *k_weight,
+                     float eps, const float *table, int64_t n_pos, int32_t rot_dim, int32_t layout,
+                     const int64_t *positions, void *q_out, int64_t q_out_row, void *k_out,
+                     int64_t k_out_row, void *stream) {
+    KDA_TRY(check_attn_config(cfg));
+    KDA_TRY(check_rows(cfg, 1, T));
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(KDA_ERR_ARG, "eps must be finite and >= 0");
+    if (table) {
+        if (layout != KDA_ROPE_HALVES && layout != KDA_ROPE_PAIRS)
+            return fail(KDA_ERR_ARG, "layout must be KDA_ROPE_HALVES or KDA_ROPE_PAIRS (got %d)", layout);
+        if (n_pos <= 0) return fail(KDA_ERR_ARG, "n_pos must be positive (got %lld)", (long long)n_pos);
+        if (rot_dim <= 0 || rot_dim % 16 != 0 || rot_dim > cfg->head_dim)
+            return fail(KDA_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16, at most head_dim (got %d)", rot_dim);
+    }
+    KDA_TRY(check_row(cfg, q_row, cfg->num_q_heads, "q_row"));
+    KDA_TRY(check_row(cfg, k_row, cfg->num_kv_heads, "k_row"));
+    KDA_TRY(check_row(cfg, q_out_row, cfg->num_q_heads, "q_out_row"));
+    KDA_TRY(check_row(cfg, k_out_row, cfg->num_kv_heads, "k_out_row"));
+    if (T == 0) return ok();
+    KDA_TRY(check_tensor(q, "q", true));
+    KDA_TRY(check_tensor(k, "k", true));
+    KDA_TRY(check_tensor(q_out, "q_out", true));
+    KDA_TRY(check_tensor(k_out, "k_out", true));
+    KDA_TRY(check_tensor(q_weight, "q_weight", false));
+    KDA_TRY(check_tensor(k_weight, "k_weight", false));
+    KDA_TRY(check_tensor(table, "table", false));
+    KDA_TRY(check_tensor(positions, "positions", table != nullptr, 8));
+    if ((q_out == q && q_out_row != q_row) || (k_out == k && k_out_row != k_row))
+        return fail(KDA_ERR_ARG, "an output in place of its input needs the same row distance");
+    kda::RotateArgs a{};
+    a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
+    a.q_row = q_row; a.k_row = k_row; a.q_out_row = q_out_row; a.k_out_row = k_out_row;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.table = table; a.positions = positions;
+    a.T = T; a.n_pos = n_pos; a.Hq = cfg->num_q_heads; a.Hk = cfg->num_kv_heads;
+    a.rot = table ? rot_dim : 0; a.eps = eps;
+    return launched(kda::launch_rotate(cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim,
+                                       layout == KDA_ROPE_PAIRS, a, (hipStream_t)stream),
+                    "q/k norm and rotation");
+}
+
+int kda_kv_write(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
+                 const int64_t *cu_seqlens, const int64_t *kv_len, const void *k, int64_t k_row,
+                 const void *v, int64_t v_row, void *stream) {
+    KDA_TRY(check_attn_config(cfg));
+    KDA_TRY(check_rows(cfg, N, T));
+    KDA_TRY(check_cache(cfg, cache));
+    KDA_TRY(check_row(cfg, k_row, cfg->num_kv_heads, "k_row"));
+    KDA_TRY(check_row(cfg, v_row, cfg->num_kv_heads, "v_row"));
+    if (T == 0) return ok();
+    KDA_TRY(check_tensor(cu_seqlens, "cu_seqlens", true, 8));
+    KDA_TRY(check_tensor(kv_len, "kv_len", true, 8));
+    KDA_TRY(check_tensor(k, "k", true));
+    KDA_TRY(check_tensor(v, "v", true));
+    kda::KvArgs a = kv_args(cfg, cache, N, T, cu_seqlens, kv_len);
+    a.k = k; a.v = v; a.k_row = k_row; a.v_row = v_row;
+    return launched(kda::launch_kv_write(cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim, a,
+                                         (hipStream_t)stream), "cache write");
+}
+
+int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
+                const int64_t *cu_seqlens, const int64_t *kv_len, void *k, void *v, void *stream) {
+    KDA_TRY(check_attn_config(cfg));
+    KDA_TRY(check_rows(cfg, N, T));
+    KDA_TRY(check_cache(cfg, cache));
+    if (T == 0) return ok();
+    KDA_TRY(check_tensor(cu_seqlens, "cu_seqlens", true, 8));
+    KDA_TRY(check_tensor(kv_len, "kv_len", true, 8));
+    KDA_TRY(check_tensor(k, "k", true));
+    KDA_TRY(check_tensor(v, "v", true));
+    kda::KvArgs a = kv_args(cfg, cache, N, T, cu_seqlens, kv_len);
+    a.k_out = k; a.v_out = v;
+    return launched(kda::launch_kv_read(cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim, a,
+                                        (hipStream_t)stream), "cache read");
+}
+
+size_t kda_attn_workspace(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N,
+                          int64_t T) {
+    if (check_attn_config(cfg) != KDA_OK || check_rows(cfg, N, T) != KDA_OK) return 0;
+    if (check_cache(cfg, cache) != KDA_OK || T == 0) return 0;
+    return round256(kda::attn_partial_bytes(cfg->head_dim, attn_plan(cfg, cache, N, T)));
+}
+
+int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
+             const int64_t *cu_seqlens, const int64_t *kv_len, const void *q, int64_t q_row,
+             float scale, int32_t causal, int32_t window, void *o, float *lse, void *ws,
+             size_t ws_bytes, void *stream) {
+    KDA_TRY(check_attn_config(cfg));
+    KDA_TRY(check_rows(cfg, N, T));
+    KDA_TRY(check_cache(cfg, cache));
+    if (!std::isfinite(scale)) return fail(KDA_ERR_ARG, "scale must be finite");
+    if (causal != 0 && causal != 1) return fail(KDA_ERR_ARG, "causal must be 0 or 1 (got %d)", causal);
+    if (window < 0) return fail(KDA_ERR_ARG, "window must be >= 0 (got %d)", window);
+    KDA_TRY(check_row(cfg, q_row, cfg->num_q_heads, "q_row"));
+    if (T == 0) return ok();
+    KDA_TRY(check_tensor(cu_seqlens, "cu_seqlens", true, 8));
+    KDA_TRY(check_tensor(kv_len, "kv_len", true, 8));
+    KDA_TRY(check_tensor(q, "q", true));
+    KDA_TRY(check_tensor(o, "o", true));
+    KDA_TRY(check_tensor(lse, "lse", false, 4));
+    if (o == q) return fail(KDA_ERR_ARG, "o must not alias q");
+    kda::AttnArgs a{};
+    a.kv = kv_args(cfg, cache, N, T, cu_seqlens, kv_len);
+    a.workers = attn_plan(cfg, cache, N, T);
+    const size_t need = round256(kda::attn_partial_bytes(cfg->head_dim, a.workers));
+    if (need && (!ws || ws_bytes < need))
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
+    if (need) KDA_TRY(check_tensor(ws, "ws", true));
+    a.q = q; a.q_row = q_row; a.o = o; a.lse = lse; a.part = need ? (float *)ws : nullptr;
+    a.Hq = cfg->num_q_heads; a.scale = scale * 1.4426950408889634f;
+    a.causal = causal; a.window = window;
+    return launched(kda::launch_attn(cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim, a,
+                                     (hipStream_t)stream), "attention");
 }
 
 }  // extern "C"

@@ -1,0 +1,74 @@
+// Internal interfaces of the attention-layer operators with the C ABI
+// (kda_api.hip): q/k norm with rotation (kda_rotate.hip), the 8-bit key/value
+// cache (kda_kv.hip) and attention over it (kda_attn.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+// RMS norm of every head of q and k with the rotation (kda_rotate.hip).
+struct RotateArgs {
+    const void *q, *k;           // rows of Hq (Hk) heads of D, I/O dtype
+    void *q_out, *k_out;
+    int64_t q_row, k_row, q_out_row, k_out_row;   // elements from token to token
+    const float *q_weight, *k_weight;             // [D] (nullable: ones)
+    const float *table;          // [n_pos, rot]: cosines, then sines (nullable: no rotation)
+    const int64_t *positions;    // [T] (nullable without a table)
+    int64_t T, n_pos;
+    int32_t Hq, Hk, rot;
+    float eps;
+};
+hipError_t launch_rotate(bool bf16, int D, bool pairs, const RotateArgs &a, hipStream_t s);
+
+// A paged key/value cache and the tokens of a call: sequence n's are the last
+// cu[n+1] - cu[n] of its kv_len[n] cached tokens, and the token at position p
+// lives in row p % page of page table[n * width + p / page].
+struct KvArgs {
+    uint8_t *k_codes, *v_codes;  // [n_pages, Hk, page, D] e4m3
+    float *k_scale, *v_scale;    // [n_pages, Hk]
+    const int32_t *table;        // [N, width]
+    int64_t n_pages;
+    int32_t page, width;
+    const int64_t *cu, *kv_len;  // [N+1], [N]
+    int32_t N, Hk;
+    int64_t T;
+    const void *k, *v;           // kda_kv_write: rows of Hk heads, I/O dtype
+    int64_t k_row, v_row;
+    void *k_out, *v_out;         // kda_kv_read: [T, Hk, D], I/O dtype
+};
+hipError_t launch_kv_write(bool bf16, int D, const KvArgs &a, hipStream_t s);
+hipError_t launch_kv_read(bool bf16, int D, const KvArgs &a, hipStream_t s);
+
+// Attention over the cache (kda_attn.hip).
+struct AttnArgs {
+    KvArgs kv;
+    const void *q;               // rows of Hq heads, I/O dtype
+    int64_t q_row;
+    void *o;                     // [T, Hq, D], I/O dtype
+    float *lse;                  // [T, Hq] (nullable)
+    float *part;                 // partial results of split units (split > 0)
+    int32_t Hq;
+    float scale;                 // of the scores, times log2(e)
+    int32_t causal, window;
+    int32_t workers;             // workgroups that share the tiles; 0: one per unit
+};
+// Workgroups for a call (0: no unit is split) and the bytes of their partials.
+int attn_workers(int cus, int N, int64_t T, int G, int Hk, int64_t max_kv);
+size_t attn_partial_bytes(int D, int workers);
+hipError_t launch_attn(bool bf16, int D, const AttnArgs &a, hipStream_t s);
+
+// Sequence holding packed row r: the last s with cu[s] <= r (skips empty sequences).
+__device__ __forceinline__ int seq_of_row(const int64_t *cu, int N, int64_t r) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace kda

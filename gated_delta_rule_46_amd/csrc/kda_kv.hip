@@ -1,0 +1,239 @@
+// kda_kv.hip -- the 8-bit key/value cache: quantised as it is written, read back.
+//
+// A page holds `page` consecutive tokens of one sequence.  For each page and
+// head the keys (and, apart from them, the values) are e4m3 codes c with one
+// scale s = 2^e, x ~ c s, where e is the smallest exponent with
+// amax <= 448 * 2^e over the finite values that the page holds.  A power of two
+// costs a floating code no precision (its relative step does not depend on the
+// scale) and makes every product with it exact: the codes are the values
+// rounded once to e4m3's grid, c s is exact in bf16 and in fp32, and a page
+// whose scale grows rounds its older codes again only where they fall below the
+// grid's smallest normal.  e stays within [-100, 119], so that c s is a normal
+// number; larger values and infinities saturate at 448 s, NaN stays NaN.
+//
+// Both kernels move each byte once and are bound by HBM for long calls and by
+// their launch for a decode step.  kv_write: one workgroup per (page touched,
+// head, keys or values) holds all new elements of its page in registers between
+// the maximum and the conversion, so they are read once.  It owns the page's
+// codes and scale of that head: no two workgroups meet.
+
+#include "kda_attn.h"
+#include "kda_mfma.h"
+
+namespace kda {
+namespace {
+
+constexpr int kKvThreads = 256;
+constexpr int kScaleExpMin = -100, kScaleExpMax = 119;
+constexpr float kCodeMax = 448.f;
+
+// Two fp32 values per half word of e4m3 codes (round to nearest even).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    uint32_t r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+// x limited to the code range; a NaN stays (both comparisons fail).
+__device__ __forceinline__ float limited(float x) {
+    x = x > kCodeMax ? kCodeMax : x;
+    return x < -kCodeMax ? -kCodeMax : x;
+}
+
+// Smallest e (in range) with amax <= 448 * 2^e.  amax = 1.f * 2^x: 448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_exp(float amax) {
+    const uint32_t b = f32_bits(amax);
+    const int x = (int)(b >> 23) - 127 - 8;
+    const int e = x + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return amax > 0.f ? min(max(e, kScaleExpMin), kScaleExpMax) : kScaleExpMin;
+}
+
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return bits_f32((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ void uncode4(uint32_t c, float *out) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+    out[0] = a[0]; out[1] = a[1]; out[2] = b[0]; out[3] = b[1];
+}
+
+// Workgroup x of the page axis -> a sequence and one of the pages that its new
+// tokens touch.  A sequence of len tokens touches at most (len - 1) / page + 2
+// pages, which is at most first(n + 1) - first(n) for first(n) = cu[n] / page +
+// 2 n: the pages of all sequences are numbered without a pass over them.
+template <int D, int PAGE, bool BF>
+__global__ __launch_bounds__(kKvThreads) void kv_write_kernel(const KvArgs a) {
+    constexpr int CH = D / 8;                                     // 8-element pieces per row
+    constexpr int NC = (PAGE * CH + kKvThreads - 1) / kKvThreads;   // pieces per thread
+    __shared__ float s_max[kKvThreads / 64];
+    const int tid = threadIdx.x;
+    const int64_t x = blockIdx.x;
+    const int h = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+
+    int lo_n = 0, hi_n = a.N - 1;                                 // last n with first(n) <= x
+    while (lo_n < hi_n) {
+        const int mid = (lo_n + hi_n + 1) >> 1;
+        if (a.cu[mid] / PAGE + 2 * (int64_t)mid <= x) lo_n = mid; else hi_n = mid - 1;
+    }
+    const int n = lo_n;
+    const int64_t c0 = a.cu[n], c1 = min(a.cu[n + 1], a.T);
+    const int64_t kvl = a.kv_len[n], start = kvl - (c1 - c0);     // position of the first new token
+    if (c0 < 0 || c1 <= c0) return;
+    const int64_t from = max(start, (int64_t)0);
+    const int64_t b = from / PAGE + (x - (c0 / PAGE + 2 * (int64_t)n));
+    const int64_t lo = max(from, b * PAGE), hi = min(kvl, (b + 1) * PAGE);
+    if (lo >= hi || b >= a.width) return;
+    const int32_t pid = a.table[(int64_t)n * a.width + b];
+    if (pid < 0 || pid >= a.n_pages) return;
+
+    const int first = (int)(lo - b * PAGE), rows = (int)(hi - lo);
+    const void *src = is_v ? a.v : a.k;
+    const int64_t row = is_v ? a.v_row : a.k_row;
+    const int64_t at = (c0 + (lo - start)) * row + (int64_t)h * D;
+    uint8_t *codes = (is_v ? a.v_codes : a.k_codes) + ((int64_t)pid * a.Hk + h) * (PAGE * D);
+    float *scale = (is_v ? a.v_scale : a.k_scale) + (int64_t)pid * a.Hk + h;
+    const float held = first > 0 ? *scale : 0.f;
+
+    float v[NC][8];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = i * kKvThreads + tid, r = c / CH;
+        if (r < rows) {
+            mf::IO<BF>::load8(src, at + r * row + (c % CH) * 8, v[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float y = fabsf(v[i][j]);
+                m = y < __builtin_inff() ? fmaxf(m, y) : m;       // finite values only
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    if ((tid & 63) == 0) s_max[tid >> 6] = m;
+    __syncthreads();                                              // and every thread has read *scale
+    m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const int e = scale_exp(m);
+    const float need = pow2(e);
+    const float s = fmaxf(held, need), inv = held > need ? 1.f / held : pow2(-e);
+
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = i * kKvThreads + tid, r = c / CH;
+        if (r < rows) {
+            uint2 w;
+            w.x = codes4(limited(v[i][0] * inv), limited(v[i][1] * inv), limited(v[i][2] * inv),
+                         limited(v[i][3] * inv));
+            w.y = codes4(limited(v[i][4] * inv), limited(v[i][5] * inv), limited(v[i][6] * inv),
+                         limited(v[i][7] * inv));
+            *(uint2 *)(codes + (first + r) * D + (c % CH) * 8) = w;
+        }
+    }
+    if (first > 0 && s > held) {                                  // older rows, to the larger scale
+        const float f = held / s;
+        for (int c = tid; c < first * CH; c += kKvThreads) {
+            uint2 w = *(const uint2 *)(codes + c * 8);
+            float y[8];
+            uncode4(w.x, y);
+            uncode4(w.y, y + 4);
+            w.x = codes4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+            w.y = codes4(y[4] * f, y[5] * f, y[6] * f, y[7] * f);
+            *(uint2 *)(codes + c * 8) = w;
+        }
+    }
+    if (tid == 0 && s != held) *scale = s;
+}
+
+// One workgroup per kReadRows packed tokens; a thread takes 8-element pieces of
+// keys and values.  Tokens without a page read as zeros.
+constexpr int kReadRows = 4;
+
+template <int D, bool BF>
+__global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const KvArgs a) {
+    constexpr int CH = D / 8;
+    const int tid = threadIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * kReadRows;
+    if (t0 >= a.cu[a.N]) return;              // rows behind the last sequence stay as they are
+    int n = seq_of_row(a.cu, a.N, t0);
+    const int per = 2 * a.Hk * CH;            // pieces per token
+    for (int i = 0; i < kReadRows; ++i) {
+        const int64_t t = t0 + i;
+        if (t >= a.T) return;
+        while (n < a.N && t >= a.cu[n + 1]) ++n;
+        if (n >= a.N || t < a.cu[n]) return;
+        const int64_t pos = a.kv_len[n] - a.cu[n + 1] + t;
+        const int64_t b = pos / a.page;
+        int32_t pid = -1;
+        if (pos >= 0 && b < a.width) pid = a.table[(int64_t)n * a.width + b];
+        const bool has = pid >= 0 && pid < a.n_pages;
+        const int r = (int)(pos - b * a.page);
+        for (int c = tid; c < per; c += kKvThreads) {
+            const bool is_v = c >= a.Hk * CH;
+            const int hc = is_v ? c - a.Hk * CH : c;
+            const int h = hc / CH, d = (hc % CH) * 8;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = 0.f;
+            if (has) {
+                const int64_t ph = (int64_t)pid * a.Hk + h;
+                const uint2 w = *(const uint2 *)((is_v ? a.v_codes : a.k_codes) +
+                                                 (ph * a.page + r) * D + d);
+                const float s = (is_v ? a.v_scale : a.k_scale)[ph];
+                uncode4(w.x, y);
+                uncode4(w.y, y + 4);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] *= s;
+            }
+            mf::IO<BF>::store8(is_v ? a.v_out : a.k_out, (t * a.Hk + h) * D + d, y);
+        }
+    }
+}
+
+template <int D, int PAGE>
+hipError_t launch_write(bool bf16, const KvArgs &a, hipStream_t s) {
+    const int64_t gx = a.T / PAGE + 2 * (int64_t)a.N;
+    if (gx > INT32_MAX || a.Hk > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)gx, (unsigned)a.Hk, 2), block(kKvThreads);
+    if (bf16) hipLaunchKernelGGL((kv_write_kernel<D, PAGE, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((kv_write_kernel<D, PAGE, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_write_page(bool bf16, const KvArgs &a, hipStream_t s) {
+    switch (a.page) {
+        case 16: return launch_write<D, 16>(bf16, a, s);
+        case 32: return launch_write<D, 32>(bf16, a, s);
+        case 64: return launch_write<D, 64>(bf16, a, s);
+        case 128: return launch_write<D, 128>(bf16, a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(bool bf16, int D, const KvArgs &a, hipStream_t s) {
+    if (a.T <= 0 || a.N <= 0) return hipSuccess;
+    if (D == 128) return launch_write_page<128>(bf16, a, s);
+    if (D == 64) return launch_write_page<64>(bf16, a, s);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_read(bool bf16, int D, const KvArgs &a, hipStream_t s) {
+    if (a.T <= 0 || a.N <= 0) return hipSuccess;
+    const int64_t g = (a.T + kReadRows - 1) / kReadRows;
+    if (g > INT32_MAX) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)g), block(kKvThreads);
+    if (D == 128) {
+        if (bf16) hipLaunchKernelGGL((kv_read_kernel<128, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((kv_read_kernel<128, false>), grid, block, 0, s, a);
+    } else if (D == 64) {
+        if (bf16) hipLaunchKernelGGL((kv_read_kernel<64, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((kv_read_kernel<64, false>), grid, block, 0, s, a);
+    } else {
+        return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -8,6 +8,7 @@ this module raises ImportError; nothing falls back to another implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -24,11 +25,13 @@ EXPORTS = ("kda_prefill_workspace", "kda_prefill", "kda_prefill_noalloc", "kda_p
            "kda_segment_scan_workspace", "kda_segment_scan", "kda_output_fixup",
            "kda_output_fixup_ckpt", "kda_segment_package_fx", "kda_output_fixup_fx",
            "kda_checkpoint_write", "kda_decode", "kda_short_conv", "kda_conv_halo",
+           "kda_qk_norm_rope", "kda_kv_write", "kda_kv_read", "kda_attn_workspace", "kda_attn",
            "kda_validate_inputs", "kda_status_string", "kda_last_error", "kda_version")
 # fields of kda_validate_inputs' report
 KDA_CHECK_FIELDS = 8
 CHECK_NAMES = ("bounds", "g_positive", "g_nonfinite", "g_block_floor", "beta_nonfinite")
 KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
+KDA_ROPE_HALVES, KDA_ROPE_PAIRS = 0, 1
 
 
 class KdaError(RuntimeError):
@@ -63,6 +66,17 @@ class kda_conv_state(ctypes.Structure):
                 ("read_idx", ctypes.c_void_p), ("write_idx", ctypes.c_void_p)]
 
 
+class kda_attn_config(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+
+
+class kda_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("table", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is missing: build it with "
@@ -73,6 +87,8 @@ def _load():
     poolp = ctypes.POINTER(kda_state_pool)
     fxp = ctypes.POINTER(kda_fixop)
     convp = ctypes.POINTER(kda_conv_state)
+    F32 = ctypes.c_float
+    acfgp, cachep = ctypes.POINTER(kda_attn_config), ctypes.POINTER(kda_kv_cache)
     sig = {
         "kda_prefill_workspace": (S, [cfgp, I64, I32]),
         "kda_prefill": (ctypes.c_int, [cfgp, P, P, P, P, P, P, I32, I64, P, P, P, ckp, P, S, P]),
@@ -95,6 +111,13 @@ def _load():
         "kda_decode": (ctypes.c_int, [cfgp, I32, P, P, P, P, P, I32, poolp, P, P]),
         "kda_short_conv": (ctypes.c_int, [I32, I32, I32, I32, P, I64, P, I32, P, P, convp, P, P]),
         "kda_conv_halo": (ctypes.c_int, [I32, I32, I32, P, I64, P, I32, convp, P]),
+        "kda_qk_norm_rope": (ctypes.c_int, [acfgp, I64, P, I64, P, I64, P, P, F32, P, I64, I32, I32,
+                                            P, P, I64, P, I64, P]),
+        "kda_kv_write": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, I64, P, I64, P]),
+        "kda_kv_read": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, P, P]),
+        "kda_attn_workspace": (S, [acfgp, cachep, I32, I64]),
+        "kda_attn": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, I64, F32, I32, I32, P, P, P, S,
+                                    P]),
         "kda_validate_inputs": (ctypes.c_int, [cfgp, I64, P, I32, I32, P, P, P, P]),
         "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "kda_last_error": (ctypes.c_char_p, []),
@@ -672,3 +695,198 @@ def kda_conv_halo(x, bounds, width, windows, write_idx, *, stream=None):
                            ctypes.byref(st), _stream(stream))
     _check(rc, "kda_conv_halo")
     return windows
+
+
+# ---------------------------------------------------------------------------
+# Softmax-attention layers
+# ---------------------------------------------------------------------------
+class KVCache:
+    """Buffers of a paged 8-bit key/value cache (kda_kv_cache): codes k, v [n_pages, Hk, page, D]
+    (uint8 or float8_e4m3fn), k_scale, v_scale [n_pages, Hk] fp32 and the table [N, width] int32 of
+    each sequence's pages (an entry outside [0, n_pages): absent).  The caller owns the tensors."""
+
+    def __init__(self, k, v, k_scale, v_scale, table):
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+
+    @classmethod
+    def empty(cls, n_pages, Hk, page, D, table):
+        """A cache of n_pages pages on the table's device."""
+        dev = table.device
+        codes = [torch.zeros((n_pages, Hk, page, D), dtype=torch.uint8, device=dev) for _ in "kv"]
+        scales = [torch.ones((n_pages, Hk), dtype=torch.float32, device=dev) for _ in "kv"]
+        return cls(*codes, *scales, table)
+
+    def c(self, N, Hk, D, dev):
+        n_pages, _, page, _ = self.k.shape
+        for x, name in ((self.k, "cache.k"), (self.v, "cache.v")):
+            if x.dtype != torch.uint8 and x.dtype != torch.float8_e4m3fn:
+                raise TypeError(f"{name} has dtype {x.dtype}, expected uint8 or float8_e4m3fn")
+            _need(x, name, (n_pages, Hk, page, D), x.dtype, dev)
+        _need(self.k_scale, "cache.k_scale", (n_pages, Hk), torch.float32, dev)
+        _need(self.v_scale, "cache.v_scale", (n_pages, Hk), torch.float32, dev)
+        _need(self.table, "cache.table", (N, self.table.shape[1]), torch.int32, dev)
+        return kda_kv_cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                            self.v_scale.data_ptr(), n_pages, page, self.table.shape[1],
+                            self.table.data_ptr())
+
+
+def _need_rows(t, name, T, D, dtype, device):
+    """Packed rows [T, heads, D] whose heads are contiguous; tokens may be apart.  Returns the
+    distance between tokens in elements."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {D})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    row, head, el = t.stride()
+    if (el != 1 and D > 1) or (head != D and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
+    return row if T > 1 else max(row, t.shape[1] * D)
+
+
+def _attn_config(Hq, Hk, D, dtype):
+    return kda_attn_config(Hq, Hk, D, _io_dtype(dtype))
+
+
+def _device(t):
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be device tensors")
+    return t.device
+
+
+def _on_stream(at, name):
+    """Runs a call on the device of its argument `name` (position `at`) and on `stream` (None: that
+    device's current one), its allocations included: buffers taken for a call are then ordered with
+    the stream that uses them."""
+    def wrap(f):
+        @functools.wraps(f)
+        def g(*args, stream=None, **kw):
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    return f(*args, **kw)
+            x = args[at] if len(args) > at else kw[name]
+            dev = (x.k if name == "cache" else x).device
+            if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+                with torch.cuda.device(dev):
+                    return f(*args, **kw)
+            return f(*args, **kw)
+        return g
+    return wrap
+
+
+def _call(name, *args):
+    _check(getattr(LIB, name)(*args, _stream(None)), name)
+
+
+@_on_stream(0, "q")
+def kda_qk_norm_rope(q, k, positions=None, rope_table=None, *, q_weight=None, k_weight=None,
+                     eps=1e-6, layout=KDA_ROPE_HALVES, q_out=None, k_out=None):
+    """RMS norm of every head of q [T,Hq,D] and k [T,Hk,D] and the rotation of its first R dims by
+    position, in one pass.  rope_table: fp32 [n_pos,R], R/2 cosines then R/2 sines of each position
+    (None: norm only); positions: int64 [T], a token outside [0, n_pos) is left as it is.  weights:
+    fp32 [D] or None (ones).  q, k and the outputs may have tokens apart (views of a projection's
+    rows); q_out / k_out may be q / k.  Returns (q_out, k_out)."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    dev = _device(q)
+    q_row = _need_rows(q, "q", T, D, q.dtype, dev)
+    k_row = _need_rows(k, "k", T, D, q.dtype, dev)
+    n_pos = rot = 0
+    if rope_table is not None:
+        n_pos, rot = rope_table.shape
+        _need(rope_table, "rope_table", (n_pos, rot), torch.float32, dev)
+        _need(positions, "positions", (T,), torch.int64, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, (D,), torch.float32, dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
+    qo_row = _need_rows(q_out, "q_out", T, D, q.dtype, dev)
+    ko_row = _need_rows(k_out, "k_out", T, D, q.dtype, dev)
+    if q_out.shape[1] != Hq or k_out.shape[1] != Hk:
+        raise ValueError("q_out / k_out must have the heads of q / k")
+    cfg = _attn_config(Hq, Hk, D, q.dtype)
+    _call("kda_qk_norm_rope", ctypes.byref(cfg), T, _p(q), q_row, _p(k), k_row,
+          _p(q_weight), _p(k_weight), float(eps), _p(rope_table), n_pos, rot, int(layout),
+          _p(positions) if rope_table is not None else None, _p(q_out), qo_row, _p(k_out), ko_row)
+    return q_out, k_out
+
+
+def _sequences(cu_seqlens, kv_len, dev):
+    N = cu_seqlens.numel() - 1
+    _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int64, dev)
+    _need(kv_len, "kv_len", (N,), torch.int64, dev)
+    return N
+
+
+@_on_stream(0, "k")
+def kda_kv_write(k, v, cu_seqlens, kv_len, cache):
+    """Stores the rows of k and v [T,Hk,D] (bf16 or fp32; tokens may be apart) in the 8-bit cache (a
+    KVCache, updated in place) as the last cu_seqlens[n+1]-cu_seqlens[n] of the kv_len[n] tokens of
+    each sequence.  cu_seqlens int64 [N+1], kv_len int64 [N] device tensors.  Returns the cache."""
+    T, Hk, D = k.shape
+    dev = _device(k)
+    k_row = _need_rows(k, "k", T, D, k.dtype, dev)
+    v_row = _need_rows(v, "v", T, D, k.dtype, dev)
+    if v.shape[1] != Hk:
+        raise ValueError(f"v has {v.shape[1]} heads, expected {Hk}")
+    N = _sequences(cu_seqlens, kv_len, dev)
+    cfg, cc = _attn_config(Hk, Hk, D, k.dtype), cache.c(N, Hk, D, dev)
+    _call("kda_kv_write", ctypes.byref(cfg), ctypes.byref(cc), N, T, _p(cu_seqlens),
+          _p(kv_len), _p(k), k_row, _p(v), v_row)
+    return cache
+
+
+@_on_stream(2, "cache")
+def kda_kv_read(cu_seqlens, kv_len, cache, T, dtype=torch.bfloat16, *, k_out=None, v_out=None):
+    """The values that the cache holds for the last cu_seqlens[n+1]-cu_seqlens[n] of the kv_len[n]
+    tokens of each sequence: (k, v) [T,Hk,D] in dtype, T = cu_seqlens[-1] (rows past it are left as
+    they are); tokens without a page are zeros."""
+    _, Hk, _, D = cache.k.shape
+    dev = _device(cache.k)
+    N = _sequences(cu_seqlens, kv_len, dev)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
+    _need(k_out, "k_out", (T, Hk, D), dtype, dev)
+    _need(v_out, "v_out", (T, Hk, D), dtype, dev)
+    cfg, cc = _attn_config(Hk, Hk, D, dtype), cache.c(N, Hk, D, dev)
+    _call("kda_kv_read", ctypes.byref(cfg), ctypes.byref(cc), N, T, _p(cu_seqlens),
+          _p(kv_len), _p(k_out), _p(v_out))
+    return k_out, v_out
+
+
+@_on_stream(0, "q")
+def kda_attn(q, cu_seqlens, kv_len, cache, *, scale=None, causal=True, window=0, want_lse=False,
+             out=None, lse_out=None, workspace=None):
+    """Softmax attention of the rows of q [T,Hq,D] (tokens may be apart) over the cached tokens of
+    their sequences; the rows are the last cu_seqlens[n+1]-cu_seqlens[n] of the kv_len[n] tokens,
+    which the cache already holds.  scale: None = 1/sqrt(D).  window: 0 = all keys.  workspace: a
+    uint8 device tensor to use instead of one of the queried size.  Returns o [T,Hq,D], or (o, lse
+    [T,Hq] fp32) with want_lse."""
+    T, Hq, D = q.shape
+    dev = _device(q)
+    q_row = _need_rows(q, "q", T, D, q.dtype, dev)
+    N = _sequences(cu_seqlens, kv_len, dev)
+    Hk = cache.k.shape[1]
+    cfg, cc = _attn_config(Hq, Hk, D, q.dtype), cache.c(N, Hk, D, dev)
+    o = out if out is not None else torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    _need(o, "out", (T, Hq, D), q.dtype, dev)
+    lse = lse_out
+    if lse is None and want_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse_out", (T, Hq), torch.float32, dev)
+    if workspace is None:
+        wsb = LIB.kda_attn_workspace(ctypes.byref(cfg), ctypes.byref(cc), N, T)
+        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    else:
+        wsb = workspace.numel()
+    _call("kda_attn", ctypes.byref(cfg), ctypes.byref(cc), N, T, _p(cu_seqlens),
+          _p(kv_len), _p(q), q_row, D ** -0.5 if scale is None else float(scale), int(bool(causal)),
+          int(window), _p(o), _p(lse), _p(workspace), wsb)
+    return (o, lse) if want_lse else o

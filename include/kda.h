@@ -42,6 +42,9 @@
  *    depthwise convolution KDA applies to q, k, v along tokens, with a
  *    per-sequence window state and the halo between segments.
  *
+ *  - The softmax-attention layers between the KDA layers (kda_qk_norm_rope,
+ *    kda_kv_write, kda_kv_read, kda_attn): their own section below.
+ *
  *  - Decode (kda_decode): one new token per sequence against a pool of
  *    states addressed by read and write slots (ROCm/ATOM PR #2709, review
  *    notes: the fused sigmoid-gated delta-rule update takes a read-side state
@@ -477,6 +480,124 @@ int kda_short_conv(int32_t io_dtype, int32_t channels, int32_t width, int32_t ac
  */
 int kda_conv_halo(int32_t io_dtype, int32_t channels, int32_t width, const void *x, int64_t T,
                   const int64_t *bounds, int32_t nseg, const kda_conv_state *dst, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Softmax-attention layers: q/k norm and rotation, 8-bit cache, attention    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Models that use KDA interleave its layers with softmax-attention layers
+ * (pegainfer PR #970's profile of one superstep: 35.8% in those layers' attention
+ * kernels, 4.2% in KDA).  These calls serve such a layer beside kda_prefill and
+ * kda_decode, on the same packed rows:
+ *     kda_qk_norm_rope -> kda_kv_write -> kda_attn
+ * for prompts, chunks of prompts, drafted tokens and single tokens alike.
+ *
+ * Rows.  q has num_q_heads heads, k and v num_kv_heads heads, of head_dim
+ * values each, in io_dtype; query head h reads key/value head
+ * h / (num_q_heads / num_kv_heads).  The heads of a token are contiguous;
+ * *_row is the distance between tokens in elements (at least the row itself, a
+ * multiple of 16 bytes), so q, k and v may be views of one projection's rows.
+ * head_dim in {64, 128}; num_q_heads a multiple of num_kv_heads.
+ * T * num_q_heads and table_width * page must fit in 31 bits.
+ */
+typedef struct {
+    int32_t num_q_heads, num_kv_heads, head_dim;
+    int32_t io_dtype;    /* KDA_DTYPE_F32 or KDA_DTYPE_BF16 */
+} kda_attn_config;
+
+#define KDA_ROPE_HALVES 0   /* pairs (i, i + rot/2) */
+#define KDA_ROPE_PAIRS  1   /* pairs (2i, 2i + 1)   */
+
+/*
+ * RMS norm of every head of q and k, then the rotation of its first rot_dim
+ * dims by the token's position, in one pass:
+ *     y = x * weight / sqrt(mean(x^2) + eps)
+ *     (y_a, y_b) <- (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i)
+ *   q_weight, k_weight [head_dim] fp32, NULL = ones;  eps >= 0;
+ *   table [n_pos, rot_dim] fp32: cos_0 .. cos_{rot/2-1}, sin_0 .. sin_{rot/2-1}
+ *       of each position; NULL = norm only (positions, layout unused);
+ *   rot_dim a multiple of 16, at most head_dim;
+ *   positions device int64 [T]; a token whose position is outside [0, n_pos)
+ *       is padding: its output rows are left as they are.
+ * fp32 arithmetic, one rounding at the store.  q_out (k_out) may be q (k)
+ * itself with the same row distance; otherwise outputs must not overlap inputs.
+ * T = 0 is a no-op.  No workspace.  One launch.
+ */
+int kda_qk_norm_rope(const kda_attn_config *cfg, int64_t T, const void *q, int64_t q_row,
+                     const void *k, int64_t k_row, const float *q_weight, const float *k_weight,
+                     float eps, const float *table, int64_t n_pos, int32_t rot_dim, int32_t layout,
+                     const int64_t *positions, void *q_out, int64_t q_out_row, void *k_out,
+                     int64_t k_out_row, void *stream);
+
+/*
+ * A paged key/value cache in 8 bits.  A page holds `page` consecutive tokens
+ * of one sequence for every key/value head: e4m3 codes and, for each page and
+ * head, one power-of-two scale for the keys and one for the values; a code c
+ * stands for c * scale (exact in bf16 and fp32).  The token at position p of
+ * sequence n is row p % page of page table[n * table_width + p / page].  A table
+ * entry outside [0, n_pages), and a position past the table, is an absent page:
+ * not written, read as zeros, masked in attention.
+ * Pages may be shared between sequences to be read (a common prefix); a page
+ * that a call writes must belong to one sequence of the call.
+ */
+typedef struct {
+    void *k, *v;                /* [n_pages, num_kv_heads, page, head_dim] codes, 16-byte aligned */
+    float *k_scale, *v_scale;   /* [n_pages, num_kv_heads] */
+    int64_t n_pages;
+    int32_t page;               /* 16, 32, 64 or 128 */
+    int32_t table_width;        /* pages per sequence in the table */
+    const int32_t *table;       /* device [N, table_width] */
+} kda_kv_cache;
+
+/*
+ * Which tokens: cu_seqlens (device int64 [N+1], as in kda_prefill; rows from
+ * cu_seqlens[N] on are padding and left as they are) splits the call's T packed
+ * rows into sequences, and kv_len (device int64 [N]) counts the tokens of each
+ * sequence that the cache holds once this call's are in it: they are its last
+ * cu_seqlens[n+1] - cu_seqlens[n] positions.  (Rows whose position would be
+ * negative have no page and see no keys.)
+ *
+ * kda_kv_write stores the rows of k and v.  The scale of a page and head is the
+ * smallest power of two s with amax <= 448 s over the finite values that the
+ * page holds, limited to 2^-100 .. 2^119; codes are x / s rounded to nearest
+ * even.  Values beyond 448 s (infinities among them) saturate, NaN stays NaN.
+ * A page is built up in order: writing its row 0 starts it afresh; a later write
+ * keeps the rows before it, which are rounded again to the new scale where
+ * that is larger, and makes the rows behind it void.  One launch, no workspace.
+ *
+ * kda_kv_read fills k, v [T, num_kv_heads, head_dim] (io_dtype, contiguous) with
+ * the values the codes stand for.  One launch, no workspace.
+ */
+int kda_kv_write(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
+                 const int64_t *cu_seqlens, const int64_t *kv_len, const void *k, int64_t k_row,
+                 const void *v, int64_t v_row, void *stream);
+int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
+                const int64_t *cu_seqlens, const int64_t *kv_len, void *k, void *v, void *stream);
+
+/*
+ * Softmax attention of the call's T rows of q over the cached tokens of their
+ * sequences (cu_seqlens and kv_len as above; the cache already holds the rows'
+ * own tokens).  The row at position p sees the keys j < kv_len with j <= p
+ * (causal = 1) and j > p - window (window > 0), on pages that are present:
+ *     o = sum_j softmax_j(scale q.k_j) v_j,    lse = log sum_j exp(scale q.k_j)
+ *   o [T, num_q_heads, head_dim] (io_dtype, contiguous);
+ *   lse [T, num_q_heads] fp32, NULL = not written.
+ * A row that sees no key gets o = 0 and lse = -inf.  Keys and values that a row
+ * does not see never reach it, infinities and NaN included.
+ * Scores, maxima, sums and outputs are accumulated in fp32; with bf16 rows the
+ * probabilities are rounded to bf16 for the product with V, with fp32 rows
+ * every operand keeps its 24 bits.
+ * ws / ws_bytes: at least kda_attn_workspace() bytes (it can be 0), not
+ * shared by calls that overlap; nothing in it needs to start at zero and
+ * nothing is kept in it between calls.
+ */
+size_t kda_attn_workspace(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N,
+                          int64_t T);
+int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
+             const int64_t *cu_seqlens, const int64_t *kv_len, const void *q, int64_t q_row,
+             float scale, int32_t causal, int32_t window, void *o, float *lse, void *ws,
+             size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
