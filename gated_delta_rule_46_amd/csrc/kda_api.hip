@@ -942,9 +942,14 @@ kda::KvArgs kv_args(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N
     return a;
 }
 
-int attn_plan(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N, int64_t T) {
-    return kda::attn_workers(device_cus(), N, T, cfg->num_q_heads / cfg->num_kv_heads,
-                             cfg->num_kv_heads, (int64_t)c->table_width * c->page);
+kda::AttnArgs attn_args(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N, int64_t T,
+                        const int64_t *cu, const int64_t *kv_len) {
+    kda::AttnArgs a{};
+    a.kv = kv_args(cfg, c, N, T, cu, kv_len);
+    a.Hq = cfg->num_q_heads;
+    kda::attn_plan(device_cus(), N, T, cfg->num_q_heads, cfg->num_kv_heads,
+                   (int64_t)c->table_width * c->page, &a);
+    return a;
 }
 
 }  // namespace
@@ -1031,7 +1036,7 @@ size_t kda_attn_workspace(const kda_attn_config *cfg, const kda_kv_cache *cache,
                           int64_t T) {
     if (check_attn_config(cfg) != KDA_OK || check_rows(cfg, N, T) != KDA_OK) return 0;
     if (check_cache(cfg, cache) != KDA_OK || T == 0) return 0;
-    return round256(kda::attn_partial_bytes(cfg->head_dim, attn_plan(cfg, cache, N, T)));
+    return round256(kda::attn_partial_bytes(cfg->head_dim, attn_args(cfg, cache, N, T, nullptr, nullptr)));
 }
 
 int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
@@ -1052,18 +1057,19 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
     KDA_TRY(check_tensor(o, "o", true));
     KDA_TRY(check_tensor(lse, "lse", false, 4));
     if (o == q) return fail(KDA_ERR_ARG, "o must not alias q");
-    kda::AttnArgs a{};
-    a.kv = kv_args(cfg, cache, N, T, cu_seqlens, kv_len);
-    a.workers = attn_plan(cfg, cache, N, T);
-    const size_t need = round256(kda::attn_partial_bytes(cfg->head_dim, a.workers));
+    kda::AttnArgs a = attn_args(cfg, cache, N, T, cu_seqlens, kv_len);
+    const size_t need = round256(kda::attn_partial_bytes(cfg->head_dim, a));
     if (need && (!ws || ws_bytes < need))
         return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
     if (need) KDA_TRY(check_tensor(ws, "ws", true));
     a.q = q; a.q_row = q_row; a.o = o; a.lse = lse; a.part = need ? (float *)ws : nullptr;
-    a.Hq = cfg->num_q_heads; a.scale = scale * 1.4426950408889634f;
+    a.scale = scale * 1.4426950408889634f;
     a.causal = causal; a.window = window;
-    return launched(kda::launch_attn(cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim, a,
-                                     (hipStream_t)stream), "attention");
+    const bool bf = cfg->io_dtype == KDA_DTYPE_BF16;
+    hipError_t e = hipSuccess;
+    if (a.workers >= 0) e = kda::launch_attn(bf, cfg->head_dim, a, (hipStream_t)stream);
+    if (e == hipSuccess && a.row_units) e = kda::launch_attn_rows(bf, cfg->head_dim, a, (hipStream_t)stream);
+    return launched(e, "attention");
 }
 
 }  // extern "C"

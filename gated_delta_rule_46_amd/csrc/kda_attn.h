@@ -50,16 +50,36 @@ struct AttnArgs {
     int64_t q_row;
     void *o;                     // [T, Hq, D], I/O dtype
     float *lse;                  // [T, Hq] (nullable)
-    float *part;                 // partial results of split units (split > 0)
+    float *part;                 // partial results of split units
     int32_t Hq;
     float scale;                 // of the scores, times log2(e)
     int32_t causal, window;
-    int32_t workers;             // workgroups that share the tiles; 0: one per unit
+    // sequences of at most short_rows query rows per kv head go to kda_attn.hip,
+    // the others to kda_attn_rows.hip
+    int32_t short_rows;
+    int32_t workers;             // kda_attn.hip: workgroups that share the tiles; 0: one per
+                                 // unit; -1: not launched
+    int32_t row_units;           // kda_attn_rows.hip: units per kv head, 0: not launched
+    int32_t row_splits;          // workgroups per unit at most
 };
-// Workgroups for a call (0: no unit is split) and the bytes of their partials.
-int attn_workers(int cus, int N, int64_t T, int G, int Hk, int64_t max_kv);
-size_t attn_partial_bytes(int D, int workers);
+// The plan of a call (short_rows, workers, row_units, row_splits) and the bytes
+// of its partial results.
+void attn_plan(int cus, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a);
+size_t attn_partial_bytes(int D, const AttnArgs &a);
 hipError_t launch_attn(bool bf16, int D, const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_rows(bool bf16, int D, const AttnArgs &a, hipStream_t s);
+
+// Two fp32 values per half word of e4m3 codes (round to nearest even).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    uint32_t r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+__device__ __forceinline__ void uncode4(uint32_t c, float *out) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+    out[0] = a[0]; out[1] = a[1]; out[2] = b[0]; out[3] = b[1];
+}
 
 // Sequence holding packed row r: the last s with cu[s] <= r (skips empty sequences).
 __device__ __forceinline__ int seq_of_row(const int64_t *cu, int N, int64_t r) {

@@ -25,56 +25,18 @@
 // tokens of a dim before the conversion to bf16.  The dims of V are numbered
 // so that a lane's 8 bytes serve the 8 products of its column.
 
-#include "kda_attn.h"
-#include "kda_mfma.h"
+#include <algorithm>
+
+#include "kda_attn_ops.h"
 
 namespace kda {
 namespace {
 
-using mf::bf16_t;
-using mf::bf16x8;
-using mf::f32x4;
-typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+using namespace attn;
 
-constexpr int kAttnThreads = 256;
-constexpr int kWaves = kAttnThreads / 64;
-constexpr int kTile = 64;             // keys per step of a wave
-constexpr int kRows = 16;             // query rows (token, head of the group) per unit
+constexpr int kShortRows = 64;        // most query rows of a sequence that this kernel takes
+constexpr int kSmallCall = 1024;      // query rows of a call that it takes alone
 constexpr int kMinShare = 4;          // fewest tiles worth a workgroup of their own
-constexpr float kLn2 = 0.6931471805599453f;
-
-// bf16 pairs of bytes (0, 1) or (2, 3) of four codes, times 2^(scale's exponent)
-template <bool HI>
-__device__ __forceinline__ uint32_t widen(uint32_t c, float scale) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, HI));
-}
-
-// Row of the packed tokens as the kernel sees a sequence.
-struct Seq {
-    int64_t c0;       // first packed token
-    int64_t kvl;      // cached tokens that the table can hold
-    int64_t pos0;     // position of the first new token
-    int rt;           // units of kRows rows per kv head
-    int lo, tiles;    // tiles of the unmasked range of all its rows; at least one
-    int len;
-};
-
-__device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
-    Seq s;
-    s.c0 = a.kv.cu[n];
-    const int64_t c1 = min(a.kv.cu[n + 1], a.kv.T);
-    const int64_t len = s.c0 < 0 ? 0 : max(c1 - s.c0, (int64_t)0);
-    const int64_t kv = a.kv.kv_len[n];
-    s.len = (int)len;
-    s.pos0 = kv - len;
-    s.kvl = max(min(kv, (int64_t)a.kv.width * a.kv.page), (int64_t)0);
-    s.rt = (int)((len * G + kRows - 1) / kRows);
-    const int64_t first = a.window > 0 ? max(s.pos0 - a.window + 1, (int64_t)0) : 0;
-    s.lo = (int)min(first / kTile, (int64_t)INT32_MAX / 2);
-    s.tiles = max((int)((s.kvl + kTile - 1) / kTile) - s.lo, 1);
-    return s;
-}
 
 template <int D> struct Codes {
     u32x4 k[4][D / 64];      // 4 groups of 16 tokens: 16 bytes of the lane's token each
@@ -126,40 +88,6 @@ __device__ __forceinline__ void load_tile(const AttnArgs &a, const Seq &s, int n
     }
 }
 
-// A operand of V^T for dims (D / 16) m + 4 w + b of token groups g, g + 1.
-template <int B>
-__device__ __forceinline__ bf16x8 v_frag(const uint32_t (&t)[8], float s0, float s1) {
-    // byte B of two tokens side by side: the low pair for even B, the high one for odd
-    constexpr uint32_t sel = B < 2 ? 0x05010400u : 0x07030602u;
-    constexpr bool HI = B & 1;
-    u32x4 r;
-    r[0] = widen<HI>(__builtin_amdgcn_perm(t[1], t[0], sel), s0);
-    r[1] = widen<HI>(__builtin_amdgcn_perm(t[3], t[2], sel), s0);
-    r[2] = widen<HI>(__builtin_amdgcn_perm(t[5], t[4], sel), s1);
-    r[3] = widen<HI>(__builtin_amdgcn_perm(t[7], t[6], sel), s1);
-    return __builtin_bit_cast(bf16x8, r);
-}
-
-template <int NS> struct Frag { bf16x8 f[NS]; };
-
-// fp32 values as NS bf16 terms
-template <int NS>
-__device__ __forceinline__ Frag<NS> split8(const float *x) {
-    Frag<NS> r;
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = x[j];
-#pragma unroll
-    for (int t = 0; t < NS; ++t)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bf16_t h = (bf16_t)y[j];
-            r.f[t][j] = h;
-            if (t + 1 < NS) y[j] -= (float)h;
-        }
-    return r;
-}
-
 // O^T += V^T P^T for one pair of token groups
 template <int D, int NS>
 __device__ __forceinline__ void add_pv(const uint32_t (&v0)[4][D / 64], const uint32_t (&v1)[4][D / 64],
@@ -176,10 +104,6 @@ __device__ __forceinline__ void add_pv(const uint32_t (&v0)[4][D / 64], const ui
             for (int i = 0; i < NS; ++i)
                 o[4 * w + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b], p.f[i], o[4 * w + b], 0, 0, 0);
     }
-}
-
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {   // 0x80 in every byte that is a NaN code
-    return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
 // Where every wave's share of a unit meets: D + 2 floats per row and wave.
@@ -566,13 +490,32 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int attn_workers(int cus, int N, int64_t T, int G, int Hk, int64_t max_kv) {
-    (void)N; (void)T; (void)G; (void)Hk;
-    return max_kv <= 8 * kTile ? 0 : 2 * cus;
+void attn_plan(int cus, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a) {
+    const int G = Hq / Hk;
+    const int64_t rows = T * G;
+    a->workers = -1;
+    a->row_units = 0;
+    a->row_splits = 1;
+    // A single sequence and small calls are of one kind; in others the lengths,
+    // which only the device knows, decide sequence by sequence.
+    const bool all_short = rows <= kShortRows || (N > 1 && rows <= kSmallCall);
+    const bool all_long = N == 1 && !all_short;
+    a->short_rows = all_short ? INT32_MAX : kShortRows;
+    if (!all_long) a->workers = max_kv <= 8 * kTile ? 0 : 2 * cus;
+    if (!all_short) {
+        a->row_units = (int32_t)(rows / kRowTile + N);
+        const int64_t units = (int64_t)a->row_units * Hk;
+        if (units < 2 * cus) {
+            const int64_t want = (4 * (int64_t)cus + units - 1) / units;
+            a->row_splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, 16, max_kv / 1024}));
+        }
+    }
 }
 
-size_t attn_partial_bytes(int D, int workers) {
-    return (size_t)workers * 2 * kRows * (D + 2) * sizeof(float);
+size_t attn_partial_bytes(int D, const AttnArgs &a) {
+    const size_t one = a.workers > 0 ? (size_t)a.workers * 2 * kRows * (D + 2) : 0;
+    const size_t rows = a.row_splits > 1 ? (size_t)a.row_units * a.kv.Hk * a.row_splits * kRowTile * (D + 2) : 0;
+    return std::max(one, rows) * sizeof(float);
 }
 
 hipError_t launch_attn(bool bf16, int D, const AttnArgs &a, hipStream_t s) {

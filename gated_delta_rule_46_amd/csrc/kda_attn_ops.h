@@ -1,0 +1,95 @@
+// kda_attn_ops.h -- what the attention kernels share (kda_attn.hip,
+// kda_attn_rows.hip): a sequence as they see it, codes to bf16, fp32 as bf16 terms.
+#pragma once
+
+#include "kda_attn.h"
+#include "kda_mfma.h"
+
+namespace kda {
+namespace attn {
+
+using mf::bf16_t;
+using mf::bf16x8;
+using mf::f32x4;
+typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kAttnThreads = 256;
+constexpr int kWaves = kAttnThreads / 64;
+constexpr int kTile = 64;             // keys per step
+constexpr int kRows = 16;             // query rows (token, head of the group) per unit of kda_attn.hip
+constexpr int kRowTile = 128;         // and of kda_attn_rows.hip
+constexpr float kLn2 = 0.6931471805599453f;
+
+// bf16 pairs of bytes (0, 1) or (2, 3) of four codes, times 2^(scale's exponent)
+template <bool HI>
+__device__ __forceinline__ uint32_t widen(uint32_t c, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, HI));
+}
+
+// Row of the packed tokens as the kernel sees a sequence.
+struct Seq {
+    int64_t c0;       // first packed token
+    int64_t kvl;      // cached tokens that the table can hold
+    int64_t pos0;     // position of the first new token
+    int rt;           // units of kRows rows per kv head (0: the other kernel's)
+    int lo, tiles;    // tiles of the unmasked range of all its rows; at least one
+    int len;
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
+    Seq s;
+    s.c0 = a.kv.cu[n];
+    const int64_t c1 = min(a.kv.cu[n + 1], a.kv.T);
+    const int64_t len = s.c0 < 0 ? 0 : max(c1 - s.c0, (int64_t)0);
+    const int64_t kv = a.kv.kv_len[n];
+    s.len = (int)len;
+    s.pos0 = kv - len;
+    s.kvl = max(min(kv, (int64_t)a.kv.width * a.kv.page), (int64_t)0);
+    s.rt = len * G <= a.short_rows ? (int)((len * G + kRows - 1) / kRows) : 0;
+    const int64_t first = a.window > 0 ? max(s.pos0 - a.window + 1, (int64_t)0) : 0;
+    s.lo = (int)min(first / kTile, (int64_t)INT32_MAX / 2);
+    s.tiles = max((int)((s.kvl + kTile - 1) / kTile) - s.lo, 1);
+    return s;
+}
+
+// A operand of V^T for dims (D / 16) m + 4 w + b of token groups g, g + 1.
+template <int B>
+__device__ __forceinline__ bf16x8 v_frag(const uint32_t (&t)[8], float s0, float s1) {
+    // byte B of two tokens side by side: the low pair for even B, the high one for odd
+    constexpr uint32_t sel = B < 2 ? 0x05010400u : 0x07030602u;
+    constexpr bool HI = B & 1;
+    u32x4 r;
+    r[0] = widen<HI>(__builtin_amdgcn_perm(t[1], t[0], sel), s0);
+    r[1] = widen<HI>(__builtin_amdgcn_perm(t[3], t[2], sel), s0);
+    r[2] = widen<HI>(__builtin_amdgcn_perm(t[5], t[4], sel), s1);
+    r[3] = widen<HI>(__builtin_amdgcn_perm(t[7], t[6], sel), s1);
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+template <int NS> struct Frag { bf16x8 f[NS]; };
+
+// fp32 values as NS bf16 terms
+template <int NS>
+__device__ __forceinline__ Frag<NS> split8(const float *x) {
+    Frag<NS> r;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = x[j];
+#pragma unroll
+    for (int t = 0; t < NS; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bf16_t h = (bf16_t)y[j];
+            r.f[t][j] = h;
+            if (t + 1 < NS) y[j] -= (float)h;
+        }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {   // 0x80 in every byte that is a NaN code
+    return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -1,0 +1,446 @@
+// kda_attn_rows.hip -- attention of long runs of new tokens (prompts and their
+// chunks) over the 8-bit cache: the formulas of kda_attn.hip with the keys
+// shared by 128 query rows, bound by the matrix cores.
+//
+// A workgroup takes 128 rows (token, head of the group) of one sequence and kv
+// head; each of its four waves owns 32 and keeps their queries, maxima, sums and
+// outputs in registers.  64 keys at a time are staged through LDS, two buffers:
+// while a tile is computed the next one is on its way from HBM in registers.
+// Wave w stages the 16 tokens of group w, so one page lookup serves a wave.
+//
+//   keys    codes as they are, rows of D bytes whose 16-byte pieces are permuted
+//           by the row (XOR) so that 8 lanes reading one piece of 8 rows meet 8
+//           different bank groups;
+//   values  as bf16 operand fragments of V^T (a lane's 16 bytes in lane order):
+//           the byte permutes and conversions are done once per workgroup.
+//
+// S^T = K Q^T on the bf16 matrix instruction, the keys converted by the wave that
+// uses them (codes in LDS are half the LDS traffic of bf16).  The 8-bit matrix
+// instruction would take the codes as they are, with a bf16 query as two e4m3
+// terms (4 + 4 bits), but it sums its products with fewer bits than fp32: scores
+// came out off by 2^-17 of sum |q k|, so it is not used.  With fp32 rows queries
+// and probabilities are three bf16 terms, as in kda_attn.hip.
+//
+// The maximum is followed lazily: outputs are scaled only when some row's
+// maximum grew by more than 2^8 since (probabilities stay below 2^8, which
+// costs neither fp32 sums nor bf16 operands any precision).
+
+#include "kda_attn_ops.h"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kWaveRows = 32;
+constexpr int kMinSplit = 8;          // fewest tiles worth a workgroup of their own
+constexpr float kLag = 8.f;           // growth of a maximum (log2) that rescales
+
+// The unit of a workgroup: rows [row0, row0 + 128) of sequence n, and the tiles
+// [beg, end) that some of them see, shared by `splits` workgroups.
+struct Unit {
+    Seq s;
+    int n, row0, beg, end, splits;
+};
+
+__device__ __forceinline__ bool find_unit(const AttnArgs &a, int64_t x, int G, Unit &u) {
+    // units of sequence n start at first(n) = cu[n] G / 128 + n
+    int lo = 0, hi = a.kv.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.kv.cu[mid] * G / kRowTile + mid <= x) lo = mid; else hi = mid - 1;
+    }
+    u.n = lo;
+    u.s = sequence(a, u.n, G);
+    const int64_t rows = (int64_t)u.s.len * G;
+    const int64_t r = (x - (u.s.c0 * G / kRowTile + u.n)) * kRowTile;
+    if (rows <= a.short_rows || r < 0 || r >= rows) return false;
+    u.row0 = (int)r;
+    const int t0 = u.row0 / G, t1 = min((u.row0 + kRowTile - 1) / G, u.s.len - 1);
+    const int64_t seen = a.causal ? min(u.s.pos0 + t1 + 1, u.s.kvl) : u.s.kvl;
+    const int64_t first = a.window > 0 ? max(u.s.pos0 + t0 - a.window + 1, (int64_t)0) : 0;
+    u.end = (int)((max(seen, (int64_t)0) + kTile - 1) / kTile);
+    u.beg = (int)min(first / kTile, (int64_t)u.end);
+    u.splits = min(a.row_splits, max((u.end - u.beg + kMinSplit - 1) / kMinSplit, 1));
+    return true;
+}
+
+template <int D> struct Stage {
+    uint8_t k[kTile * D];
+    u32x4 v[4][D / 32][64];
+    float kscale[4];                  // of the groups of 16 tokens
+    int ok[4];                        // group has a page
+};
+
+// Piece c (16 bytes) of key row m.
+template <int D>
+__device__ __forceinline__ int k_at(int m, int c) {
+    return D == 128 ? m * 128 + ((c ^ (m & 7)) << 4) : m * 64 + ((c ^ ((m >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ float both_max(float x) {       // over lanes l and l ^ 32
+    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(x), f32_bits(x), false, false);
+    return fmaxf(bits_f32(r[0]), bits_f32(r[1]));
+}
+__device__ __forceinline__ float both_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(x), f32_bits(x), false, false);
+    return bits_f32(r[0]) + bits_f32(r[1]);
+}
+
+// Queries of a lane's row as operand fragments, NS bf16 terms each.
+template <int D, int NS> struct Query {
+    Frag<NS> f[D / 32][2];            // dims 32 i + 16 kg + 8 h + 0..7
+    __device__ void load(const void *q, int64_t at, int kg, bool neg) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[8];
+                mf::IO<NS == 1>::load8(q, at + 32 * i + 16 * kg + 8 * h, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = neg ? -x[j] : x[j];
+                f[i][h] = split8<NS>(x);
+            }
+    }
+    // S^T of tokens 32 tt .. 32 tt + 31
+    __device__ f32x16 scores(const Stage<D> &st, int tt, int lane) const {
+        f32x16 c = {};
+        const int m = 32 * tt + (lane & 31), kg = lane >> 5;
+        const float ks = st.kscale[2 * tt + ((lane >> 4) & 1)];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const u32x4 x = *(const u32x4 *)&st.k[k_at<D>(m, 2 * i + kg)];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 kf;
+                kf[0] = widen<false>(x[2 * h], ks);
+                kf[1] = widen<true>(x[2 * h], ks);
+                kf[2] = widen<false>(x[2 * h + 1], ks);
+                kf[3] = widen<true>(x[2 * h + 1], ks);
+#pragma unroll
+                for (int t = 0; t < NS; ++t)
+                    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf), f[i][h].f[t], c, 0, 0, 0);
+            }
+        }
+        return c;
+    }
+};
+
+// A tile on its way from HBM: wave w holds group w (16 tokens).
+template <int D> struct Flight {
+    u32x4 k[D / 64];
+    uint32_t v[8];
+    float ks, vs;
+    int ok;
+
+    __device__ void load(const AttnArgs &a, int pid, int hk, int64_t at, int lane) {
+        ok = pid >= 0 && pid < a.kv.n_pages;
+        ks = vs = 1.f;
+        if (ok) {
+            const int64_t ph = (int64_t)pid * a.kv.Hk + hk;
+            const int64_t base = (ph * a.kv.page + (int)(at & (a.kv.page - 1))) * D;
+            const uint8_t *kp = a.kv.k_codes + base + lane * 16;
+            const uint8_t *vp = a.kv.v_codes + base + 4 * (lane >> 5) * D + (lane & 31) * (D / 32);
+#pragma unroll
+            for (int r = 0; r < D / 64; ++r) k[r] = *(const u32x4 *)(kp + r * 1024);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint8_t *p = vp + ((i >> 2) * 8 + (i & 3)) * D;
+                if constexpr (D == 128) v[i] = *(const uint32_t *)p;
+                else v[i] = *(const uint16_t *)p;
+            }
+            ks = a.kv.k_scale[ph];
+            vs = a.kv.v_scale[ph];
+        } else {
+#pragma unroll
+            for (int r = 0; r < D / 64; ++r) k[r] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0;
+        }
+    }
+
+    // left: tokens of the group that the sequence has (16 for a whole one)
+    __device__ void store(Stage<D> &st, int *s_nan, int t, int w, int lane, int left) {
+        if (left < 16) {              // what lies behind them on the page is anything
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((i >> 2) * 8 + 4 * (lane >> 5) + (i & 3) >= left) v[i] = 0;
+        }
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bad |= nan_bytes(v[i]);
+        if (bad) *s_nan = t;          // every writer stores the same value
+#pragma unroll
+        for (int r = 0; r < D / 64; ++r) {
+            const int piece = lane + 64 * r;
+            *(u32x4 *)&st.k[k_at<D>(16 * w + piece / (D / 16), piece % (D / 16))] = k[r];
+        }
+        st.v[w][0][lane] = __builtin_bit_cast(u32x4, v_frag<0>(v, vs, vs));
+        st.v[w][1][lane] = __builtin_bit_cast(u32x4, v_frag<1>(v, vs, vs));
+        if constexpr (D == 128) {
+            st.v[w][2][lane] = __builtin_bit_cast(u32x4, v_frag<2>(v, vs, vs));
+            st.v[w][3][lane] = __builtin_bit_cast(u32x4, v_frag<3>(v, vs, vs));
+        }
+        if (lane == 0) {
+            st.kscale[w] = ks;
+            st.ok[w] = ok;
+        }
+    }
+};
+
+template <int D, bool BF>
+__global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const AttnArgs a) {
+    constexpr int NS = BF ? 1 : 3;
+    constexpr int NJ = D / 32;
+    __shared__ __align__(16) Stage<D> stage[2];
+    __shared__ int s_nan[2];
+
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, kg = lane >> 5;
+    const int G = a.Hq / a.kv.Hk;
+    const int hk = blockIdx.x % a.kv.Hk;
+    // the last rows see the most keys: they go first
+    const int64_t y = blockIdx.x / a.kv.Hk;
+    const int split = (int)(y % a.row_splits);
+    Unit u;
+    if (!find_unit(a, a.row_units - 1 - y / a.row_splits, G, u) || split >= u.splits) return;
+    const Seq &s = u.s;
+    const int tiles = u.end - u.beg;
+    const int t0 = u.beg + (int)((int64_t)tiles * split / u.splits);
+    const int t1 = u.beg + (int)((int64_t)tiles * (split + 1) / u.splits);
+
+    // the lane's row, the keys it sees, and what all / any rows of the wave see
+    const int R = u.row0 + kWaveRows * w + col;
+    const bool live = R < s.len * G;
+    const int tok = min(R / G, s.len - 1);
+    const int64_t pos = s.pos0 + tok;
+    const int64_t vis_hi = live ? (a.causal ? min(pos + 1, s.kvl) : s.kvl) : 0;
+    const int64_t vis_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int wt0 = min((u.row0 + kWaveRows * w) / G, s.len - 1);
+    const int wt1 = min((u.row0 + kWaveRows * w + kWaveRows - 1) / G, s.len - 1);
+    const bool wave_live = u.row0 + kWaveRows * w < s.len * G;
+    const int64_t any_hi = wave_live ? (a.causal ? min(s.pos0 + wt1 + 1, s.kvl) : s.kvl) : 0;
+    const int64_t any_lo = a.window > 0 ? s.pos0 + wt0 - a.window + 1 : 0;
+    const int64_t all_hi = a.causal ? min(s.pos0 + wt0 + 1, s.kvl) : s.kvl;
+    const int64_t all_lo = a.window > 0 ? s.pos0 + wt1 - a.window + 1 : 0;
+
+    const float sl = fabsf(a.scale);
+    Query<D, NS> q;
+    q.load(a.q, (s.c0 + tok) * a.q_row + (int64_t)(hk * G + R % G) * D, kg, a.scale < 0.f);
+
+    float m = -__builtin_inff(), l = 0.f;
+    f32x16 o[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) o[j] = f32x16{};
+    if (tid < 2) s_nan[tid] = -1;
+
+    const int shift = __builtin_ctz(a.kv.page);
+    const int32_t *table = a.kv.table + (int64_t)u.n * a.kv.width;
+    auto page_of = [&](int t) {
+        const int64_t at = (int64_t)t * kTile + 16 * w;
+        return t < t1 && at < s.kvl ? table[at >> shift] : -1;
+    };
+    auto left_of = [&](int t) {
+        return (int)min(max(s.kvl - ((int64_t)t * kTile + 16 * w), (int64_t)0), (int64_t)16);
+    };
+    Flight<D> fl;
+    int pid = page_of(t0);
+    if (t0 < t1) {
+        fl.load(a, pid, hk, (int64_t)t0 * kTile + 16 * w, lane);
+        pid = page_of(t0 + 1);
+        __syncthreads();                       // s_nan
+        fl.store(stage[t0 & 1], &s_nan[t0 & 1], t0, w, lane, left_of(t0));
+    }
+    __syncthreads();
+
+    for (int t = t0; t < t1; ++t) {
+        const Stage<D> &st = stage[t & 1];
+        const int64_t kb = (int64_t)t * kTile;
+        const bool more = t + 1 < t1;
+        if (more) {
+            fl.load(a, pid, hk, kb + kTile + 16 * w, lane);
+            pid = page_of(t + 2);
+        }
+        if (kb < any_hi && kb + kTile > any_lo) {
+            f32x16 sc[2] = {q.scores(st, 0, lane), q.scores(st, 1, lane)};
+            const int okm = st.ok[0] & st.ok[1] & st.ok[2] & st.ok[3];
+            const bool full = okm && kb >= all_lo && kb + kTile <= all_hi;
+            uint32_t sees = ~0u;               // bit 16 tt + i
+            if (!full) {
+                const int lo = (int)min(max(vis_lo - kb, (int64_t)0), (int64_t)kTile);
+                const int hi = (int)min(max(vis_hi - kb, (int64_t)0), (int64_t)kTile);
+                const int gm = st.ok[0] | st.ok[1] << 1 | st.ok[2] << 2 | st.ok[3] << 3;
+                sees = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int j = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * kg + (i & 3);
+                    const bool v = j >= lo && j < hi && (gm >> (j >> 4) & 1);
+                    sees |= (uint32_t)v << i;
+                    if (!v) sc[i >> 4][i & 15] = -__builtin_inff();
+                }
+            }
+            float mx = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, sc[i >> 4][i & 15]);
+            mx = both_max(mx);
+            mx = mx == -__builtin_inff() ? mx : mx * sl;
+            if (__ballot(mx > m + kLag) != 0) {
+                const float mn = fmaxf(m, mx);
+                const float f = mf::ex2(m - (mn == -__builtin_inff() ? 0.f : mn));
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) o[j] *= f;
+            }
+            const float ms = m == -__builtin_inff() ? 0.f : m;
+            float p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) p[i] = mf::ex2(__builtin_fmaf(sc[i >> 4][i & 15], sl, -ms));
+            bool repair = false;
+            if (!full) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) p[i] = sees >> i & 1 ? p[i] : 0.f;
+                repair = s_nan[t & 1] == t;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) l += p[i];
+            if (repair) {
+                // A NaN among the values reaches only the rows that see it: the products
+                // take zeros in its place, and 1 x (row sees it) counts it.
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    f32x16 cnt = {};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        u32x4 x = st.v[k][j][lane], one;
+                        float vis[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t lo = (x[i] & 0x7fffu) > 0x7f80u, hi = (x[i] & 0x7fff0000u) > 0x7f800000u;
+                            one[i] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
+                            x[i] &= ~((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) vis[i] = sees >> (8 * k + i) & 1 ? 1.f : 0.f;
+                        cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, one),
+                                                                      split8<1>(vis).f[0], cnt, 0, 0, 0);
+                        const Frag<NS> pf = split8<NS>(p + 8 * k);
+#pragma unroll
+                        for (int i = 0; i < NS; ++i)
+                            o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), pf.f[i], o[j],
+                                                                           0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (cnt[i] > 0.f) o[j][i] = __builtin_nanf("");
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const Frag<NS> pf = split8<NS>(p + 8 * k);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const u32x4 x = st.v[k][j][lane];
+                        const bf16x8 vf = __builtin_bit_cast(bf16x8, x);
+#pragma unroll
+                        for (int i = 0; i < NS; ++i)
+                            o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf.f[i], o[j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        if (more) fl.store(stage[(t + 1) & 1], &s_nan[(t + 1) & 1], t + 1, w, lane, left_of(t + 1));
+        __syncthreads();
+    }
+
+    l = both_sum(l);
+    if (!live) return;
+    constexpr int E = D / 8;                   // contiguous dims per group of 4 results
+    if (u.splits == 1) {
+        const int64_t row = (s.c0 + tok) * a.Hq + hk * G + R % G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float z[E];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) z[NJ * i + j] = o[j][4 * e + i] * inv;
+#pragma unroll
+            for (int i = 0; i < E; i += 8) mf::IO<BF>::store8(a.o, row * D + 2 * E * e + E * kg + i, z + i);
+        }
+        if (a.lse && kg == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+        float *dst = a.part + (int64_t)blockIdx.x * (kRowTile * (D + 2));
+        const int r = kWaveRows * w + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float z[E];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) z[NJ * i + j] = o[j][4 * e + i];
+#pragma unroll
+            for (int i = 0; i < E; i += 8) mf::IO<false>::store8(dst, r * D + 2 * E * e + E * kg + i, z + i);
+        }
+        if (kg == 0) { dst[kRowTile * D + r] = m; dst[kRowTile * (D + 1) + r] = l; }
+    }
+}
+
+// Joins the splits of a unit: D / 8 threads take a row.
+template <int D, bool BF>
+__global__ __launch_bounds__(kAttnThreads) void join_rows_kernel(const AttnArgs a) {
+    constexpr int RP = kAttnThreads / (D / 8);          // rows per workgroup
+    const int G = a.Hq / a.kv.Hk;
+    const int64_t x = blockIdx.x / (kRowTile / RP);
+    const int hk = (int)(x % a.kv.Hk);
+    const int64_t y = x / a.kv.Hk;
+    Unit u;
+    if (!find_unit(a, a.row_units - 1 - y, G, u) || u.splits == 1) return;
+    const int r = (int)(blockIdx.x % (kRowTile / RP)) * RP + threadIdx.x / (D / 8), d = threadIdx.x % (D / 8) * 8;
+    const int R = u.row0 + r;
+    if (R >= u.s.len * G) return;
+    float M = -__builtin_inff(), L = 0.f, z[8] = {};
+    for (int i = 0; i < u.splits; ++i) {
+        const float *src = a.part + ((y * a.row_splits + i) * a.kv.Hk + hk) * (kRowTile * (D + 2));
+        const float m = src[kRowTile * D + r], l = src[kRowTile * (D + 1) + r];
+        const float mn = fmaxf(M, m), ms = mn == -__builtin_inff() ? 0.f : mn;
+        const float f0 = mf::ex2(M - ms), f1 = mf::ex2(m - ms);
+        float v[8];
+        mf::load8f(src + r * D + d, v);
+        M = mn;
+        L = L * f0 + l * f1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = z[j] * f0 + v[j] * f1;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] *= inv;
+    const int64_t row = (u.s.c0 + R / G) * a.Hq + hk * G + R % G;
+    mf::IO<BF>::store8(a.o, row * D + d, z);
+    if (a.lse && d == 0) a.lse[row] = L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+template <int D, bool BF>
+hipError_t launch(const AttnArgs &a, hipStream_t s) {
+    const int64_t units = (int64_t)a.row_units * a.kv.Hk;
+    const int64_t per = kRowTile / (kAttnThreads / (D / 8));
+    if (units * a.row_splits > INT32_MAX || units * per > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((rows_kernel<D, BF>), dim3((unsigned)(units * a.row_splits)), dim3(kAttnThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.row_splits == 1) return e;
+    hipLaunchKernelGGL((join_rows_kernel<D, BF>), dim3((unsigned)(units * per)), dim3(kAttnThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_rows(bool bf16, int D, const AttnArgs &a, hipStream_t s) {
+    if (D == 128) return bf16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    if (D == 64) return bf16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace kda

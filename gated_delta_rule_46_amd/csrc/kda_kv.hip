@@ -27,12 +27,6 @@ constexpr int kKvThreads = 256;
 constexpr int kScaleExpMin = -100, kScaleExpMax = 119;
 constexpr float kCodeMax = 448.f;
 
-// Two fp32 values per half word of e4m3 codes (round to nearest even).
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-    uint32_t r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
-}
-
 // x limited to the code range; a NaN stays (both comparisons fail).
 __device__ __forceinline__ float limited(float x) {
     x = x > kCodeMax ? kCodeMax : x;
@@ -49,12 +43,6 @@ __device__ __forceinline__ int scale_exp(float amax) {
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return bits_f32((uint32_t)(e + 127) << 23); }
-
-__device__ __forceinline__ void uncode4(uint32_t c, float *out) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
-    out[0] = a[0]; out[1] = a[1]; out[2] = b[0]; out[3] = b[1];
-}
 
 // Workgroup x of the page axis -> a sequence and one of the pages that its new
 // tokens touch.  A sequence of len tokens touches at most (len - 1) / page + 2

@@ -336,6 +336,48 @@ def test_attn_rows(K, dtype, D, page, Hk, G, causal, window):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,page,Hk,G", [(128, 64, 1, 4), (64, 16, 2, 2), (128, 128, 1, 3), (64, 32, 1, 8), (128, 16, 1, 1)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (False, 0), (True, 7)])
+def test_attn_prompts(K, dtype, D, page, Hk, G, causal, window):
+    """Prompts and chunks long enough for units of 128 rows beside short ones and an empty sequence."""
+    say(f"attn prompts {dtype} D={D} page={page} Hk={Hk} G={G} causal={causal} window={window}")
+    new = [1, 300, 0, 65, 620, 3]
+    kv = [40, 300, 20, 411, 1500, 130]
+    m, rng = plain_model(K, dtype, Hk, D, page, kv, 6 + D + G + window)
+    attn_check(K, m, dtype, queries(rng, sum(new), Hk * G, D, dtype), cum(new), kv, D ** -0.5, causal, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,kv,window", [(33, 33, 0), (129, 4200, 0), (257, 70, 0), (64, 2100, 200)])
+def test_attn_one_sequence(K, dtype, new, kv, window):
+    """A sequence alone: a prompt, a chunk that is split over the keys, more rows than keys, a window."""
+    say(f"attn one sequence {dtype} new={new} kv={kv} window={window}")
+    m, rng = plain_model(K, dtype, 2, 128, 64, [kv], new)
+    attn_check(K, m, dtype, queries(rng, new, 8, 128, dtype), [0, new], [kv], 0.1, True, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attn_prompt_queries_of_all_sizes(K, dtype):
+    """Query elements from 2^-40 to 2^30 in one row, rows of zeros, NaN and infinite queries."""
+    import torch
+    say(f"attn query sizes {dtype}")
+    new, kv, D = 200, 330, 128
+    m, rng = plain_model(K, dtype, 1, D, 64, [kv], 51)
+    q = queries(rng, new, 2, D, dtype).clone()
+    q *= torch.exp2(torch.randint(-8, 5, q.shape, device="cuda")).to(q.dtype)
+    q[10] = 0
+    q[11] *= 2.0 ** -100
+    q[12, 0, ::3] *= 2.0 ** -30
+    attn_check(K, m, dtype, q, [0, new], [kv], 0.02)
+    q[20, 0, 7], q[21, 1, 9], q[22, 0] = float("nan"), float("inf"), float("-inf")
+    o, lse = K.kda_attn(q, i64([0, new]), i64([kv]), m.gpu, want_lse=True)
+    bad = torch.zeros(new, 2, dtype=torch.bool, device="cuda")
+    bad[20, 0] = bad[21, 1] = bad[22, 0] = True
+    assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
+    assert torch.equal(torch.isnan(lse), bad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attn_rows_that_see_nothing(K, dtype):
     """kv_len below the new tokens, absent pages, a table that ends early, padded rows: o = 0 and lse =
     -inf for rows without keys, rows behind the last sequence untouched."""
@@ -403,6 +445,29 @@ def test_attn_hidden_nan_and_extremes(K, dtype, width):
     attn_check(K, m, dtype, queries(rng, 41, 4, 64, dtype), cum(new), kv, 8.0, name="scores of hundreds")
     attn_check(K, m, dtype, queries(rng, 41, 4, 64, dtype), cum(new), kv, 0.0, name="scale 0")
     attn_check(K, m, dtype, queries(rng, 41, 4, 64, dtype), cum(new), kv, -0.125, name="negative scale")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_attn_prompt_hidden_nan(K, dtype, page):
+    """NaN keys and values in a prompt and its context reach exactly the rows that see them."""
+    import torch
+    say(f"attn prompt NaN {dtype} page={page}")
+    new, kv, D = 150, 300, 128
+    m, rng = plain_model(K, dtype, 1, D, page, [kv], 61)
+    for half, pos, d, code in (("v", 205, 5, 0x7F), ("v", 206, 127, 0xFF), ("k", 280, 3, 0x7F), ("v", 299, 64, 0x7F)):
+        c = m.keys if half == "k" else m.values
+        pid = c.pid(0, pos)
+        getattr(m.gpu, half)[pid, 0, pos % page, d] = code
+        c.codes[pid, 0, pos % page, d] = np.nan
+    q = queries(rng, new, 4, D, dtype)
+    for window in (0, 20):
+        o, lse = K.kda_attn(q, i64([0, new]), i64([kv]), m.gpu, window=window, want_lse=True)
+        torch.cuda.synchronize()
+        ro, rl, _, _ = A.attn(to_numpy_f64(q), [0, new], [kv], m.keys, m.values, D ** -0.5, True, window)
+        assert np.isnan(ro).any() and not np.isnan(ro).all()
+        assert np.array_equal(np.isnan(to_numpy_f64(o)), np.isnan(ro))
+        assert np.array_equal(np.isnan(to_numpy_f64(lse)), np.isnan(rl))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
