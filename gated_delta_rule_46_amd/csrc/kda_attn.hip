@@ -36,31 +36,46 @@ using namespace attn;
 
 constexpr int kShortRows = 64;        // most query rows of a sequence that this kernel takes
 constexpr int kSmallCall = 1024;      // query rows of a call that it takes alone
-constexpr int kMinShare = 4;          // fewest tiles worth a workgroup of their own
+constexpr int kMinShare = 4;          // fewest tiles worth a workgroup of their own (one per wave)
 
+// A tile's codes in a wave's registers, as the products read them.
 template <int D> struct Codes {
-    u32x4 k[4][D / 64];      // 4 groups of 16 tokens: 16 bytes of the lane's token each
+    u32x4 k[4][D / 64];         // 4 groups of 16 tokens: 16 bytes of the lane's token each
     uint32_t v[4][4][D / 64];   // 4 groups, 4 tokens: D / 16 bytes each
     float ks[4], vs[4];
-    int ok;                  // groups with a page
+    int ok;                     // groups with a page
 };
 
+// The pages of a tile's four groups, looked up one tile ahead of its codes.
+struct Pages { int id[4]; };
+
+// Tables and scales are only read here: loads of one value for the whole wave.
+template <typename T> __device__ __forceinline__ T uniform_load(const T *p) {
+    return *(const __attribute__((address_space(4))) T *)p;
+}
+
+__device__ __forceinline__ Pages pages_of(const int32_t *table, int shift, int kvl, int t, int t_end) {
+    Pages p;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int at = t * kTile + 16 * g;
+        p.id[g] = t < t_end && at < kvl ? uniform_load(table + (at >> shift)) : -1;
+    }
+    return p;
+}
+
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs &a, const Seq &s, int n, int hk, int64_t kb,
-                                          int lane, Codes<D> &c) {
+__device__ __forceinline__ void load_tile(const AttnArgs &a, const Pages &pg, int hk, int t, int lane, Codes<D> &c) {
     const int col = lane & 15, kg = lane >> 4;
     c.ok = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        const int64_t at = kb + 16 * g;
-        int pid = -1;
-        if (at < s.kvl) pid = a.kv.table[(int64_t)n * a.kv.width + at / a.kv.page];
-        pid = __builtin_amdgcn_readfirstlane(pid);
+        const int pid = pg.id[g];
         c.ks[g] = c.vs[g] = 1.f;
         if (pid >= 0 && pid < a.kv.n_pages) {
             c.ok |= 1 << g;
             const int64_t ph = (int64_t)pid * a.kv.Hk + hk;
-            const int64_t base = (ph * a.kv.page + at % a.kv.page) * D;
+            const int64_t base = (ph * a.kv.page + ((t * kTile + 16 * g) & (a.kv.page - 1))) * D;
             const uint8_t *kp = a.kv.k_codes + base + col * D + kg * 16;
             const uint8_t *vp = a.kv.v_codes + base + (4 * kg) * D + col * (D / 16);
 #pragma unroll
@@ -75,8 +90,8 @@ __device__ __forceinline__ void load_tile(const AttnArgs &a, const Seq &s, int n
                     c.v[g][i][0] = *(const uint32_t *)(vp + i * D);
                 }
             }
-            c.ks[g] = a.kv.k_scale[ph];
-            c.vs[g] = a.kv.v_scale[ph];
+            c.ks[g] = uniform_load(a.kv.k_scale + ph);
+            c.vs[g] = uniform_load(a.kv.v_scale + ph);
         } else {
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) c.k[g][i] = u32x4{0, 0, 0, 0};
@@ -106,246 +121,323 @@ __device__ __forceinline__ void add_pv(const uint32_t (&v0)[4][D / 64], const ui
     }
 }
 
+// Tiles per workgroup when `workers` of them share all.
+__device__ __forceinline__ int64_t share_of(int64_t total, int workers) {
+    return max((total + workers - 1) / workers, (int64_t)kMinShare);
+}
+
+// x / y, the usual case in 32 bits
+__device__ __forceinline__ uint32_t quotient(int64_t x, int y) {
+    return x >> 32 ? (uint32_t)(x / y) : (uint32_t)x / (uint32_t)y;
+}
+
 // Where every wave's share of a unit meets: D + 2 floats per row and wave.
 template <int D> struct Meet {
     float o[kWaves][kRows][D + 4];
     float m[kWaves][kRows], l[kWaves][kRows];
 };
 
-// BF: bf16 rows.  One workgroup takes a contiguous share of all (unit, tile)
-// pairs, or, with workers = 0, one unit; its waves take the tiles of a unit in
-// turn and meet in LDS at the unit's end.
-template <int D, bool BF>
-__global__ __launch_bounds__(kAttnThreads) void attn_kernel(const AttnArgs a) {
-    constexpr int NS = BF ? 1 : 3;
-    constexpr int NF = D / 32;                 // contraction steps of Q K^T
-    constexpr int NT = D / 16;                 // 16-dim blocks of O
-    __shared__ Meet<D> sm;
-    __shared__ int64_t s_scan[kWaves];
+// The lane's query row of a unit and the keys it sees.
+template <int D, int NS> struct Row {
+    Frag<NS> q[D / 32];
+    int lo, hi;               // keys lo <= j < hi
+    int all_lo, all_hi;       // keys that every row of the unit sees
+
+    __device__ void load(const AttnArgs &a, const Seq &s, int rb, int hk, int G, int lane) {
+        const int kg = lane >> 4;
+        const int R = rb * kRows + (lane & 15);
+        const int tok = min(R / G, s.len - 1), gh = R % G;
+        const int64_t qi = (s.c0 + tok) * a.q_row + (int64_t)(hk * G + gh) * D;
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+            float x[8];
+            mf::IO<NS == 1>::load8(a.q, qi + (f >> 1) * 64 + kg * 16 + (f & 1) * 8, x);
+            q[f] = split8<NS>(x);
+        }
+        const int t0 = rb * kRows / G, t1 = min((rb * kRows + kRows - 1) / G, s.len - 1);
+        hi = R < s.len * G ? s.end_of(a, tok) : 0;
+        lo = s.begin_of(a, tok);
+        all_hi = s.end_of(a, t0);
+        all_lo = s.begin_of(a, t1);
+    }
+};
+
+// One tile of 64 keys for the 16 rows of a unit.  True: values that were NaN are left
+// out, see_nans() is to follow.
+template <int D, int NS>
+__device__ __forceinline__ bool tile_step(const Row<D, NS> &row, Codes<D> &c, int t, float scale, int lane, float &m,
+                                          float &l, f32x4 *o) {
+    constexpr int NT = D / 16;
+    const int kg = lane >> 4, kb = t * kTile;
+    f32x4 sc[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        sc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+            const u32x4 x = c.k[g][f >> 1];
+            const uint32_t c0 = (f & 1) ? x[2] : x[0], c1 = (f & 1) ? x[3] : x[1];
+            u32x4 kf;
+            kf[0] = widen<false>(c0, c.ks[g]);
+            kf[1] = widen<true>(c0, c.ks[g]);
+            kf[2] = widen<false>(c1, c.ks[g]);
+            kf[3] = widen<true>(c1, c.ks[g]);
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), row.q[f].f[i], sc[g],
+                                                                0, 0, 0);
+        }
+    }
+    const bool full = c.ok == 15 && kb >= row.all_lo && kb + kTile <= row.all_hi;
+    float tm = -__builtin_inff();
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x = sc[g][i] * scale;
+            if (!full) {
+                const int j = kb + 16 * g + 4 * kg + i;
+                const bool y = j >= row.lo && j < row.hi && (c.ok >> g & 1);
+                x = y ? x : -__builtin_inff();
+            }
+            sc[g][i] = x;
+            tm = fmaxf(tm, x);
+        }
+    tm = fmaxf(tm, __shfl_xor(tm, 16));
+    tm = fmaxf(tm, __shfl_xor(tm, 32));
+    if (__ballot(tm > m) != 0) {
+        const float mn = fmaxf(m, tm);
+        const float alpha = mf::ex2(m - (mn == -__builtin_inff() ? 0.f : mn));
+        m = mn;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i] *= alpha;
+    }
+    const float ms = m == -__builtin_inff() ? 0.f : m;
+    float p[16];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[4 * g + i] = mf::ex2(sc[g][i] - ms);
+            l += p[4 * g + i];
+        }
+
+    bool repair = false;
+    if (!full) {
+        // a NaN among the values would reach rows that do not see it (0 x NaN)
+        uint32_t any = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    const uint32_t b = nan_bytes(c.v[g][i][j]);
+                    any |= b;
+                    c.v[g][i][j] &= ~((b >> 7) * 0xffu);
+                }
+        repair = __ballot(any != 0) != 0;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; g += 2)
+        add_pv<D, NS>(c.v[g], c.v[g + 1], c.vs[g], c.vs[g + 1], split8<NS>(p + 4 * g), o);
+    return repair;
+}
+
+// NaN into the outputs of the lane's row whose values are NaN at a key lo <= j < hi.
+template <int D>
+__device__ __forceinline__ void see_nans(const AttnArgs &a, const int32_t *table, int shift, int hk, int lo, int hi, int kg,
+                                         f32x4 *o) {
+    constexpr int NT = D / 16;
+#pragma unroll 1
+    for (int j = lo; j < hi; ++j) {
+        const int pid = table[j >> shift];
+        if (pid < 0 || pid >= a.kv.n_pages) continue;
+        const int64_t row = ((int64_t)pid * a.kv.Hk + hk) * a.kv.page + (j & (a.kv.page - 1));
+        const uint32_t *p = (const uint32_t *)(a.kv.v_codes + row * D + kg * (D / 4));
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {            // dims (D / 16)(4 kg + i) + j of the lane
+            const uint32_t b = nan_bytes(p[x]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (b >> (8 * y) & 0x80) o[(4 * x + y) % NT][(4 * x + y) / NT] = __builtin_nanf("");
+        }
+    }
+}
+
+template <bool BF, int E>
+__device__ __forceinline__ void store_row(void *o, int64_t at, const float *y, float f) {
+    float z[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) z[j] = y[j] * f;
+    if constexpr (E == 8) {
+        mf::IO<BF>::store8(o, at, z);
+    } else if constexpr (BF) {
+        *(mf::bf16x4 *)((bf16_t *)o + at) = mf::Ops<true>::cvt4(f32x4{z[0], z[1], z[2], z[3]});
+    } else {
+        *(f32x4 *)((float *)o + at) = f32x4{z[0], z[1], z[2], z[3]};
+    }
+}
+
+// The tiles of all units in a row: their number, and where sequence `of` (>= 0) or
+// tile `from` (of < 0) lies; n: that sequence, base: the tiles before it.
+struct Place { int64_t total, base; int n; };
+
+__device__ __forceinline__ Place place(const AttnArgs &a, int G, int of, int block, int tid) {
+    __shared__ int64_t s_sum[kWaves];
     __shared__ int64_t s_base;
     __shared__ int s_n;
+    const int lane = tid & 63, w = tid >> 6, N = a.kv.N;
+    // first: up to 256 sequences at a time, in order; the usual call ends after one
+    int64_t mine = 0, inc = 0, total = 0;
+    for (int n0 = 0; n0 < N; n0 += kAttnThreads) {
+        int64_t c = 0;
+        if (n0 + tid < N) c = sequence(a, n0 + tid, G).cost(a);
+        int64_t x = c;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int64_t y = __shfl_up(x, off);
+            if (lane >= off) x += y;
+        }
+        if (n0 > 0) __syncthreads();
+        if (lane == 63) s_sum[w] = x;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            if (i < w) x += s_sum[i];
+        }
+        mine = c;
+        inc = total + x;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) total += s_sum[i];
+        if (of >= n0 && of < n0 + kAttnThreads && tid == of - n0) { s_base = inc - c; s_n = of; }
+    }
+    Place p;
+    p.total = total;
+    if (of < 0) {
+        const int64_t from = share_of(total, a.workers) * block;
+        if (N <= kAttnThreads) {
+            if (inc - mine <= from && from < inc) { s_base = inc - mine; s_n = tid; }
+        } else if (from < total) {          // again, now that the total is known
+            int64_t before = 0;
+            for (int n0 = 0; n0 < N && before <= from; n0 += kAttnThreads) {
+                int64_t c = 0;
+                if (n0 + tid < N) c = sequence(a, n0 + tid, G).cost(a);
+                int64_t x = c;
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const int64_t y = __shfl_up(x, off);
+                    if (lane >= off) x += y;
+                }
+                __syncthreads();
+                if (lane == 63) s_sum[w] = x;
+                __syncthreads();
+                x += before;
+#pragma unroll
+                for (int i = 0; i < kWaves; ++i) {
+                    if (i < w) x += s_sum[i];
+                    before += s_sum[i];
+                }
+                if (x - c <= from && from < x) { s_base = x - c; s_n = n0 + tid; }
+            }
+        }
+    }
+    __syncthreads();
+    p.base = s_base;
+    p.n = s_n;
+    return p;
+}
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+// The sequence and unit of number x in the order of the packed rows: sequence n's
+// units start at first(n) = cu[n] G / kRows + n (at least as many apart as it has).
+__device__ __forceinline__ bool packed_unit(const AttnArgs &a, int64_t x, int G, int &n, Seq &s, int &rb) {
+    int lo = 0, hi = a.kv.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.kv.cu[mid] * G / kRows + mid <= x) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+    s = sequence(a, n, G);
+    const int64_t r = x - (s.c0 * G / kRows + n);
+    rb = (int)r;
+    return r >= 0 && r < s.rt;
+}
+
+// BF: bf16 rows.  One workgroup takes a contiguous share of all (unit, tile)
+// pairs, or, with workers = 0, one unit; its waves take the tiles of a unit in
+// turn, each with its next tile on the way from HBM, and meet in LDS at the end.
+template <int D, bool BF>
+__global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void attn_kernel(const AttnArgs a) {
+    constexpr int NS = BF ? 1 : 3;
+    constexpr int NT = D / 16;                 // 16-dim blocks of O
+    __shared__ Meet<D> sm;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, kg = lane >> 4;
     const int G = a.Hq / a.kv.Hk;
-    const int N = a.kv.N;
+    const int shift = __builtin_ctz(a.kv.page);
 
-    // this workgroup's share [from, to) of the tiles of all units; n0: the
-    // sequence that holds `from`, base: the tiles before that sequence
+    // this workgroup's share [from, to) of the tiles
     int64_t from, to, base = 0;
     int n = 0;
+    Seq s;
     if (a.workers == 0) {
-        // units are numbered like the packed rows: first(n) = cu[n] G / kRows + n
-        const int64_t x = blockIdx.x / a.kv.Hk;
-        int lo = 0, hi = N - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.kv.cu[mid] * G / kRows + mid <= x) lo = mid; else hi = mid - 1;
-        }
-        n = lo;
-        const Seq s = sequence(a, n, G);
-        const int64_t r = x - (s.c0 * G / kRows + n);
-        if (r < 0 || r >= s.rt) return;
-        from = ((int64_t)(blockIdx.x % a.kv.Hk) * s.rt + r) * s.tiles;
+        int rb;
+        if (!packed_unit(a, blockIdx.x / a.kv.Hk, G, n, s, rb)) return;
+        from = (int64_t)((int)(blockIdx.x % a.kv.Hk) * s.rt + rb) * s.tiles;
         to = from + s.tiles;
     } else {
-        // total, then the sequence in which the share starts
-        int64_t total = 0;
-        for (int n0 = 0; n0 < N; n0 += kAttnThreads) {
-            int64_t c = 0;
-            if (n0 + tid < N) {
-                const Seq s = sequence(a, n0 + tid, G);
-                c = (int64_t)a.kv.Hk * s.rt * s.tiles;
-            }
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) c += __shfl_xor(c, off);
-            if (lane == 0) s_scan[w] = c;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kWaves; ++i) total += s_scan[i];
-            __syncthreads();
-        }
-        const int64_t share = max((total + a.workers - 1) / a.workers, (int64_t)kMinShare);
+        const Place p = place(a, G, -1, blockIdx.x, tid);
+        const int64_t share = share_of(p.total, a.workers);
         from = share * blockIdx.x;
-        to = min(from + share, total);
+        to = min(from + share, p.total);
         if (from >= to) return;
-        int64_t before = 0;
-        for (int n0 = 0; n0 < N; n0 += kAttnThreads) {
-            int64_t c = 0;
-            if (n0 + tid < N) {
-                const Seq s = sequence(a, n0 + tid, G);
-                c = (int64_t)a.kv.Hk * s.rt * s.tiles;
-            }
-            int64_t inc = c;
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const int64_t y = __shfl_up(inc, off);
-                if (lane >= off) inc += y;
-            }
-            if (lane == 63) s_scan[w] = inc;
-            __syncthreads();
-            for (int i = 0; i < kWaves; ++i) {
-                if (i < w) inc += s_scan[i];
-            }
-            inc += before;
-            if (inc - c <= from && from < inc) {
-                s_n = n0 + tid;
-                s_base = inc - c;
-            }
-            for (int i = 0; i < kWaves; ++i) before += s_scan[i];
-            __syncthreads();
-            if (before > from) break;
-        }
-        n = s_n;
-        base = s_base;
+        n = p.n;
+        base = p.base;
+        s = sequence(a, n, G);
     }
 
-    for (int64_t at = from; at < to; ++n) {
-        const Seq s = sequence(a, n, G);
-        const int64_t end = base + (int64_t)a.kv.Hk * s.rt * s.tiles;   // of this sequence
+    for (int64_t at = from; at < to; s = sequence(a, ++n, G)) {
+        const int64_t end = base + s.cost(a);  // of this sequence
+        const int32_t *table = a.kv.table + (int64_t)n * a.kv.width;
         while (at < to && at < end) {
-            const int64_t rel = at - base;
-            const int unit = (int)(rel / s.tiles);
-            const int64_t ubase = base + (int64_t)unit * s.tiles;
-            const int t_lo = s.lo + (int)(at - ubase);
-            const int64_t uend = ubase + s.tiles;
-            const int t_hi = s.lo + (int)(min(uend, to) - ubase);
-            const int hk = unit / s.rt, rb = unit % s.rt;
+            const uint32_t unit = quotient(at - base, s.tiles);
+            const int64_t ubase = base + (int64_t)unit * s.tiles, uend = ubase + s.tiles;
+            const int hk = (int)(unit / (uint32_t)s.rt), rb = (int)(unit % (uint32_t)s.rt);
             const bool whole = ubase >= from && uend <= to;
-
-            // the lane's query row and the keys it sees
-            const int R = rb * kRows + col;
-            const int tok = min(R / G, s.len - 1), gh = R % G;
-            const bool live = R < s.len * G;
-            const int64_t pos = s.pos0 + tok;
-            const int64_t vis_hi = live ? (a.causal ? min(pos + 1, s.kvl) : s.kvl) : 0;
-            const int64_t vis_lo = a.window > 0 ? pos - a.window + 1 : 0;
-            Frag<NS> q[NF];
-            {
-                const int64_t qi = (s.c0 + tok) * a.q_row + (int64_t)(hk * G + gh) * D;
-#pragma unroll
-                for (int f = 0; f < NF; ++f) {
-                    float x[8];
-                    mf::IO<BF>::load8(a.q, qi + (f >> 1) * 64 + kg * 16 + (f & 1) * 8, x);
-                    q[f] = split8<NS>(x);
-                }
-            }
-            // tiles that some row of the unit sees
-            const int tok_last = min((rb * kRows + kRows - 1) / G, s.len - 1);
-            const int64_t seen = a.causal ? min(s.pos0 + tok_last + 1, s.kvl) : s.kvl;
-            const int64_t all_lo = a.window > 0 ? s.pos0 + tok_last - a.window + 1 : 0;
-            const int64_t all_hi = a.causal ? min(s.pos0 + rb * kRows / G + 1, s.kvl) : s.kvl;
-            const int t_end = min(t_hi, (int)((max(seen, (int64_t)0) + kTile - 1) / kTile));
-            const int64_t first = a.window > 0 ? max(s.pos0 + rb * kRows / G - a.window + 1, (int64_t)0) : 0;
-            const int t_beg = max(t_lo, (int)min(first / kTile, (int64_t)INT32_MAX / 2));
+            // its tiles here, less those that no row of the unit sees
+            const int t0 = min(rb * kRows / G, s.len - 1), t1 = min((rb * kRows + kRows - 1) / G, s.len - 1);
+            const int beg = max(s.lo + (int)(at - ubase), s.begin_of(a, t0) / kTile);
+            const int stop = min(s.lo + (int)(min(uend, to) - ubase), (s.end_of(a, t1) + kTile - 1) / kTile);
 
             float m = -__builtin_inff(), l = 0.f;
             f32x4 o[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-            for (int t = t_beg + w; t < t_end; t += kWaves) {
-                const int64_t kb = (int64_t)t * kTile;
-                Codes<D> c;
-                load_tile<D>(a, s, n, hk, kb, lane, c);
-                f32x4 sc[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    sc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int f = 0; f < NF; ++f) {
-                        const u32x4 x = c.k[g][f >> 1];
-                        const uint32_t c0 = (f & 1) ? x[2] : x[0], c1 = (f & 1) ? x[3] : x[1];
-                        u32x4 kf;
-                        kf[0] = widen<false>(c0, c.ks[g]);
-                        kf[1] = widen<true>(c0, c.ks[g]);
-                        kf[2] = widen<false>(c1, c.ks[g]);
-                        kf[3] = widen<true>(c1, c.ks[g]);
-#pragma unroll
-                        for (int i = 0; i < NS; ++i)
-                            sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, kf), q[f].f[i], sc[g], 0, 0, 0);
-                    }
+            Row<D, NS> row;
+            Codes<D> c0, c1;
+            int t = beg + w;
+            if (t < stop) load_tile<D>(a, pages_of(table, shift, s.kvl, t, stop), hk, t, lane, c0);
+            Pages pg = pages_of(table, shift, s.kvl, t + kWaves, stop);
+            row.load(a, s, rb, hk, G, lane);
+            while (t < stop) {
+                if (t + kWaves < stop) {
+                    load_tile<D>(a, pg, hk, t + kWaves, lane, c1);
+                    pg = pages_of(table, shift, s.kvl, t + 2 * kWaves, stop);
                 }
-                const bool full = c.ok == 15 && kb >= all_lo && kb + kTile <= all_hi;
-                float tm = -__builtin_inff();
-                bool sees[16];
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = sc[g][i] * a.scale;
-                        if (!full) {
-                            const int64_t j = kb + 16 * g + 4 * kg + i;
-                            const bool y = j >= vis_lo && j < vis_hi && (c.ok >> g & 1);
-                            sees[4 * g + i] = y;
-                            x = y ? x : -__builtin_inff();
-                        }
-                        sc[g][i] = x;
-                        tm = fmaxf(tm, x);
-                    }
-                tm = fmaxf(tm, __shfl_xor(tm, 16));
-                tm = fmaxf(tm, __shfl_xor(tm, 32));
-                const float mn = fmaxf(m, tm);
-                const float ms = mn == -__builtin_inff() ? 0.f : mn;
-                const float alpha = mf::ex2(m - ms);
-                m = mn;
-                float p[16], ps = 0.f;
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float y = mf::ex2(sc[g][i] - ms);
-                        p[4 * g + i] = y;
-                        ps += y;
-                    }
-                l = l * alpha + ps;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) o[i] *= alpha;
-
-                if (!full) {
-                    // A NaN among the values reaches only the rows that see it: the
-                    // products take zeros in its place, and 1 x (row sees it) counts it.
-                    uint32_t any = 0;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < D / 64; ++j) any |= nan_bytes(c.v[g][i][j]);
-                    if (__ballot(any != 0) != 0) {
-                        f32x4 cnt[NT];
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) cnt[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int g = 0; g < 4; g += 2) {
-                            uint32_t one[2][4][D / 64];
-                            float vis[8];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    vis[4 * h + i] = sees[4 * (g + h) + i] ? 1.f : 0.f;
-#pragma unroll
-                                    for (int j = 0; j < D / 64; ++j) {
-                                        uint32_t &x = c.v[g + h][i][j];
-                                        const uint32_t b = nan_bytes(x) >> 7;     // 1 per NaN byte
-                                        one[h][i][j] = b * 0x38u;                 // the code of 1.0
-                                        x &= ~(b * 0xffu);
-                                    }
-                                }
-                            add_pv<D, 1>(one[0], one[1], 1.f, 1.f, split8<1>(vis), cnt);
-                        }
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (cnt[i][j] > 0.f) o[i][j] = __builtin_nanf("");
-                    }
+                if (tile_step<D, NS>(row, c0, t, a.scale, lane, m, l, o))
+                    see_nans<D>(a, table, shift, hk, max(row.lo, t * kTile), min(row.hi, (t + 1) * kTile), kg, o);
+                t += kWaves;
+                if (t >= stop) break;
+                if (t + kWaves < stop) {
+                    load_tile<D>(a, pg, hk, t + kWaves, lane, c0);
+                    pg = pages_of(table, shift, s.kvl, t + 2 * kWaves, stop);
                 }
-#pragma unroll
-                for (int g = 0; g < 4; g += 2)
-                    add_pv<D, NS>(c.v[g], c.v[g + 1], c.vs[g], c.vs[g + 1], split8<NS>(p + 4 * g), o);
+                if (tile_step<D, NS>(row, c1, t, a.scale, lane, m, l, o))
+                    see_nans<D>(a, table, shift, hk, max(row.lo, t * kTile), min(row.hi, (t + 1) * kTile), kg, o);
+                t += kWaves;
             }
 
             // the waves meet
@@ -376,25 +468,17 @@ __global__ __launch_bounds__(kAttnThreads) void attn_kernel(const AttnArgs a) {
 #pragma unroll
                     for (int j = 0; j < E; ++j) y[j] += f * sm.o[i][r][d + j];
                 }
-                const int RR = rb * kRows + r;
+                const int R = rb * kRows + r;
                 if (whole) {
-                    if (RR < s.len * G) {
-                        const int64_t row = (s.c0 + RR / G) * a.Hq + hk * G + RR % G;
-                        const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            const float z = y[j] * inv;
-                            if (BF) ((bf16_t *)a.o)[row * D + d + j] = (bf16_t)z;
-                            else ((float *)a.o)[row * D + d + j] = z;
-                        }
-                        if (a.lse && d == 0)
-                            a.lse[row] = L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+                    if (R < s.len * G) {
+                        const int64_t at_row = (s.c0 + R / G) * a.Hq + hk * G + R % G;
+                        store_row<BF, E>(a.o, at_row * D + d, y, L == 0.f ? 0.f : 1.f / L);
+                        if (a.lse && d == 0) a.lse[at_row] = lse_of(M, L);
                     }
                 } else {
                     // cut at this workgroup's end: its second slot; at its start: the first
                     float *dst = a.part + (2 * (int64_t)blockIdx.x + (ubase >= from ? 1 : 0)) * (kRows * (D + 2));
-#pragma unroll
-                    for (int j = 0; j < E; ++j) dst[r * D + d + j] = y[j];
+                    store_row<false, E>(dst, r * D + d, y, 1.f);
                     if (d == 0) { dst[kRows * D + r] = M; dst[kRows * D + kRows + r] = L; }
                 }
             }
@@ -402,76 +486,73 @@ __global__ __launch_bounds__(kAttnThreads) void attn_kernel(const AttnArgs a) {
             at = uend;
         }
         base = end;
+        if (at >= to) break;
     }
 }
 
-// Joins the parts of every unit that attn_kernel cut: one workgroup per unit.
-template <int D, bool BF>
+// Joins the parts of every unit that attn_kernel cut.  A workgroup takes RW rows
+// of a unit; 256 / RW threads share a row: D / E of them its dims, the rest its parts.
+template <int D, bool BF, int RW>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
-    __shared__ int64_t s_scan[2][kWaves];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int G = a.Hq / a.kv.Hk, N = a.kv.N;
-    const int64_t x = blockIdx.x / a.kv.Hk;
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.kv.cu[mid] * G / kRows + mid <= x) lo = mid; else hi = mid - 1;
-    }
-    const int n = lo;
-    const Seq s = sequence(a, n, G);
-    const int64_t rb = x - (s.c0 * G / kRows + n);
-    if (rb < 0 || rb >= s.rt) return;
-    const int hk = blockIdx.x % a.kv.Hk;
-    int64_t total = 0, base = 0;
-    for (int n0 = 0; n0 < N; n0 += kAttnThreads) {
-        int64_t c = 0;
-        if (n0 + tid < N) {
-            const Seq y = sequence(a, n0 + tid, G);
-            c = (int64_t)a.kv.Hk * y.rt * y.tiles;
-        }
-        int64_t b = n0 + tid < n ? c : 0;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            c += __shfl_xor(c, off);
-            b += __shfl_xor(b, off);
-        }
-        if (lane == 0) { s_scan[0][w] = c; s_scan[1][w] = b; }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) { total += s_scan[0][i]; base += s_scan[1][i]; }
-        __syncthreads();
-    }
-    const int64_t share = max((total + a.workers - 1) / a.workers, (int64_t)kMinShare);
-    const int64_t ubase = base + ((int64_t)hk * s.rt + rb) * s.tiles;
-    const int64_t w0 = ubase / share, w1 = (ubase + s.tiles - 1) / share;
-    if (w0 == w1) return;                     // written whole
     constexpr int E = kRows * D / kAttnThreads;
-    const int r = tid / (D / E), d = (tid % (D / E)) * E;
-    const int64_t R = rb * kRows + r;
-    if (R >= (int64_t)s.len * G) return;
+    constexpr int TD = D / E;                           // 16 threads over the dims
+    constexpr int SL = kAttnThreads / (RW * TD);        // slices of the parts
+    __shared__ float s_o[SL][RW][D + 4];
+    __shared__ float s_m[SL][RW], s_l[SL][RW];
+    const int tid = threadIdx.x;
+    const int G = a.Hq / a.kv.Hk;
+    const uint32_t u = blockIdx.x / (kRows / RW);
+    const int hk = u % a.kv.Hk;
+    int n, rb;
+    Seq s;
+    if (!packed_unit(a, u / a.kv.Hk, G, n, s, rb)) return;
+    const Place p = place(a, G, n, 0, tid);
+    const int64_t share = share_of(p.total, a.workers);
+    const int64_t ubase = p.base + (int64_t)(hk * s.rt + rb) * s.tiles;
+    const int64_t w0 = ubase / share, w1 = (ubase + s.tiles - 1) / share;
+    if (w0 == w1) return;                               // written whole
+    const int d = (tid % TD) * E, sl = tid / TD % SL, rr = tid / (TD * SL);
+    const int r = (blockIdx.x % (kRows / RW)) * RW + rr;
     float M = -__builtin_inff(), L = 0.f, y[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) y[j] = 0.f;
-    for (int64_t i = w0; i <= w1; ++i) {
+    for (int64_t i = w0 + sl; i <= w1; i += SL) {
         const float *src = a.part + (2 * i + (ubase >= i * share ? 1 : 0)) * (kRows * (D + 2));
         const float m = src[kRows * D + r], l = src[kRows * D + kRows + r];
+        float v[E];
+#pragma unroll
+        for (int j = 0; j < E; j += 4) *(f32x4 *)(v + j) = *(const f32x4 *)(src + r * D + d + j);
         const float mn = fmaxf(M, m), ms = mn == -__builtin_inff() ? 0.f : mn;
         const float f0 = mf::ex2(M - ms), f1 = mf::ex2(m - ms);
         M = mn;
         L = L * f0 + l * f1;
 #pragma unroll
-        for (int j = 0; j < E; ++j) y[j] = y[j] * f0 + src[r * D + d + j] * f1;
+        for (int j = 0; j < E; ++j) y[j] = y[j] * f0 + v[j] * f1;
     }
-    const int64_t row = (s.c0 + R / G) * a.Hq + hk * G + R % G;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    if constexpr (SL > 1) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const float z = y[j] * inv;
-        if (BF) ((bf16_t *)a.o)[row * D + d + j] = (bf16_t)z;
-        else ((float *)a.o)[row * D + d + j] = z;
+        for (int j = 0; j < E; ++j) s_o[sl][rr][d + j] = y[j];
+        if (d == 0) { s_m[sl][rr] = M; s_l[sl][rr] = L; }
+        __syncthreads();
+        if (sl != 0) return;
+        M = -__builtin_inff();
+        for (int i = 0; i < SL; ++i) M = fmaxf(M, s_m[i][rr]);
+        const float ms = M == -__builtin_inff() ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int j = 0; j < E; ++j) y[j] = 0.f;
+        for (int i = 0; i < SL; ++i) {
+            const float f = mf::ex2(s_m[i][rr] - ms);
+            L += s_l[i][rr] * f;
+#pragma unroll
+            for (int j = 0; j < E; ++j) y[j] += s_o[i][rr][d + j] * f;
+        }
     }
-    if (a.lse && d == 0)
-        a.lse[row] = L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    const int R = rb * kRows + r;
+    if (R >= s.len * G) return;
+    const int64_t row = (s.c0 + R / G) * a.Hq + hk * G + R % G;
+    store_row<BF, E>(a.o, row * D + d, y, L == 0.f ? 0.f : 1.f / L);
+    if (a.lse && d == 0) a.lse[row] = lse_of(M, L);
 }
 
 template <int D, bool BF>
@@ -479,12 +560,16 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     const int G = a.Hq / a.kv.Hk;
     // units over all sequences: at most first(N) of them per kv head
     const int64_t units = (a.kv.T * G / kRows + a.kv.N) * a.kv.Hk;
-    if (units > INT32_MAX) return hipErrorInvalidValue;
+    if (units > INT32_MAX / kRows) return hipErrorInvalidValue;
     const dim3 block(kAttnThreads);
     hipLaunchKernelGGL((attn_kernel<D, BF>), dim3((unsigned)(a.workers ? a.workers : units)), block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.workers == 0) return e;
-    hipLaunchKernelGGL((join_kernel<D, BF>), dim3((unsigned)units), block, 0, s, a);
+    // few units have many parts each: more workgroups per unit and threads per row
+    if (units < a.workers / 8)
+        hipLaunchKernelGGL((join_kernel<D, BF, 1>), dim3((unsigned)(units * kRows)), block, 0, s, a);
+    else
+        hipLaunchKernelGGL((join_kernel<D, BF, kRows>), dim3((unsigned)units), block, 0, s, a);
     return hipGetLastError();
 }
 

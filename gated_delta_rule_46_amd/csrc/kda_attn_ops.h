@@ -27,30 +27,45 @@ __device__ __forceinline__ uint32_t widen(uint32_t c, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, HI));
 }
 
-// Row of the packed tokens as the kernel sees a sequence.
+// A sequence as the kernels see it.  Positions are clamped to what the table can
+// hold (31 bits), on the far side of every key.
 struct Seq {
     int64_t c0;       // first packed token
-    int64_t kvl;      // cached tokens that the table can hold
     int64_t pos0;     // position of the first new token
+    int kvl;          // cached tokens that the table can hold
+    int len;
     int rt;           // units of kRows rows per kv head (0: the other kernel's)
     int lo, tiles;    // tiles of the unmasked range of all its rows; at least one
-    int len;
+
+    // keys that new token i sees: begin_of(i) <= j < end_of(i)
+    __device__ __forceinline__ int end_of(const AttnArgs &a, int i) const {
+        return a.causal ? (int)max(min(pos0 + i + 1, (int64_t)kvl), (int64_t)0) : kvl;
+    }
+    __device__ __forceinline__ int begin_of(const AttnArgs &a, int i) const {
+        return a.window > 0 ? (int)max(min(pos0 + i + 1 - a.window, (int64_t)kvl), (int64_t)0) : 0;
+    }
+    // (unit, tile) pairs of the sequence
+    __device__ __forceinline__ int64_t cost(const AttnArgs &a) const { return (int64_t)a.kv.Hk * rt * tiles; }
 };
 
 __device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
-    Seq s;
+    Seq s = {};
+    if (n >= a.kv.N) return s;
     s.c0 = a.kv.cu[n];
     const int64_t c1 = min(a.kv.cu[n + 1], a.kv.T);
-    const int64_t len = s.c0 < 0 ? 0 : max(c1 - s.c0, (int64_t)0);
     const int64_t kv = a.kv.kv_len[n];
-    s.len = (int)len;
-    s.pos0 = kv - len;
-    s.kvl = max(min(kv, (int64_t)a.kv.width * a.kv.page), (int64_t)0);
-    s.rt = len * G <= a.short_rows ? (int)((len * G + kRows - 1) / kRows) : 0;
-    const int64_t first = a.window > 0 ? max(s.pos0 - a.window + 1, (int64_t)0) : 0;
-    s.lo = (int)min(first / kTile, (int64_t)INT32_MAX / 2);
-    s.tiles = max((int)((s.kvl + kTile - 1) / kTile) - s.lo, 1);
+    s.len = s.c0 < 0 ? 0 : (int)max(c1 - s.c0, (int64_t)0);
+    s.pos0 = kv - s.len;
+    s.kvl = (int)max(min(kv, (int64_t)a.kv.width * a.kv.page), (int64_t)0);
+    s.rt = (int64_t)s.len * G <= a.short_rows ? (s.len * G + kRows - 1) / kRows : 0;
+    s.lo = s.begin_of(a, 0) / kTile;
+    s.tiles = max((s.kvl + kTile - 1) / kTile - s.lo, 1);
     return s;
+}
+
+// log sum exp from a maximum (log2) and a sum
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // A operand of V^T for dims (D / 16) m + 4 w + b of token groups g, g + 1.

@@ -59,10 +59,8 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int64_t x, int G, U
     if (rows <= a.short_rows || r < 0 || r >= rows) return false;
     u.row0 = (int)r;
     const int t0 = u.row0 / G, t1 = min((u.row0 + kRowTile - 1) / G, u.s.len - 1);
-    const int64_t seen = a.causal ? min(u.s.pos0 + t1 + 1, u.s.kvl) : u.s.kvl;
-    const int64_t first = a.window > 0 ? max(u.s.pos0 + t0 - a.window + 1, (int64_t)0) : 0;
-    u.end = (int)((max(seen, (int64_t)0) + kTile - 1) / kTile);
-    u.beg = (int)min(first / kTile, (int64_t)u.end);
+    u.end = (u.s.end_of(a, t1) + kTile - 1) / kTile;
+    u.beg = min(u.s.begin_of(a, t0) / kTile, u.end);
     u.splits = min(a.row_splits, max((u.end - u.beg + kMinSplit - 1) / kMinSplit, 1));
     return true;
 }
@@ -135,12 +133,12 @@ template <int D> struct Flight {
     float ks, vs;
     int ok;
 
-    __device__ void load(const AttnArgs &a, int pid, int hk, int64_t at, int lane) {
+    __device__ void load(const AttnArgs &a, int pid, int hk, int at, int lane) {
         ok = pid >= 0 && pid < a.kv.n_pages;
         ks = vs = 1.f;
         if (ok) {
             const int64_t ph = (int64_t)pid * a.kv.Hk + hk;
-            const int64_t base = (ph * a.kv.page + (int)(at & (a.kv.page - 1))) * D;
+            const int64_t base = (ph * a.kv.page + (at & (a.kv.page - 1))) * D;
             const uint8_t *kp = a.kv.k_codes + base + lane * 16;
             const uint8_t *vp = a.kv.v_codes + base + 4 * (lane >> 5) * D + (lane & 31) * (D / 32);
 #pragma unroll
@@ -162,16 +160,24 @@ template <int D> struct Flight {
     }
 
     // left: tokens of the group that the sequence has (16 for a whole one)
-    __device__ void store(Stage<D> &st, int *s_nan, int t, int w, int lane, int left) {
+    // part: some rows of the unit do not see all of the tile; NaN values are then left
+    // out (0 x NaN is a NaN) and see_nans() follows
+    __device__ void store(Stage<D> &st, int *s_nan, int t, int w, int lane, int left, bool part) {
         if (left < 16) {              // what lies behind them on the page is anything
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if ((i >> 2) * 8 + 4 * (lane >> 5) + (i & 3) >= left) v[i] = 0;
         }
-        uint32_t bad = 0;
+        if (part) {
+            uint32_t bad = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) bad |= nan_bytes(v[i]);
-        if (bad) *s_nan = t;          // every writer stores the same value
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = nan_bytes(v[i]);
+                bad |= b;
+                v[i] &= ~((b >> 7) * 0xffu);
+            }
+            if (bad) *s_nan = t;      // every writer stores the same value
+        }
 #pragma unroll
         for (int r = 0; r < D / 64; ++r) {
             const int piece = lane + 64 * r;
@@ -189,6 +195,29 @@ template <int D> struct Flight {
         }
     }
 };
+
+// NaN into the outputs of the lane's row whose values are NaN at a key lo <= j < hi.
+template <int D>
+__device__ __forceinline__ void see_nans(const AttnArgs &a, const int32_t *table, int shift, int hk, int lo, int hi, int kg,
+                                         f32x16 *o) {
+    constexpr int NJ = D / 32, E = D / 8;
+#pragma unroll 1
+    for (int j = lo; j < hi; ++j) {
+        const int pid = table[j >> shift];
+        if (pid < 0 || pid >= a.kv.n_pages) continue;
+        const int64_t row = ((int64_t)pid * a.kv.Hk + hk) * a.kv.page + (j & (a.kv.page - 1));
+        const uint8_t *p = a.kv.v_codes + row * D + E * kg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)                   // dims 2 E e + E kg + NJ i + j of the lane
+#pragma unroll
+            for (int x = 0; x < E / 4; ++x) {
+                const uint32_t b = nan_bytes(*(const uint32_t *)(p + 2 * E * e + 4 * x));
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (b >> (8 * y) & 0x80) o[(4 * x + y) % NJ][4 * e + (4 * x + y) / NJ] = __builtin_nanf("");
+            }
+    }
+}
 
 template <int D, bool BF>
 __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const AttnArgs a) {
@@ -215,16 +244,11 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     const int R = u.row0 + kWaveRows * w + col;
     const bool live = R < s.len * G;
     const int tok = min(R / G, s.len - 1);
-    const int64_t pos = s.pos0 + tok;
-    const int64_t vis_hi = live ? (a.causal ? min(pos + 1, s.kvl) : s.kvl) : 0;
-    const int64_t vis_lo = a.window > 0 ? pos - a.window + 1 : 0;
-    const int wt0 = min((u.row0 + kWaveRows * w) / G, s.len - 1);
-    const int wt1 = min((u.row0 + kWaveRows * w + kWaveRows - 1) / G, s.len - 1);
-    const bool wave_live = u.row0 + kWaveRows * w < s.len * G;
-    const int64_t any_hi = wave_live ? (a.causal ? min(s.pos0 + wt1 + 1, s.kvl) : s.kvl) : 0;
-    const int64_t any_lo = a.window > 0 ? s.pos0 + wt0 - a.window + 1 : 0;
-    const int64_t all_hi = a.causal ? min(s.pos0 + wt0 + 1, s.kvl) : s.kvl;
-    const int64_t all_lo = a.window > 0 ? s.pos0 + wt1 - a.window + 1 : 0;
+    const int vis_hi = live ? s.end_of(a, tok) : 0, vis_lo = s.begin_of(a, tok);
+    const int first = u.row0 + kWaveRows * w;
+    const int wt0 = min(first / G, s.len - 1), wt1 = min((first + kWaveRows - 1) / G, s.len - 1);
+    const int any_hi = first < s.len * G ? s.end_of(a, wt1) : 0, any_lo = s.begin_of(a, wt0);
+    const int all_hi = s.end_of(a, wt0), all_lo = s.begin_of(a, wt1);
 
     const float sl = fabsf(a.scale);
     Query<D, NS> q;
@@ -239,25 +263,29 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     const int shift = __builtin_ctz(a.kv.page);
     const int32_t *table = a.kv.table + (int64_t)u.n * a.kv.width;
     auto page_of = [&](int t) {
-        const int64_t at = (int64_t)t * kTile + 16 * w;
+        const int at = t * kTile + 16 * w;
         return t < t1 && at < s.kvl ? table[at >> shift] : -1;
     };
+    // tiles outside [whole_lo, whole_hi) are not seen whole by every row of the unit
+    const int u0 = min(u.row0 / G, s.len - 1), u1 = min((u.row0 + kRowTile - 1) / G, s.len - 1);
+    const int whole_lo = s.begin_of(a, u1), whole_hi = u.row0 + kRowTile <= s.len * G ? s.end_of(a, u0) : 0;
+    auto part = [&](int t) { return t * kTile < whole_lo || (t + 1) * kTile > whole_hi; };
     auto left_of = [&](int t) {
-        return (int)min(max(s.kvl - ((int64_t)t * kTile + 16 * w), (int64_t)0), (int64_t)16);
+        return min(max(s.kvl - (t * kTile + 16 * w), 0), 16);
     };
     Flight<D> fl;
     int pid = page_of(t0);
     if (t0 < t1) {
-        fl.load(a, pid, hk, (int64_t)t0 * kTile + 16 * w, lane);
+        fl.load(a, pid, hk, t0 * kTile + 16 * w, lane);
         pid = page_of(t0 + 1);
         __syncthreads();                       // s_nan
-        fl.store(stage[t0 & 1], &s_nan[t0 & 1], t0, w, lane, left_of(t0));
+        fl.store(stage[t0 & 1], &s_nan[t0 & 1], t0, w, lane, left_of(t0), part(t0));
     }
     __syncthreads();
 
     for (int t = t0; t < t1; ++t) {
         const Stage<D> &st = stage[t & 1];
-        const int64_t kb = (int64_t)t * kTile;
+        const int kb = t * kTile;
         const bool more = t + 1 < t1;
         if (more) {
             fl.load(a, pid, hk, kb + kTile + 16 * w, lane);
@@ -267,18 +295,13 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
             f32x16 sc[2] = {q.scores(st, 0, lane), q.scores(st, 1, lane)};
             const int okm = st.ok[0] & st.ok[1] & st.ok[2] & st.ok[3];
             const bool full = okm && kb >= all_lo && kb + kTile <= all_hi;
-            uint32_t sees = ~0u;               // bit 16 tt + i
             if (!full) {
-                const int lo = (int)min(max(vis_lo - kb, (int64_t)0), (int64_t)kTile);
-                const int hi = (int)min(max(vis_hi - kb, (int64_t)0), (int64_t)kTile);
+                const int lo = vis_lo - kb, hi = vis_hi - kb;
                 const int gm = st.ok[0] | st.ok[1] << 1 | st.ok[2] << 2 | st.ok[3] << 3;
-                sees = 0;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int j = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * kg + (i & 3);
-                    const bool v = j >= lo && j < hi && (gm >> (j >> 4) & 1);
-                    sees |= (uint32_t)v << i;
-                    if (!v) sc[i >> 4][i & 15] = -__builtin_inff();
+                    if (!(j >= lo && j < hi && (gm >> (j >> 4) & 1))) sc[i >> 4][i & 15] = -__builtin_inff();
                 }
             }
             float mx = -__builtin_inff();
@@ -297,61 +320,26 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
             const float ms = m == -__builtin_inff() ? 0.f : m;
             float p[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) p[i] = mf::ex2(__builtin_fmaf(sc[i >> 4][i & 15], sl, -ms));
-            bool repair = false;
-            if (!full) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) p[i] = sees >> i & 1 ? p[i] : 0.f;
-                repair = s_nan[t & 1] == t;
+            for (int i = 0; i < 32; ++i) {
+                p[i] = mf::ex2(__builtin_fmaf(sc[i >> 4][i & 15], sl, -ms));
+                l += p[i];
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) l += p[i];
-            if (repair) {
-                // A NaN among the values reaches only the rows that see it: the products
-                // take zeros in its place, and 1 x (row sees it) counts it.
+            for (int k = 0; k < 4; ++k) {
+                const Frag<NS> pf = split8<NS>(p + 8 * k);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    f32x16 cnt = {};
+                    const u32x4 x = st.v[k][j][lane];
+                    const bf16x8 vf = __builtin_bit_cast(bf16x8, x);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        u32x4 x = st.v[k][j][lane], one;
-                        float vis[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t lo = (x[i] & 0x7fffu) > 0x7f80u, hi = (x[i] & 0x7fff0000u) > 0x7f800000u;
-                            one[i] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
-                            x[i] &= ~((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) vis[i] = sees >> (8 * k + i) & 1 ? 1.f : 0.f;
-                        cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, one),
-                                                                      split8<1>(vis).f[0], cnt, 0, 0, 0);
-                        const Frag<NS> pf = split8<NS>(p + 8 * k);
-#pragma unroll
-                        for (int i = 0; i < NS; ++i)
-                            o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), pf.f[i], o[j],
-                                                                           0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (cnt[i] > 0.f) o[j][i] = __builtin_nanf("");
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const Frag<NS> pf = split8<NS>(p + 8 * k);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const u32x4 x = st.v[k][j][lane];
-                        const bf16x8 vf = __builtin_bit_cast(bf16x8, x);
-#pragma unroll
-                        for (int i = 0; i < NS; ++i)
-                            o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf.f[i], o[j], 0, 0, 0);
-                    }
+                    for (int i = 0; i < NS; ++i)
+                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf.f[i], o[j], 0, 0, 0);
                 }
             }
+            if (s_nan[t & 1] == t)
+                see_nans<D>(a, table, shift, hk, max(vis_lo, kb), min(vis_hi, kb + kTile), kg, o);
         }
-        if (more) fl.store(stage[(t + 1) & 1], &s_nan[(t + 1) & 1], t + 1, w, lane, left_of(t + 1));
+        if (more) fl.store(stage[(t + 1) & 1], &s_nan[(t + 1) & 1], t + 1, w, lane, left_of(t + 1), part(t + 1));
         __syncthreads();
     }
 
@@ -371,7 +359,7 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
 #pragma unroll
             for (int i = 0; i < E; i += 8) mf::IO<BF>::store8(a.o, row * D + 2 * E * e + E * kg + i, z + i);
         }
-        if (a.lse && kg == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        if (a.lse && kg == 0) a.lse[row] = lse_of(m, l);
     } else {
         float *dst = a.part + (int64_t)blockIdx.x * (kRowTile * (D + 2));
         const int r = kWaveRows * w + col;
@@ -420,7 +408,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_rows_kernel(const AttnArgs 
     for (int j = 0; j < 8; ++j) z[j] *= inv;
     const int64_t row = (u.s.c0 + R / G) * a.Hq + hk * G + R % G;
     mf::IO<BF>::store8(a.o, row * D + d, z);
-    if (a.lse && d == 0) a.lse[row] = L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    if (a.lse && d == 0) a.lse[row] = lse_of(M, L);
 }
 
 template <int D, bool BF>

@@ -717,17 +717,29 @@ class KVCache:
         return cls(*codes, *scales, table)
 
     def c(self, N, Hk, D, dev):
-        n_pages, _, page, _ = self.k.shape
-        for x, name in ((self.k, "cache.k"), (self.v, "cache.v")):
-            if x.dtype != torch.uint8 and x.dtype != torch.float8_e4m3fn:
-                raise TypeError(f"{name} has dtype {x.dtype}, expected uint8 or float8_e4m3fn")
-            _need(x, name, (n_pages, Hk, page, D), x.dtype, dev)
-        _need(self.k_scale, "cache.k_scale", (n_pages, Hk), torch.float32, dev)
-        _need(self.v_scale, "cache.v_scale", (n_pages, Hk), torch.float32, dev)
-        _need(self.table, "cache.table", (N, self.table.shape[1]), torch.int32, dev)
-        return kda_kv_cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                            self.v_scale.data_ptr(), n_pages, page, self.table.shape[1],
-                            self.table.data_ptr())
+        k, v, ks, vs, table = self.k, self.v, self.k_scale, self.v_scale, self.table
+        n_pages, _, page, _ = shape = k.shape
+        if k.dtype not in _CODES or v.dtype not in _CODES:
+            raise TypeError(f"cache.k and cache.v have dtypes {k.dtype}, {v.dtype}, expected uint8 or float8_e4m3fn")
+        if shape[1] != Hk or shape[3] != D:
+            raise ValueError(f"cache.k has shape {tuple(shape)}, expected ({n_pages}, {Hk}, {page}, {D})")
+        _want(k, "cache.k", shape, k.dtype, dev)
+        _want(v, "cache.v", shape, v.dtype, dev)
+        _want(ks, "cache.k_scale", (n_pages, Hk), torch.float32, dev)
+        _want(vs, "cache.v_scale", (n_pages, Hk), torch.float32, dev)
+        width = table.shape[1]
+        _want(table, "cache.table", (N, width), torch.int32, dev)
+        return kda_kv_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page,
+                            width, table.data_ptr())
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _want(t, name, shape, dtype, dev):
+    """_need with one pass over the attributes (a decode step's calls are bound by their host time)."""
+    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _need(t, name, shape, dtype, dev)
 
 
 def _need_rows(t, name, T, D, dtype, device):
@@ -745,14 +757,20 @@ def _need_rows(t, name, T, D, dtype, device):
     return row if T > 1 else max(row, t.shape[1] * D)
 
 
+@functools.lru_cache(maxsize=256)
 def _attn_config(Hq, Hk, D, dtype):
-    return kda_attn_config(Hq, Hk, D, _io_dtype(dtype))
+    return ctypes.byref(kda_attn_config(Hq, Hk, D, _io_dtype(dtype)))
 
 
 def _device(t):
-    if t.device.type != "cuda":
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError("inputs must be device tensors")
-    return t.device
+    return dev
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _on_stream(at, name):
@@ -775,8 +793,12 @@ def _on_stream(at, name):
     return wrap
 
 
-def _call(name, *args):
-    _check(getattr(LIB, name)(*args, _stream(None)), name)
+_current_stream = torch._C._cuda_getCurrentRawStream   # its handle, without a Stream object
+
+
+def _raised(status, where):
+    if status != KDA_OK:
+        _check(status, where)
 
 
 @_on_stream(0, "q")
@@ -795,30 +817,34 @@ def kda_qk_norm_rope(q, k, positions=None, rope_table=None, *, q_weight=None, k_
     n_pos = rot = 0
     if rope_table is not None:
         n_pos, rot = rope_table.shape
-        _need(rope_table, "rope_table", (n_pos, rot), torch.float32, dev)
-        _need(positions, "positions", (T,), torch.int64, dev)
+        _want(rope_table, "rope_table", (n_pos, rot), torch.float32, dev)
+        _want(positions, "positions", (T,), torch.int64, dev)
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            _need(w, name, (D,), torch.float32, dev)
+            _want(w, name, (D,), torch.float32, dev)
+    qo_row, ko_row = Hq * D, Hk * D
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        q_out = q.new_empty((T, Hq, D))
+    else:
+        qo_row = _need_rows(q_out, "q_out", T, D, q.dtype, dev)
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
-    qo_row = _need_rows(q_out, "q_out", T, D, q.dtype, dev)
-    ko_row = _need_rows(k_out, "k_out", T, D, q.dtype, dev)
+        k_out = q.new_empty((T, Hk, D))
+    else:
+        ko_row = _need_rows(k_out, "k_out", T, D, q.dtype, dev)
     if q_out.shape[1] != Hq or k_out.shape[1] != Hk:
         raise ValueError("q_out / k_out must have the heads of q / k")
-    cfg = _attn_config(Hq, Hk, D, q.dtype)
-    _call("kda_qk_norm_rope", ctypes.byref(cfg), T, _p(q), q_row, _p(k), k_row,
-          _p(q_weight), _p(k_weight), float(eps), _p(rope_table), n_pos, rot, int(layout),
-          _p(positions) if rope_table is not None else None, _p(q_out), qo_row, _p(k_out), ko_row)
+    _raised(LIB.kda_qk_norm_rope(
+        _attn_config(Hq, Hk, D, q.dtype), T, q.data_ptr(), q_row, k.data_ptr(), k_row, _ptr(q_weight),
+        _ptr(k_weight), eps, _ptr(rope_table), n_pos, rot, layout,
+        _ptr(positions) if rope_table is not None else None, q_out.data_ptr(), qo_row,
+        k_out.data_ptr(), ko_row, _current_stream(dev.index)), "kda_qk_norm_rope")
     return q_out, k_out
 
 
 def _sequences(cu_seqlens, kv_len, dev):
     N = cu_seqlens.numel() - 1
-    _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int64, dev)
-    _need(kv_len, "kv_len", (N,), torch.int64, dev)
+    _want(cu_seqlens, "cu_seqlens", (N + 1,), torch.int64, dev)
+    _want(kv_len, "kv_len", (N,), torch.int64, dev)
     return N
 
 
@@ -834,9 +860,11 @@ def kda_kv_write(k, v, cu_seqlens, kv_len, cache):
     if v.shape[1] != Hk:
         raise ValueError(f"v has {v.shape[1]} heads, expected {Hk}")
     N = _sequences(cu_seqlens, kv_len, dev)
-    cfg, cc = _attn_config(Hk, Hk, D, k.dtype), cache.c(N, Hk, D, dev)
-    _call("kda_kv_write", ctypes.byref(cfg), ctypes.byref(cc), N, T, _p(cu_seqlens),
-          _p(kv_len), _p(k), k_row, _p(v), v_row)
+    cc = cache.c(N, Hk, D, dev)
+    _raised(LIB.kda_kv_write(
+        _attn_config(Hk, Hk, D, k.dtype), ctypes.byref(cc), N, T, cu_seqlens.data_ptr(),
+        kv_len.data_ptr(), k.data_ptr(), k_row, v.data_ptr(), v_row, _current_stream(dev.index)),
+        "kda_kv_write")
     return cache
 
 
@@ -852,11 +880,13 @@ def kda_kv_read(cu_seqlens, kv_len, cache, T, dtype=torch.bfloat16, *, k_out=Non
         k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
     if v_out is None:
         v_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
-    _need(k_out, "k_out", (T, Hk, D), dtype, dev)
-    _need(v_out, "v_out", (T, Hk, D), dtype, dev)
-    cfg, cc = _attn_config(Hk, Hk, D, dtype), cache.c(N, Hk, D, dev)
-    _call("kda_kv_read", ctypes.byref(cfg), ctypes.byref(cc), N, T, _p(cu_seqlens),
-          _p(kv_len), _p(k_out), _p(v_out))
+    _want(k_out, "k_out", (T, Hk, D), dtype, dev)
+    _want(v_out, "v_out", (T, Hk, D), dtype, dev)
+    cc = cache.c(N, Hk, D, dev)
+    _raised(LIB.kda_kv_read(
+        _attn_config(Hk, Hk, D, dtype), ctypes.byref(cc), N, T, cu_seqlens.data_ptr(),
+        kv_len.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _current_stream(dev.index)),
+        "kda_kv_read")
     return k_out, v_out
 
 
@@ -873,20 +903,24 @@ def kda_attn(q, cu_seqlens, kv_len, cache, *, scale=None, causal=True, window=0,
     q_row = _need_rows(q, "q", T, D, q.dtype, dev)
     N = _sequences(cu_seqlens, kv_len, dev)
     Hk = cache.k.shape[1]
-    cfg, cc = _attn_config(Hq, Hk, D, q.dtype), cache.c(N, Hk, D, dev)
-    o = out if out is not None else torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    _need(o, "out", (T, Hq, D), q.dtype, dev)
+    cfg, cc = _attn_config(Hq, Hk, D, q.dtype), ctypes.byref(cache.c(N, Hk, D, dev))
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+    else:
+        _want(out, "out", (T, Hq, D), q.dtype, dev)
     lse = lse_out
     if lse is None and want_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     if lse is not None:
-        _need(lse, "lse_out", (T, Hq), torch.float32, dev)
+        _want(lse, "lse_out", (T, Hq), torch.float32, dev)
     if workspace is None:
-        wsb = LIB.kda_attn_workspace(ctypes.byref(cfg), ctypes.byref(cc), N, T)
+        wsb = LIB.kda_attn_workspace(cfg, cc, N, T)
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
     else:
+        _want(workspace, "workspace", workspace.shape, torch.uint8, dev)
         wsb = workspace.numel()
-    _call("kda_attn", ctypes.byref(cfg), ctypes.byref(cc), N, T, _p(cu_seqlens),
-          _p(kv_len), _p(q), q_row, D ** -0.5 if scale is None else float(scale), int(bool(causal)),
-          int(window), _p(o), _p(lse), _p(workspace), wsb)
-    return (o, lse) if want_lse else o
+    _raised(LIB.kda_attn(
+        cfg, cc, N, T, cu_seqlens.data_ptr(), kv_len.data_ptr(), q.data_ptr(), q_row,
+        D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), _ptr(lse),
+        _ptr(workspace), wsb, _current_stream(dev.index)), "kda_attn")
+    return (out, lse) if want_lse else out
