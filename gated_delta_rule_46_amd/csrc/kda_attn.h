@@ -81,12 +81,18 @@ __device__ __forceinline__ void uncode4(uint32_t c, float *out) {
     out[0] = a[0]; out[1] = a[1]; out[2] = b[0]; out[3] = b[1];
 }
 
-// Sequence holding packed row r: the last s with cu[s] <= r (skips empty sequences).
-__device__ __forceinline__ int seq_of_row(const int64_t *cu, int N, int64_t r) {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= r) lo = mid; else hi = mid - 1;
+// The last n in [0, N) with first(n) <= x, 0 if there is none, for a first that does
+// not decrease: 64 probes at a time by the whole wave (x the same in all lanes).
+template <typename F>
+__device__ __forceinline__ int last_not_above(int N, int64_t x, F first) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    for (int size = N; size > 1;) {
+        const int step = (size + 63) / 64, at = lane * step;
+        const bool le = at < size && first(lo + at) <= x;
+        const int k = max(__popcll(__ballot(le)), 1) - 1;
+        lo += k * step;
+        size = min(step, size - k * step);
     }
     return lo;
 }

@@ -203,8 +203,7 @@ __device__ __forceinline__ bool tile_step(const Row<D, NS> &row, Codes<D> &c, in
             sc[g][i] = x;
             tm = fmaxf(tm, x);
         }
-    tm = fmaxf(tm, __shfl_xor(tm, 16));
-    tm = fmaxf(tm, __shfl_xor(tm, 32));
+    tm = max_16(tm);
     if (__ballot(tm > m) != 0) {
         const float mn = fmaxf(m, tm);
         const float alpha = mf::ex2(m - (mn == -__builtin_inff() ? 0.f : mn));
@@ -261,7 +260,7 @@ __device__ __forceinline__ void see_nans(const AttnArgs &a, const int32_t *table
             const uint32_t b = nan_bytes(p[x]);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-                if (b >> (8 * y) & 0x80) o[(4 * x + y) % NT][(4 * x + y) / NT] = __builtin_nanf("");
+                o[(4 * x + y) % NT][(4 * x + y) / NT] += nan_or_zero(b, y);
         }
     }
 }
@@ -352,12 +351,7 @@ __device__ __forceinline__ Place place(const AttnArgs &a, int G, int of, int blo
 // The sequence and unit of number x in the order of the packed rows: sequence n's
 // units start at first(n) = cu[n] G / kRows + n (at least as many apart as it has).
 __device__ __forceinline__ bool packed_unit(const AttnArgs &a, int64_t x, int G, int &n, Seq &s, int &rb) {
-    int lo = 0, hi = a.kv.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.kv.cu[mid] * G / kRows + mid <= x) lo = mid; else hi = mid - 1;
-    }
-    n = lo;
+    n = last_not_above(a.kv.N, x, [&](int i) { return a.kv.cu[i] * G / kRows + i; });
     s = sequence(a, n, G);
     const int64_t r = x - (s.c0 * G / kRows + n);
     rb = (int)r;
@@ -441,8 +435,7 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void attn_kernel(const At
             }
 
             // the waves meet
-            l += __shfl_xor(l, 16);
-            l += __shfl_xor(l, 32);
+            l = sum_16(l);
             if (kg == 0) { sm.m[w][col] = m; sm.l[w][col] = l; }
 #pragma unroll
             for (int i = 0; i < 4; ++i)       // dims (D / 16)(4 kg + i) + j, j < NT

@@ -63,6 +63,24 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
     return s;
 }
 
+// Over lanes l and l ^ 32, and over the four groups of 16 lanes.
+__device__ __forceinline__ float max_32(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(x), f32_bits(x), false, false);
+    return fmaxf(bits_f32(r[0]), bits_f32(r[1]));
+}
+__device__ __forceinline__ float sum_32(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(x), f32_bits(x), false, false);
+    return bits_f32(r[0]) + bits_f32(r[1]);
+}
+__device__ __forceinline__ float max_16(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(f32_bits(x), f32_bits(x), false, false);
+    return max_32(fmaxf(bits_f32(r[0]), bits_f32(r[1])));
+}
+__device__ __forceinline__ float sum_16(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(f32_bits(x), f32_bits(x), false, false);
+    return sum_32(bits_f32(r[0]) + bits_f32(r[1]));
+}
+
 // log sum exp from a maximum (log2) and a sum
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
@@ -104,6 +122,12 @@ __device__ __forceinline__ Frag<NS> split8(const float *x) {
 
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {   // 0x80 in every byte that is a NaN code
     return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// NaN if byte y of nan_bytes() is set, else 0 (no comparison: those would hold a
+// lane mask each).
+__device__ __forceinline__ float nan_or_zero(uint32_t b, int y) {
+    return bits_f32((uint32_t)((int32_t)(b << (24 - 8 * y)) >> 31) & 0x7fc00000u);
 }
 
 }  // namespace attn

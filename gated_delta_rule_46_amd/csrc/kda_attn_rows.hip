@@ -8,18 +8,15 @@
 // while a tile is computed the next one is on its way from HBM in registers.
 // Wave w stages the 16 tokens of group w, so one page lookup serves a wave.
 //
-//   keys    codes as they are, rows of D bytes whose 16-byte pieces are permuted
-//           by the row (XOR) so that 8 lanes reading one piece of 8 rows meet 8
-//           different bank groups;
-//   values  as bf16 operand fragments of V^T (a lane's 16 bytes in lane order):
-//           the byte permutes and conversions are done once per workgroup.
-//
-// S^T = K Q^T on the bf16 matrix instruction, the keys converted by the wave that
-// uses them (codes in LDS are half the LDS traffic of bf16).  The 8-bit matrix
-// instruction would take the codes as they are, with a bf16 query as two e4m3
-// terms (4 + 4 bits), but it sums its products with fewer bits than fp32: scores
-// came out off by 2^-17 of sum |q k|, so it is not used.  With fp32 rows queries
-// and probabilities are three bf16 terms, as in kda_attn.hip.
+// Both are staged as bf16 operand fragments, a lane's 16 bytes in lane order (no
+// bank conflicts), the values transposed by byte permutes: the conversions are
+// done once per workgroup.  (Keys left as codes halve their LDS traffic, 28% of
+// the cycles, but every wave converts them again: the vector pipe is the busier
+// one, 60%.)  The 8-bit matrix instruction would take codes as they are, with a
+// bf16 query as two e4m3 terms (4 + 4 bits), but it sums its products with fewer
+// bits than fp32: scores came out off by 2^-17 of sum |q k|, so it is not used.
+// With fp32 rows queries and probabilities are three bf16 terms, as in
+// kda_attn.hip.
 //
 // The maximum is followed lazily: outputs are scaled only when some row's
 // maximum grew by more than 2^8 since (probabilities stay below 2^8, which
@@ -47,12 +44,7 @@ struct Unit {
 
 __device__ __forceinline__ bool find_unit(const AttnArgs &a, int64_t x, int G, Unit &u) {
     // units of sequence n start at first(n) = cu[n] G / 128 + n
-    int lo = 0, hi = a.kv.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.kv.cu[mid] * G / kRowTile + mid <= x) lo = mid; else hi = mid - 1;
-    }
-    u.n = lo;
+    u.n = last_not_above(a.kv.N, x, [&](int n) { return a.kv.cu[n] * G / kRowTile + n; });
     u.s = sequence(a, u.n, G);
     const int64_t rows = (int64_t)u.s.len * G;
     const int64_t r = (x - (u.s.c0 * G / kRowTile + u.n)) * kRowTile;
@@ -66,63 +58,49 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int64_t x, int G, U
 }
 
 template <int D> struct Stage {
-    uint8_t k[kTile * D];
-    u32x4 v[4][D / 32][64];
-    float kscale[4];                  // of the groups of 16 tokens
-    int ok[4];                        // group has a page
+    u32x4 k[2][D / 16][64];           // 32 tokens: steps of 16 dims, (token, 8 dims) per lane
+    u32x4 v[4][D / 32][64];           // 16 tokens: 32 dims, (dim, 8 tokens) per lane
+    int ok[4];                        // group of 16 tokens has a page (or lies behind the last key)
+    int nan, hole;                    // the tile if it held a NaN value, an absent page
 };
 
-// Piece c (16 bytes) of key row m.
-template <int D>
-__device__ __forceinline__ int k_at(int m, int c) {
-    return D == 128 ? m * 128 + ((c ^ (m & 7)) << 4) : m * 64 + ((c ^ ((m >> 1) & 3)) << 4);
-}
-
-__device__ __forceinline__ float both_max(float x) {       // over lanes l and l ^ 32
-    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(x), f32_bits(x), false, false);
-    return fmaxf(bits_f32(r[0]), bits_f32(r[1]));
-}
-__device__ __forceinline__ float both_sum(float x) {
-    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(x), f32_bits(x), false, false);
-    return bits_f32(r[0]) + bits_f32(r[1]);
+__device__ __forceinline__ f32x16 mma(u32x4 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b, c, 0, 0, 0);
 }
 
 // Queries of a lane's row as operand fragments, NS bf16 terms each.
 template <int D, int NS> struct Query {
-    Frag<NS> f[D / 32][2];            // dims 32 i + 16 kg + 8 h + 0..7
+    Frag<NS> f[D / 16];               // step i: dims 16 i + 8 kg + 0..7
     __device__ void load(const void *q, int64_t at, int kg, bool neg) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
+        for (int i = 0; i < D / 16; ++i) {
+            float x[8];
+            mf::IO<NS == 1>::load8(q, at + 16 * i + 8 * kg, x);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[8];
-                mf::IO<NS == 1>::load8(q, at + 32 * i + 16 * kg + 8 * h, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = neg ? -x[j] : x[j];
-                f[i][h] = split8<NS>(x);
-            }
+            for (int j = 0; j < 8; ++j) x[j] = neg ? -x[j] : x[j];
+            f[i] = split8<NS>(x);
+        }
     }
-    // S^T of tokens 32 tt .. 32 tt + 31
-    __device__ f32x16 scores(const Stage<D> &st, int tt, int lane) const {
-        f32x16 c = {};
-        const int m = 32 * tt + (lane & 31), kg = lane >> 5;
-        const float ks = st.kscale[2 * tt + ((lane >> 4) & 1)];
+    // S^T of both halves of a tile, the fragments of the next four products read
+    // while four run
+    __device__ void scores(const Stage<D> &st, int lane, f32x16 (&c)[2]) const {
+        c[0] = c[1] = f32x16{};
+        u32x4 x[2][4];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const u32x4 x = *(const u32x4 *)&st.k[k_at<D>(m, 2 * i + kg)];
+        for (int y = 0; y < 4; ++y) x[0][y] = st.k[y & 1][y >> 1][lane];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 kf;
-                kf[0] = widen<false>(x[2 * h], ks);
-                kf[1] = widen<true>(x[2 * h], ks);
-                kf[2] = widen<false>(x[2 * h + 1], ks);
-                kf[3] = widen<true>(x[2 * h + 1], ks);
+        for (int g = 0; g < D / 32; ++g) {
+            if (g + 1 < D / 32) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) x[(g + 1) & 1][y] = st.k[y & 1][2 * g + 2 + (y >> 1)][lane];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
 #pragma unroll
                 for (int t = 0; t < NS; ++t)
-                    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf), f[i][h].f[t], c, 0, 0, 0);
-            }
+                    c[y & 1] = mma(x[g & 1][y], f[2 * g + (y >> 1)].f[t], c[y & 1]);
         }
-        return c;
     }
 };
 
@@ -139,10 +117,10 @@ template <int D> struct Flight {
         if (ok) {
             const int64_t ph = (int64_t)pid * a.kv.Hk + hk;
             const int64_t base = (ph * a.kv.page + (at & (a.kv.page - 1))) * D;
-            const uint8_t *kp = a.kv.k_codes + base + lane * 16;
+            const uint8_t *kp = a.kv.k_codes + base + (lane & 15) * D + (lane >> 4) * 16;
             const uint8_t *vp = a.kv.v_codes + base + 4 * (lane >> 5) * D + (lane & 31) * (D / 32);
 #pragma unroll
-            for (int r = 0; r < D / 64; ++r) k[r] = *(const u32x4 *)(kp + r * 1024);
+            for (int r = 0; r < D / 64; ++r) k[r] = *(const u32x4 *)(kp + r * 64);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint8_t *p = vp + ((i >> 2) * 8 + (i & 3)) * D;
@@ -162,7 +140,7 @@ template <int D> struct Flight {
     // left: tokens of the group that the sequence has (16 for a whole one)
     // part: some rows of the unit do not see all of the tile; NaN values are then left
     // out (0 x NaN is a NaN) and see_nans() follows
-    __device__ void store(Stage<D> &st, int *s_nan, int t, int w, int lane, int left, bool part) {
+    __device__ void store(Stage<D> &st, int t, int w, int lane, int left, bool part) {
         if (left < 16) {              // what lies behind them on the page is anything
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -176,12 +154,17 @@ template <int D> struct Flight {
                 bad |= b;
                 v[i] &= ~((b >> 7) * 0xffu);
             }
-            if (bad) *s_nan = t;      // every writer stores the same value
+            if (bad) st.nan = t;      // every writer stores the same value
         }
+        // group w: tokens 16 (w & 1) + .. of half w >> 1; piece p: dims 16 p + 0..15
 #pragma unroll
         for (int r = 0; r < D / 64; ++r) {
-            const int piece = lane + 64 * r;
-            *(u32x4 *)&st.k[k_at<D>(16 * w + piece / (D / 16), piece % (D / 16))] = k[r];
+            u32x4 *dst = &st.k[w >> 1][4 * r + (lane >> 4)][16 * (w & 1) + (lane & 15)];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t c0 = h ? k[r][2] : k[r][0], c1 = h ? k[r][3] : k[r][1];
+                dst[32 * h] = u32x4{widen<false>(c0, ks), widen<true>(c0, ks), widen<false>(c1, ks), widen<true>(c1, ks)};
+            }
         }
         st.v[w][0][lane] = __builtin_bit_cast(u32x4, v_frag<0>(v, vs, vs));
         st.v[w][1][lane] = __builtin_bit_cast(u32x4, v_frag<1>(v, vs, vs));
@@ -190,8 +173,8 @@ template <int D> struct Flight {
             st.v[w][3][lane] = __builtin_bit_cast(u32x4, v_frag<3>(v, vs, vs));
         }
         if (lane == 0) {
-            st.kscale[w] = ks;
             st.ok[w] = ok;
+            if (!ok) st.hole = t;
         }
     }
 };
@@ -214,7 +197,7 @@ __device__ __forceinline__ void see_nans(const AttnArgs &a, const int32_t *table
                 const uint32_t b = nan_bytes(*(const uint32_t *)(p + 2 * E * e + 4 * x));
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                    if (b >> (8 * y) & 0x80) o[(4 * x + y) % NJ][4 * e + (4 * x + y) / NJ] = __builtin_nanf("");
+                    o[(4 * x + y) % NJ][4 * e + (4 * x + y) / NJ] += nan_or_zero(b, y);
             }
     }
 }
@@ -224,7 +207,6 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     constexpr int NS = BF ? 1 : 3;
     constexpr int NJ = D / 32;
     __shared__ __align__(16) Stage<D> stage[2];
-    __shared__ int s_nan[2];
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, kg = lane >> 5;
@@ -258,13 +240,16 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     f32x16 o[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) o[j] = f32x16{};
-    if (tid < 2) s_nan[tid] = -1;
+    if (tid < 2) stage[tid].nan = stage[tid].hole = -1;
 
     const int shift = __builtin_ctz(a.kv.page);
     const int32_t *table = a.kv.table + (int64_t)u.n * a.kv.width;
+    // A lane's copy of the wave's page: made uniform where it is used, one tile later, so
+    // that nothing waits for the lookup together with the codes on their way.
+    const int zero = opaque(0);
     auto page_of = [&](int t) {
         const int at = t * kTile + 16 * w;
-        return t < t1 && at < s.kvl ? table[at >> shift] : -1;
+        return t < t1 && at < s.kvl ? table[(at >> shift) + zero] : -1;
     };
     // tiles outside [whole_lo, whole_hi) are not seen whole by every row of the unit
     const int u0 = min(u.row0 / G, s.len - 1), u1 = min((u.row0 + kRowTile - 1) / G, s.len - 1);
@@ -276,10 +261,10 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     Flight<D> fl;
     int pid = page_of(t0);
     if (t0 < t1) {
-        fl.load(a, pid, hk, t0 * kTile + 16 * w, lane);
+        fl.load(a, __builtin_amdgcn_readfirstlane(pid), hk, t0 * kTile + 16 * w, lane);
         pid = page_of(t0 + 1);
-        __syncthreads();                       // s_nan
-        fl.store(stage[t0 & 1], &s_nan[t0 & 1], t0, w, lane, left_of(t0), part(t0));
+        __syncthreads();                       // nan, hole
+        fl.store(stage[t0 & 1], t0, w, lane, left_of(t0), part(t0));
     }
     __syncthreads();
 
@@ -288,13 +273,18 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
         const int kb = t * kTile;
         const bool more = t + 1 < t1;
         if (more) {
-            fl.load(a, pid, hk, kb + kTile + 16 * w, lane);
+            fl.load(a, __builtin_amdgcn_readfirstlane(pid), hk, kb + kTile + 16 * w, lane);
             pid = page_of(t + 2);
         }
         if (kb < any_hi && kb + kTile > any_lo) {
-            f32x16 sc[2] = {q.scores(st, 0, lane), q.scores(st, 1, lane)};
-            const int okm = st.ok[0] & st.ok[1] & st.ok[2] & st.ok[3];
-            const bool full = okm && kb >= all_lo && kb + kTile <= all_hi;
+            const int nan = st.nan, hole = st.hole;
+            f32x16 sc[2];
+            q.scores(st, lane, sc);
+            u32x4 vf[2][NJ];                   // values of step k, and of the next
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) vf[0][j] = st.v[0][j][lane];
+            __builtin_amdgcn_sched_barrier(0);
+            const bool full = hole != t && kb >= all_lo && kb + kTile <= all_hi;
             if (!full) {
                 const int lo = vis_lo - kb, hi = vis_hi - kb;
                 const int gm = st.ok[0] | st.ok[1] << 1 | st.ok[2] << 2 | st.ok[3] << 3;
@@ -307,7 +297,7 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
             float mx = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < 32; ++i) mx = fmaxf(mx, sc[i >> 4][i & 15]);
-            mx = both_max(mx);
+            mx = max_32(mx);
             mx = mx == -__builtin_inff() ? mx : mx * sl;
             if (__ballot(mx > m + kLag) != 0) {
                 const float mn = fmaxf(m, mx);
@@ -326,24 +316,25 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                if (k < 3) {
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) vf[(k + 1) & 1][j] = st.v[k + 1][j][lane];
+                }
                 const Frag<NS> pf = split8<NS>(p + 8 * k);
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const u32x4 x = st.v[k][j][lane];
-                    const bf16x8 vf = __builtin_bit_cast(bf16x8, x);
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int i = 0; i < NS; ++i)
-                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf.f[i], o[j], 0, 0, 0);
-                }
+                        o[j] = mma(vf[k & 1][j], pf.f[i], o[j]);
             }
-            if (s_nan[t & 1] == t)
+            if (nan == t)
                 see_nans<D>(a, table, shift, hk, max(vis_lo, kb), min(vis_hi, kb + kTile), kg, o);
         }
-        if (more) fl.store(stage[(t + 1) & 1], &s_nan[(t + 1) & 1], t + 1, w, lane, left_of(t + 1), part(t + 1));
+        if (more) fl.store(stage[(t + 1) & 1], t + 1, w, lane, left_of(t + 1), part(t + 1));
         __syncthreads();
     }
 
-    l = both_sum(l);
+    l = sum_32(l);
     if (!live) return;
     constexpr int E = D / 8;                   // contiguous dims per group of 4 results
     if (u.splits == 1) {

@@ -54,16 +54,12 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(const KvArgs a) {
     constexpr int NC = (PAGE * CH + kKvThreads - 1) / kKvThreads;   // pieces per thread
     __shared__ float s_max[kKvThreads / 64];
     const int tid = threadIdx.x;
-    const int64_t x = blockIdx.x;
-    const int h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
-
-    int lo_n = 0, hi_n = a.N - 1;                                 // last n with first(n) <= x
-    while (lo_n < hi_n) {
-        const int mid = (lo_n + hi_n + 1) >> 1;
-        if (a.cu[mid] / PAGE + 2 * (int64_t)mid <= x) lo_n = mid; else hi_n = mid - 1;
-    }
-    const int n = lo_n;
+    // heads, keys and values of the same tokens are neighbours: their rows lie together
+    const uint32_t hz = blockIdx.x % (2 * (uint32_t)a.Hk);
+    const int64_t x = blockIdx.x / (2 * (uint32_t)a.Hk);
+    const bool is_v = hz >= (uint32_t)a.Hk;
+    const int h = (int)(is_v ? hz - a.Hk : hz);
+    const int n = last_not_above(a.N, x, [&](int i) { return a.cu[i] / PAGE + 2 * (int64_t)i; });
     const int64_t c0 = a.cu[n], c1 = min(a.cu[n + 1], a.T);
     const int64_t kvl = a.kv_len[n], start = kvl - (c1 - c0);     // position of the first new token
     if (c0 < 0 || c1 <= c0) return;
@@ -132,56 +128,87 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(const KvArgs a) {
     if (tid == 0 && s != held) *scale = s;
 }
 
-// One workgroup per kReadRows packed tokens; a thread takes 8-element pieces of
-// keys and values.  Tokens without a page read as zeros.
-constexpr int kReadRows = 4;
+// One workgroup per kReadRows packed tokens, whose places are looked up side by
+// side first; then a thread takes 16 codes at a time (16 bytes in, 32 or 64 out),
+// kReadDeep of them in flight.  Tokens without a page read as zeros.
+constexpr int kReadRows = 16;
+constexpr int kReadDeep = 4;
 
 template <int D, bool BF>
 __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const KvArgs a) {
-    constexpr int CH = D / 8;
+    constexpr int CH = D / 16;                // pieces per row
+    __shared__ int64_t s_row[kReadRows];      // pid * Hk * page + row of the page, -1: absent, -2: not there
+    __shared__ int s_pid[kReadRows];
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * kReadRows;
     if (t0 >= a.cu[a.N]) return;              // rows behind the last sequence stay as they are
-    int n = seq_of_row(a.cu, a.N, t0);
-    const int per = 2 * a.Hk * CH;            // pieces per token
-    for (int i = 0; i < kReadRows; ++i) {
-        const int64_t t = t0 + i;
-        if (t >= a.T) return;
+    int n = last_not_above(a.N, t0, [&](int i) { return a.cu[i]; });
+    if (tid < kReadRows) {
+        const int64_t t = t0 + tid;
         while (n < a.N && t >= a.cu[n + 1]) ++n;
-        if (n >= a.N || t < a.cu[n]) return;
-        const int64_t pos = a.kv_len[n] - a.cu[n + 1] + t;
-        const int64_t b = pos / a.page;
-        int32_t pid = -1;
-        if (pos >= 0 && b < a.width) pid = a.table[(int64_t)n * a.width + b];
-        const bool has = pid >= 0 && pid < a.n_pages;
-        const int r = (int)(pos - b * a.page);
-        for (int c = tid; c < per; c += kKvThreads) {
-            const bool is_v = c >= a.Hk * CH;
-            const int hc = is_v ? c - a.Hk * CH : c;
-            const int h = hc / CH, d = (hc % CH) * 8;
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = 0.f;
-            if (has) {
-                const int64_t ph = (int64_t)pid * a.Hk + h;
-                const uint2 w = *(const uint2 *)((is_v ? a.v_codes : a.k_codes) +
-                                                 (ph * a.page + r) * D + d);
-                const float s = (is_v ? a.v_scale : a.k_scale)[ph];
-                uncode4(w.x, y);
-                uncode4(w.y, y + 4);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= s;
+        int64_t place = -2;
+        int pid = -1;
+        if (t < a.T && n < a.N && t >= a.cu[n]) {
+            const int64_t pos = a.kv_len[n] - a.cu[n + 1] + t;
+            const int shift = __builtin_ctz(a.page);
+            place = -1;
+            if (pos >= 0 && (pos >> shift) < a.width) {
+                pid = a.table[(int64_t)n * a.width + (pos >> shift)];
+                if (pid >= 0 && pid < a.n_pages)
+                    place = (int64_t)pid * a.Hk * a.page + (pos & (a.page - 1));
             }
-            mf::IO<BF>::store8(is_v ? a.v_out : a.k_out, (t * a.Hk + h) * D + d, y);
+        }
+        s_row[tid] = place;
+        s_pid[tid] = pid;
+    }
+    __syncthreads();
+    const int per = 2 * a.Hk * CH;            // pieces per token
+    const int all = kReadRows * per;
+    for (int c0 = tid; c0 < all; c0 += kReadDeep * kKvThreads) {
+        uint4 w[kReadDeep];
+        float s[kReadDeep];
+        int64_t to[kReadDeep];
+        bool is_v[kReadDeep];
+#pragma unroll
+        for (int u = 0; u < kReadDeep; ++u) {
+            const int c = c0 + u * kKvThreads;
+            w[u] = make_uint4(0, 0, 0, 0);
+            s[u] = 1.f;
+            to[u] = -1;
+            if (c >= all) continue;
+            const int i = (int)((uint32_t)c / (uint32_t)per), x = c - i * per;
+            const int64_t place = s_row[i];
+            if (place == -2) continue;
+            is_v[u] = x >= a.Hk * CH;
+            const int y = is_v[u] ? x - a.Hk * CH : x, h = y / CH, d = y % CH * 16;
+            to[u] = ((t0 + i) * a.Hk + h) * D + d;
+            if (place >= 0) {
+                w[u] = *(const uint4 *)((is_v[u] ? a.v_codes : a.k_codes) + (place + (int64_t)h * a.page) * D + d);
+                s[u] = (is_v[u] ? a.v_scale : a.k_scale)[(int64_t)s_pid[i] * a.Hk + h];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kReadDeep; ++u) {
+            if (to[u] < 0) continue;
+            float y[16];
+            uncode4(w[u].x, y);
+            uncode4(w[u].y, y + 4);
+            uncode4(w[u].z, y + 8);
+            uncode4(w[u].w, y + 12);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] *= s[u];
+            void *out = is_v[u] ? a.v_out : a.k_out;
+            mf::IO<BF>::store8(out, to[u], y);
+            mf::IO<BF>::store8(out, to[u] + 8, y + 8);
         }
     }
 }
 
 template <int D, int PAGE>
 hipError_t launch_write(bool bf16, const KvArgs &a, hipStream_t s) {
-    const int64_t gx = a.T / PAGE + 2 * (int64_t)a.N;
-    if (gx > INT32_MAX || a.Hk > 65535) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)gx, (unsigned)a.Hk, 2), block(kKvThreads);
+    const int64_t blocks = (a.T / PAGE + 2 * (int64_t)a.N) * 2 * a.Hk;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), block(kKvThreads);
     if (bf16) hipLaunchKernelGGL((kv_write_kernel<D, PAGE, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((kv_write_kernel<D, PAGE, false>), grid, block, 0, s, a);
     return hipGetLastError();
