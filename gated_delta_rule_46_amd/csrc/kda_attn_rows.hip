@@ -81,26 +81,32 @@ template <int D, int NS> struct Query {
             f[i] = split8<NS>(x);
         }
     }
-    // S^T of both halves of a tile, the fragments of the next four products read
-    // while four run
-    __device__ void scores(const Stage<D> &st, int lane, f32x16 (&c)[2]) const {
+    // S^T of both halves of a tile: fragments are read two steps ahead, and other(i) is
+    // work for the vector pipe beside step i of D / 16.
+    template <typename F>
+    __device__ __forceinline__ void scores(const Stage<D> &st, int lane, f32x16 (&c)[2], F other) const {
+        constexpr int N = D / 16;
         c[0] = c[1] = f32x16{};
-        u32x4 x[2][4];
+        u32x4 x[3][2];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) x[0][y] = st.k[y & 1][y >> 1][lane];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g) {
-            if (g + 1 < D / 32) {
+            for (int tt = 0; tt < 2; ++tt) x[i][tt] = st.k[tt][i][lane];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) x[(g + 1) & 1][y] = st.k[y & 1][2 * g + 2 + (y >> 1)][lane];
+        for (int i = 0; i < N; ++i) {
+            if (i + 2 < N) {
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) x[(i + 2) % 3][tt] = st.k[tt][i + 2][lane];
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int t = 0; t < NS; ++t)
-                    c[y & 1] = mma(x[g & 1][y], f[2 * g + (y >> 1)].f[t], c[y & 1]);
+            for (int t = 0; t < NS; ++t) {
+                c[0] = mma(x[i % 3][0], f[i].f[t], c[0]);
+                c[1] = mma(x[i % 3][1], f[i].f[t], c[1]);
+            }
+            other(i);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 };
 
@@ -137,11 +143,12 @@ template <int D> struct Flight {
         }
     }
 
-    // left: tokens of the group that the sequence has (16 for a whole one)
-    // part: some rows of the unit do not see all of the tile; NaN values are then left
-    // out (0 x NaN is a NaN) and see_nans() follows
-    __device__ void store(Stage<D> &st, int t, int w, int lane, int left, bool part) {
-        if (left < 16) {              // what lies behind them on the page is anything
+    // Values that must not take part, out; what the tile is, noted.  left: tokens of the
+    // group that the sequence has (16 for a whole one); what lies behind them on the page
+    // is anything.  part: some rows of the unit do not see all of the tile; NaN values are
+    // then left out (0 x NaN is a NaN) and see_nans() follows.
+    __device__ void settle(Stage<D> &st, int t, int w, int lane, int left, bool part) {
+        if (left < 16) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if ((i >> 2) * 8 + 4 * (lane >> 5) + (i & 3) >= left) v[i] = 0;
@@ -156,25 +163,30 @@ template <int D> struct Flight {
             }
             if (bad) st.nan = t;      // every writer stores the same value
         }
+        if (!ok) st.hole = t;
+        if (lane == 0) st.ok[w] = ok;
+    }
+
+    // Part i of kParts of the operand fragments.
+    static constexpr int kParts = D / 16;
+    u32x4 kf[D / 32], vf[D / 32];
+    __device__ __forceinline__ void widen_part(int i) {
+        if (i < D / 32) {
+            const uint32_t c0 = i & 1 ? k[i >> 1][2] : k[i >> 1][0], c1 = i & 1 ? k[i >> 1][3] : k[i >> 1][1];
+            kf[i] = u32x4{widen<false>(c0, ks), widen<true>(c0, ks), widen<false>(c1, ks), widen<true>(c1, ks)};
+        } else {
+            const int j = i - D / 32;
+            const bf16x8 f = j == 0 ? v_frag<0>(v, vs, vs) : j == 1 ? v_frag<1>(v, vs, vs)
+                           : j == 2 ? v_frag<2>(v, vs, vs) : v_frag<3>(v, vs, vs);
+            vf[j] = __builtin_bit_cast(u32x4, f);
+        }
+    }
+    __device__ __forceinline__ void store(Stage<D> &st, int w, int lane) const {
         // group w: tokens 16 (w & 1) + .. of half w >> 1; piece p: dims 16 p + 0..15
 #pragma unroll
-        for (int r = 0; r < D / 64; ++r) {
-            u32x4 *dst = &st.k[w >> 1][4 * r + (lane >> 4)][16 * (w & 1) + (lane & 15)];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t c0 = h ? k[r][2] : k[r][0], c1 = h ? k[r][3] : k[r][1];
-                dst[32 * h] = u32x4{widen<false>(c0, ks), widen<true>(c0, ks), widen<false>(c1, ks), widen<true>(c1, ks)};
-            }
-        }
-        st.v[w][0][lane] = __builtin_bit_cast(u32x4, v_frag<0>(v, vs, vs));
-        st.v[w][1][lane] = __builtin_bit_cast(u32x4, v_frag<1>(v, vs, vs));
-        if constexpr (D == 128) {
-            st.v[w][2][lane] = __builtin_bit_cast(u32x4, v_frag<2>(v, vs, vs));
-            st.v[w][3][lane] = __builtin_bit_cast(u32x4, v_frag<3>(v, vs, vs));
-        }
-        if (lane == 0) {
-            st.ok[w] = ok;
-            if (!ok) st.hole = t;
+        for (int i = 0; i < D / 32; ++i) {
+            st.k[w >> 1][4 * (i >> 1) + (lane >> 4)][16 * (w & 1) + (lane & 15) + 32 * (i & 1)] = kf[i];
+            st.v[w][i][lane] = vf[i];
         }
     }
 };
@@ -259,27 +271,40 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
         return min(max(s.kvl - (t * kTile + 16 * w), 0), 16);
     };
     Flight<D> fl;
+    auto load = [&](int t, int pid) {
+        fl.load(a, __builtin_amdgcn_readfirstlane(pid), hk, t * kTile + 16 * w, lane);
+    };
     int pid = page_of(t0);
     if (t0 < t1) {
-        fl.load(a, __builtin_amdgcn_readfirstlane(pid), hk, t0 * kTile + 16 * w, lane);
+        load(t0, pid);
         pid = page_of(t0 + 1);
         __syncthreads();                       // nan, hole
-        fl.store(stage[t0 & 1], t0, w, lane, left_of(t0), part(t0));
+        fl.settle(stage[t0 & 1], t0, w, lane, left_of(t0), part(t0));
+#pragma unroll
+        for (int i = 0; i < Flight<D>::kParts; ++i) fl.widen_part(i);
+        fl.store(stage[t0 & 1], w, lane);
+        if (t0 + 1 < t1) {
+            load(t0 + 1, pid);
+            pid = page_of(t0 + 2);
+        }
     }
     __syncthreads();
 
     for (int t = t0; t < t1; ++t) {
         const Stage<D> &st = stage[t & 1];
         const int kb = t * kTile;
-        const bool more = t + 1 < t1;
-        if (more) {
-            fl.load(a, __builtin_amdgcn_readfirstlane(pid), hk, kb + kTile + 16 * w, lane);
-            pid = page_of(t + 2);
+        const int nan = st.nan, hole = st.hole;
+        if (t + 1 < t1) fl.settle(stage[(t + 1) & 1], t + 1, w, lane, left_of(t + 1), part(t + 1));
+        // The next tile's conversions beside this one's products; past the last tile they
+        // write what nobody reads.
+        f32x16 sc[2];
+        q.scores(st, lane, sc, [&](int i) { fl.widen_part(i); });
+        fl.store(stage[(t + 1) & 1], w, lane);
+        if (t + 2 < t1) {
+            load(t + 2, pid);
+            pid = page_of(t + 3);
         }
         if (kb < any_hi && kb + kTile > any_lo) {
-            const int nan = st.nan, hole = st.hole;
-            f32x16 sc[2];
-            q.scores(st, lane, sc);
             u32x4 vf[2][NJ];                   // values of step k, and of the next
 #pragma unroll
             for (int j = 0; j < NJ; ++j) vf[0][j] = st.v[0][j][lane];
@@ -330,7 +355,6 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
             if (nan == t)
                 see_nans<D>(a, table, shift, hk, max(vis_lo, kb), min(vis_hi, kb + kTile), kg, o);
         }
-        if (more) fl.store(stage[(t + 1) & 1], t + 1, w, lane, left_of(t + 1), part(t + 1));
         __syncthreads();
     }
 
