@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -947,7 +948,7 @@ kda::AttnArgs attn_args(const kda_attn_config *cfg, const kda_kv_cache *c, int32
     kda::AttnArgs a{};
     a.kv = kv_args(cfg, c, N, T, cu, kv_len);
     a.Hq = cfg->num_q_heads;
-    kda::attn_plan(device_cus(), N, T, cfg->num_q_heads, cfg->num_kv_heads,
+    kda::attn_plan(device_cus(), cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim, N, T, cfg->num_q_heads, cfg->num_kv_heads,
                    (int64_t)c->table_width * c->page, &a);
     return a;
 }
@@ -1063,7 +1064,9 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
         return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
     if (need) KDA_TRY(check_tensor(ws, "ws", true));
     a.q = q; a.q_row = q_row; a.o = o; a.lse = lse; a.part = need ? (float *)ws : nullptr;
+    // (a scale of zero as the smallest that keeps -inf x scale = -inf: masked scores)
     a.scale = scale * 1.4426950408889634f;
+    if (std::fabs(a.scale) < FLT_MIN) a.scale = FLT_MIN;
     a.causal = causal; a.window = window;
     const bool bf = cfg->io_dtype == KDA_DTYPE_BF16;
     hipError_t e = hipSuccess;

@@ -64,7 +64,7 @@ struct AttnArgs {
 };
 // The plan of a call (short_rows, workers, row_units, row_splits) and the bytes
 // of its partial results.
-void attn_plan(int cus, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a);
+void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a);
 size_t attn_partial_bytes(int D, const AttnArgs &a);
 hipError_t launch_attn(bool bf16, int D, const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_rows(bool bf16, int D, const AttnArgs &a, hipStream_t s);

@@ -36,71 +36,60 @@ using namespace attn;
 
 constexpr int kShortRows = 64;        // most query rows of a sequence that this kernel takes
 constexpr int kSmallCall = 1024;      // query rows of a call that it takes alone
-constexpr int kMinShare = 4;          // fewest tiles worth a workgroup of their own (one per wave)
+constexpr int kMinShare = 8;          // fewest steps worth a workgroup of their own (two per wave)
 
-// A tile's codes in a wave's registers, as the products read them.
+// A step's codes in a wave's registers, as the products read them.
 template <int D> struct Codes {
-    u32x4 k[4][D / 64];         // 4 groups of 16 tokens: 16 bytes of the lane's token each
-    uint32_t v[4][4][D / 64];   // 4 groups, 4 tokens: D / 16 bytes each
-    float ks[4], vs[4];
+    u32x4 k[2][D / 64];         // 2 groups of 16 tokens: 16 bytes of the lane's token each
+    uint32_t v[2][4][D / 64];   // 2 groups, 4 tokens: D / 16 bytes each
+    float scale;                // lane 2 x + g: the group's scale of keys (x = 0), values (1)
     int ok;                     // groups with a page
 };
 
-// The pages of a tile's four groups, looked up one tile ahead of its codes.
-struct Pages { int id[4]; };
+// The pages of a wave's next steps.  Memory answers vector loads in order, so a step's
+// lookup is issued before the codes of the step ahead of it, and waiting for it leaves
+// those codes in flight.  (Scalar loads would not do: any wait for one is a wait for
+// all, the lookups on their way among them.)
+struct Lookup {
+    const int32_t *table;
+    int shift, kvl, page;       // page: lanes 0..31 and 32..63 hold group 0's and 1's
 
-// Tables and scales are only read here: loads of one value for the whole wave.
-template <typename T> __device__ __forceinline__ T uniform_load(const T *p) {
-    return *(const __attribute__((address_space(4))) T *)p;
-}
-
-__device__ __forceinline__ Pages pages_of(const int32_t *table, int shift, int kvl, int t, int t_end) {
-    Pages p;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int at = t * kTile + 16 * g;
-        p.id[g] = t < t_end && at < kvl ? uniform_load(table + (at >> shift)) : -1;
+    __device__ __forceinline__ void ask(int t, int lane) {
+        const int at = min(t * kStep + 16 * (lane >> 5), kvl - 1);
+        page = __builtin_nontemporal_load(table + (at >> shift));
     }
-    return p;
-}
+};
 
+// kvl > 0.  Groups without a page (or behind the last key) read page 0 and are masked.
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs &a, const Pages &pg, int hk, int t, int lane, Codes<D> &c) {
+__device__ __forceinline__ void load_step(const AttnArgs &a, const Lookup &pg, int hk, int t, int lane, Codes<D> &c) {
     const int col = lane & 15, kg = lane >> 4;
+    int64_t ph[2];
     c.ok = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int pid = pg.id[g];
-        c.ks[g] = c.vs[g] = 1.f;
-        if (pid >= 0 && pid < a.kv.n_pages) {
-            c.ok |= 1 << g;
-            const int64_t ph = (int64_t)pid * a.kv.Hk + hk;
-            const int64_t base = (ph * a.kv.page + ((t * kTile + 16 * g) & (a.kv.page - 1))) * D;
-            const uint8_t *kp = a.kv.k_codes + base + col * D + kg * 16;
-            const uint8_t *vp = a.kv.v_codes + base + (4 * kg) * D + col * (D / 16);
+    for (int g = 0; g < 2; ++g) {
+        int pid = __builtin_amdgcn_readlane(pg.page, 32 * g);
+        const bool ok = pid >= 0 && pid < a.kv.n_pages && t * kStep + 16 * g < pg.kvl;
+        c.ok |= ok << g;
+        pid = ok ? pid : 0;
+        ph[g] = (int64_t)pid * a.kv.Hk + hk;
+        const int64_t base = (ph[g] * a.kv.page + ((t * kStep + 16 * g) & (a.kv.page - 1))) * D;
+        const uint8_t *kp = a.kv.k_codes + base, *vp = a.kv.v_codes + base;
+        const uint32_t ko = col * D + kg * 16, vo = 4 * kg * D + col * (D / 16);
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) c.k[g][i] = *(const u32x4 *)(kp + 64 * i);
+        for (int i = 0; i < D / 64; ++i) c.k[g][i] = __builtin_nontemporal_load((const u32x4 *)(kp + ko + 64 * i));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (D == 128) {
-                    const uint2 w = *(const uint2 *)(vp + i * D);
-                    c.v[g][i][0] = w.x;
-                    c.v[g][i][1] = w.y;
-                } else {
-                    c.v[g][i][0] = *(const uint32_t *)(vp + i * D);
-                }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+                const u32x2 w = __builtin_nontemporal_load((const u32x2 *)(vp + vo + i * D));
+                c.v[g][i][0] = w[0];
+                c.v[g][i][1] = w[1];
+            } else {
+                c.v[g][i][0] = __builtin_nontemporal_load((const uint32_t *)(vp + vo + i * D));
             }
-            c.ks[g] = uniform_load(a.kv.k_scale + ph);
-            c.vs[g] = uniform_load(a.kv.v_scale + ph);
-        } else {
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) c.k[g][i] = u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) c.v[g][i][j] = 0;
         }
     }
+    c.scale = ((lane & 2) ? a.kv.v_scale : a.kv.k_scale)[(lane & 1) ? ph[1] : ph[0]];
 }
 
 // O^T += V^T P^T for one pair of token groups
@@ -121,7 +110,7 @@ __device__ __forceinline__ void add_pv(const uint32_t (&v0)[4][D / 64], const ui
     }
 }
 
-// Tiles per workgroup when `workers` of them share all.
+// Steps per workgroup when `workers` of them share all.
 __device__ __forceinline__ int64_t share_of(int64_t total, int workers) {
     return max((total + workers - 1) / workers, (int64_t)kMinShare);
 }
@@ -152,8 +141,22 @@ template <int D, int NS> struct Row {
         for (int f = 0; f < D / 32; ++f) {
             float x[8];
             mf::IO<NS == 1>::load8(a.q, qi + (f >> 1) * 64 + kg * 16 + (f & 1) * 8, x);
+            if (a.scale < 0.f) {          // the maximum is taken before the scale
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = -x[j];
+            }
             q[f] = split8<NS>(x);
         }
+        // The loads end here: were they still on their way at the loop's first entry, its
+        // waits would count them in every pass.
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                u32x4 x = __builtin_bit_cast(u32x4, q[f].f[i]);
+                asm volatile("" : "+v"(x));
+                q[f].f[i] = __builtin_bit_cast(bf16x8, x);
+            }
         const int t0 = rb * kRows / G, t1 = min((rb * kRows + kRows - 1) / G, s.len - 1);
         hi = R < s.len * G ? s.end_of(a, tok) : 0;
         lo = s.begin_of(a, tok);
@@ -162,48 +165,57 @@ template <int D, int NS> struct Row {
     }
 };
 
-// One tile of 64 keys for the 16 rows of a unit.  True: values that were NaN are left
+// One step of 32 keys for the 16 rows of a unit.  True: values that were NaN are left
 // out, see_nans() is to follow.
 template <int D, int NS>
-__device__ __forceinline__ bool tile_step(const Row<D, NS> &row, Codes<D> &c, int t, float scale, int lane, float &m,
+__device__ __forceinline__ bool one_step(const Row<D, NS> &row, Codes<D> &c, int t, float scale, int lane, float &m,
                                           float &l, f32x4 *o) {
     constexpr int NT = D / 16;
-    const int kg = lane >> 4, kb = t * kTile;
-    f32x4 sc[4];
+    const int kg = lane >> 4, kb = t * kStep;
+    const uint32_t sv = f32_bits(c.ok >> (lane & 1) & 1 ? c.scale : 1.f);
+    float ks[2], vs[2];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 2; ++g) {
+        ks[g] = bits_f32(__builtin_amdgcn_readlane(sv, g));
+        vs[g] = bits_f32(__builtin_amdgcn_readlane(sv, 2 + g));
+    }
+    f32x4 sc[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
         sc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int f = 0; f < D / 32; ++f) {
             const u32x4 x = c.k[g][f >> 1];
             const uint32_t c0 = (f & 1) ? x[2] : x[0], c1 = (f & 1) ? x[3] : x[1];
             u32x4 kf;
-            kf[0] = widen<false>(c0, c.ks[g]);
-            kf[1] = widen<true>(c0, c.ks[g]);
-            kf[2] = widen<false>(c1, c.ks[g]);
-            kf[3] = widen<true>(c1, c.ks[g]);
+            kf[0] = widen<false>(c0, ks[g]);
+            kf[1] = widen<true>(c0, ks[g]);
+            kf[2] = widen<false>(c1, ks[g]);
+            kf[3] = widen<true>(c1, ks[g]);
 #pragma unroll
             for (int i = 0; i < NS; ++i)
                 sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), row.q[f].f[i], sc[g],
                                                                 0, 0, 0);
         }
     }
-    const bool full = c.ok == 15 && kb >= row.all_lo && kb + kTile <= row.all_hi;
+    const bool full = c.ok == 3 && kb >= row.all_lo && kb + kStep <= row.all_hi;
+    if (!full) {
+        asm volatile("");             // a branch: whole steps are the rule
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = kb + 16 * g + 4 * kg + i;
+                if (!(j >= row.lo && j < row.hi && (c.ok >> g & 1))) sc[g][i] = -__builtin_inff();
+            }
+    }
     float tm = -__builtin_inff();
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x = sc[g][i] * scale;
-            if (!full) {
-                const int j = kb + 16 * g + 4 * kg + i;
-                const bool y = j >= row.lo && j < row.hi && (c.ok >> g & 1);
-                x = y ? x : -__builtin_inff();
-            }
-            sc[g][i] = x;
-            tm = fmaxf(tm, x);
-        }
+        for (int i = 0; i < 4; ++i) tm = fmaxf(tm, sc[g][i]);
     tm = max_16(tm);
+    tm = tm == -__builtin_inff() ? tm : tm * scale;
     if (__ballot(tm > m) != 0) {
         const float mn = fmaxf(m, tm);
         const float alpha = mf::ex2(m - (mn == -__builtin_inff() ? 0.f : mn));
@@ -213,13 +225,12 @@ __device__ __forceinline__ bool tile_step(const Row<D, NS> &row, Codes<D> &c, in
         for (int i = 0; i < NT; ++i) o[i] *= alpha;
     }
     const float ms = m == -__builtin_inff() ? 0.f : m;
-    float p[16];
+    float p[8];
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            p[4 * g + i] = mf::ex2(sc[g][i] - ms);
-            l += p[4 * g + i];
+            p[4 * g + i] = mf::ex2(__builtin_fmaf(sc[g][i], scale, -ms));
         }
 
     bool repair = false;
@@ -227,7 +238,7 @@ __device__ __forceinline__ bool tile_step(const Row<D, NS> &row, Codes<D> &c, in
         // a NaN among the values would reach rows that do not see it (0 x NaN)
         uint32_t any = 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -239,8 +250,8 @@ __device__ __forceinline__ bool tile_step(const Row<D, NS> &row, Codes<D> &c, in
         repair = __ballot(any != 0) != 0;
     }
 #pragma unroll
-    for (int g = 0; g < 4; g += 2)
-        add_pv<D, NS>(c.v[g], c.v[g + 1], c.vs[g], c.vs[g + 1], split8<NS>(p + 4 * g), o);
+    for (int i = 0; i < 8; ++i) l += p[i];
+    add_pv<D, NS>(c.v[0], c.v[1], vs[0], vs[1], split8<NS>(p), o);
     return repair;
 }
 
@@ -279,8 +290,8 @@ __device__ __forceinline__ void store_row(void *o, int64_t at, const float *y, f
     }
 }
 
-// The tiles of all units in a row: their number, and where sequence `of` (>= 0) or
-// tile `from` (of < 0) lies; n: that sequence, base: the tiles before it.
+// The steps of all units in a row: their number, and where sequence `of` (>= 0) or the
+// share of workgroup `block` (of < 0) starts; n: that sequence, base: the steps before it.
 struct Place { int64_t total, base; int n; };
 
 __device__ __forceinline__ Place place(const AttnArgs &a, int G, int of, int block, int tid) {
@@ -358,11 +369,11 @@ __device__ __forceinline__ bool packed_unit(const AttnArgs &a, int64_t x, int G,
     return r >= 0 && r < s.rt;
 }
 
-// BF: bf16 rows.  One workgroup takes a contiguous share of all (unit, tile)
-// pairs, or, with workers = 0, one unit; its waves take the tiles of a unit in
-// turn, each with its next tile on the way from HBM, and meet in LDS at the end.
+// BF: bf16 rows.  One workgroup takes a contiguous share of all (unit, step)
+// pairs, or, with workers = 0, one unit; its waves take the steps of a unit in
+// turn, each with its next step on the way from HBM, and meet in LDS at the end.
 template <int D, bool BF>
-__global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void attn_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const AttnArgs a) {
     constexpr int NS = BF ? 1 : 3;
     constexpr int NT = D / 16;                 // 16-dim blocks of O
     __shared__ Meet<D> sm;
@@ -373,15 +384,15 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void attn_kernel(const At
     const int G = a.Hq / a.kv.Hk;
     const int shift = __builtin_ctz(a.kv.page);
 
-    // this workgroup's share [from, to) of the tiles
+    // this workgroup's share [from, to) of the steps
     int64_t from, to, base = 0;
     int n = 0;
     Seq s;
     if (a.workers == 0) {
         int rb;
         if (!packed_unit(a, blockIdx.x / a.kv.Hk, G, n, s, rb)) return;
-        from = (int64_t)((int)(blockIdx.x % a.kv.Hk) * s.rt + rb) * s.tiles;
-        to = from + s.tiles;
+        from = (int64_t)((int)(blockIdx.x % a.kv.Hk) * s.rt + rb) * s.steps;
+        to = from + s.steps;
     } else {
         const Place p = place(a, G, -1, blockIdx.x, tid);
         const int64_t share = share_of(p.total, a.workers);
@@ -397,14 +408,14 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void attn_kernel(const At
         const int64_t end = base + s.cost(a);  // of this sequence
         const int32_t *table = a.kv.table + (int64_t)n * a.kv.width;
         while (at < to && at < end) {
-            const uint32_t unit = quotient(at - base, s.tiles);
-            const int64_t ubase = base + (int64_t)unit * s.tiles, uend = ubase + s.tiles;
+            const uint32_t unit = quotient(at - base, s.steps);
+            const int64_t ubase = base + (int64_t)unit * s.steps, uend = ubase + s.steps;
             const int hk = (int)(unit / (uint32_t)s.rt), rb = (int)(unit % (uint32_t)s.rt);
             const bool whole = ubase >= from && uend <= to;
-            // its tiles here, less those that no row of the unit sees
+            // its steps here, less those that no row of the unit sees
             const int t0 = min(rb * kRows / G, s.len - 1), t1 = min((rb * kRows + kRows - 1) / G, s.len - 1);
-            const int beg = max(s.lo + (int)(at - ubase), s.begin_of(a, t0) / kTile);
-            const int stop = min(s.lo + (int)(min(uend, to) - ubase), (s.end_of(a, t1) + kTile - 1) / kTile);
+            const int beg = max(s.lo + (int)(at - ubase), s.begin_of(a, t0) / kStep);
+            const int stop = min(s.lo + (int)(min(uend, to) - ubase), (s.end_of(a, t1) + kStep - 1) / kStep);
 
             float m = -__builtin_inff(), l = 0.f;
             f32x4 o[NT];
@@ -413,25 +424,33 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void attn_kernel(const At
             Row<D, NS> row;
             Codes<D> c0, c1;
             int t = beg + w;
-            if (t < stop) load_tile<D>(a, pages_of(table, shift, s.kvl, t, stop), hk, t, lane, c0);
-            Pages pg = pages_of(table, shift, s.kvl, t + kWaves, stop);
-            row.load(a, s, rb, hk, G, lane);
-            while (t < stop) {
-                if (t + kWaves < stop) {
-                    load_tile<D>(a, pg, hk, t + kWaves, lane, c1);
-                    pg = pages_of(table, shift, s.kvl, t + 2 * kWaves, stop);
-                }
-                if (tile_step<D, NS>(row, c0, t, a.scale, lane, m, l, o))
-                    see_nans<D>(a, table, shift, hk, max(row.lo, t * kTile), min(row.hi, (t + 1) * kTile), kg, o);
-                t += kWaves;
-                if (t >= stop) break;
-                if (t + kWaves < stop) {
-                    load_tile<D>(a, pg, hk, t + kWaves, lane, c0);
-                    pg = pages_of(table, shift, s.kvl, t + 2 * kWaves, stop);
-                }
-                if (tile_step<D, NS>(row, c1, t, a.scale, lane, m, l, o))
-                    see_nans<D>(a, table, shift, hk, max(row.lo, t * kTile), min(row.hi, (t + 1) * kTile), kg, o);
-                t += kWaves;
+            if (t < stop) {
+                // In flight from here on: the codes of the next step, the lookup of the one
+                // after.  Past the last step they are the last one's again: a load that
+                // might not be issued would make every wait one for all loads.
+                const int last = stop - 1;
+                Lookup pg{table, shift, s.kvl, 0};
+                pg.ask(t, lane);
+                row.load(a, s, rb, hk, G, lane);
+                row.hi = min(row.hi, stop * kStep);      // the keys behind are another share's
+                row.all_hi = min(row.all_hi, stop * kStep);
+                Lookup next = pg;
+                next.ask(min(t + kWaves, last), lane);
+                load_step<D>(a, pg, hk, t, lane, c0);
+                auto step = [&](Codes<D> &c, Codes<D> &ahead) {
+                    pg = next;
+                    next.ask(min(t + 2 * kWaves, last), lane);
+                    load_step<D>(a, pg, hk, min(t + kWaves, last), lane, ahead);
+                    if (one_step<D, NS>(row, c, t, fabsf(a.scale), lane, m, l, o))
+                        see_nans<D>(a, table, shift, hk, max(row.lo, t * kStep), min(row.hi, (t + 1) * kStep), kg, o);
+                    t += kWaves;
+                };
+                // Two steps a pass with one way out, so that the waits of a pass know what is
+                // on its way; the second of an odd last pair sees no key.
+                do {
+                    step(c0, c1);
+                    step(c1, c0);
+                } while (t < stop);
             }
 
             // the waves meet
@@ -501,8 +520,8 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
     if (!packed_unit(a, u / a.kv.Hk, G, n, s, rb)) return;
     const Place p = place(a, G, n, 0, tid);
     const int64_t share = share_of(p.total, a.workers);
-    const int64_t ubase = p.base + (int64_t)(hk * s.rt + rb) * s.tiles;
-    const int64_t w0 = ubase / share, w1 = (ubase + s.tiles - 1) / share;
+    const int64_t ubase = p.base + (int64_t)(hk * s.rt + rb) * s.steps;
+    const int64_t w0 = ubase / share, w1 = (ubase + s.steps - 1) / share;
     if (w0 == w1) return;                               // written whole
     const int d = (tid % TD) * E, sl = tid / TD % SL, rr = tid / (TD * SL);
     const int r = (blockIdx.x % (kRows / RW)) * RW + rr;
@@ -568,7 +587,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 
 }  // namespace
 
-void attn_plan(int cus, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a) {
+// Workgroups of attn_kernel that a compute unit holds (by their registers).  The shares
+// are cut for just these: half as many take 258 us for 64 sequences of 512 to 32,768
+// tokens at 32 / 8 heads of 128, these 231, twice as many 256 (more parts to write and
+// join).  Counting a unit's start and end as kUnitCost steps evens out shares of many
+// short units and of few long ones (246 us without).
+static int resident(bool bf16, int D) { return D == 64 ? (bf16 ? 4 : 3) : (bf16 ? 3 : 2); }
+
+void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a) {
     const int G = Hq / Hk;
     const int64_t rows = T * G;
     a->workers = -1;
@@ -579,7 +605,7 @@ void attn_plan(int cus, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnAr
     const bool all_short = rows <= kShortRows || (N > 1 && rows <= kSmallCall);
     const bool all_long = N == 1 && !all_short;
     a->short_rows = all_short ? INT32_MAX : kShortRows;
-    if (!all_long) a->workers = max_kv <= 8 * kTile ? 0 : 2 * cus;
+    if (!all_long) a->workers = max_kv <= 16 * kStep ? 0 : cus * resident(bf16, D);
     if (!all_short) {
         a->row_units = (int32_t)(rows / kRowTile + N);
         const int64_t units = (int64_t)a->row_units * Hk;

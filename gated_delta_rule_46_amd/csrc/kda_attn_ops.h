@@ -12,11 +12,14 @@ using mf::bf16_t;
 using mf::bf16x8;
 using mf::f32x4;
 typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kWaves = kAttnThreads / 64;
-constexpr int kTile = 64;             // keys per step
+constexpr int kTile = 64;             // keys per step of kda_attn_rows.hip
+constexpr int kStep = 32;             // and of kda_attn.hip
+constexpr int kUnitCost = 12;         // steps that starting and ending a unit there costs
 constexpr int kRows = 16;             // query rows (token, head of the group) per unit of kda_attn.hip
 constexpr int kRowTile = 128;         // and of kda_attn_rows.hip
 constexpr float kLn2 = 0.6931471805599453f;
@@ -35,7 +38,7 @@ struct Seq {
     int kvl;          // cached tokens that the table can hold
     int len;
     int rt;           // units of kRows rows per kv head (0: the other kernel's)
-    int lo, tiles;    // tiles of the unmasked range of all its rows; at least one
+    int lo, steps;    // first step that some row sees; steps of a unit, kUnitCost among them
 
     // keys that new token i sees: begin_of(i) <= j < end_of(i)
     __device__ __forceinline__ int end_of(const AttnArgs &a, int i) const {
@@ -44,8 +47,8 @@ struct Seq {
     __device__ __forceinline__ int begin_of(const AttnArgs &a, int i) const {
         return a.window > 0 ? (int)max(min(pos0 + i + 1 - a.window, (int64_t)kvl), (int64_t)0) : 0;
     }
-    // (unit, tile) pairs of the sequence
-    __device__ __forceinline__ int64_t cost(const AttnArgs &a) const { return (int64_t)a.kv.Hk * rt * tiles; }
+    // (unit, step) pairs of the sequence
+    __device__ __forceinline__ int64_t cost(const AttnArgs &a) const { return (int64_t)a.kv.Hk * rt * steps; }
 };
 
 __device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
@@ -58,8 +61,8 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
     s.pos0 = kv - s.len;
     s.kvl = (int)max(min(kv, (int64_t)a.kv.width * a.kv.page), (int64_t)0);
     s.rt = (int64_t)s.len * G <= a.short_rows ? (s.len * G + kRows - 1) / kRows : 0;
-    s.lo = s.begin_of(a, 0) / kTile;
-    s.tiles = max((s.kvl + kTile - 1) / kTile - s.lo, 1);
+    s.lo = s.begin_of(a, 0) / kStep;
+    s.steps = (s.kvl + kStep - 1) / kStep - s.lo + kUnitCost;
     return s;
 }
 

@@ -335,10 +335,9 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
             const float ms = m == -__builtin_inff() ? 0.f : m;
             float p[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                p[i] = mf::ex2(__builtin_fmaf(sc[i >> 4][i & 15], sl, -ms));
-                l += p[i];
-            }
+            for (int i = 0; i < 32; ++i) p[i] = mf::ex2(__builtin_fmaf(sc[i >> 4][i & 15], sl, -ms));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) l += p[i];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (k < 3) {

@@ -364,6 +364,9 @@ def test_attn_prompt_queries_of_all_sizes(K, dtype):
     new, kv, D = 200, 330, 128
     m, rng = plain_model(K, dtype, 1, D, 64, [kv], 51)
     q = queries(rng, new, 2, D, dtype).clone()
+    attn_check(K, m, dtype, q, [0, new], [kv], 0.0, name="scale 0")
+    attn_check(K, m, dtype, q, [0, new], [kv], -0.1, name="negative scale")
+    attn_check(K, m, dtype, q, [0, new], [kv], 5.0, name="scores of hundreds")
     q *= torch.exp2(torch.randint(-8, 5, q.shape, device="cuda")).to(q.dtype)
     q[10] = 0
     q[11] *= 2.0 ** -100
