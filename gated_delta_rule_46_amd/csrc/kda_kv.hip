@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(const KvArgs a) {
     for (int i = 0; i < NC; ++i) {
         const int c = i * kKvThreads + tid, r = c / CH;
         if (r < rows) {
-            mf::IO<BF>::load8(src, at + r * row + (c % CH) * 8, v[i]);
+            load8_once<BF>(src, at + r * row + (c % CH) * 8, v[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float y = fabsf(v[i][j]);

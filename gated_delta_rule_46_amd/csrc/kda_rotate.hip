@@ -77,8 +77,8 @@ __global__ __launch_bounds__(kRotThreads) void rotate_kernel(const RotateArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = 0.f;
         if (live) {
-            if (isq) mf::IO<BF>::load8(a.q, t * a.q_row + (int64_t)h * D + d0, x);
-            else mf::IO<BF>::load8(a.k, t * a.k_row + (int64_t)(h - a.Hq) * D + d0, x);
+            if (isq) load8_once<BF>(a.q, t * a.q_row + (int64_t)h * D + d0, x);
+            else load8_once<BF>(a.k, t * a.k_row + (int64_t)(h - a.Hq) * D + d0, x);
         }
         float ss = 0.f;
 #pragma unroll
