@@ -128,22 +128,23 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(const KvArgs a) {
     if (tid == 0 && s != held) *scale = s;
 }
 
-// One workgroup per kReadRows packed tokens, whose places are looked up side by
-// side first; then a thread takes 16 codes at a time (16 bytes in, 32 or 64 out),
-// kReadDeep of them in flight.  Tokens without a page read as zeros.
-constexpr int kReadRows = 16;
-constexpr int kReadDeep = 4;
+// One workgroup per ROWS packed tokens, whose places are looked up side by side first;
+// then a thread takes the codes of 16 bytes of output at a time, kReadDeep of them in
+// flight.  Tokens without a page read as zeros.  ROWS: 16, or 4 while that leaves
+// compute units idle.
+constexpr int kReadDeep = 8;
 
-template <int D, bool BF>
+template <int D, bool BF, int ROWS>
 __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const KvArgs a) {
-    constexpr int CH = D / 16;                // pieces per row
-    __shared__ int64_t s_row[kReadRows];      // pid * Hk * page + row of the page, -1: absent, -2: not there
-    __shared__ int s_pid[kReadRows];
+    constexpr int PC = BF ? 8 : 4;            // codes per piece
+    constexpr int CH = D / PC;                // pieces per row
+    __shared__ int64_t s_row[ROWS];           // pid * Hk * page + row of the page, -1: absent, -2: not there
+    __shared__ int s_pid[ROWS];
     const int tid = threadIdx.x;
-    const int64_t t0 = (int64_t)blockIdx.x * kReadRows;
+    const int64_t t0 = (int64_t)blockIdx.x * ROWS;
     if (t0 >= a.cu[a.N]) return;              // rows behind the last sequence stay as they are
     int n = last_not_above(a.N, t0, [&](int i) { return a.cu[i]; });
-    if (tid < kReadRows) {
+    if (tid < ROWS) {
         const int64_t t = t0 + tid;
         while (n < a.N && t >= a.cu[n + 1]) ++n;
         int64_t place = -2;
@@ -162,44 +163,46 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const KvArgs a) {
         s_pid[tid] = pid;
     }
     __syncthreads();
-    const int per = 2 * a.Hk * CH;            // pieces per token
-    const int all = kReadRows * per;
+    const int per = a.Hk * CH;                // pieces per token of keys, and of values
+    const int all = 2 * ROWS * per;
     for (int c0 = tid; c0 < all; c0 += kReadDeep * kKvThreads) {
-        uint4 w[kReadDeep];
+        uint32_t w[kReadDeep][PC / 4];
         float s[kReadDeep];
         int64_t to[kReadDeep];
         bool is_v[kReadDeep];
 #pragma unroll
         for (int u = 0; u < kReadDeep; ++u) {
             const int c = c0 + u * kKvThreads;
-            w[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < PC / 4; ++j) w[u][j] = 0;
             s[u] = 1.f;
             to[u] = -1;
+            is_v[u] = false;
             if (c >= all) continue;
-            const int i = (int)((uint32_t)c / (uint32_t)per), x = c - i * per;
+            const int ix = (int)((uint32_t)c / (uint32_t)per), x = c - ix * per, i = ix >> 1;
             const int64_t place = s_row[i];
             if (place == -2) continue;
-            is_v[u] = x >= a.Hk * CH;
-            const int y = is_v[u] ? x - a.Hk * CH : x, h = y / CH, d = y % CH * 16;
+            is_v[u] = ix & 1;
+            const int h = x / CH, d = x % CH * PC;
             to[u] = ((t0 + i) * a.Hk + h) * D + d;
             if (place >= 0) {
-                w[u] = *(const uint4 *)((is_v[u] ? a.v_codes : a.k_codes) + (place + (int64_t)h * a.page) * D + d);
+                const uint8_t *p = (is_v[u] ? a.v_codes : a.k_codes) + (place + (int64_t)h * a.page) * D + d;
+#pragma unroll
+                for (int j = 0; j < PC / 4; ++j) w[u][j] = ((const uint32_t *)p)[j];
                 s[u] = (is_v[u] ? a.v_scale : a.k_scale)[(int64_t)s_pid[i] * a.Hk + h];
             }
         }
 #pragma unroll
         for (int u = 0; u < kReadDeep; ++u) {
             if (to[u] < 0) continue;
-            float y[16];
-            uncode4(w[u].x, y);
-            uncode4(w[u].y, y + 4);
-            uncode4(w[u].z, y + 8);
-            uncode4(w[u].w, y + 12);
+            float y[PC];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] *= s[u];
+            for (int j = 0; j < PC / 4; ++j) uncode4(w[u][j], y + 4 * j);
+#pragma unroll
+            for (int j = 0; j < PC; ++j) y[j] *= s[u];
             void *out = is_v[u] ? a.v_out : a.k_out;
-            mf::IO<BF>::store8(out, to[u], y);
-            mf::IO<BF>::store8(out, to[u] + 8, y + 8);
+            if constexpr (BF) mf::IO<true>::store8(out, to[u], y);
+            else *(float4 *)((float *)out + to[u]) = make_float4(y[0], y[1], y[2], y[3]);
         }
     }
 }
@@ -234,21 +237,24 @@ hipError_t launch_kv_write(bool bf16, int D, const KvArgs &a, hipStream_t s) {
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_kv_read(bool bf16, int D, const KvArgs &a, hipStream_t s) {
-    if (a.T <= 0 || a.N <= 0) return hipSuccess;
-    const int64_t g = (a.T + kReadRows - 1) / kReadRows;
-    if (g > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)g), block(kKvThreads);
-    if (D == 128) {
-        if (bf16) hipLaunchKernelGGL((kv_read_kernel<128, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((kv_read_kernel<128, false>), grid, block, 0, s, a);
-    } else if (D == 64) {
-        if (bf16) hipLaunchKernelGGL((kv_read_kernel<64, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((kv_read_kernel<64, false>), grid, block, 0, s, a);
+template <int D, bool BF>
+static hipError_t launch_read(const KvArgs &a, hipStream_t s) {
+    const dim3 block(kKvThreads);
+    if (a.T < 16 * 1024) {
+        hipLaunchKernelGGL((kv_read_kernel<D, BF, 4>), dim3((unsigned)((a.T + 3) / 4)), block, 0, s, a);
     } else {
-        return hipErrorInvalidValue;
+        const int64_t g = (a.T + 15) / 16;
+        if (g > INT32_MAX) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((kv_read_kernel<D, BF, 16>), dim3((unsigned)g), block, 0, s, a);
     }
     return hipGetLastError();
+}
+
+hipError_t launch_kv_read(bool bf16, int D, const KvArgs &a, hipStream_t s) {
+    if (a.T <= 0 || a.N <= 0) return hipSuccess;
+    if (D == 128) return bf16 ? launch_read<128, true>(a, s) : launch_read<128, false>(a, s);
+    if (D == 64) return bf16 ? launch_read<64, true>(a, s) : launch_read<64, false>(a, s);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace kda

@@ -699,7 +699,63 @@ def kda_conv_halo(x, bounds, width, windows, write_idx, *, stream=None):
 
 # ---------------------------------------------------------------------------
 # Softmax-attention layers
+#
+# A decode step's calls are bound by their host time, so what does not depend on
+# addresses (shapes, strides, types, devices) is checked once for each
+# combination and remembered: the _*_plan functions see no tensor.
 # ---------------------------------------------------------------------------
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_current_stream = torch._C._cuda_getCurrentRawStream   # its handle, without a Stream object
+_current_device = torch._C._cuda_getDevice
+
+
+def _form(t):
+    """What a plan sees of a tensor (None of a missing one)."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _dense(form, name, shape, dtype, dev):
+    """Checks the form of a contiguous tensor."""
+    if form is None:
+        raise ValueError(f"{name} is required")
+    if form[0] != shape:
+        raise ValueError(f"{name} has shape {tuple(form[0])}, expected {tuple(shape)}")
+    if form[2] != dtype:
+        raise TypeError(f"{name} has dtype {form[2]}, expected {dtype}")
+    if form[3] != dev:
+        raise ValueError(f"{name} is on device {form[3]}, expected {dev}")
+    step = 1
+    for n, st in zip(reversed(shape), reversed(form[1])):
+        if n > 1 and st != step:
+            raise ValueError(f"{name} must be contiguous")
+        step *= n
+
+
+def _rows(form, name, T, D, dtype, dev, heads=None):
+    """Checks the form of packed rows [T, heads, D] whose heads are contiguous; tokens may be
+    apart.  Returns the distance between tokens in elements."""
+    shape, stride = form[0], form[1]
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or (heads and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({T}, {heads or 'heads'}, {D})")
+    if form[2] != dtype:
+        raise TypeError(f"{name} has dtype {form[2]}, expected {dtype}")
+    if form[3] != dev:
+        raise ValueError(f"{name} is on device {form[3]}, expected {dev}")
+    if (stride[2] != 1 and D > 1) or (stride[1] != D and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {stride})")
+    return stride[0] if T > 1 else max(stride[0], shape[1] * D)
+
+
+def _on_device(form):
+    if form[3] < 0:
+        raise ValueError("inputs must be device tensors")
+    return form[3]
+
+
+def _attn_config(Hq, Hk, D, dtype):
+    return ctypes.byref(kda_attn_config(Hq, Hk, D, _io_dtype(dtype)))
+
+
 class KVCache:
     """Buffers of a paged 8-bit key/value cache (kda_kv_cache): codes k, v [n_pages, Hk, page, D]
     (uint8 or float8_e4m3fn), k_scale, v_scale [n_pages, Hk] fp32 and the table [N, width] int32 of
@@ -716,211 +772,210 @@ class KVCache:
         scales = [torch.ones((n_pages, Hk), dtype=torch.float32, device=dev) for _ in "kv"]
         return cls(*codes, *scales, table)
 
-    def c(self, N, Hk, D, dev):
-        k, v, ks, vs, table = self.k, self.v, self.k_scale, self.v_scale, self.table
-        n_pages, _, page, _ = shape = k.shape
-        if k.dtype not in _CODES or v.dtype not in _CODES:
-            raise TypeError(f"cache.k and cache.v have dtypes {k.dtype}, {v.dtype}, expected uint8 or float8_e4m3fn")
-        if shape[1] != Hk or shape[3] != D:
-            raise ValueError(f"cache.k has shape {tuple(shape)}, expected ({n_pages}, {Hk}, {page}, {D})")
-        _want(k, "cache.k", shape, k.dtype, dev)
-        _want(v, "cache.v", shape, v.dtype, dev)
-        _want(ks, "cache.k_scale", (n_pages, Hk), torch.float32, dev)
-        _want(vs, "cache.v_scale", (n_pages, Hk), torch.float32, dev)
-        width = table.shape[1]
-        _want(table, "cache.table", (N, width), torch.int32, dev)
-        return kda_kv_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page,
-                            width, table.data_ptr())
+    def form(self):
+        return (_form(self.k), _form(self.v), _form(self.k_scale), _form(self.v_scale), _form(self.table))
+
+    def c(self, sizes):
+        """The C struct; sizes: (n_pages, page, width) of a plan."""
+        return ctypes.byref(kda_kv_cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                                         self.v_scale.data_ptr(), *sizes, self.table.data_ptr()))
 
 
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+def _cache_sizes(form, N, Hk, D, dev):
+    k, v, ks, vs, table = form
+    for f, name in ((k, "cache.k"), (v, "cache.v")):
+        if f[2] not in _CODES:
+            raise TypeError(f"{name} has dtype {f[2]}, expected uint8 or float8_e4m3fn")
+    if len(k[0]) != 4 or len(table[0]) != 2:
+        raise ValueError("cache.k / cache.v are [n_pages, Hk, page, D], cache.table is [N, width]")
+    n_pages, _, page, _ = k[0]
+    for f, name in ((k, "cache.k"), (v, "cache.v")):
+        _dense(f, name, (n_pages, Hk, page, D), f[2], dev)
+    _dense(ks, "cache.k_scale", (n_pages, Hk), torch.float32, dev)
+    _dense(vs, "cache.v_scale", (n_pages, Hk), torch.float32, dev)
+    _dense(table, "cache.table", (N, table[0][1]), torch.int32, dev)
+    return n_pages, page, table[0][1]
 
 
-def _want(t, name, shape, dtype, dev):
-    """_need with one pass over the attributes (a decode step's calls are bound by their host time)."""
-    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        _need(t, name, shape, dtype, dev)
+def _sequences(cu, kv_len, dev):
+    if len(cu[0]) != 1 or cu[0][0] < 1:
+        raise ValueError(f"cu_seqlens has shape {tuple(cu[0])}, expected (N + 1,)")
+    N = cu[0][0] - 1
+    _dense(cu, "cu_seqlens", (N + 1,), torch.int64, dev)
+    _dense(kv_len, "kv_len", (N,), torch.int64, dev)
+    return N
 
 
-def _need_rows(t, name, T, D, dtype, device):
-    """Packed rows [T, heads, D] whose heads are contiguous; tokens may be apart.  Returns the
-    distance between tokens in elements."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {D})")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    row, head, el = t.stride()
-    if (el != 1 and D > 1) or (head != D and t.shape[1] > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
-    return row if T > 1 else max(row, t.shape[1] * D)
+@functools.lru_cache(maxsize=1024)
+def _rotate_plan(q, k, positions, table, q_weight, k_weight, q_out, k_out):
+    dev = _on_device(q)
+    if len(q[0]) != 3 or len(k[0]) != 3:
+        raise ValueError("q and k are [T, heads, D]")
+    T, Hq, D = q[0]
+    Hk, dtype = k[0][1], q[2]
+    rows = [_rows(q, "q", T, D, dtype, dev), _rows(k, "k", T, D, dtype, dev)]
+    n_pos = rot = 0
+    if table is not None:
+        if len(table[0]) != 2:
+            raise ValueError("rope_table is [n_pos, R]")
+        n_pos, rot = table[0]
+        _dense(table, "rope_table", (n_pos, rot), torch.float32, dev)
+        _dense(positions, "positions", (T,), torch.int64, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _dense(w, name, (D,), torch.float32, dev)
+    rows.append(Hq * D if q_out is None else _rows(q_out, "q_out", T, D, dtype, dev, Hq))
+    rows.append(Hk * D if k_out is None else _rows(k_out, "k_out", T, D, dtype, dev, Hk))
+    return (_attn_config(Hq, Hk, D, dtype), dev, n_pos, rot, *rows)
 
 
-@functools.lru_cache(maxsize=256)
-def _attn_config(Hq, Hk, D, dtype):
-    return ctypes.byref(kda_attn_config(Hq, Hk, D, _io_dtype(dtype)))
-
-
-def _device(t):
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be device tensors")
-    return dev
+def kda_qk_norm_rope(q, k, positions=None, rope_table=None, *, q_weight=None, k_weight=None,
+                     eps=1e-6, layout=KDA_ROPE_HALVES, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [T,Hq,D] and k [T,Hk,D] and the rotation of its first R dims by
+    position, in one pass.  rope_table: fp32 [n_pos,R], R/2 cosines then R/2 sines of each position
+    (None: norm only); positions: int64 [T], a token outside [0, n_pos) is left as it is.  weights:
+    fp32 [D] or None (ones).  q, k and the outputs may have tokens apart (views of a projection's
+    rows); q_out / k_out may be q / k.  Returns (q_out, k_out).  stream: a torch.cuda.Stream to run
+    and allocate on (None: the current one of the tensors' device)."""
+    cfg, dev, n_pos, rot, q_row, k_row, qo_row, ko_row = _rotate_plan(
+        _form(q), _form(k), _form(positions), _form(rope_table), _form(q_weight), _form(k_weight),
+        _form(q_out), _form(k_out))
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_qk_norm_rope(q, k, positions, rope_table, q_weight=q_weight, k_weight=k_weight,
+                                    eps=eps, layout=layout, q_out=q_out, k_out=k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    st = LIB.kda_qk_norm_rope(cfg, q.shape[0], q.data_ptr(), q_row, k.data_ptr(), k_row,
+                              _ptr(q_weight), _ptr(k_weight), eps, _ptr(rope_table), n_pos, rot,
+                              layout, _ptr(positions) if rot else None, q_out.data_ptr(), qo_row,
+                              k_out.data_ptr(), ko_row, _current_stream(dev))
+    if st:
+        _check(st, "kda_qk_norm_rope")
+    return q_out, k_out
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_stream(at, name):
-    """Runs a call on the device of its argument `name` (position `at`) and on `stream` (None: that
-    device's current one), its allocations included: buffers taken for a call are then ordered with
-    the stream that uses them."""
-    def wrap(f):
-        @functools.wraps(f)
-        def g(*args, stream=None, **kw):
-            if stream is not None:
-                with torch.cuda.stream(stream):
-                    return f(*args, **kw)
-            x = args[at] if len(args) > at else kw[name]
-            dev = (x.k if name == "cache" else x).device
-            if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-                with torch.cuda.device(dev):
-                    return f(*args, **kw)
-            return f(*args, **kw)
-        return g
-    return wrap
+def _placed(dev, stream):
+    """The device of a call's tensors, or the stream given for it, as the current one: what the call
+    allocates is then ordered with the stream that uses it."""
+    return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream   # its handle, without a Stream object
+@functools.lru_cache(maxsize=1024)
+def _write_plan(k, v, cu, kv_len, cache):
+    dev = _on_device(k)
+    if len(k[0]) != 3:
+        raise ValueError("k and v are [T, Hk, D]")
+    T, Hk, D = k[0]
+    rows = _rows(k, "k", T, D, k[2], dev), _rows(v, "v", T, D, k[2], dev, Hk)
+    N = _sequences(cu, kv_len, dev)
+    return (_attn_config(Hk, Hk, D, k[2]), dev, N, _cache_sizes(cache, N, Hk, D, dev), *rows)
 
 
-def _raised(status, where):
-    if status != KDA_OK:
-        _check(status, where)
-
-
-@_on_stream(0, "q")
-def kda_qk_norm_rope(q, k, positions=None, rope_table=None, *, q_weight=None, k_weight=None,
-                     eps=1e-6, layout=KDA_ROPE_HALVES, q_out=None, k_out=None):
-    """RMS norm of every head of q [T,Hq,D] and k [T,Hk,D] and the rotation of its first R dims by
-    position, in one pass.  rope_table: fp32 [n_pos,R], R/2 cosines then R/2 sines of each position
-    (None: norm only); positions: int64 [T], a token outside [0, n_pos) is left as it is.  weights:
-    fp32 [D] or None (ones).  q, k and the outputs may have tokens apart (views of a projection's
-    rows); q_out / k_out may be q / k.  Returns (q_out, k_out)."""
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    dev = _device(q)
-    q_row = _need_rows(q, "q", T, D, q.dtype, dev)
-    k_row = _need_rows(k, "k", T, D, q.dtype, dev)
-    n_pos = rot = 0
-    if rope_table is not None:
-        n_pos, rot = rope_table.shape
-        _want(rope_table, "rope_table", (n_pos, rot), torch.float32, dev)
-        _want(positions, "positions", (T,), torch.int64, dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _want(w, name, (D,), torch.float32, dev)
-    qo_row, ko_row = Hq * D, Hk * D
-    if q_out is None:
-        q_out = q.new_empty((T, Hq, D))
-    else:
-        qo_row = _need_rows(q_out, "q_out", T, D, q.dtype, dev)
-    if k_out is None:
-        k_out = q.new_empty((T, Hk, D))
-    else:
-        ko_row = _need_rows(k_out, "k_out", T, D, q.dtype, dev)
-    if q_out.shape[1] != Hq or k_out.shape[1] != Hk:
-        raise ValueError("q_out / k_out must have the heads of q / k")
-    _raised(LIB.kda_qk_norm_rope(
-        _attn_config(Hq, Hk, D, q.dtype), T, q.data_ptr(), q_row, k.data_ptr(), k_row, _ptr(q_weight),
-        _ptr(k_weight), eps, _ptr(rope_table), n_pos, rot, layout,
-        _ptr(positions) if rope_table is not None else None, q_out.data_ptr(), qo_row,
-        k_out.data_ptr(), ko_row, _current_stream(dev.index)), "kda_qk_norm_rope")
-    return q_out, k_out
-
-
-def _sequences(cu_seqlens, kv_len, dev):
-    N = cu_seqlens.numel() - 1
-    _want(cu_seqlens, "cu_seqlens", (N + 1,), torch.int64, dev)
-    _want(kv_len, "kv_len", (N,), torch.int64, dev)
-    return N
-
-
-@_on_stream(0, "k")
-def kda_kv_write(k, v, cu_seqlens, kv_len, cache):
+def kda_kv_write(k, v, cu_seqlens, kv_len, cache, *, stream=None):
     """Stores the rows of k and v [T,Hk,D] (bf16 or fp32; tokens may be apart) in the 8-bit cache (a
     KVCache, updated in place) as the last cu_seqlens[n+1]-cu_seqlens[n] of the kv_len[n] tokens of
-    each sequence.  cu_seqlens int64 [N+1], kv_len int64 [N] device tensors.  Returns the cache."""
-    T, Hk, D = k.shape
-    dev = _device(k)
-    k_row = _need_rows(k, "k", T, D, k.dtype, dev)
-    v_row = _need_rows(v, "v", T, D, k.dtype, dev)
-    if v.shape[1] != Hk:
-        raise ValueError(f"v has {v.shape[1]} heads, expected {Hk}")
-    N = _sequences(cu_seqlens, kv_len, dev)
-    cc = cache.c(N, Hk, D, dev)
-    _raised(LIB.kda_kv_write(
-        _attn_config(Hk, Hk, D, k.dtype), ctypes.byref(cc), N, T, cu_seqlens.data_ptr(),
-        kv_len.data_ptr(), k.data_ptr(), k_row, v.data_ptr(), v_row, _current_stream(dev.index)),
-        "kda_kv_write")
+    each sequence.  cu_seqlens int64 [N+1], kv_len int64 [N] device tensors.  Returns the cache.
+    stream: as kda_qk_norm_rope."""
+    cfg, dev, N, sizes, k_row, v_row = _write_plan(_form(k), _form(v), _form(cu_seqlens),
+                                                   _form(kv_len), cache.form())
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_kv_write(k, v, cu_seqlens, kv_len, cache)
+    st = LIB.kda_kv_write(cfg, cache.c(sizes), N, k.shape[0], cu_seqlens.data_ptr(),
+                          kv_len.data_ptr(), k.data_ptr(), k_row, v.data_ptr(), v_row,
+                          _current_stream(dev))
+    if st:
+        _check(st, "kda_kv_write")
     return cache
 
 
-@_on_stream(2, "cache")
-def kda_kv_read(cu_seqlens, kv_len, cache, T, dtype=torch.bfloat16, *, k_out=None, v_out=None):
+@functools.lru_cache(maxsize=1024)
+def _read_plan(cu, kv_len, cache, T, dtype, k_out, v_out):
+    dev = _on_device(cache[0])
+    if len(cache[0][0]) != 4:
+        raise ValueError("cache.k is [n_pages, Hk, page, D]")
+    _, Hk, _, D = cache[0][0]
+    N = _sequences(cu, kv_len, dev)
+    for f, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if f is not None:
+            _dense(f, name, (T, Hk, D), dtype, dev)
+    return _attn_config(Hk, Hk, D, dtype), dev, N, _cache_sizes(cache, N, Hk, D, dev), (T, Hk, D)
+
+
+def kda_kv_read(cu_seqlens, kv_len, cache, T, dtype=torch.bfloat16, *, k_out=None, v_out=None,
+                stream=None):
     """The values that the cache holds for the last cu_seqlens[n+1]-cu_seqlens[n] of the kv_len[n]
     tokens of each sequence: (k, v) [T,Hk,D] in dtype, T = cu_seqlens[-1] (rows past it are left as
-    they are); tokens without a page are zeros."""
-    _, Hk, _, D = cache.k.shape
-    dev = _device(cache.k)
-    N = _sequences(cu_seqlens, kv_len, dev)
+    they are); tokens without a page are zeros.  stream: as kda_qk_norm_rope."""
+    cfg, dev, N, sizes, shape = _read_plan(_form(cu_seqlens), _form(kv_len), cache.form(), T, dtype,
+                                           _form(k_out), _form(v_out))
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_kv_read(cu_seqlens, kv_len, cache, T, dtype, k_out=k_out, v_out=v_out)
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
+        k_out = cache.k.new_empty(shape, dtype=dtype)
     if v_out is None:
-        v_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
-    _want(k_out, "k_out", (T, Hk, D), dtype, dev)
-    _want(v_out, "v_out", (T, Hk, D), dtype, dev)
-    cc = cache.c(N, Hk, D, dev)
-    _raised(LIB.kda_kv_read(
-        _attn_config(Hk, Hk, D, dtype), ctypes.byref(cc), N, T, cu_seqlens.data_ptr(),
-        kv_len.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _current_stream(dev.index)),
-        "kda_kv_read")
+        v_out = cache.k.new_empty(shape, dtype=dtype)
+    st = LIB.kda_kv_read(cfg, cache.c(sizes), N, T, cu_seqlens.data_ptr(), kv_len.data_ptr(),
+                         k_out.data_ptr(), v_out.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st, "kda_kv_read")
     return k_out, v_out
 
 
-@_on_stream(0, "q")
+@functools.lru_cache(maxsize=1024)
+def _attn_plan(q, cu, kv_len, cache, out, lse, workspace):
+    dev = _on_device(q)
+    if len(q[0]) != 3 or len(cache[0][0]) != 4:
+        raise ValueError("q is [T, Hq, D], cache.k is [n_pages, Hk, page, D]")
+    T, Hq, D = q[0]
+    Hk = cache[0][0][1]
+    q_row = _rows(q, "q", T, D, q[2], dev)
+    N = _sequences(cu, kv_len, dev)
+    sizes = _cache_sizes(cache, N, Hk, D, dev)
+    if out is not None:
+        _dense(out, "out", (T, Hq, D), q[2], dev)
+    if lse is not None:
+        _dense(lse, "lse_out", (T, Hq), torch.float32, dev)
+    if workspace is not None:
+        _dense(workspace, "workspace", workspace[0], torch.uint8, dev)
+    return _attn_config(Hq, Hk, D, q[2]), dev, N, sizes, q_row
+
+
 def kda_attn(q, cu_seqlens, kv_len, cache, *, scale=None, causal=True, window=0, want_lse=False,
-             out=None, lse_out=None, workspace=None):
+             out=None, lse_out=None, workspace=None, stream=None):
     """Softmax attention of the rows of q [T,Hq,D] (tokens may be apart) over the cached tokens of
     their sequences; the rows are the last cu_seqlens[n+1]-cu_seqlens[n] of the kv_len[n] tokens,
     which the cache already holds.  scale: None = 1/sqrt(D).  window: 0 = all keys.  workspace: a
     uint8 device tensor to use instead of one of the queried size.  Returns o [T,Hq,D], or (o, lse
-    [T,Hq] fp32) with want_lse."""
+    [T,Hq] fp32) with want_lse.  stream: as kda_qk_norm_rope."""
+    cfg, dev, N, sizes, q_row = _attn_plan(_form(q), _form(cu_seqlens), _form(kv_len), cache.form(),
+                                           _form(out), _form(lse_out), _form(workspace))
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_attn(q, cu_seqlens, kv_len, cache, scale=scale, causal=causal, window=window,
+                            want_lse=want_lse, out=out, lse_out=lse_out, workspace=workspace)
     T, Hq, D = q.shape
-    dev = _device(q)
-    q_row = _need_rows(q, "q", T, D, q.dtype, dev)
-    N = _sequences(cu_seqlens, kv_len, dev)
-    Hk = cache.k.shape[1]
-    cfg, cc = _attn_config(Hq, Hk, D, q.dtype), ctypes.byref(cache.c(N, Hk, D, dev))
+    c = cache.c(sizes)
     if out is None:
-        out = q.new_empty((T, Hq, D))
-    else:
-        _want(out, "out", (T, Hq, D), q.dtype, dev)
-    lse = lse_out
-    if lse is None and want_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    if lse is not None:
-        _want(lse, "lse_out", (T, Hq), torch.float32, dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse_out is None and want_lse:
+        lse_out = q.new_empty((T, Hq), dtype=torch.float32)
     if workspace is None:
-        wsb = LIB.kda_attn_workspace(cfg, cc, N, T)
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        wsb = LIB.kda_attn_workspace(cfg, c, N, T)
+        workspace = q.new_empty(wsb, dtype=torch.uint8) if wsb else None
     else:
-        _want(workspace, "workspace", workspace.shape, torch.uint8, dev)
         wsb = workspace.numel()
-    _raised(LIB.kda_attn(
-        cfg, cc, N, T, cu_seqlens.data_ptr(), kv_len.data_ptr(), q.data_ptr(), q_row,
-        D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), _ptr(lse),
-        _ptr(workspace), wsb, _current_stream(dev.index)), "kda_attn")
-    return (out, lse) if want_lse else out
+    st = LIB.kda_attn(cfg, c, N, T, cu_seqlens.data_ptr(), kv_len.data_ptr(), q.data_ptr(), q_row,
+                      D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
+                      _ptr(lse_out), _ptr(workspace), wsb, _current_stream(dev))
+    if st:
+        _check(st, "kda_attn")
+    return (out, lse_out) if want_lse else out

@@ -207,17 +207,38 @@ def test_binding_refuses_host_tensors_and_bad_layouts():
     x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):
         K.kda_qk_norm_rope(x, x)
+    f = K._form
     with pytest.raises(ValueError, match="contiguous"):
-        K._need_rows(x.transpose(0, 1).contiguous().transpose(0, 1), "q", 4, 64, x.dtype, x.device)
+        K._rows(f(x.transpose(0, 1).contiguous().transpose(0, 1)), "q", 4, 64, x.dtype, -1)
     with pytest.raises(ValueError, match="shape"):
-        K._need_rows(x, "q", 4, 128, x.dtype, x.device)
+        K._rows(f(x), "q", 4, 128, x.dtype, -1)
+    with pytest.raises(ValueError, match="shape"):
+        K._rows(f(x), "q", 4, 64, x.dtype, -1, 3)
+    with pytest.raises(TypeError, match="dtype"):
+        K._rows(f(x), "q", 4, 64, torch.float32, -1)
     wide = torch.zeros((4, 6, 64), dtype=torch.bfloat16)
-    assert K._need_rows(wide[:, 2:4], "k", 4, 64, x.dtype, x.device) == 384
-    assert K._need_rows(wide[:1, 2:4], "k", 1, 64, x.dtype, x.device) == 384
-    c = K.KVCache(torch.zeros(3, 2, 16, 64), torch.zeros(3, 2, 16, 64), torch.ones(3, 2), torch.ones(3, 2),
-                  torch.zeros((1, 4), dtype=torch.int32))
+    assert K._rows(f(wide[:, 2:4]), "k", 4, 64, x.dtype, -1) == 384
+    assert K._rows(f(wide[:1, 2:4]), "k", 1, 64, x.dtype, -1) == 384
+    K._dense(f(wide[:1, 2:4]), "w", (1, 2, 64), x.dtype, -1)
+    for bad in (wide[:, 2:4], wide.transpose(1, 2)):
+        with pytest.raises(ValueError, match="contiguous"):
+            K._dense(f(bad), "w", bad.shape, x.dtype, -1)
+    with pytest.raises(ValueError, match="required"):
+        K._dense(None, "w", (4,), x.dtype, -1)
+
+    def cache(k=torch.uint8, table=(1, 4), scale=(3, 2)):
+        return K.KVCache(torch.zeros((3, 2, 16, 64), dtype=k), torch.zeros((3, 2, 16, 64), dtype=torch.uint8),
+                         torch.ones(scale), torch.ones(3, 2), torch.zeros(table, dtype=torch.int32)).form()
+    assert K._cache_sizes(cache(), 1, 2, 64, -1) == (3, 16, 4)
     with pytest.raises(TypeError, match="uint8"):
-        c.c(1, 2, 64, x.device)
-    c.k = c.v = torch.zeros((3, 2, 16, 64), dtype=torch.uint8)
+        K._cache_sizes(cache(k=torch.float32), 1, 2, 64, -1)
     with pytest.raises(ValueError, match="cache.table"):
-        c.c(2, 2, 64, x.device)
+        K._cache_sizes(cache(), 2, 2, 64, -1)
+    with pytest.raises(ValueError, match="k_scale"):
+        K._cache_sizes(cache(scale=(3, 1)), 1, 2, 64, -1)
+    with pytest.raises(ValueError, match="cache.k"):
+        K._cache_sizes(cache(), 1, 4, 64, -1)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        K._sequences(f(torch.zeros((2, 2), dtype=torch.int64)), f(torch.zeros(1, dtype=torch.int64)), -1)
+    with pytest.raises(TypeError, match="kv_len"):
+        K._sequences(f(torch.zeros(2, dtype=torch.int64)), f(torch.zeros(1, dtype=torch.int32)), -1)

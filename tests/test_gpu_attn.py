@@ -540,9 +540,8 @@ def test_attn_layer_in_a_captured_graph(K):
     table = dev(rope_table(1024, D))
     x = torch.zeros((N, Hq + 2 * Hk, D), dtype=torch.bfloat16, device="cuda")
     cu, kv, pos = i64(cum([1] * N)), i64(start), i64(start)
-    cfg, cc = K._attn_config(Hq, Hk, D, torch.bfloat16), m.gpu.c(N, Hk, D, x.device)
-    import ctypes
-    ws = torch.empty(K.LIB.kda_attn_workspace(cfg, ctypes.byref(cc), N, N), dtype=torch.uint8, device="cuda")
+    cfg, cc = K._attn_config(Hq, Hk, D, torch.bfloat16), m.gpu.c((n_pages, page, 12))
+    ws = torch.empty(K.LIB.kda_attn_workspace(cfg, cc, N, N), dtype=torch.uint8, device="cuda")
     assert ws.numel() > 0
 
     def step(c):
