@@ -907,8 +907,10 @@ int check_row(const kda_attn_config *cfg, int64_t row, int heads, const char *na
 int check_rows(const kda_attn_config *cfg, int32_t N, int64_t T) {
     if (N < 0) return fail(KDA_ERR_ARG, "N must be non-negative (got %d)", N);
     if (T < 0) return fail(KDA_ERR_ARG, "T must be non-negative (got %lld)", (long long)T);
-    if (T > INT32_MAX / cfg->num_q_heads)
-        return fail(KDA_ERR_UNSUPPORTED, "T * num_q_heads must fit in 31 bits (got T = %lld)", (long long)T);
+    if (T > (1 << 30) / cfg->num_q_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "T * num_q_heads must fit in 30 bits (got T = %lld)", (long long)T);
+    if (N > (1 << 25) / cfg->num_q_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "N * num_q_heads must fit in 25 bits (got N = %d)", N);
     if (T > 0 && N == 0) return fail(KDA_ERR_ARG, "T > 0 needs at least one sequence");
     return KDA_OK;
 }
@@ -922,8 +924,8 @@ int check_cache(const kda_attn_config *cfg, const kda_kv_cache *c) {
         return fail(KDA_ERR_ARG, "cache->n_pages must be positive (got %lld)", (long long)c->n_pages);
     if (c->table_width <= 0)
         return fail(KDA_ERR_ARG, "cache->table_width must be positive (got %d)", c->table_width);
-    if (c->table_width > INT32_MAX / c->page)
-        return fail(KDA_ERR_UNSUPPORTED, "cache->table_width * cache->page must fit in 31 bits (got %d, %d)",
+    if (c->table_width > (1 << 30) / c->page)
+        return fail(KDA_ERR_UNSUPPORTED, "cache->table_width * cache->page must fit in 30 bits (got %d, %d)",
                     c->table_width, c->page);
     KDA_TRY(check_tensor(c->k, "cache->k", true));
     KDA_TRY(check_tensor(c->v, "cache->v", true));
@@ -944,8 +946,9 @@ kda::KvArgs kv_args(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N
 }
 
 kda::AttnArgs attn_args(const kda_attn_config *cfg, const kda_kv_cache *c, int32_t N, int64_t T,
-                        const int64_t *cu, const int64_t *kv_len) {
+                        const int64_t *cu, const int64_t *kv_len, int32_t window) {
     kda::AttnArgs a{};
+    a.window = window;
     a.kv = kv_args(cfg, c, N, T, cu, kv_len);
     a.Hq = cfg->num_q_heads;
     kda::attn_plan(device_cus(), cfg->io_dtype == KDA_DTYPE_BF16, cfg->head_dim, N, T, cfg->num_q_heads, cfg->num_kv_heads,
@@ -1034,10 +1037,10 @@ int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N
 }
 
 size_t kda_attn_workspace(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N,
-                          int64_t T) {
+                          int64_t T, int32_t window) {
     if (check_attn_config(cfg) != KDA_OK || check_rows(cfg, N, T) != KDA_OK) return 0;
     if (check_cache(cfg, cache) != KDA_OK || T == 0) return 0;
-    return round256(kda::attn_partial_bytes(cfg->head_dim, attn_args(cfg, cache, N, T, nullptr, nullptr)));
+    return round256(kda::attn_partial_bytes(cfg->head_dim, attn_args(cfg, cache, N, T, nullptr, nullptr, window)));
 }
 
 int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
@@ -1047,7 +1050,7 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
     KDA_TRY(check_attn_config(cfg));
     KDA_TRY(check_rows(cfg, N, T));
     KDA_TRY(check_cache(cfg, cache));
-    if (!std::isfinite(scale)) return fail(KDA_ERR_ARG, "scale must be finite");
+    if (!std::isfinite(scale * 1.4426950408889634f)) return fail(KDA_ERR_ARG, "scale must be finite");
     if (causal != 0 && causal != 1) return fail(KDA_ERR_ARG, "causal must be 0 or 1 (got %d)", causal);
     if (window < 0) return fail(KDA_ERR_ARG, "window must be >= 0 (got %d)", window);
     KDA_TRY(check_row(cfg, q_row, cfg->num_q_heads, "q_row"));
@@ -1058,7 +1061,7 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
     KDA_TRY(check_tensor(o, "o", true));
     KDA_TRY(check_tensor(lse, "lse", false, 4));
     if (o == q) return fail(KDA_ERR_ARG, "o must not alias q");
-    kda::AttnArgs a = attn_args(cfg, cache, N, T, cu_seqlens, kv_len);
+    kda::AttnArgs a = attn_args(cfg, cache, N, T, cu_seqlens, kv_len, window);
     const size_t need = round256(kda::attn_partial_bytes(cfg->head_dim, a));
     if (need && (!ws || ws_bytes < need))
         return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
@@ -1067,7 +1070,7 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
     // (a scale of zero as the smallest that keeps -inf x scale = -inf: masked scores)
     a.scale = scale * 1.4426950408889634f;
     if (std::fabs(a.scale) < FLT_MIN) a.scale = FLT_MIN;
-    a.causal = causal; a.window = window;
+    a.causal = causal;
     const bool bf = cfg->io_dtype == KDA_DTYPE_BF16;
     hipError_t e = hipSuccess;
     if (a.workers >= 0) e = kda::launch_attn(bf, cfg->head_dim, a, (hipStream_t)stream);

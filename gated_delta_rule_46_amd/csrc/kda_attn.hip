@@ -34,8 +34,18 @@ namespace {
 
 using namespace attn;
 
-constexpr int kShortRows = 64;        // most query rows of a sequence that this kernel takes
-constexpr int kSmallCall = 1024;      // query rows of a call that it takes alone
+// Which kernel: units of 16 rows read their keys once each, units of 128 rows (kda_attn_rows.hip) an
+// eighth as often, but they start later.  us per call at 32 / 8 heads of 128, this kernel / the other,
+// sequences x keys x rows per kv head: 8 x 12,000 x 16 54 / 75, x 32 86 / 79, x 64 153 / 91;
+// 1 x 12,000 x 16 19 / 25, x 32 26 / 26, x 64 34 / 29; 8 x 2,000 x 32 20 / 27, x 64 34 / 30;
+// 1 x 2,000 x 128 18 / 21.
+constexpr int kShortRows = 16;        // most query rows of a sequence that come here ...
+constexpr int kSmallCall = 1 << 18;   // ... unless all units x keys are no more than this
+// One workgroup per unit, without parts and their launch, up to this many keys, twice as
+// many from 64 units on.  us per call, unit by unit / in shares, head_dim 128: 1 sequence
+// of 1,000 keys at 1 kv head 10.7 / 11.8, 64 at 8 heads 36 / 46; of 2,000 keys 18.7 / 12.1
+// and 64 / 69; of 4,000 28 / 12 and 119 / 115.
+constexpr int kDirect = 1024;
 constexpr int kMinShare = 8;          // fewest steps worth a workgroup of their own (two per wave)
 
 // A step's codes in a wave's registers, as the products read them.
@@ -600,18 +610,28 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     a->workers = -1;
     a->row_units = 0;
     a->row_splits = 1;
-    // A single sequence and small calls are of one kind; in others the lengths,
-    // which only the device knows, decide sequence by sequence.
-    const bool all_short = rows <= kShortRows || (N > 1 && rows <= kSmallCall);
+    // keys that a unit can see: the table's, or its window's
+    const int64_t keys = a->window > 0 ? std::min<int64_t>(max_kv, (int64_t)a->window + kRows + 2 * kStep) : max_kv;
+    // The lengths are known on the device only.  A call goes to this kernel alone where it is small, or
+    // where equal lengths would be short (a decode step, equally many drafted tokens); a single long
+    // sequence to the other; else each sequence goes to its own.
+    const bool all_short = rows <= kShortRows || (T % N == 0 && rows / N <= kShortRows) ||
+                           std::max<int64_t>(rows / kRows, N) * Hk * keys <= kSmallCall;
     const bool all_long = N == 1 && !all_short;
     a->short_rows = all_short ? INT32_MAX : kShortRows;
-    if (!all_long) a->workers = max_kv <= 16 * kStep ? 0 : cus * resident(bf16, D);
+    if (!all_long) {
+        const int64_t units = (rows / kRows + N) * Hk;
+        const bool direct = keys <= kDirect || (keys <= 2 * kDirect && units >= 64);
+        a->workers = direct ? 0 : cus * resident(bf16, D);
+    }
     if (!all_short) {
         a->row_units = (int32_t)(rows / kRowTile + N);
         const int64_t units = (int64_t)a->row_units * Hk;
         if (units < 2 * cus) {
+            // parts of at least kMinSplit tiles: 1 sequence of 2,000 keys and 32 rows 51 us with two
+            // parts of 16 tiles, 18 with eight of 4
             const int64_t want = (4 * (int64_t)cus + units - 1) / units;
-            a->row_splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, 16, max_kv / 1024}));
+            a->row_splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, 32, max_kv / (kMinSplit * kTile)}));
         }
     }
 }

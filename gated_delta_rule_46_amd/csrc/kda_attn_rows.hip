@@ -32,7 +32,6 @@ using namespace attn;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kWaveRows = 32;
-constexpr int kMinSplit = 8;          // fewest tiles worth a workgroup of their own
 constexpr float kLag = 8.f;           // growth of a maximum (log2) that rescales
 
 // The unit of a workgroup: rows [row0, row0 + 128) of sequence n, and the tiles
@@ -409,6 +408,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_rows_kernel(const AttnArgs 
     const int R = u.row0 + r;
     if (R >= u.s.len * G) return;
     float M = -__builtin_inff(), L = 0.f, z[8] = {};
+#pragma unroll 4
     for (int i = 0; i < u.splits; ++i) {
         const float *src = a.part + ((y * a.row_splits + i) * a.kv.Hk + hk) * (kRowTile * (D + 2));
         const float m = src[kRowTile * D + r], l = src[kRowTile * (D + 1) + r];

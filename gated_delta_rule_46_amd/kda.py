@@ -115,7 +115,7 @@ def _load():
                                             P, P, I64, P, I64, P]),
         "kda_kv_write": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, I64, P, I64, P]),
         "kda_kv_read": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, P, P]),
-        "kda_attn_workspace": (S, [acfgp, cachep, I32, I64]),
+        "kda_attn_workspace": (S, [acfgp, cachep, I32, I64, I32]),
         "kda_attn": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, I64, F32, I32, I32, P, P, P, S,
                                     P]),
         "kda_validate_inputs": (ctypes.c_int, [cfgp, I64, P, I32, I32, P, P, P, P]),
@@ -969,7 +969,7 @@ def kda_attn(q, cu_seqlens, kv_len, cache, *, scale=None, causal=True, window=0,
     if lse_out is None and want_lse:
         lse_out = q.new_empty((T, Hq), dtype=torch.float32)
     if workspace is None:
-        wsb = LIB.kda_attn_workspace(cfg, c, N, T)
+        wsb = LIB.kda_attn_workspace(cfg, c, N, T, window)
         workspace = q.new_empty(wsb, dtype=torch.uint8) if wsb else None
     else:
         wsb = workspace.numel()

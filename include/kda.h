@@ -499,7 +499,7 @@ int kda_conv_halo(int32_t io_dtype, int32_t channels, int32_t width, const void 
  * *_row is the distance between tokens in elements (at least the row itself, a
  * multiple of 16 bytes), so q, k and v may be views of one projection's rows.
  * head_dim in {64, 128}; num_q_heads a multiple of num_kv_heads.
- * T * num_q_heads and table_width * page must fit in 31 bits.
+ * T * num_q_heads and table_width * page must fit in 30 bits, N * num_q_heads in 25.
  */
 typedef struct {
     int32_t num_q_heads, num_kv_heads, head_dim;
@@ -539,7 +539,7 @@ int kda_qk_norm_rope(const kda_attn_config *cfg, int64_t T, const void *q, int64
  * entry outside [0, n_pages), and a position past the table, is an absent page:
  * not written, read as zeros, masked in attention.
  * Pages may be shared between sequences to be read (a common prefix); a page
- * that a call writes must belong to one sequence of the call.
+ * that a call writes must stand in one place of the call's table only.
  */
 typedef struct {
     void *k, *v;                /* [n_pages, num_kv_heads, page, head_dim] codes, 16-byte aligned */
@@ -583,8 +583,10 @@ int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N
  *     o = sum_j softmax_j(scale q.k_j) v_j,    lse = log sum_j exp(scale q.k_j)
  *   o [T, num_q_heads, head_dim] (io_dtype, contiguous);
  *   lse [T, num_q_heads] fp32, NULL = not written.
- * A row that sees no key gets o = 0 and lse = -inf.  Keys and values that a row
- * does not see never reach it, infinities and NaN included.
+ * A row that sees no key gets o = 0 and lse = -inf (one whose scores are all
+ * -inf, from infinities in q, too).  Keys and values that a row does not see
+ * never reach it, NaN included.  The sums are normalised at the end: the
+ * number of keys times the largest |v| must stay below 2^119.
  * Scores, maxima, sums and outputs are accumulated in fp32; with bf16 rows the
  * probabilities are rounded to bf16 for the product with V, with fp32 rows
  * every operand keeps its 24 bits.
@@ -593,7 +595,7 @@ int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N
  * nothing is kept in it between calls.
  */
 size_t kda_attn_workspace(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N,
-                          int64_t T);
+                          int64_t T, int32_t window);
 int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, int64_t T,
              const int64_t *cu_seqlens, const int64_t *kv_len, const void *q, int64_t q_row,
              float scale, int32_t causal, int32_t window, void *o, float *lse, void *ws,

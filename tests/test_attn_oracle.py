@@ -140,7 +140,7 @@ def test_attn_config_refusals(call):
     assert call(c=cfg(dtype=2)) == K.KDA_ERR_ARG
     assert call(c=cfg(D=96)) == K.KDA_ERR_UNSUPPORTED
     assert call(T=-1) == K.KDA_ERR_ARG
-    assert call(T=1 << 29) == K.KDA_ERR_UNSUPPORTED and "31 bits" in err()
+    assert call(T=1 << 28) == K.KDA_ERR_UNSUPPORTED and "30 bits" in err()
     assert call(T=0) == K.KDA_OK and err() == ""
 
 
@@ -149,6 +149,7 @@ def test_cache_refusals(call):
     assert call(kc=None) == K.KDA_ERR_ARG and "cache" in err()
     assert call(N=-1) == K.KDA_ERR_ARG
     assert call(N=0) == K.KDA_ERR_ARG
+    assert call(N=1 << 23) == K.KDA_ERR_UNSUPPORTED and "25 bits" in err()
     assert call(N=0, T=0) == K.KDA_OK
     for page in (0, 8, 48, 256):
         assert call(kc=cache(page=page)) == K.KDA_ERR_UNSUPPORTED
@@ -184,18 +185,22 @@ def test_write_read_refusals():
 
 
 def test_attn_refusals():
-    assert attn(scale=float("inf")) == K.KDA_ERR_ARG
+    assert attn(scale=float("inf")) == K.KDA_ERR_ARG and attn(scale=-3e38) == K.KDA_ERR_ARG
     assert attn(causal=2) == K.KDA_ERR_ARG and attn(window=-1) == K.KDA_ERR_ARG
     assert attn(q=None) == K.KDA_ERR_ARG and attn(o=MISALIGNED) == K.KDA_ERR_ALIGN
     assert attn(o=FAKE) == K.KDA_ERR_ARG and "alias" in err()
     assert attn(lse=MISALIGNED) == K.KDA_ERR_ALIGN
     assert attn(cu=FAKE + 4) == K.KDA_ERR_ALIGN
-    need = K.LIB.kda_attn_workspace(ref(cfg()), ref(cache()), 2, 8)
+    need = K.LIB.kda_attn_workspace(ref(cfg()), ref(cache(width=64)), 2, 8, 0)
     assert need > 0 and need % 256 == 0
-    assert attn(ws=None) == K.KDA_ERR_WORKSPACE and attn(wsb=need - 1) == K.KDA_ERR_WORKSPACE
-    assert attn(ws=FAKE + 8) == K.KDA_ERR_ALIGN
-    assert K.LIB.kda_attn_workspace(ref(cfg()), ref(cache()), 2, 0) == 0
-    assert K.LIB.kda_attn_workspace(None, ref(cache()), 2, 8) == 0
+    big = cache(width=64)
+    assert attn(kc=big, ws=None) == K.KDA_ERR_WORKSPACE and attn(kc=big, wsb=need - 1) == K.KDA_ERR_WORKSPACE
+    assert attn(kc=big, ws=FAKE + 8) == K.KDA_ERR_ALIGN
+    assert K.LIB.kda_attn_workspace(ref(cfg()), ref(cache(width=64)), 2, 0, 0) == 0
+    assert K.LIB.kda_attn_workspace(None, ref(cache(width=64)), 2, 8, 0) == 0
+    # a unit per workgroup: no parts
+    assert K.LIB.kda_attn_workspace(ref(cfg()), ref(cache(width=8)), 2, 8, 0) == 0
+    assert K.LIB.kda_attn_workspace(ref(cfg()), ref(cache(width=64)), 2, 8, 100) == 0
 
 
 def test_attn_struct_layouts():

@@ -318,20 +318,22 @@ def test_attn_decode(K, dtype, D, page, Hk, G, wide):
     """One new token per sequence: lengths 0, 1, around tiles and pages, long ones; a capacity that
     makes the call split its units and one that does not."""
     say(f"attn decode {dtype} D={D} page={page} Hk={Hk} G={G} wide={wide}")
-    kv = [1, 63, 64, 65, 0, 17, 200, 300] + ([1500, 777] if wide else [])
+    kv = [1, 63, 64, 65, 0, 17, 200, 300] + ([2500, 777] if wide else [])
     m, rng = plain_model(K, dtype, Hk, D, page, kv, 11 + D + G, width=None if wide else 512 // page)
     attn_check(K, m, dtype, queries(rng, len(kv), Hk * G, D, dtype), cum([1] * len(kv)), kv, 0.3 * D ** -0.5)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("D,page,Hk,G", [(128, 64, 2, 4), (64, 16, 2, 1), (128, 128, 1, 3), (64, 32, 1, 8)])
-@pytest.mark.parametrize("causal,window", [(True, 0), (True, 50), (False, 0), (False, 33), (True, 1)])
-def test_attn_rows(K, dtype, D, page, Hk, G, causal, window):
-    """Packed sequences of many lengths, an empty one, one whose new tokens are all it has."""
-    say(f"attn rows {dtype} D={D} page={page} Hk={Hk} G={G} causal={causal} window={window}")
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 50), (False, 0), (False, 33), (True, 1), (True, 2000)])
+@pytest.mark.parametrize("room", [0, 20000])
+def test_attn_rows(K, dtype, D, page, Hk, G, causal, window, room):
+    """Packed sequences of many lengths, an empty one, one whose new tokens are all it has; a table for
+    just these lengths (a workgroup per unit) and a wide one (shares that cut units)."""
+    say(f"attn rows {dtype} D={D} page={page} Hk={Hk} G={G} causal={causal} window={window} room={room}")
     new = [1, 33, 0, 150, 2, 64]
     kv = [40, 33, 20, 411, 130, 700]
-    m, rng = plain_model(K, dtype, Hk, D, page, kv, 5 + D + G + window)
+    m, rng = plain_model(K, dtype, Hk, D, page, kv, 5 + D + G + window, width=room // page or None)
     attn_check(K, m, dtype, queries(rng, sum(new), Hk * G, D, dtype), cum(new), kv, D ** -0.5, causal, window)
 
 
@@ -343,16 +345,18 @@ def test_attn_prompts(K, dtype, D, page, Hk, G, causal, window):
     say(f"attn prompts {dtype} D={D} page={page} Hk={Hk} G={G} causal={causal} window={window}")
     new = [1, 300, 0, 65, 620, 3]
     kv = [40, 300, 20, 411, 1500, 130]
-    m, rng = plain_model(K, dtype, Hk, D, page, kv, 6 + D + G + window)
+    m, rng = plain_model(K, dtype, Hk, D, page, kv, 6 + D + G + window, width=6400 // page)
     attn_check(K, m, dtype, queries(rng, sum(new), Hk * G, D, dtype), cum(new), kv, D ** -0.5, causal, window)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("new,kv,window", [(33, 33, 0), (129, 4200, 0), (257, 70, 0), (64, 2100, 200)])
-def test_attn_one_sequence(K, dtype, new, kv, window):
-    """A sequence alone: a prompt, a chunk that is split over the keys, more rows than keys, a window."""
-    say(f"attn one sequence {dtype} new={new} kv={kv} window={window}")
-    m, rng = plain_model(K, dtype, 2, 128, 64, [kv], new)
+@pytest.mark.parametrize("new,kv,window", [(33, 33, 0), (129, 4200, 0), (257, 70, 0), (64, 2100, 200), (5, 1000, 0)])
+@pytest.mark.parametrize("room", [0, 50000])
+def test_attn_one_sequence(K, dtype, new, kv, window, room):
+    """A sequence alone: a prompt, a chunk that is split over the keys, more rows than keys, a window; a
+    table for just this length (small calls: units of 16 rows) and a wide one (units of 128)."""
+    say(f"attn one sequence {dtype} new={new} kv={kv} window={window} room={room}")
+    m, rng = plain_model(K, dtype, 2, 128, 64, [kv], new, width=room // 64 or None)
     attn_check(K, m, dtype, queries(rng, new, 8, 128, dtype), [0, new], [kv], 0.1, True, window)
 
 
@@ -362,7 +366,7 @@ def test_attn_prompt_queries_of_all_sizes(K, dtype):
     import torch
     say(f"attn query sizes {dtype}")
     new, kv, D = 200, 330, 128
-    m, rng = plain_model(K, dtype, 1, D, 64, [kv], 51)
+    m, rng = plain_model(K, dtype, 1, D, 64, [kv], 51, width=400)
     q = queries(rng, new, 2, D, dtype).clone()
     attn_check(K, m, dtype, q, [0, new], [kv], 0.0, name="scale 0")
     attn_check(K, m, dtype, q, [0, new], [kv], -0.1, name="negative scale")
@@ -457,7 +461,7 @@ def test_attn_prompt_hidden_nan(K, dtype, page):
     import torch
     say(f"attn prompt NaN {dtype} page={page}")
     new, kv, D = 150, 300, 128
-    m, rng = plain_model(K, dtype, 1, D, page, [kv], 61)
+    m, rng = plain_model(K, dtype, 1, D, page, [kv], 61, width=25600 // page)
     for half, pos, d, code in (("v", 205, 5, 0x7F), ("v", 206, 127, 0xFF), ("k", 280, 3, 0x7F), ("v", 299, 64, 0x7F)):
         c = m.keys if half == "k" else m.values
         pid = c.pid(0, pos)
@@ -479,7 +483,7 @@ def test_attn_long_rows(K, dtype):
     import torch
     say(f"attn long rows {dtype}")
     new, kv = [301], [1201]
-    m, rng = plain_model(K, dtype, 1, 128, 64, kv, 44)
+    m, rng = plain_model(K, dtype, 1, 128, 64, kv, 44, width=400)
     q = queries(rng, 301, 4, 128, dtype)
     o, lse = attn_check(K, m, dtype, q, cum(new), kv, 128 ** -0.5)
     o2, lse2 = K.kda_attn(q, i64(cum(new)), i64(kv), m.gpu, want_lse=True)
@@ -493,7 +497,7 @@ def test_attn_many_sequences(K, n):
     rng = np.random.default_rng(n)
     kv = [int(x) for x in rng.integers(0, 90, n)]
     kv[5] = 640
-    m, rng = plain_model(K, "bf16", 1, 64, 16, kv, n)
+    m, rng = plain_model(K, "bf16", 1, 64, 16, kv, n, width=200)
     attn_check(K, m, "bf16", queries(rng, n, 2, 64, "bf16"), cum([1] * n), kv, 0.1)
 
 
@@ -530,7 +534,7 @@ def test_attn_layer_in_a_captured_graph(K):
     say("attention layer in a graph")
     Hq, Hk, D, page, N = 8, 2, 128, 64, 3
     rng = np.random.default_rng(5)
-    tab, n_pages = tables(N, 12, rng)
+    tab, n_pages = tables(N, 40, rng)
     m = Model(K, "bf16", Hk, D, page, n_pages, tab)
     eager = K.KVCache(m.gpu.k.clone(), m.gpu.v.clone(), m.gpu.k_scale.clone(), m.gpu.v_scale.clone(), m.gpu.table)
     start = [600, 64, 5]
@@ -540,8 +544,8 @@ def test_attn_layer_in_a_captured_graph(K):
     table = dev(rope_table(1024, D))
     x = torch.zeros((N, Hq + 2 * Hk, D), dtype=torch.bfloat16, device="cuda")
     cu, kv, pos = i64(cum([1] * N)), i64(start), i64(start)
-    cfg, cc = K._attn_config(Hq, Hk, D, torch.bfloat16), m.gpu.c((n_pages, page, 12))
-    ws = torch.empty(K.LIB.kda_attn_workspace(cfg, cc, N, N), dtype=torch.uint8, device="cuda")
+    cfg, cc = K._attn_config(Hq, Hk, D, torch.bfloat16), m.gpu.c((n_pages, page, 40))
+    ws = torch.empty(K.LIB.kda_attn_workspace(cfg, cc, N, N, 0), dtype=torch.uint8, device="cuda")
     assert ws.numel() > 0
 
     def step(c):
