@@ -907,10 +907,13 @@ int check_row(const kda_attn_config *cfg, int64_t row, int heads, const char *na
 int check_rows(const kda_attn_config *cfg, int32_t N, int64_t T) {
     if (N < 0) return fail(KDA_ERR_ARG, "N must be non-negative (got %d)", N);
     if (T < 0) return fail(KDA_ERR_ARG, "T must be non-negative (got %lld)", (long long)T);
-    if (T > (1 << 30) / cfg->num_q_heads)
-        return fail(KDA_ERR_UNSUPPORTED, "T * num_q_heads must fit in 30 bits (got T = %lld)", (long long)T);
-    if (N > (1 << 25) / cfg->num_q_heads)
-        return fail(KDA_ERR_UNSUPPORTED, "N * num_q_heads must fit in 25 bits (got N = %d)", N);
+    // no launch may reach 2^32 threads: 256 for each token, for 1 / 8 of its (token, head) pairs
+    // and for 4 (sequence, head) pairs at most
+    if (T >= 1 << 24) return fail(KDA_ERR_UNSUPPORTED, "T must be below 2^24 (got %lld)", (long long)T);
+    if (T > (1 << 26) / cfg->num_q_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "T * num_q_heads must be at most 2^26 (got T = %lld)", (long long)T);
+    if (N > (1 << 20) / cfg->num_q_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "N * num_q_heads must be at most 2^20 (got N = %d)", N);
     if (T > 0 && N == 0) return fail(KDA_ERR_ARG, "T > 0 needs at least one sequence");
     return KDA_OK;
 }

@@ -12,7 +12,7 @@
 // Products on the matrix cores.  A code times its page's power-of-two scale is
 // exact in bf16, so K and V enter as the values they stand for; bf16 queries
 // are exact as well, and the only rounding of operands is that of the
-// probabilities to bf16 (half an ulp, 2^-9 relative, independent per key).
+// probabilities to bf16 (at most 2^-8 of each, to either side).
 // With fp32 rows, queries and probabilities enter as three bf16 terms each
 // (8 + 8 + 8 bits hold the 24 of fp32), three products instead of one.
 //
@@ -618,7 +618,8 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     const bool all_short = rows <= kShortRows || (T % N == 0 && rows / N <= kShortRows) ||
                            std::max<int64_t>(rows / kRows, N) * Hk * keys <= kSmallCall;
     const bool all_long = N == 1 && !all_short;
-    a->short_rows = all_short ? INT32_MAX : kShortRows;
+    // (alone, it also takes a sequence that padding made look long)
+    a->short_rows = all_short ? INT32_MAX : all_long ? 0 : kShortRows;
     if (!all_long) {
         const int64_t units = (rows / kRows + N) * Hk;
         const bool direct = keys <= kDirect || (keys <= 2 * kDirect && units >= 64);

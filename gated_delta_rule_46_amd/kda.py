@@ -864,7 +864,11 @@ def _ptr(t):
 def _placed(dev, stream):
     """The device of a call's tensors, or the stream given for it, as the current one: what the call
     allocates is then ordered with the stream that uses it."""
-    return torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream is of device {stream.device.index}, the tensors of {dev}")
+    return torch.cuda.stream(stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -963,6 +967,8 @@ def kda_attn(q, cu_seqlens, kv_len, cache, *, scale=None, causal=True, window=0,
             return kda_attn(q, cu_seqlens, kv_len, cache, scale=scale, causal=causal, window=window,
                             want_lse=want_lse, out=out, lse_out=lse_out, workspace=workspace)
     T, Hq, D = q.shape
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window must be in [0, 2^31) (got {window})")
     c = cache.c(sizes)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)

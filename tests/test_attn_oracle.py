@@ -140,7 +140,8 @@ def test_attn_config_refusals(call):
     assert call(c=cfg(dtype=2)) == K.KDA_ERR_ARG
     assert call(c=cfg(D=96)) == K.KDA_ERR_UNSUPPORTED
     assert call(T=-1) == K.KDA_ERR_ARG
-    assert call(T=1 << 28) == K.KDA_ERR_UNSUPPORTED and "30 bits" in err()
+    assert call(T=1 << 28) == K.KDA_ERR_UNSUPPORTED and "2^24" in err()
+    assert call(T=(1 << 24) - 1) == K.KDA_ERR_UNSUPPORTED and "2^26" in err()
     assert call(T=0) == K.KDA_OK and err() == ""
 
 
@@ -149,7 +150,7 @@ def test_cache_refusals(call):
     assert call(kc=None) == K.KDA_ERR_ARG and "cache" in err()
     assert call(N=-1) == K.KDA_ERR_ARG
     assert call(N=0) == K.KDA_ERR_ARG
-    assert call(N=1 << 23) == K.KDA_ERR_UNSUPPORTED and "25 bits" in err()
+    assert call(N=1 << 23) == K.KDA_ERR_UNSUPPORTED and "2^20" in err()
     assert call(N=0, T=0) == K.KDA_OK
     for page in (0, 8, 48, 256):
         assert call(kc=cache(page=page)) == K.KDA_ERR_UNSUPPORTED

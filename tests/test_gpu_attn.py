@@ -134,6 +134,17 @@ def test_rotate_non_finite_stays_in_its_head(K):
     assert (ko[2, 1] == 0).all() and torch.isfinite(ko).all()
 
 
+def test_rotate_infinity_stays_in_its_dim_where_nothing_rotates(K):
+    import torch
+    say("rotate with an infinity among the dims behind rot, pairs")
+    q, k = torch.randn(2, 2, 64, device="cuda"), torch.randn(2, 1, 64, device="cuda")
+    q[0, 1, 40] = float("inf")
+    qo, _ = K.kda_qk_norm_rope(q, k, i64([3, 5]), dev(rope_table(8, 32)), layout=K.KDA_ROPE_PAIRS)
+    torch.cuda.synchronize()
+    rest = [i for i in range(64) if i != 40]           # x / inf = 0
+    assert torch.isnan(qo[0, 1, 40]) and (qo[0, 1, rest] == 0).all() and torch.isfinite(qo[1]).all()
+
+
 # ---------------------------------------------------------------------------
 # the cache
 # ---------------------------------------------------------------------------
@@ -358,6 +369,42 @@ def test_attn_one_sequence(K, dtype, new, kv, window, room):
     say(f"attn one sequence {dtype} new={new} kv={kv} window={window} room={room}")
     m, rng = plain_model(K, dtype, 2, 128, 64, [kv], new, width=room // 64 or None)
     attn_check(K, m, dtype, queries(rng, new, 8, 128, dtype), [0, new], [kv], 0.1, True, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,new,kv", [(400, 1, 30), (400, 4, 2000), (400, 0, 50), (130, 129, 500)])
+def test_attn_one_padded_sequence(K, dtype, T, new, kv):
+    """A sequence alone in a call padded to more rows: its rows right, the others left as they are."""
+    import torch
+    say(f"attn one padded sequence {dtype} T={T} new={new} kv={kv}")
+    m, rng = plain_model(K, dtype, 2, 128, 64, [kv], 9 + new, width=800)
+    q = queries(rng, T, 8, 128, dtype)
+    out, lse = torch.full((T, 8, 128), 5.0, dtype=dt(dtype), device="cuda"), torch.full((T, 8), 5.0, device="cuda")
+    attn_check(K, m, dtype, q, [0, new], [kv], 0.1, out=out, lse_out=lse)
+    assert (out[new:] == 5.0).all() and (lse[new:] == 5.0).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_shared_pages(K, wide):
+    """A common prefix: pages that stand in several sequences' tables, and twice in one."""
+    say(f"attn shared pages wide={wide}")
+    new, kv = [1, 40, 2], [300, 300, 200]
+    m, rng = plain_model(K, "bf16", 2, 64, 32, kv, 4, width=200 if wide else 10)
+    m.table[1, :6] = m.table[0, :6]
+    m.table[2, 3] = m.table[2, 2]
+    m.gpu.table = dev(m.table)
+    m.keys.table = m.values.table = m.table
+    attn_check(K, m, "bf16", queries(rng, sum(new), 4, 64, "bf16"), cum(new), kv, 0.1)
+
+
+def test_attn_window_argument(K):
+    say("attn window beyond 31 bits")
+    m, rng = plain_model(K, "bf16", 1, 64, 16, [20], 1)
+    q = queries(rng, 1, 1, 64, "bf16")
+    for bad in (1 << 31, (1 << 32) + 5, -1):
+        with pytest.raises(ValueError, match="window"):
+            K.kda_attn(q, i64([0, 1]), i64([20]), m.gpu, window=bad)
+    attn_check(K, m, "bf16", q, [0, 1], [20], 0.1, window=(1 << 31) - 1)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
