@@ -370,8 +370,15 @@ __device__ __forceinline__ Place place(const AttnArgs &a, int G, int of, int blo
 }
 
 // The sequence and unit of number x in the order of the packed rows: sequence n's
-// units start at first(n) = cu[n] G / kRows + n (at least as many apart as it has).
+// units start at first(n) = cu[n] G / kRows + n (at least as many apart as it has),
+// at n where no sequence here has more than one (host_units() of them in all).
 __device__ __forceinline__ bool packed_unit(const AttnArgs &a, int64_t x, int G, int &n, Seq &s, int &rb) {
+    if (a.short_rows <= kRows) {
+        n = (int)x;
+        rb = 0;
+        s = sequence(a, n, G);
+        return s.rt > 0;
+    }
     n = last_not_above(a.kv.N, x, [&](int i) { return a.kv.cu[i] * G / kRows + i; });
     s = sequence(a, n, G);
     const int64_t r = x - (s.c0 * G / kRows + n);
@@ -577,11 +584,14 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
     if (a.lse && d == 0) a.lse[row] = lse_of(M, L);
 }
 
+// Units over all sequences at most, per kv head.
+int64_t host_units(int64_t T, int G, int N, int short_rows) {
+    return short_rows <= kRows ? N : T * G / kRows + N;
+}
+
 template <int D, bool BF>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
-    const int G = a.Hq / a.kv.Hk;
-    // units over all sequences: at most first(N) of them per kv head
-    const int64_t units = (a.kv.T * G / kRows + a.kv.N) * a.kv.Hk;
+    const int64_t units = host_units(a.kv.T, a.Hq / a.kv.Hk, a.kv.N, a.short_rows) * a.kv.Hk;
     if (units > INT32_MAX / kRows) return hipErrorInvalidValue;
     const dim3 block(kAttnThreads);
     hipLaunchKernelGGL((attn_kernel<D, BF>), dim3((unsigned)(a.workers ? a.workers : units)), block, 0, s, a);
@@ -621,7 +631,7 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     // (alone, it also takes a sequence that padding made look long)
     a->short_rows = all_short ? INT32_MAX : all_long ? 0 : kShortRows;
     if (!all_long) {
-        const int64_t units = (rows / kRows + N) * Hk;
+        const int64_t units = host_units(T, G, N, a->short_rows) * Hk;
         const bool direct = keys <= kDirect || (keys <= 2 * kDirect && units >= 64);
         a->workers = direct ? 0 : cus * resident(bf16, D);
     }
