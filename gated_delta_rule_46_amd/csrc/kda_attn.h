@@ -57,6 +57,7 @@ struct AttnArgs {
     // sequences of at most short_rows query rows per kv head go to kda_attn.hip,
     // the others to kda_attn_rows.hip
     int32_t short_rows;
+    int32_t unit_rows;           // kda_attn.hip: rows per unit, 16 or 32
     int32_t workers;             // kda_attn.hip: workgroups that share the tiles; 0: one per
                                  // unit; -1: not launched
     int32_t row_units;           // kda_attn_rows.hip: units per kv head, 0: not launched

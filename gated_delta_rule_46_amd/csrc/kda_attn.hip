@@ -34,13 +34,18 @@ namespace {
 
 using namespace attn;
 
-// Which kernel: units of 16 rows read their keys once each, units of 128 rows (kda_attn_rows.hip) an
-// eighth as often, but they start later.  us per call at 32 / 8 heads of 128, this kernel / the other,
-// sequences x keys x rows per kv head: 8 x 12,000 x 16 54 / 75, x 32 86 / 79, x 64 153 / 91;
-// 1 x 12,000 x 16 19 / 25, x 32 26 / 26, x 64 34 / 29; 8 x 2,000 x 32 20 / 27, x 64 34 / 30;
-// 1 x 2,000 x 128 18 / 21.
-constexpr int kShortRows = 16;        // most query rows of a sequence that come here ...
-constexpr int kSmallCall = 1 << 18;   // ... unless all units x keys are no more than this
+// Which kernel: units of 16 or 32 rows read their keys once each, units of 128 rows (kda_attn_rows.hip)
+// less often, but they start later and wait for their tiles.  us per call at 32 / 8 heads of 128, here /
+// there, sequences x keys x rows per kv head: bf16 64 x 8,000 x 20 184 / 416, x 32 185 / 273, x 64
+// 366 / 432; 8 x 8,000 x 20 46 / 67, x 64 67 / 76; 1 x 100,000 x 32 55 / 96; fp32 64 x 8,000 x 32
+// 365 / 747, x 64 750 / 1,121; 8 x 8,000 x 64 110 / 152, x 128 195 / 136.
+constexpr int kShortRows = 64;        // most query rows of a sequence that come here ...
+constexpr int kSmallCall = 1 << 18;   // ... unless all units x keys are no more than this (bf16, 1 x 2,000 x
+                                      // 128 18 / 21)
+// Rows of a unit: 32 where a sequence has more than 16 (bf16 64 x 8,000 x 20 184 us in units of 32, 380 in
+// units of 16; 64 x 8,000 x 4 takes as long in either).  In a small call 16, which are twice as many
+// workgroups (6 x 500 x 32 11.9 / 14.4), and with fp32 rows, whose three terms for two blocks of rows
+// would not fit a wave's registers at two waves per SIMD.
 // One workgroup per unit, without parts and their launch, up to this many keys, twice as
 // many from 64 units on.  us per call, unit by unit / in shares, head_dim 128: 1 sequence
 // of 1,000 keys at 1 kv head 10.7 / 11.8, 64 at 8 heads 36 / 46; of 2,000 keys 18.7 / 12.1
@@ -103,9 +108,9 @@ __device__ __forceinline__ void load_step(const AttnArgs &a, const Lookup &pg, i
 }
 
 // O^T += V^T P^T for one pair of token groups
-template <int D, int NS>
+template <int D, int NS, int RB>
 __device__ __forceinline__ void add_pv(const uint32_t (&v0)[4][D / 64], const uint32_t (&v1)[4][D / 64],
-                                       float s0, float s1, const Frag<NS> &p, f32x4 *o) {
+                                       float s0, float s1, const Frag<NS> (&p)[RB], f32x4 (&o)[RB][D / 16]) {
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
         const uint32_t t[8] = {v0[0][w], v0[1][w], v0[2][w], v0[3][w],
@@ -116,7 +121,9 @@ __device__ __forceinline__ void add_pv(const uint32_t (&v0)[4][D / 64], const ui
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                o[4 * w + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b], p.f[i], o[4 * w + b], 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+                    o[r][4 * w + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b], p[r].f[i], o[r][4 * w + b], 0, 0, 0);
     }
 }
 
@@ -131,55 +138,62 @@ __device__ __forceinline__ uint32_t quotient(int64_t x, int y) {
 }
 
 // Where every wave's share of a unit meets: D + 2 floats per row and wave.
-template <int D> struct Meet {
-    float o[kWaves][kRows][D + 4];
-    float m[kWaves][kRows], l[kWaves][kRows];
+template <int D, int RB> struct Meet {
+    float o[kWaves][kRows * RB][D + 4];
+    float m[kWaves][kRows * RB], l[kWaves][kRows * RB];
 };
 
-// The lane's query row of a unit and the keys it sees.
-template <int D, int NS> struct Row {
-    Frag<NS> q[D / 32];
-    int lo, hi;               // keys lo <= j < hi
+// The lane's query rows of a unit (16 apart) and the keys they see.
+template <int D, int NS, int RB> struct Rows {
+    Frag<NS> q[RB][D / 32];
+    int lo[RB], num[RB];      // keys lo <= j < lo + num
     int all_lo, all_hi;       // keys that every row of the unit sees
 
-    __device__ void load(const AttnArgs &a, const Seq &s, int rb, int hk, int G, int lane) {
+    // end: the keys from there on are another share's
+    __device__ void load(const AttnArgs &a, const Seq &s, int rb, int hk, int G, int end, int lane) {
+        constexpr int UR = kRows * RB;
         const int kg = lane >> 4;
-        const int R = rb * kRows + (lane & 15);
-        const int tok = min(R / G, s.len - 1), gh = R % G;
-        const int64_t qi = (s.c0 + tok) * a.q_row + (int64_t)(hk * G + gh) * D;
 #pragma unroll
-        for (int f = 0; f < D / 32; ++f) {
-            float x[8];
-            mf::IO<NS == 1>::load8(a.q, qi + (f >> 1) * 64 + kg * 16 + (f & 1) * 8, x);
-            if (a.scale < 0.f) {          // the maximum is taken before the scale
+        for (int b = 0; b < RB; ++b) {
+            const int R = rb * UR + kRows * b + (lane & 15);
+            const int tok = min(R / G, s.len - 1), gh = R % G;
+            const int64_t qi = (s.c0 + tok) * a.q_row + (int64_t)(hk * G + gh) * D;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = -x[j];
+            for (int f = 0; f < D / 32; ++f) {
+                float x[8];
+                mf::IO<NS == 1>::load8(a.q, qi + (f >> 1) * 64 + kg * 16 + (f & 1) * 8, x);
+                if (a.scale < 0.f) {          // the maximum is taken before the scale
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = -x[j];
+                }
+                q[b][f] = split8<NS>(x);
             }
-            q[f] = split8<NS>(x);
+            lo[b] = s.begin_of(a, tok);
+            num[b] = R < s.len * G ? max(min(s.end_of(a, tok), end) - lo[b], 0) : 0;
         }
         // The loads end here: were they still on their way at the loop's first entry, its
         // waits would count them in every pass.
 #pragma unroll
-        for (int f = 0; f < D / 32; ++f)
+        for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                u32x4 x = __builtin_bit_cast(u32x4, q[f].f[i]);
-                asm volatile("" : "+v"(x));
-                q[f].f[i] = __builtin_bit_cast(bf16x8, x);
-            }
-        const int t0 = rb * kRows / G, t1 = min((rb * kRows + kRows - 1) / G, s.len - 1);
-        hi = R < s.len * G ? s.end_of(a, tok) : 0;
-        lo = s.begin_of(a, tok);
-        all_hi = s.end_of(a, t0);
+            for (int f = 0; f < D / 32; ++f)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    u32x4 x = __builtin_bit_cast(u32x4, q[b][f].f[i]);
+                    asm volatile("" : "+v"(x));
+                    q[b][f].f[i] = __builtin_bit_cast(bf16x8, x);
+                }
+        const int t0 = rb * UR / G, t1 = min((rb * UR + UR - 1) / G, s.len - 1);
+        all_hi = min(s.end_of(a, t0), end);
         all_lo = s.begin_of(a, t1);
     }
 };
 
-// One step of 32 keys for the 16 rows of a unit.  True: values that were NaN are left
-// out, see_nans() is to follow.
-template <int D, int NS>
-__device__ __forceinline__ bool one_step(const Row<D, NS> &row, Codes<D> &c, int t, float scale, int lane, float &m,
-                                          float &l, f32x4 *o) {
+// One step of 32 keys for the rows of a unit.  True: values that were NaN are left out,
+// see_nans() is to follow.
+template <int D, int NS, int RB>
+__device__ __forceinline__ bool one_step(const Rows<D, NS, RB> &row, Codes<D> &c, int t, float scale, int lane,
+                                          float (&m)[RB], float (&l)[RB], f32x4 (&o)[RB][D / 16]) {
     constexpr int NT = D / 16;
     const int kg = lane >> 4, kb = t * kStep;
     const uint32_t sv = f32_bits(c.ok >> (lane & 1) & 1 ? c.scale : 1.f);
@@ -189,10 +203,11 @@ __device__ __forceinline__ bool one_step(const Row<D, NS> &row, Codes<D> &c, int
         ks[g] = bits_f32(__builtin_amdgcn_readlane(sv, g));
         vs[g] = bits_f32(__builtin_amdgcn_readlane(sv, 2 + g));
     }
-    f32x4 sc[2];
+    f32x4 sc[RB][2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        sc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < RB; ++b) sc[b][g] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int f = 0; f < D / 32; ++f) {
             const u32x4 x = c.k[g][f >> 1];
@@ -204,44 +219,49 @@ __device__ __forceinline__ bool one_step(const Row<D, NS> &row, Codes<D> &c, int
             kf[3] = widen<true>(c1, ks[g]);
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), row.q[f].f[i], sc[g],
-                                                                0, 0, 0);
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    sc[b][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf),
+                                                                       row.q[b][f].f[i], sc[b][g], 0, 0, 0);
         }
     }
     const bool full = c.ok == 3 && kb >= row.all_lo && kb + kStep <= row.all_hi;
     if (!full) {
         asm volatile("");             // a branch: whole steps are the rule
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = kb + 16 * g + 4 * kg + i;
-                if (!(j >= row.lo && j < row.hi && (c.ok >> g & 1))) sc[g][i] = -__builtin_inff();
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t n = c.ok >> g & 1 ? row.num[b] : 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((uint32_t)(kb + 16 * g + 4 * kg + i - row.lo[b]) >= n) sc[b][g][i] = -__builtin_inff();
             }
     }
-    float tm = -__builtin_inff();
+    float p[RB][8];
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
+    for (int b = 0; b < RB; ++b) {
+        float tm = -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tm = fmaxf(tm, sc[g][i]);
-    tm = max_16(tm);
-    tm = tm == -__builtin_inff() ? tm : tm * scale;
-    if (__ballot(tm > m) != 0) {
-        const float mn = fmaxf(m, tm);
-        const float alpha = mf::ex2(m - (mn == -__builtin_inff() ? 0.f : mn));
-        m = mn;
-        l *= alpha;
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[i] *= alpha;
-    }
-    const float ms = m == -__builtin_inff() ? 0.f : m;
-    float p[8];
+            for (int i = 0; i < 4; ++i) tm = fmaxf(tm, sc[b][g][i]);
+        tm = max_16(tm);
+        tm = tm == -__builtin_inff() ? tm : tm * scale;
+        if (__ballot(tm > m[b]) != 0) {
+            const float mn = fmaxf(m[b], tm);
+            const float alpha = mf::ex2(m[b] - (mn == -__builtin_inff() ? 0.f : mn));
+            m[b] = mn;
+            l[b] *= alpha;
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[4 * g + i] = mf::ex2(__builtin_fmaf(sc[g][i], scale, -ms));
+            for (int i = 0; i < NT; ++i) o[b][i] *= alpha;
         }
+        const float ms = m[b] == -__builtin_inff() ? 0.f : m[b];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[b][4 * g + i] = mf::ex2(__builtin_fmaf(sc[b][g][i], scale, -ms));
+    }
 
     bool repair = false;
     if (!full) {
@@ -259,9 +279,14 @@ __device__ __forceinline__ bool one_step(const Row<D, NS> &row, Codes<D> &c, int
                 }
         repair = __ballot(any != 0) != 0;
     }
+    Frag<NS> pf[RB];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l += p[i];
-    add_pv<D, NS>(c.v[0], c.v[1], vs[0], vs[1], split8<NS>(p), o);
+    for (int b = 0; b < RB; ++b) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[b] += p[b][i];
+        pf[b] = split8<NS>(p[b]);
+    }
+    add_pv<D, NS, RB>(c.v[0], c.v[1], vs[0], vs[1], pf, o);
     return repair;
 }
 
@@ -369,19 +394,19 @@ __device__ __forceinline__ Place place(const AttnArgs &a, int G, int of, int blo
     return p;
 }
 
-// The sequence and unit of number x in the order of the packed rows: sequence n's
-// units start at first(n) = cu[n] G / kRows + n (at least as many apart as it has),
-// at n where no sequence here has more than one (host_units() of them in all).
+// The sequence and unit of number x of host_units(): where all sequences are here, in the
+// order of the packed rows, sequence n's starting at first(n) = cu[n] G / unit_rows + n (at
+// least as many apart as it has); else the same number for each, enough for a short one.
 __device__ __forceinline__ bool packed_unit(const AttnArgs &a, int64_t x, int G, int &n, Seq &s, int &rb) {
-    if (a.short_rows <= kRows) {
-        n = (int)x;
-        rb = 0;
+    if (a.short_rows <= kShortRows) {
+        n = (int)x / (kShortRows / a.unit_rows);
+        rb = (int)x % (kShortRows / a.unit_rows);
         s = sequence(a, n, G);
-        return s.rt > 0;
+        return rb < s.rt;
     }
-    n = last_not_above(a.kv.N, x, [&](int i) { return a.kv.cu[i] * G / kRows + i; });
+    n = last_not_above(a.kv.N, x, [&](int i) { return a.kv.cu[i] * G / a.unit_rows + i; });
     s = sequence(a, n, G);
-    const int64_t r = x - (s.c0 * G / kRows + n);
+    const int64_t r = x - (s.c0 * G / a.unit_rows + n);
     rb = (int)r;
     return r >= 0 && r < s.rt;
 }
@@ -389,11 +414,12 @@ __device__ __forceinline__ bool packed_unit(const AttnArgs &a, int64_t x, int G,
 // BF: bf16 rows.  One workgroup takes a contiguous share of all (unit, step)
 // pairs, or, with workers = 0, one unit; its waves take the steps of a unit in
 // turn, each with its next step on the way from HBM, and meet in LDS at the end.
-template <int D, bool BF>
-__global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const AttnArgs a) {
+template <int D, bool BF, int RB>
+__global__ __launch_bounds__(kAttnThreads, BF && RB == 1 ? 3 : 2) void attn_kernel(const AttnArgs a) {
     constexpr int NS = BF ? 1 : 3;
+    constexpr int UR = kRows * RB;             // rows of a unit
     constexpr int NT = D / 16;                 // 16-dim blocks of O
-    __shared__ Meet<D> sm;
+    __shared__ Meet<D, RB> sm;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -430,15 +456,20 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
             const int hk = (int)(unit / (uint32_t)s.rt), rb = (int)(unit % (uint32_t)s.rt);
             const bool whole = ubase >= from && uend <= to;
             // its steps here, less those that no row of the unit sees
-            const int t0 = min(rb * kRows / G, s.len - 1), t1 = min((rb * kRows + kRows - 1) / G, s.len - 1);
+            const int t0 = min(rb * UR / G, s.len - 1), t1 = min((rb * UR + UR - 1) / G, s.len - 1);
             const int beg = max(s.lo + (int)(at - ubase), s.begin_of(a, t0) / kStep);
             const int stop = min(s.lo + (int)(min(uend, to) - ubase), (s.end_of(a, t1) + kStep - 1) / kStep);
 
-            float m = -__builtin_inff(), l = 0.f;
-            f32x4 o[NT];
+            float m[RB], l[RB];
+            f32x4 o[RB][NT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-            Row<D, NS> row;
+            for (int b = 0; b < RB; ++b) {
+                m[b] = -__builtin_inff();
+                l[b] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) o[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            Rows<D, NS, RB> row;
             Codes<D> c0, c1;
             int t = beg + w;
             if (t < stop) {
@@ -448,9 +479,7 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
                 const int last = stop - 1;
                 Lookup pg{table, shift, s.kvl, 0};
                 pg.ask(t, lane);
-                row.load(a, s, rb, hk, G, lane);
-                row.hi = min(row.hi, stop * kStep);      // the keys behind are another share's
-                row.all_hi = min(row.all_hi, stop * kStep);
+                row.load(a, s, rb, hk, G, stop * kStep, lane);
                 Lookup next = pg;
                 next.ask(min(t + kWaves, last), lane);
                 load_step<D>(a, pg, hk, t, lane, c0);
@@ -458,8 +487,12 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
                     pg = next;
                     next.ask(min(t + 2 * kWaves, last), lane);
                     load_step<D>(a, pg, hk, min(t + kWaves, last), lane, ahead);
-                    if (one_step<D, NS>(row, c, t, fabsf(a.scale), lane, m, l, o))
-                        see_nans<D>(a, table, shift, hk, max(row.lo, t * kStep), min(row.hi, (t + 1) * kStep), kg, o);
+                    if (one_step<D, NS, RB>(row, c, t, fabsf(a.scale), lane, m, l, o)) {
+#pragma unroll
+                        for (int b = 0; b < RB; ++b)
+                            see_nans<D>(a, table, shift, hk, max(row.lo[b], t * kStep), min(row.lo[b] + row.num[b], (t + 1) * kStep),
+                                        kg, o[b]);
+                    }
                     t += kWaves;
                 };
                 // Two steps a pass with one way out, so that the waits of a pass know what is
@@ -471,18 +504,22 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
             }
 
             // the waves meet
-            l = sum_16(l);
-            if (kg == 0) { sm.m[w][col] = m; sm.l[w][col] = l; }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)       // dims (D / 16)(4 kg + i) + j, j < NT
+            for (int b = 0; b < RB; ++b) {
+                const float sum = sum_16(l[b]);
+                if (kg == 0) { sm.m[w][kRows * b + col] = m[b]; sm.l[w][kRows * b + col] = sum; }
 #pragma unroll
-                for (int j = 0; j < NT; j += 4)
-                    *(f32x4 *)&sm.o[w][col][NT * (4 * kg + i) + j] =
-                        f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+                for (int i = 0; i < 4; ++i)       // dims (D / 16)(4 kg + i) + j, j < NT
+#pragma unroll
+                    for (int j = 0; j < NT; j += 4)
+                        *(f32x4 *)&sm.o[w][kRows * b + col][NT * (4 * kg + i) + j] =
+                            f32x4{o[b][j][i], o[b][j + 1][i], o[b][j + 2][i], o[b][j + 3][i]};
+            }
             __syncthreads();
-            {
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
                 constexpr int E = kRows * D / kAttnThreads;      // 8 or 4 dims per thread
-                const int r = tid / (D / E), d = (tid % (D / E)) * E;
+                const int r = kRows * b + tid / (D / E), d = (tid % (D / E)) * E;
                 float M = -__builtin_inff();
 #pragma unroll
                 for (int i = 0; i < kWaves; ++i) M = fmaxf(M, sm.m[i][r]);
@@ -497,7 +534,7 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
 #pragma unroll
                     for (int j = 0; j < E; ++j) y[j] += f * sm.o[i][r][d + j];
                 }
-                const int R = rb * kRows + r;
+                const int R = rb * UR + r;
                 if (whole) {
                     if (R < s.len * G) {
                         const int64_t at_row = (s.c0 + R / G) * a.Hq + hk * G + R % G;
@@ -506,9 +543,9 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
                     }
                 } else {
                     // cut at this workgroup's end: its second slot; at its start: the first
-                    float *dst = a.part + (2 * (int64_t)blockIdx.x + (ubase >= from ? 1 : 0)) * (kRows * (D + 2));
+                    float *dst = a.part + (2 * (int64_t)blockIdx.x + (ubase >= from ? 1 : 0)) * (UR * (D + 2));
                     store_row<false, E>(dst, r * D + d, y, 1.f);
-                    if (d == 0) { dst[kRows * D + r] = M; dst[kRows * D + kRows + r] = L; }
+                    if (d == 0) { dst[UR * D + r] = M; dst[UR * D + UR + r] = L; }
                 }
             }
             __syncthreads();
@@ -521,8 +558,9 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 3 : 2) void attn_kernel(const At
 
 // Joins the parts of every unit that attn_kernel cut.  A workgroup takes RW rows
 // of a unit; 256 / RW threads share a row: D / E of them its dims, the rest its parts.
-template <int D, bool BF, int RW>
+template <int D, bool BF, int RB, int RW>
 __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
+    constexpr int UR = kRows * RB;
     constexpr int E = kRows * D / kAttnThreads;
     constexpr int TD = D / E;                           // 16 threads over the dims
     constexpr int SL = kAttnThreads / (RW * TD);        // slices of the parts
@@ -530,7 +568,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
     __shared__ float s_m[SL][RW], s_l[SL][RW];
     const int tid = threadIdx.x;
     const int G = a.Hq / a.kv.Hk;
-    const uint32_t u = blockIdx.x / (kRows / RW);
+    const uint32_t u = blockIdx.x / (UR / RW);
     const int hk = u % a.kv.Hk;
     int n, rb;
     Seq s;
@@ -541,13 +579,13 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
     const int64_t w0 = ubase / share, w1 = (ubase + s.steps - 1) / share;
     if (w0 == w1) return;                               // written whole
     const int d = (tid % TD) * E, sl = tid / TD % SL, rr = tid / (TD * SL);
-    const int r = (blockIdx.x % (kRows / RW)) * RW + rr;
+    const int r = (blockIdx.x % (UR / RW)) * RW + rr;
     float M = -__builtin_inff(), L = 0.f, y[E];
 #pragma unroll
     for (int j = 0; j < E; ++j) y[j] = 0.f;
     for (int64_t i = w0 + sl; i <= w1; i += SL) {
-        const float *src = a.part + (2 * i + (ubase >= i * share ? 1 : 0)) * (kRows * (D + 2));
-        const float m = src[kRows * D + r], l = src[kRows * D + kRows + r];
+        const float *src = a.part + (2 * i + (ubase >= i * share ? 1 : 0)) * (UR * (D + 2));
+        const float m = src[UR * D + r], l = src[UR * D + UR + r];
         float v[E];
 #pragma unroll
         for (int j = 0; j < E; j += 4) *(f32x4 *)(v + j) = *(const f32x4 *)(src + r * D + d + j);
@@ -577,7 +615,7 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
             for (int j = 0; j < E; ++j) y[j] += s_o[i][rr][d + j] * f;
         }
     }
-    const int R = rb * kRows + r;
+    const int R = rb * UR + r;
     if (R >= s.len * G) return;
     const int64_t row = (s.c0 + R / G) * a.Hq + hk * G + R % G;
     store_row<BF, E>(a.o, row * D + d, y, L == 0.f ? 0.f : 1.f / L);
@@ -585,23 +623,24 @@ __global__ __launch_bounds__(kAttnThreads) void join_kernel(const AttnArgs a) {
 }
 
 // Units over all sequences at most, per kv head.
-int64_t host_units(int64_t T, int G, int N, int short_rows) {
-    return short_rows <= kRows ? N : T * G / kRows + N;
+int64_t host_units(int64_t T, int G, int N, const AttnArgs &a) {
+    return a.short_rows <= kShortRows ? (int64_t)N * (kShortRows / a.unit_rows) : T * G / a.unit_rows + N;
 }
 
-template <int D, bool BF>
+template <int D, bool BF, int RB>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
-    const int64_t units = host_units(a.kv.T, a.Hq / a.kv.Hk, a.kv.N, a.short_rows) * a.kv.Hk;
-    if (units > INT32_MAX / kRows) return hipErrorInvalidValue;
+    constexpr int UR = kRows * RB;
+    const int64_t units = host_units(a.kv.T, a.Hq / a.kv.Hk, a.kv.N, a) * a.kv.Hk;
+    if (units > INT32_MAX / UR) return hipErrorInvalidValue;
     const dim3 block(kAttnThreads);
-    hipLaunchKernelGGL((attn_kernel<D, BF>), dim3((unsigned)(a.workers ? a.workers : units)), block, 0, s, a);
+    hipLaunchKernelGGL((attn_kernel<D, BF, RB>), dim3((unsigned)(a.workers ? a.workers : units)), block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.workers == 0) return e;
     // few units have many parts each: more workgroups per unit and threads per row
     if (units < a.workers / 8)
-        hipLaunchKernelGGL((join_kernel<D, BF, 1>), dim3((unsigned)(units * kRows)), block, 0, s, a);
+        hipLaunchKernelGGL((join_kernel<D, BF, RB, 1>), dim3((unsigned)(units * UR)), block, 0, s, a);
     else
-        hipLaunchKernelGGL((join_kernel<D, BF, kRows>), dim3((unsigned)units), block, 0, s, a);
+        hipLaunchKernelGGL((join_kernel<D, BF, RB, kRows>), dim3((unsigned)(units * RB)), block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -612,7 +651,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 // tokens at 32 / 8 heads of 128, these 231, twice as many 256 (more parts to write and
 // join).  Counting a unit's start and end as kUnitCost steps evens out shares of many
 // short units and of few long ones (246 us without).
-static int resident(bool bf16, int D) { return D == 64 ? (bf16 ? 4 : 3) : (bf16 ? 3 : 2); }
+static int resident(bool bf16, int D, int unit_rows) {
+    if (unit_rows > kRows) return 2;
+    return D == 64 ? (bf16 ? 4 : 3) : (bf16 ? 3 : 2);
+}
 
 void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int64_t max_kv, AttnArgs *a) {
     const int G = Hq / Hk;
@@ -621,19 +663,22 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     a->row_units = 0;
     a->row_splits = 1;
     // keys that a unit can see: the table's, or its window's
-    const int64_t keys = a->window > 0 ? std::min<int64_t>(max_kv, (int64_t)a->window + kRows + 2 * kStep) : max_kv;
+    const int64_t keys = a->window > 0 ? std::min<int64_t>(max_kv, (int64_t)a->window + 2 * kRows + 2 * kStep) : max_kv;
     // The lengths are known on the device only.  A call goes to this kernel alone where it is small, or
-    // where equal lengths would be short (a decode step, equally many drafted tokens); a single long
-    // sequence to the other; else each sequence goes to its own.
-    const bool all_short = rows <= kShortRows || (T % N == 0 && rows / N <= kShortRows) ||
-                           std::max<int64_t>(rows / kRows, N) * Hk * keys <= kSmallCall;
+    // where equal lengths would be short (a decode step, equally many drafted tokens: if they are not
+    // equal after all, its units are twice as many at most); a single long sequence to the other; else
+    // each sequence goes to its own, and a kernel that has none costs 3 us.
+    const bool small = std::max<int64_t>(rows / kRows, N) * Hk * keys <= kSmallCall;
+    const int64_t most = T % N == 0 ? rows / N : rows;      // rows of a sequence if they are equally long
+    const bool all_short = small || most <= (N == 1 ? kShortRows : 2 * kRows);
     const bool all_long = N == 1 && !all_short;
+    a->unit_rows = bf16 && !small && most > kRows ? 2 * kRows : kRows;
     // (alone, it also takes a sequence that padding made look long)
     a->short_rows = all_short ? INT32_MAX : all_long ? 0 : kShortRows;
     if (!all_long) {
-        const int64_t units = host_units(T, G, N, a->short_rows) * Hk;
+        const int64_t units = host_units(T, G, N, *a) * Hk;
         const bool direct = keys <= kDirect || (keys <= 2 * kDirect && units >= 64);
-        a->workers = direct ? 0 : cus * resident(bf16, D);
+        a->workers = direct ? 0 : cus * resident(bf16, D, a->unit_rows);
     }
     if (!all_short) {
         a->row_units = (int32_t)(rows / kRowTile + N);
@@ -648,14 +693,19 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
 }
 
 size_t attn_partial_bytes(int D, const AttnArgs &a) {
-    const size_t one = a.workers > 0 ? (size_t)a.workers * 2 * kRows * (D + 2) : 0;
+    const size_t one = a.workers > 0 ? (size_t)a.workers * 2 * a.unit_rows * (D + 2) : 0;
     const size_t rows = a.row_splits > 1 ? (size_t)a.row_units * a.kv.Hk * a.row_splits * kRowTile * (D + 2) : 0;
     return std::max(one, rows) * sizeof(float);
 }
 
 hipError_t launch_attn(bool bf16, int D, const AttnArgs &a, hipStream_t s) {
-    if (D == 128) return bf16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
-    if (D == 64) return bf16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    if (a.unit_rows > kRows) {
+        if (bf16 && D == 128) return launch<128, true, 2>(a, s);
+        if (bf16 && D == 64) return launch<64, true, 2>(a, s);
+        return hipErrorInvalidValue;
+    }
+    if (D == 128) return bf16 ? launch<128, true, 1>(a, s) : launch<128, false, 1>(a, s);
+    if (D == 64) return bf16 ? launch<64, true, 1>(a, s) : launch<64, false, 1>(a, s);
     return hipErrorInvalidValue;
 }
 

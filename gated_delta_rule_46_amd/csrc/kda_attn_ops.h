@@ -20,7 +20,7 @@ constexpr int kWaves = kAttnThreads / 64;
 constexpr int kTile = 64;             // keys per step of kda_attn_rows.hip
 constexpr int kStep = 32;             // and of kda_attn.hip
 constexpr int kUnitCost = 12;         // steps that starting and ending a unit there costs
-constexpr int kRows = 16;             // query rows (token, head of the group) per unit of kda_attn.hip
+constexpr int kRows = 16;             // query rows (token, head of the group) of a block; kda_attn.hip: 1 or 2 a unit
 constexpr int kRowTile = 128;         // and of kda_attn_rows.hip
 constexpr int kMinSplit = 4;          // fewest tiles there worth a workgroup of their own
 constexpr float kLn2 = 0.6931471805599453f;
@@ -38,7 +38,7 @@ struct Seq {
     int64_t pos0;     // position of the first new token
     int kvl;          // cached tokens that the table can hold
     int len;
-    int rt;           // units of kRows rows per kv head (0: the other kernel's)
+    int rt;           // units of unit_rows rows per kv head (0: the other kernel's)
     int lo, steps;    // first step that some row sees; steps of a unit, kUnitCost among them
 
     // keys that new token i sees: begin_of(i) <= j < end_of(i)
@@ -61,7 +61,7 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int n, int G) {
     s.len = s.c0 < 0 ? 0 : (int)max(c1 - s.c0, (int64_t)0);
     s.pos0 = kv - s.len;
     s.kvl = (int)max(min(kv, (int64_t)a.kv.width * a.kv.page), (int64_t)0);
-    s.rt = (int64_t)s.len * G <= a.short_rows ? (s.len * G + kRows - 1) / kRows : 0;
+    s.rt = (int64_t)s.len * G <= a.short_rows ? (s.len * G + a.unit_rows - 1) / a.unit_rows : 0;
     s.lo = s.begin_of(a, 0) / kStep;
     s.steps = (s.kvl + kStep - 1) / kStep - s.lo + kUnitCost;
     return s;

@@ -365,7 +365,8 @@ def test_attn_prompts(K, dtype, D, page, Hk, G, causal, window):
 @pytest.mark.parametrize("room", [0, 50000])
 def test_attn_one_sequence(K, dtype, new, kv, window, room):
     """A sequence alone: a prompt, a chunk that is split over the keys, more rows than keys, a window; a
-    table for just this length (small calls: units of 16 rows) and a wide one (units of 128)."""
+    table for just this length (small calls: units of 16 rows) and a wide one (units of 128,
+    of 16 and 32 for the shortest)."""
     say(f"attn one sequence {dtype} new={new} kv={kv} window={window} room={room}")
     m, rng = plain_model(K, dtype, 2, 128, 64, [kv], new, width=room // 64 or None)
     attn_check(K, m, dtype, queries(rng, new, 8, 128, dtype), [0, new], [kv], 0.1, True, window)
@@ -382,6 +383,20 @@ def test_attn_one_padded_sequence(K, dtype, T, new, kv):
     out, lse = torch.full((T, 8, 128), 5.0, dtype=dt(dtype), device="cuda"), torch.full((T, 8), 5.0, device="cuda")
     attn_check(K, m, dtype, q, [0, new], [kv], 0.1, out=out, lse_out=lse)
     assert (out[new:] == 5.0).all() and (lse[new:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,page,Hk,G,new", [(128, 64, 2, 4, [5] * 5), (64, 16, 1, 8, [4] * 3), (128, 128, 1, 3, [7] * 4),
+                                             (64, 32, 2, 1, [31, 31]), (128, 16, 1, 24, [1] * 6), (64, 64, 1, 1, [18] * 4),
+                                             (128, 32, 1, 8, [1, 8, 0, 3, 9, 5]), (64, 64, 2, 4, [16, 2, 17, 4, 8])])
+@pytest.mark.parametrize("window", [0, 70])
+def test_attn_drafted_tokens(K, dtype, D, page, Hk, G, new, window):
+    """A few tokens on each sequence with a large table: 17 to 32 query rows per kv head (units of 32),
+    equally many or not, and sequences of just over and under 64 rows side by side."""
+    say(f"attn drafts {dtype} D={D} page={page} Hk={Hk} G={G} new={new} window={window}")
+    kv = [900, 65, 31, 333, 64, 2000][:len(new)]
+    m, rng = plain_model(K, dtype, Hk, D, page, kv, 40 + D + G, width=300000 // page)
+    attn_check(K, m, dtype, queries(rng, sum(new), Hk * G, D, dtype), cum(new), kv, D ** -0.5, True, window)
 
 
 @pytest.mark.parametrize("wide", [False, True])
@@ -469,12 +484,13 @@ def test_attn_rows_that_see_nothing(K, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("width", [8, 40])
-def test_attn_hidden_nan_and_extremes(K, dtype, width):
-    """NaN keys and values reach exactly the rows that see them; scores of hundreds and a constant key."""
+@pytest.mark.parametrize("width,len0", [(8, 40), (40, 40), (20000, 14)])
+def test_attn_hidden_nan_and_extremes(K, dtype, width, len0):
+    """NaN keys and values reach exactly the rows that see them; scores of hundreds, a scale of zero and a
+    negative one; units of 16 rows with and without shares, of 32 rows."""
     import torch
-    say(f"attn NaN and extremes {dtype} width={width}")
-    new, kv = [40, 1], [200, 131]
+    say(f"attn NaN and extremes {dtype} width={width} new={len0}")
+    new, kv = [len0, 1], [200, 131]
     m, rng = plain_model(K, dtype, 1, 64, 64, kv, 33, width=width)
     vals = A.e4m3_values()
 
@@ -487,7 +503,7 @@ def test_attn_hidden_nan_and_extremes(K, dtype, width):
     put("v", 0, 171, 9, 0xFF)
     put("k", 0, 190, 3, 0x7F)                          # whole rows from position 190 on
     put("v", 1, 131 - 1, 0, 0x7F)                      # the last key of a full tail
-    q = queries(rng, 41, 4, 64, dtype)
+    q = queries(rng, len0 + 1, 4, 64, dtype)
     for causal, window in ((True, 0), (True, 12)):
         o, lse = K.kda_attn(q, i64(cum(new)), i64(kv), m.gpu, scale=0.125, causal=causal, window=window, want_lse=True)
         torch.cuda.synchronize()
@@ -496,9 +512,9 @@ def test_attn_hidden_nan_and_extremes(K, dtype, width):
         assert np.array_equal(np.isnan(to_numpy_f64(o)), np.isnan(ro))
         assert np.array_equal(np.isnan(to_numpy_f64(lse)), np.isnan(rl))
     m, rng = plain_model(K, dtype, 1, 64, 64, kv, 34, width=width)
-    attn_check(K, m, dtype, queries(rng, 41, 4, 64, dtype), cum(new), kv, 8.0, name="scores of hundreds")
-    attn_check(K, m, dtype, queries(rng, 41, 4, 64, dtype), cum(new), kv, 0.0, name="scale 0")
-    attn_check(K, m, dtype, queries(rng, 41, 4, 64, dtype), cum(new), kv, -0.125, name="negative scale")
+    attn_check(K, m, dtype, queries(rng, len0 + 1, 4, 64, dtype), cum(new), kv, 8.0, name="scores of hundreds")
+    attn_check(K, m, dtype, queries(rng, len0 + 1, 4, 64, dtype), cum(new), kv, 0.0, name="scale 0")
+    attn_check(K, m, dtype, queries(rng, len0 + 1, 4, 64, dtype), cum(new), kv, -0.125, name="negative scale")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
