@@ -681,7 +681,7 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
         a->workers = direct ? 0 : cus * resident(bf16, D, a->unit_rows);
     }
     if (!all_short) {
-        a->row_units = (int32_t)(rows / kRowTile + N);
+        a->row_units = a->row_fold = (int32_t)(rows / kRowTile + N);
         const int64_t units = (int64_t)a->row_units * Hk;
         if (units < 2 * cus) {
             // parts of at least kMinSplit tiles: 1 sequence of 2,000 keys and 32 rows 51 us with two
@@ -689,6 +689,7 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
             const int64_t want = (4 * (int64_t)cus + units - 1) / units;
             a->row_splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, 32, max_kv / (kMinSplit * kTile)}));
         }
+        if (a->row_splits == 1 && rows / kRowTile * Hk <= 2 * cus) a->row_fold = (a->row_units + 1) / 2;
     }
 }
 

@@ -223,11 +223,12 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     const int col = lane & 31, kg = lane >> 5;
     const int G = a.Hq / a.kv.Hk;
     const int hk = blockIdx.x % a.kv.Hk;
-    // the last rows see the most keys: they go first
-    const int64_t y = blockIdx.x / a.kv.Hk;
+    // the last rows see the most keys: they go first; where all units fit the card at once, the second
+    // half in turn (a long one and a short one on each compute unit)
+    const int64_t y = blockIdx.x / a.kv.Hk, z = y / a.row_splits;
     const int split = (int)(y % a.row_splits);
     Unit u;
-    if (!find_unit(a, a.row_units - 1 - y / a.row_splits, G, u) || split >= u.splits) return;
+    if (!find_unit(a, z < a.row_fold ? a.row_units - 1 - z : z - a.row_fold, G, u) || split >= u.splits) return;
     const Seq &s = u.s;
     const int tiles = u.end - u.beg;
     const int t0 = u.beg + (int)((int64_t)tiles * split / u.splits);
