@@ -62,6 +62,7 @@ struct AttnArgs {
                                  // unit; -1: not launched
     int32_t row_units;           // kda_attn_rows.hip: units per kv head, 0: not launched
     int32_t row_splits;          // workgroups per unit at most
+    int32_t split_tiles;         // one for each so many tiles of 64 keys
     int32_t row_fold;            // units from the last one that start in order, the others after them
 };
 // The plan of a call (short_rows, workers, row_units, row_splits) and the bytes

@@ -661,7 +661,7 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     const int64_t rows = T * G;
     a->workers = -1;
     a->row_units = 0;
-    a->row_splits = 1;
+    a->row_splits = a->split_tiles = 1;
     // keys that a unit can see: the table's, or its window's
     const int64_t keys = a->window > 0 ? std::min<int64_t>(max_kv, (int64_t)a->window + 2 * kRows + 2 * kStep) : max_kv;
     // The lengths are known on the device only.  A call goes to this kernel alone where it is small, or
@@ -682,14 +682,19 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     }
     if (!all_short) {
         a->row_units = a->row_fold = (int32_t)(rows / kRowTile + N);
-        const int64_t units = (int64_t)a->row_units * Hk;
+        const int64_t units = std::max<int64_t>((rows + kRowTile - 1) / kRowTile, N) * Hk;
         if (units < 2 * cus) {
-            // parts of at least kMinSplit tiles: 1 sequence of 2,000 keys and 32 rows 51 us with two
-            // parts of 16 tiles, 18 with eight of 4
-            const int64_t want = (4 * (int64_t)cus + units - 1) / units;
-            a->row_splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, 32, max_kv / (kMinSplit * kTile)}));
+            // Two workgroups for every compute unit; the more units, the more their parts cost against
+            // what sharing the keys gains.  us whole / 2 / 4 / 8 parts at 32 / 8 heads of 128: 64 units,
+            // 2,000 keys 53 / 39 / 33 / 38, 15,000 329 / 180 / 102 / 86; 128 units, 512 keys
+            // 21 / 23 / 23 / 23, 4,000 94 / 64 / 59 / 71; 256 units, 1,024 keys 32 / 37 / 49 / 49, 4,000
+            // 96 / 83 / 98 / 125; 384 units, 1,536 keys 46 / 53 / 73 / 74, 6,144 147 / 112 / 129 / 173.
+            a->split_tiles = units < cus / 4 ? 4 : units < cus ? 8 : 16;
+            const int64_t want = (2 * (int64_t)cus + units - 1) / units;
+            a->row_splits =
+                (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, 32, max_kv / (a->split_tiles * kTile)}));
         }
-        if (a->row_splits == 1 && rows / kRowTile * Hk <= 2 * cus) a->row_fold = (a->row_units + 1) / 2;
+        if (a->row_splits == 1 && units <= 2 * cus) a->row_fold = (a->row_units + 1) / 2;
     }
 }
 

@@ -22,7 +22,6 @@ constexpr int kStep = 32;             // and of kda_attn.hip
 constexpr int kUnitCost = 12;         // steps that starting and ending a unit there costs
 constexpr int kRows = 16;             // query rows (token, head of the group) of a block; kda_attn.hip: 1 or 2 a unit
 constexpr int kRowTile = 128;         // and of kda_attn_rows.hip
-constexpr int kMinSplit = 4;          // fewest tiles there worth a workgroup of their own
 constexpr float kLn2 = 0.6931471805599453f;
 
 // bf16 pairs of bytes (0, 1) or (2, 3) of four codes, times 2^(scale's exponent)

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int64_t x, int G, U
     const int t0 = u.row0 / G, t1 = min((u.row0 + kRowTile - 1) / G, u.s.len - 1);
     u.end = (u.s.end_of(a, t1) + kTile - 1) / kTile;
     u.beg = min(u.s.begin_of(a, t0) / kTile, u.end);
-    u.splits = min(a.row_splits, max((u.end - u.beg + kMinSplit - 1) / kMinSplit, 1));
+    u.splits = min(a.row_splits, max((u.end - u.beg + a.split_tiles - 1) / a.split_tiles, 1));
     return true;
 }
 
