@@ -24,6 +24,12 @@
 // V is read row by row (8 bytes: 8 dims of one token); byte permutes pair two
 // tokens of a dim before the conversion to bf16.  The dims of V are numbered
 // so that a lane's 8 bytes serve the 8 products of its column.
+//
+// Bound by reading the codes once: 64 sequences of 512 to 32,768 tokens, one new one each,
+// at 32 / 8 heads of 128 with bf16 rows 231 us (5.5 TB/s; reads of shuffled 8 KiB pages
+// alone reach 6.8), 131,072 keys 62 us (4.3), 257 keys 10.6 (one chain of memory latencies).
+// Hence all of the card on any mix of lengths (shares of equal steps, joined after), loads
+// of one step ahead without a branch, and few registers, for three waves per SIMD.
 
 #include <algorithm>
 
@@ -42,10 +48,10 @@ using namespace attn;
 constexpr int kShortRows = 64;        // most query rows of a sequence that come here ...
 constexpr int kSmallCall = 1 << 18;   // ... unless all units x keys are no more than this (bf16, 1 x 2,000 x
                                       // 128 18 / 21)
-// Rows of a unit: 32 where a sequence has more than 16 (bf16 64 x 8,000 x 20 184 us in units of 32, 380 in
-// units of 16; 64 x 8,000 x 4 takes as long in either).  In a small call 16, which are twice as many
-// workgroups (6 x 500 x 32 11.9 / 14.4), and with fp32 rows, whose three terms for two blocks of rows
-// would not fit a wave's registers at two waves per SIMD.
+// Rows of a unit: 32 where a sequence has more than 16 (bf16 64 x 8,000 x 20 197 us in units of 32, 395 in
+// units of 16; x 64 376 / 723).  In a small call 16, which are twice as many workgroups (6 x 500 x 32 14.4 / 11.9), and with
+// fp32 rows, whose three terms for two blocks of rows would not fit a wave's registers at two waves per SIMD.
+
 // One workgroup per unit, without parts and their launch, up to this many keys, twice as
 // many from 64 units on.  us per call, unit by unit / in shares, head_dim 128: 1 sequence
 // of 1,000 keys at 1 kv head 10.7 / 11.8, 64 at 8 heads 36 / 46; of 2,000 keys 18.7 / 12.1
