@@ -46,8 +46,10 @@ using namespace attn;
 // 366 / 432; 8 x 8,000 x 20 46 / 67, x 64 67 / 76; 1 x 100,000 x 32 55 / 96; fp32 64 x 8,000 x 32
 // 365 / 747, x 64 750 / 1,121; 8 x 8,000 x 64 110 / 152, x 128 195 / 136.
 constexpr int kShortRows = 64;        // most query rows of a sequence that come here ...
-constexpr int kSmallCall = 1 << 18;   // ... unless all units x keys are no more than this (bf16, 1 x 2,000 x
-                                      // 128 18 / 21)
+// ... unless all units x keys are no more than this: 1 x 2,000 x 128 with bf16 rows 18 / 21, 4 x 2,000 x 128
+// 32 / 36, 1 x 4,000 x 256 39 / 31; with fp32 rows 3 x 3,000 x 140 46 / 76, 1 x 1,000 x 1,024 23 / 42; with
+// heads of 64 and bf16 rows 3 x 1,900 x 140 25 / 32, 1 x 1,000 x 1,024 14 / 23.
+static int64_t small_call(bool bf16, int D) { return bf16 && D == 128 ? 1 << 18 : 1 << 20; }
 // Rows of a unit: 32 where a sequence has more than 16 (bf16 64 x 8,000 x 20 197 us in units of 32, 395 in
 // units of 16; x 64 376 / 723).  In a small call 16, which are twice as many workgroups (6 x 500 x 32 14.4 / 11.9), and with
 // fp32 rows, whose three terms for two blocks of rows would not fit a wave's registers at two waves per SIMD.
@@ -673,8 +675,8 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     // The lengths are known on the device only.  A call goes to this kernel alone where it is small, or
     // where equal lengths would be short (a decode step, equally many drafted tokens: if they are not
     // equal after all, its units are twice as many at most); a single long sequence to the other; else
-    // each sequence goes to its own, and a kernel that has none costs 3 us.
-    const bool small = std::max<int64_t>(rows / kRows, N) * Hk * keys <= kSmallCall;
+    // each sequence goes to its own, and a kernel that has none costs 5 us, its join as much.
+    const bool small = std::max<int64_t>(rows / kRows, N) * Hk * keys <= small_call(bf16, D);
     const int64_t most = T % N == 0 ? rows / N : rows;      // rows of a sequence if they are equally long
     const bool all_short = small || most <= (N == 1 ? kShortRows : 2 * kRows);
     const bool all_long = N == 1 && !all_short;

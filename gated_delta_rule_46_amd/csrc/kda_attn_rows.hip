@@ -22,9 +22,9 @@
 // maximum grew by more than 2^8 since (probabilities stay below 2^8, which
 // costs neither fp32 sums nor bf16 operands any precision).
 //
-// A prompt of 8,192 tokens at 32 / 8 heads of 128 with bf16 rows takes 554 to 571 us (960 to
-// 990 TFLOP/s; an 8192^3 product of the library 1,210 to 1,240), four chunks of 300 to 1,024
-// over up to 15,000 keys 470 (940).  The matrix cores are busy 43% of the cycles and the
+// A prompt of 8,192 tokens at 32 / 8 heads of 128 with bf16 rows takes 555 us (990 TFLOP/s;
+// an 8192^3 product of the library 1,210 to 1,240), four chunks of 300 to 1,024 over up to
+// 15,000 keys 461 (958).  The matrix cores are busy 43% of the cycles and the
 // vector pipe 47%, at 2.0 to 2.2 GHz.  Two workgroups per compute unit, each at its own
 // place in a tile, overlap the two better than one of 256 rows: as eight waves of 32 rows
 // (half the conversions and LDS writes) 578, as four of 64, each computing the next tile's
