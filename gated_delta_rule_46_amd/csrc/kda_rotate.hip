@@ -12,7 +12,9 @@
 // token; D/8 lanes take a head, 8 dims each (a 16-byte bf16 vector), so a
 // lane's dims are the same for all of its heads and the weights, cosines and
 // sines are loaded once per lane.  All arithmetic in fp32, one rounding at the
-// store.  16,384 tokens at 32 / 8 heads of 128 with bf16 rows: 57 us (343 MB, 6.0
+// store.  A head whose mean square leaves fp32's range (elements beyond about 2^63,
+// or tiny ones with an eps as small) is scaled by a power of two first, which costs
+// the others a comparison.  16,384 tokens at 32 / 8 heads of 128 with bf16 rows: 57 us (343 MB, 6.0
 // TB/s; a large copy 5.1); 64 tokens 4.5 us, the launch.
 
 #include "kda_attn.h"
@@ -22,6 +24,32 @@ namespace kda {
 namespace {
 
 constexpr int kRotThreads = 256;
+
+// Least mean square (eps in it) that is used as it stands: what its squares lost below
+// fp32's smallest normal, 2^-126 each, is less than 2^-24 of it.
+constexpr float kLeastMean = 0x1p-100f;
+
+// The head x of L lanes as x / 2^k, and eps as eps / 4^k, with the larger of max |x| and
+// sqrt(eps) within [1/2, 1): the mean square is then at least 2^-9.  Returns its
+// reciprocal root.  All lanes of the head call it; infinities and NaN are left as they are.
+template <int L>
+__device__ __forceinline__ float rescale(float (&x)[8], float eps) {
+    float top = sqrtf(eps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const int k = top > 0.f && top < __builtin_inff() ? __builtin_amdgcn_frexp_expf(top) : 0;
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        x[j] = ldexpf(x[j], -k);
+        ss += x[j] * x[j];
+    }
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) ss += __shfl_xor(ss, off);
+    return rsqrtf(ss * (1.f / (8 * L)) + ldexpf(eps, -2 * k));
+}
 
 template <int D, bool BF, bool PAIRS>
 __global__ __launch_bounds__(kRotThreads) void rotate_kernel(const RotateArgs a) {
@@ -86,7 +114,10 @@ __global__ __launch_bounds__(kRotThreads) void rotate_kernel(const RotateArgs a)
         for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
 #pragma unroll
         for (int off = 1; off < L; off <<= 1) ss += __shfl_xor(ss, off);
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const float mean = ss * (1.f / D) + a.eps;
+        float r = rsqrtf(mean);
+        if (live && !(mean >= kLeastMean && mean < __builtin_inff()))   // rare; the same in a head's lanes
+            r = rescale<L>(x, a.eps);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= r * (isq ? wq[j] : wk[j]);
         if (a.table) {

@@ -521,7 +521,9 @@ typedef struct {
  *   rot_dim a multiple of 16, at most head_dim;
  *   positions device int64 [T]; a token whose position is outside [0, n_pos)
  *       is padding: its output rows are left as they are.
- * fp32 arithmetic, one rounding at the store.  q_out (k_out) may be q (k)
+ * fp32 arithmetic, one rounding at the store; the squares of any finite head
+ * neither overflow nor vanish (it is scaled by a power of two where they
+ * would).  q_out (k_out) may be q (k)
  * itself with the same row distance; otherwise outputs must not overlap inputs.
  * T = 0 is a no-op.  No workspace.  One launch.
  */
