@@ -123,7 +123,10 @@ __global__ __launch_bounds__(kRotThreads) void rotate_kernel(const RotateArgs a)
         if (a.table) {
             float y[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = PAIRS ? (d0 < a.rot ? x[j ^ 1] : 0.f) : __shfl(x[j], partner);
+            for (int j = 0; j < 8; ++j) {
+                y[j] = PAIRS ? x[j ^ 1] : __shfl(x[j], partner);
+                if (d0 >= a.rot) y[j] = 0.f;  // not rotated: an infinity stays (times sn = 0 it is a NaN)
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[j] + y[j] * sn[j];
         }

@@ -59,3 +59,25 @@ def test_rotate_heads_of_any_magnitude(K, dtype, D, rot, pairs, eps):
                 np.concatenate([np.hypot(y[..., :rot // 2], y[..., rot // 2:])] * 2, -1)
         within(name, to_numpy_f64(g), r,
                G.HALF[dtype] * np.abs(r) + (D / 2 + 16) * 2.0 ** -24 * np.maximum(np.abs(r), 2 * pair) + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 32), (128, 16)])
+def test_rotate_infinite_results_behind_the_rotated_dims(K, D, rot, pairs):
+    """A dim behind rot whose weight makes it infinite stays an infinity of its sign; its neighbours are as ever."""
+    import torch
+    say(f"rotate infinite results D={D} rot={rot} pairs={pairs}")
+    rng = np.random.default_rng(D)
+    x = dev(rng.normal(size=(5, 3, D)).astype(np.float32))
+    w = np.ones(D, np.float32)
+    w[rot], w[D - 7] = np.inf, -np.inf
+    pos, table = rng.integers(0, 500, 5), G.rope_table(500, rot)
+    q, k = K.kda_qk_norm_rope(x[:, :2], x[:, 2:], i64(pos), dev(table), q_weight=dev(w), k_weight=dev(w),
+                              layout=K.KDA_ROPE_PAIRS if pairs else K.KDA_ROPE_HALVES)
+    torch.cuda.synchronize()
+    for name, g, src in (("q", q, x[:, :2]), ("k", k, x[:, 2:])):
+        r = A.norm_rope(to_numpy_f64(src), w, 1e-6, pos, table, pairs)
+        assert np.isinf(r).sum() == 2 * r.shape[0] * r.shape[1] and not np.isnan(r).any()
+        fin = np.where(np.isinf(r), 0, r)
+        within(name, to_numpy_f64(g), r, G.HALF["f32"] * np.abs(fin) + (D / 2 + 16) * 2.0 ** -24 * (np.abs(fin) + 2 * 2 ** 0.5 * np.abs(
+            fin).max(-1, keepdims=True)))
