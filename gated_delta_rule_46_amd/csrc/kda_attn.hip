@@ -174,7 +174,7 @@ template <int D, int NS, int RB> struct Rows {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = -x[j];
                 }
-                q[b][f] = split8<NS>(x);
+                q[b][f] = split_query8<NS>(x);
             }
             lo[b] = s.begin_of(a, tok);
             num[b] = R < s.len * G ? max(min(s.end_of(a, tok), end) - lo[b], 0) : 0;

@@ -123,6 +123,30 @@ __device__ __forceinline__ Frag<NS> split8(const float *x) {
     return r;
 }
 
+// The same for queries, which can be infinite, or so large that the first term would be
+// rounded to an infinity (what is left of x would then be a NaN): an infinity is its
+// first term alone, and the largest values are cut instead of rounded.
+template <int NS>
+__device__ __forceinline__ Frag<NS> split_query8(const float *x) {
+    if constexpr (NS == 1) return split8<1>(x);
+    Frag<NS> r;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t b = f32_bits(x[j]), mag = b & 0x7fffffffu;
+        const bool cut = mag >= 0x7f7f8000u && mag <= 0x7f800000u;
+        const bf16_t h = (bf16_t)(cut ? bits_f32(b & 0xffff0000u) : x[j]);
+        r.f[0][j] = h;
+        y[j] = mag == 0x7f800000u ? 0.f : x[j] - (float)h;
+    }
+    if constexpr (NS > 1) {
+        const Frag<NS - 1> rest = split8<NS - 1>(y);
+#pragma unroll
+        for (int t = 1; t < NS; ++t) r.f[t] = rest.f[t - 1];
+    }
+    return r;
+}
+
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {   // 0x80 in every byte that is a NaN code
     return ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }

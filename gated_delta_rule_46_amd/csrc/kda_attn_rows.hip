@@ -85,7 +85,7 @@ template <int D, int NS> struct Query {
             mf::IO<NS == 1>::load8(q, at + 16 * i + 8 * kg, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = neg ? -x[j] : x[j];
-            f[i] = split8<NS>(x);
+            f[i] = split_query8<NS>(x);
         }
     }
     // S^T of both halves of a tile: fragments are read two steps ahead, and other(i) is

@@ -81,3 +81,64 @@ def test_rotate_infinite_results_behind_the_rotated_dims(K, D, rot, pairs):
         fin = np.where(np.isinf(r), 0, r)
         within(name, to_numpy_f64(g), r, G.HALF["f32"] * np.abs(fin) + (D / 2 + 16) * 2.0 ** -24 * (np.abs(fin) + 2 * 2 ** 0.5 * np.abs(
             fin).max(-1, keepdims=True)))
+
+
+# new tokens, cached tokens, pages in the table: a unit per workgroup, shares that cut units, units of 128 rows
+PLANS = [([1, 5], [40, 90], 8), ([1, 5], [40, 3000], 400), ([150], [300], 400), ([40, 3], [300, 70], 400)]
+
+
+def set_keys(m, half, codes=None, scale=None):
+    """Codes (uint8 [n_pages, Hk, page, D]) or scales of one half, on the GPU and in the oracle."""
+    c = m.keys if half == "k" else m.values
+    if codes is not None:
+        setattr(m.gpu, half, dev(codes))
+        c.codes = A.e4m3_values()[codes]
+    if scale is not None:
+        setattr(m.gpu, half + "_scale", dev(scale))
+        c.scale = np.asarray(scale, np.float64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,kv,width", PLANS)
+def test_attn_infinite_queries(K, dtype, D, new, kv, width):
+    """An infinity in a query times keys of one sign: scores that are all -inf give o = 0 and lse = -inf, +inf
+    gives NaN, and so do infinities of both signs; the other rows are as without them."""
+    import torch
+    say(f"attn infinite queries {dtype} D={D} new={new} kv={kv} width={width}")
+    m, rng = G.plain_model(K, dtype, 1, D, 16, kv, 3 + D, width=width)
+    codes = m.gpu.k.view(torch.uint8).cpu().numpy()
+    codes[..., 5] &= 0x7F                                          # dim 5: all keys positive and no zero
+    codes[..., 5] |= 1
+    set_keys(m, "k", codes)
+    T = sum(new)
+    q = G.queries(rng, T, 4, D, dtype).clone()
+    ref = q.clone()
+    q[0, 0, 5], q[0, 1, 5], q[T - 1, 2, 9], q[T - 1, 3, 5] = -np.inf, np.inf, np.inf, -np.inf
+    o, lse = K.kda_attn(q, i64(G.cum(new)), i64(kv), m.gpu, scale=0.2, want_lse=True)
+    torch.cuda.synchronize()
+    for t, h in ((0, 0), (T - 1, 3)):
+        assert not o[t, h].any() and lse[t, h] == -np.inf, (t, h)
+    for t, h in ((0, 1), (T - 1, 2)):
+        assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h]), (t, h)
+    # the four rows replaced by what the ordinary call gives, all is compared
+    ro, rl = K.kda_attn(ref, i64(G.cum(new)), i64(kv), m.gpu, scale=0.2, want_lse=True)
+    for t, h in ((0, 0), (0, 1), (T - 1, 2), (T - 1, 3)):
+        o[t, h], lse[t, h] = ro[t, h], rl[t, h]
+    G.attn_compare(m, dtype, ref, G.cum(new), kv, 0.2, True, 0, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,kv,width", PLANS)
+def test_attn_largest_queries(K, dtype, new, kv, width):
+    """Queries up to the type's largest value (in fp32 it would be rounded to an infinity in bf16) over the
+    smallest scale of keys."""
+    import torch
+    say(f"attn largest queries {dtype} new={new} kv={kv} width={width}")
+    m, rng = G.plain_model(K, dtype, 1, 64, 16, kv, 8, width=width)
+    set_keys(m, "k", scale=np.full(tuple(m.gpu.k_scale.shape), 2.0 ** -100, np.float32))
+    top = torch.finfo(dt(dtype)).max
+    q = (G.queries(rng, sum(new), 4, 64, dtype).float().clamp(-4, 4) / 4 * top).to(dt(dtype)).clamp(-top, top)
+    q[..., 3] = top
+    q[..., 17] = -top
+    G.attn_check(K, m, dtype, q, G.cum(new), kv, 1e-12)
