@@ -1070,9 +1070,10 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
         return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
     if (need) KDA_TRY(check_tensor(ws, "ws", true));
     a.q = q; a.q_row = q_row; a.o = o; a.lse = lse; a.part = need ? (float *)ws : nullptr;
-    // (a scale of zero as the smallest that keeps -inf x scale = -inf: masked scores)
-    a.scale = scale * 1.4426950408889634f;
-    if (std::fabs(a.scale) < FLT_MIN) a.scale = FLT_MIN;
+    // masked scores are -inf x a.scale, and maxima are taken before it: it is positive, and the
+    // queries take the sign, or become zeros
+    a.scale = std::max(std::fabs(scale * 1.4426950408889634f), FLT_MIN);
+    a.q_sign = scale < 0.f ? -1.f : scale > 0.f ? 1.f : 0.f;
     a.causal = causal;
     const bool bf = cfg->io_dtype == KDA_DTYPE_BF16;
     hipError_t e = hipSuccess;

@@ -52,7 +52,8 @@ struct AttnArgs {
     float *lse;                  // [T, Hq] (nullable)
     float *part;                 // partial results of split units
     int32_t Hq;
-    float scale;                 // of the scores, times log2(e)
+    float scale;                 // of the scores, times log2(e): its size, at least the smallest normal
+    float q_sign;                // its sign, which the queries take: -1, 0 or 1
     int32_t causal, window;
     // sequences of at most short_rows query rows per kv head go to kda_attn.hip,
     // the others to kda_attn_rows.hip

@@ -170,10 +170,8 @@ template <int D, int NS, int RB> struct Rows {
             for (int f = 0; f < D / 32; ++f) {
                 float x[8];
                 mf::IO<NS == 1>::load8(a.q, qi + (f >> 1) * 64 + kg * 16 + (f & 1) * 8, x);
-                if (a.scale < 0.f) {          // the maximum is taken before the scale
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = -x[j];
-                }
+                for (int j = 0; j < 8; ++j) x[j] *= a.q_sign;     // exact
                 q[b][f] = split_query8<NS>(x);
             }
             lo[b] = s.begin_of(a, tok);
@@ -495,7 +493,7 @@ __global__ __launch_bounds__(kAttnThreads, BF && RB == 1 ? 3 : 2) void attn_kern
                     pg = next;
                     next.ask(min(t + 2 * kWaves, last), lane);
                     load_step<D>(a, pg, hk, min(t + kWaves, last), lane, ahead);
-                    if (one_step<D, NS, RB>(row, c, t, fabsf(a.scale), lane, m, l, o)) {
+                    if (one_step<D, NS, RB>(row, c, t, a.scale, lane, m, l, o)) {
 #pragma unroll
                         for (int b = 0; b < RB; ++b)
                             see_nans<D>(a, table, shift, hk, max(row.lo[b], t * kStep), min(row.lo[b] + row.num[b], (t + 1) * kStep),

@@ -78,13 +78,13 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, bf16x8 b, f32x16 c) {
 // Queries of a lane's row as operand fragments, NS bf16 terms each.
 template <int D, int NS> struct Query {
     Frag<NS> f[D / 16];               // step i: dims 16 i + 8 kg + 0..7
-    __device__ void load(const void *q, int64_t at, int kg, bool neg) {
+    __device__ void load(const void *q, int64_t at, int kg, float sign) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             float x[8];
             mf::IO<NS == 1>::load8(q, at + 16 * i + 8 * kg, x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = neg ? -x[j] : x[j];
+            for (int j = 0; j < 8; ++j) x[j] *= sign;       // exact
             f[i] = split_query8<NS>(x);
         }
     }
@@ -252,9 +252,9 @@ __global__ __launch_bounds__(kAttnThreads, BF ? 2 : 1) void rows_kernel(const At
     const int any_hi = first < s.len * G ? s.end_of(a, wt1) : 0, any_lo = s.begin_of(a, wt0);
     const int all_hi = s.end_of(a, wt0), all_lo = s.begin_of(a, wt1);
 
-    const float sl = fabsf(a.scale);
+    const float sl = a.scale;
     Query<D, NS> q;
-    q.load(a.q, (s.c0 + tok) * a.q_row + (int64_t)(hk * G + R % G) * D, kg, a.scale < 0.f);
+    q.load(a.q, (s.c0 + tok) * a.q_row + (int64_t)(hk * G + R % G) * D, kg, a.q_sign);
 
     float m = -__builtin_inff(), l = 0.f;
     f32x16 o[NJ];

@@ -142,3 +142,14 @@ def test_attn_largest_queries(K, dtype, new, kv, width):
     q[..., 3] = top
     q[..., 17] = -top
     G.attn_check(K, m, dtype, q, G.cum(new), kv, 1e-12)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,kv,width", PLANS)
+def test_attn_scale_zero_over_large_scores(K, dtype, new, kv, width):
+    """A scale of 0 weighs every key alike, however large q.k is (up to 10^37 here)."""
+    say(f"attn scale 0 {dtype} new={new} kv={kv} width={width}")
+    m, rng = G.plain_model(K, dtype, 1, 64, 16, kv, 9, width=width)
+    set_keys(m, "k", scale=np.full(tuple(m.gpu.k_scale.shape), 2.0 ** 20, np.float32))
+    q = (G.queries(rng, sum(new), 4, 64, dtype).float() * 4e27).to(dt(dtype))
+    G.attn_check(K, m, dtype, q, G.cum(new), kv, 0.0)
