@@ -918,14 +918,14 @@ int check_rows(const kda_attn_config *cfg, int32_t N, int64_t T) {
     return KDA_OK;
 }
 
-int check_cache(const kda_attn_config *cfg, const kda_kv_cache *c) {
-    (void)cfg;
+// The table of no sequences is not looked at: it may be NULL (an empty tensor's address).
+int check_cache(const kda_kv_cache *c, int32_t N) {
     if (!c) return fail(KDA_ERR_ARG, "cache is NULL");
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
         return fail(KDA_ERR_UNSUPPORTED, "cache->page must be 16, 32, 64 or 128 (got %d)", c->page);
     if (c->n_pages <= 0)
         return fail(KDA_ERR_ARG, "cache->n_pages must be positive (got %lld)", (long long)c->n_pages);
-    if (c->table_width <= 0)
+    if (c->table_width <= 0 && N > 0)
         return fail(KDA_ERR_ARG, "cache->table_width must be positive (got %d)", c->table_width);
     if (c->table_width > (1 << 30) / c->page)
         return fail(KDA_ERR_UNSUPPORTED, "cache->table_width * cache->page must fit in 30 bits (got %d, %d)",
@@ -934,7 +934,7 @@ int check_cache(const kda_attn_config *cfg, const kda_kv_cache *c) {
     KDA_TRY(check_tensor(c->v, "cache->v", true));
     KDA_TRY(check_tensor(c->k_scale, "cache->k_scale", true, 4));
     KDA_TRY(check_tensor(c->v_scale, "cache->v_scale", true, 4));
-    KDA_TRY(check_tensor(c->table, "cache->table", true, 4));
+    KDA_TRY(check_tensor(c->table, "cache->table", N > 0, 4));
     return KDA_OK;
 }
 
@@ -1009,7 +1009,7 @@ int kda_kv_write(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t 
                  const void *v, int64_t v_row, void *stream) {
     KDA_TRY(check_attn_config(cfg));
     KDA_TRY(check_rows(cfg, N, T));
-    KDA_TRY(check_cache(cfg, cache));
+    KDA_TRY(check_cache(cache, N));
     KDA_TRY(check_row(cfg, k_row, cfg->num_kv_heads, "k_row"));
     KDA_TRY(check_row(cfg, v_row, cfg->num_kv_heads, "v_row"));
     if (T == 0) return ok();
@@ -1027,7 +1027,7 @@ int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N
                 const int64_t *cu_seqlens, const int64_t *kv_len, void *k, void *v, void *stream) {
     KDA_TRY(check_attn_config(cfg));
     KDA_TRY(check_rows(cfg, N, T));
-    KDA_TRY(check_cache(cfg, cache));
+    KDA_TRY(check_cache(cache, N));
     if (T == 0) return ok();
     KDA_TRY(check_tensor(cu_seqlens, "cu_seqlens", true, 8));
     KDA_TRY(check_tensor(kv_len, "kv_len", true, 8));
@@ -1042,7 +1042,7 @@ int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N
 size_t kda_attn_workspace(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N,
                           int64_t T, int32_t window) {
     if (check_attn_config(cfg) != KDA_OK || check_rows(cfg, N, T) != KDA_OK) return 0;
-    if (check_cache(cfg, cache) != KDA_OK || T == 0) return 0;
+    if (check_cache(cache, N) != KDA_OK || T == 0) return 0;
     return round256(kda::attn_partial_bytes(cfg->head_dim, attn_args(cfg, cache, N, T, nullptr, nullptr, window)));
 }
 
@@ -1052,7 +1052,7 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
              size_t ws_bytes, void *stream) {
     KDA_TRY(check_attn_config(cfg));
     KDA_TRY(check_rows(cfg, N, T));
-    KDA_TRY(check_cache(cfg, cache));
+    KDA_TRY(check_cache(cache, N));
     if (!std::isfinite(scale * 1.4426950408889634f)) return fail(KDA_ERR_ARG, "scale must be finite");
     if (causal != 0 && causal != 1) return fail(KDA_ERR_ARG, "causal must be 0 or 1 (got %d)", causal);
     if (window < 0) return fail(KDA_ERR_ARG, "window must be >= 0 (got %d)", window);

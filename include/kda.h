@@ -499,6 +499,7 @@ int kda_conv_halo(int32_t io_dtype, int32_t channels, int32_t width, const void 
  * *_row is the distance between tokens in elements (at least the row itself, a
  * multiple of 16 bytes), so q, k and v may be views of one projection's rows.
  * head_dim in {64, 128}; num_q_heads a multiple of num_kv_heads.
+ * T = 0 is a no-op, also with N = 0 (then cache->table may be NULL).
  * T is below 2^24, T * num_q_heads at most 2^26, N * num_q_heads at most 2^20
  * and table_width * page at most 2^30 (larger calls are split by the caller).
  */

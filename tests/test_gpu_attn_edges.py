@@ -153,3 +153,26 @@ def test_attn_scale_zero_over_large_scores(K, dtype, new, kv, width):
     set_keys(m, "k", scale=np.full(tuple(m.gpu.k_scale.shape), 2.0 ** 20, np.float32))
     q = (G.queries(rng, sum(new), 4, 64, dtype).float() * 4e27).to(dt(dtype))
     G.attn_check(K, m, dtype, q, G.cum(new), kv, 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attn_layer_calls_without_rows(K, dtype):
+    """No sequences at all, and sequences without new tokens: empty results, the cache as it was."""
+    import torch
+    say(f"attention layer without rows {dtype}")
+    for N in (0, 3):
+        table = torch.zeros((N, 4), dtype=torch.int32, device="cuda")
+        cache = K.KVCache.empty(5, 2, 16, 64, table)
+        cache.k += 3
+        before = [x.clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+        rows = torch.zeros((0, 6, 64), dtype=dt(dtype), device="cuda")
+        cu, kv = i64([0] * (N + 1)), i64([7] * N)
+        q, k = K.kda_qk_norm_rope(rows[:, :4], rows[:, 4:], i64([]), dev(G.rope_table(8, 64)))
+        assert q.shape == (0, 4, 64) and k.shape == (0, 2, 64)
+        K.kda_kv_write(k, rows[:, 4:], cu, kv, cache)
+        k, v = K.kda_kv_read(cu, kv, cache, 0, dt(dtype))
+        assert k.shape == v.shape == (0, 2, 64)
+        o, lse = K.kda_attn(q, cu, kv, cache, want_lse=True)
+        torch.cuda.synchronize()
+        assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+        assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)))
