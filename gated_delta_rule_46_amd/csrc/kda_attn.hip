@@ -48,10 +48,10 @@ using namespace attn;
 constexpr int kShortRows = 64;        // most query rows of a sequence that come here ...
 // ... unless all units x keys are no more than this: 1 x 2,000 x 128 with bf16 rows 18 / 21, 4 x 2,000 x 128
 // 32 / 36, 1 x 4,000 x 256 39 / 31; with fp32 rows 3 x 3,000 x 140 46 / 76, 1 x 1,000 x 1,024 23 / 42; with
-// heads of 64 and bf16 rows 3 x 1,900 x 140 25 / 32, 1 x 1,000 x 1,024 14 / 23.
+// heads of 64 and bf16 rows 3 x 1,900 x 140 16 / 24, 1 x 1,000 x 1,024 14 / 22.
 static int64_t small_call(bool bf16, int D) { return bf16 && D == 128 ? 1 << 18 : 1 << 20; }
-// Rows of a unit: 32 where a sequence has more than 16 (bf16 64 x 8,000 x 20 197 us in units of 32, 395 in
-// units of 16; x 64 376 / 723).  In a small call 16, which are twice as many workgroups (6 x 500 x 32 14.4 / 11.9), and with
+// Rows of a unit: 32 where a sequence has more than 16 (bf16 64 x 8,000 x 20 185 us in units of 32, 378 in
+// units of 16; x 64 366 / 720).  In a small call 16, which are twice as many workgroups (6 x 500 x 32 13.1 / 12.3), and with
 // fp32 rows, whose three terms for two blocks of rows would not fit a wave's registers at two waves per SIMD.
 
 // One workgroup per unit, without parts and their launch, up to this many keys, twice as
@@ -671,9 +671,15 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
     // keys that a unit can see: the table's, or its window's
     const int64_t keys = a->window > 0 ? std::min<int64_t>(max_kv, (int64_t)a->window + 2 * kRows + 2 * kStep) : max_kv;
     // The lengths are known on the device only.  A call goes to this kernel alone where it is small, or
-    // where equal lengths would be short (a decode step, equally many drafted tokens: if they are not
-    // equal after all, its units are twice as many at most); a single long sequence to the other; else
-    // each sequence goes to its own, and a kernel that has none costs 5 us, its join as much.
+    // where equal lengths would be short (a decode step, equally many drafted tokens); a single long
+    // sequence to the other; else each sequence goes to its own, and a kernel that has none costs 5 us,
+    // its join as much.  Lengths that could be equal and are not: a long sequence then reads its keys
+    // once for each 32 rows, in shares on all of the card beside the short ones, instead of for each 128
+    // after them.  us for T = a multiple of N / one row more (32 / 8 heads of 128, bf16, decoding
+    // sequences over 2,000 keys and a chunk): 63 and 449 tokens over 4,000 keys 160 / 193, over 16,000
+    // 390 / 488; 255 and 1,793 over 0 273 / 354, over 4,000 686 / 424, over 16,000 1,491 / 783, over 60,000
+    // 4,558 / 2,045 (the worst found).  And lengths that are equal but for a padded row: 64 decoding
+    // sequences over 2,000 keys 62, 63 in 64 rows 91; 64 of 5 tokens 58, with one more row 84.
     const bool small = std::max<int64_t>(rows / kRows, N) * Hk * keys <= small_call(bf16, D);
     const int64_t most = T % N == 0 ? rows / N : rows;      // rows of a sequence if they are equally long
     const bool all_short = small || most <= (N == 1 ? kShortRows : 2 * kRows);
@@ -694,7 +700,7 @@ void attn_plan(int cus, bool bf16, int D, int N, int64_t T, int Hq, int Hk, int6
             // what sharing the keys gains.  us whole / 2 / 4 / 8 parts at 32 / 8 heads of 128: 64 units,
             // 2,000 keys 53 / 39 / 33 / 38, 15,000 329 / 180 / 102 / 86; 128 units, 512 keys
             // 21 / 23 / 23 / 23, 4,000 94 / 64 / 59 / 71; 256 units, 1,024 keys 32 / 37 / 49 / 49, 4,000
-            // 96 / 83 / 98 / 125; 384 units, 1,536 keys 46 / 53 / 73 / 74, 6,144 147 / 112 / 129 / 173.
+            // 96 / 83 / 98 / 125; 384 units, 1,536 keys 46 / 53 / 73 / 74, 6,144 177 / 188 / 185 / 225 (2 are taken).
             a->split_tiles = units < cus / 4 ? 4 : units < cus ? 8 : 16;
             const int64_t want = (2 * (int64_t)cus + units - 1) / units;
             a->row_splits =

@@ -67,8 +67,8 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int64_t x, int G, U
 template <int D> struct Stage {
     u32x4 k[2][D / 16][64];           // 32 tokens: steps of 16 dims, (token, 8 dims) per lane
     u32x4 v[4][D / 32][64];           // 16 tokens: 32 dims, (dim, 8 tokens) per lane
-    int ok[4];                        // group of 16 tokens has a page (or lies behind the last key)
-    int nan, hole;                    // the tile if it held a NaN value, an absent page
+    int ok[4];                        // group of 16 tokens has a page and starts before the last key
+    int nan, hole;                    // the tile if it held a NaN value, a group that is not ok
 };
 
 __device__ __forceinline__ f32x16 mma(u32x4 a, bf16x8 b, f32x16 c) {

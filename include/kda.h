@@ -486,12 +486,12 @@ int kda_conv_halo(int32_t io_dtype, int32_t channels, int32_t width, const void 
 /* ------------------------------------------------------------------------ */
 
 /*
- * Models that use KDA interleave its layers with softmax-attention layers
- * (pegainfer PR #970's profile of one superstep: 35.8% in those layers' attention
- * kernels, 4.2% in KDA).  These calls serve such a layer beside kda_prefill and
- * kda_decode, on the same packed rows:
+ * Hybrid models put softmax-attention layers between their delta-rule layers.
+ * These calls serve such a layer, with grouped heads whose keys and values are
+ * equally wide, beside kda_prefill and kda_decode, on the same packed rows:
  *     kda_qk_norm_rope -> kda_kv_write -> kda_attn
  * for prompts, chunks of prompts, drafted tokens and single tokens alike.
+ * (Latent attention, MLA, is another form: its layers are not served.)
  *
  * Rows.  q has num_q_heads heads, k and v num_kv_heads heads, of head_dim
  * values each, in io_dtype; query head h reads key/value head
