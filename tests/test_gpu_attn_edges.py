@@ -176,3 +176,58 @@ def test_attn_layer_calls_without_rows(K, dtype):
         torch.cuda.synchronize()
         assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
         assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+
+
+def test_attn_layer_offsets_beyond_32_bits(K):
+    """Pages that lie more than 2^32 bytes into the cache, and rows 2^31 + 64 elements apart: the same bits as
+    with a small cache and dense rows."""
+    import torch
+    say("attention layer, offsets beyond 32 bits")
+    Hq, Hk, D, page, pages = 4, 2, 128, 128, 140000
+    far = pages * Hk * page * D
+    assert far > 1 << 32
+    if torch.cuda.mem_get_info()[0] < 4 * far:
+        pytest.skip("not enough memory")
+    rng = np.random.default_rng(1)
+    new, kv = [300, 1, 4], [300, 700, 515]
+    T = sum(new)
+    order = rng.permutation(64)
+    table = order[:18].reshape(3, 6).astype(np.int32)
+    small = K.KVCache.empty(64, Hk, page, D, dev(table))
+    big = K.KVCache.empty(pages, Hk, page, D, dev(table + np.int32(pages - 64)))
+    rope, pos = dev(G.rope_table(1024, D)), i64(np.concatenate([np.arange(L - n, L) for n, L in zip(new, kv)]))
+    ctx = [L - n for n, L in zip(new, kv)]
+    old = dev(rng.normal(size=(sum(ctx), 2 * Hk, D)), torch.bfloat16)
+    x = dev(rng.normal(size=(T, Hq + 2 * Hk, D)), torch.bfloat16)
+    got = []
+    for cache in (small, big):
+        K.kda_kv_write(old[:, :Hk], old[:, Hk:], i64(G.cum(ctx)), i64(ctx), cache)
+        q, k = K.kda_qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hk], pos, rope)
+        K.kda_kv_write(k, x[:, Hq + Hk:], i64(G.cum(new)), i64(kv), cache)
+        back = K.kda_kv_read(i64(G.cum(kv)), i64(kv), cache, sum(kv))
+        outs = []
+        for window in (0, 200):
+            outs += K.kda_attn(q, i64(G.cum(new)), i64(kv), cache, window=window, want_lse=True)
+        got.append([*back, *outs])
+        # one token of each sequence, two sequences' rows far apart
+        outs = K.kda_attn(q[-2:], i64([0, 0, 1, 2]), i64(kv), cache, want_lse=True)
+        got[-1] += outs
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and all(torch.isfinite(t).all() for t in got[0])
+    assert not big.k[:pages - 64].any() and torch.equal(small.k, big.k[pages - 64:]) and torch.equal(
+        small.v_scale, big.v_scale[pages - 64:])
+    del big
+    row = (1 << 31) + 64
+    buf = torch.empty(2 * row, dtype=torch.bfloat16, device="cuda")
+    apart = torch.as_strided(buf, (2, Hq + 2 * Hk, D), (row, D, 1))
+    apart.copy_(x[:2])
+    near = x[:2].contiguous()
+    results = []
+    for y in (near, apart):
+        cache = K.KVCache.empty(64, Hk, page, D, dev(table[:2]))
+        q_out = torch.as_strided(buf, (2, Hq, D), (row, D, 1), 16 * D) if y is apart else None
+        q, k = K.kda_qk_norm_rope(y[:, :Hq], y[:, Hq:Hq + Hk], pos[:2], rope, q_out=q_out)
+        K.kda_kv_write(y[:, Hq:Hq + Hk], y[:, Hq + Hk:], i64([0, 1, 2]), i64([1, 1]), cache)
+        results.append([q.clone(), k, cache.k, cache.v_scale, K.kda_attn(q, i64([0, 1, 2]), i64([1, 1]), cache)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
