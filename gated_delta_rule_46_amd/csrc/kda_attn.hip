@@ -12,7 +12,10 @@
 // Products on the matrix cores.  A code times its page's power-of-two scale is
 // exact in bf16, so K and V enter as the values they stand for; bf16 queries
 // are exact as well, and the only rounding of operands is that of the
-// probabilities to bf16 (at most 2^-8 of each, to either side).
+// probabilities to bf16 (at most 2^-8 of each, to either side; outputs, 0.0017 off the
+// exact ones by their own rounding, are 0.0018 off for one token over 257 keys and 0.0020
+// to 0.0021 for prompts, relative in the 2-norm, where a second term would cost half as
+// many matrix products again).
 // With fp32 rows, queries and probabilities enter as three bf16 terms each
 // (8 + 8 + 8 bits hold the 24 of fp32), three products instead of one.
 //

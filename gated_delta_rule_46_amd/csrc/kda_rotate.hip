@@ -14,8 +14,9 @@
 // sines are loaded once per lane.  All arithmetic in fp32, one rounding at the
 // store.  A head whose mean square leaves fp32's range (elements beyond about 2^63,
 // or tiny ones with an eps as small) is scaled by a power of two first, which costs
-// the others a comparison.  16,384 tokens at 32 / 8 heads of 128 with bf16 rows: 57 us (343 MB, 6.0
-// TB/s; a large copy 5.1); 64 tokens 4.5 us, the launch.
+// the others a comparison (57.2 -> 58.6 us below).  16,384 tokens at 32 / 8 heads of 128
+// with bf16 rows: 58.6 us (343 MB, 5.9 TB/s; a large copy 5.15), with fp32 rows 139 (4.9);
+// 64 tokens 4.7 us, the launch.
 
 #include "kda_attn.h"
 #include "kda_mfma.h"
