@@ -588,7 +588,7 @@ int kda_kv_read(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N
  *   o [T, num_q_heads, head_dim] (io_dtype, contiguous);
  *   lse [T, num_q_heads] fp32, NULL = not written.
  *   scale: any finite value (one nearer to zero than 2^-126 / log2(e) counts as
- *       that; 0 itself is exact); q.k is summed in fp32 and must not overflow.
+ *       that; 0 itself is exact); q.k and scale log2(e) q.k must be finite in fp32.
  * A row that sees no key gets o = 0 and lse = -inf (one whose scores are all
  * -inf, from infinities in q, too).  Keys and values that a row does not see
  * never reach it, NaN included.  The sums are normalised at the end: the

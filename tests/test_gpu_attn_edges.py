@@ -231,3 +231,14 @@ def test_attn_layer_offsets_beyond_32_bits(K):
         results.append([q.clone(), k, cache.k, cache.v_scale, K.kda_attn(q, i64([0, 1, 2]), i64([1, 1]), cache)])
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Gr,new,kv,width", [(40, [1, 1, 1], [77, 1, 30], 8), (100, [1, 2], [300, 65], 600), (200, [1], [90], 600),
+                                             (130, [3, 0, 1], [40, 9, 260], 20)])
+def test_attn_many_query_heads_per_kv_head(K, dtype, Gr, new, kv, width):
+    """A token's heads that fill several units: of 16, 32 and 128 rows, whole and in shares."""
+    say(f"attn group {Gr} {dtype} new={new} kv={kv} width={width}")
+    m, rng = G.plain_model(K, dtype, 2, 64, 16, kv, Gr, width=max(width, -(-max(kv) // 16)))
+    G.attn_check(K, m, dtype, G.queries(rng, sum(new), 2 * Gr, 64, dtype), G.cum(new), kv, 0.1, True, 0)
+    G.attn_check(K, m, dtype, G.queries(rng, sum(new), 2 * Gr, 64, dtype), G.cum(new), kv, 0.1, True, 33, name="window")

@@ -4,10 +4,11 @@ last sequence, show.  Tolerances as in test_gpu_attn.py."""
 import numpy as np
 import pytest
 
-import attn_plans as P
-import test_gpu_attn as G
-from test_gpu_attn import HALF, cum, dev, dt, i64, say, within
-from workloads.device import to_numpy_f64
+pytest.importorskip("gated_delta_rule_46_amd.kda", reason="libkda.so not built (run __graft_entry__.build())")
+import attn_plans as P  # noqa: E402
+import test_gpu_attn as G  # noqa: E402
+from test_gpu_attn import HALF, cum, dev, dt, i64, say, within  # noqa: E402
+from workloads.device import to_numpy_f64  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
