@@ -16,6 +16,7 @@
 #include "kda.h"
 #include "kda_attn.h"
 #include "kda_internal.h"
+#include "kda_lin.h"
 #include "kda_ops.h"
 
 namespace {
@@ -1080,6 +1081,177 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
     if (a.workers >= 0) e = kda::launch_attn(bf, cfg->head_dim, a, (hipStream_t)stream);
     if (e == hipSuccess && a.row_units) e = kda::launch_attn_rows(bf, cfg->head_dim, a, (hipStream_t)stream);
     return launched(e, "attention");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Linear-attention layers with one decay per head; the norm of the heads
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_lin_config(const kda_lin_config *cfg) {
+    if (!cfg) return fail(KDA_ERR_ARG, "cfg is NULL");
+    if (cfg->num_qk_heads <= 0 || cfg->num_v_heads <= 0)
+        return fail(KDA_ERR_ARG, "num_qk_heads and num_v_heads must be positive (got %d, %d)",
+                    cfg->num_qk_heads, cfg->num_v_heads);
+    if (cfg->num_v_heads % cfg->num_qk_heads != 0)
+        return fail(KDA_ERR_ARG, "num_v_heads must be a multiple of num_qk_heads (got %d, %d)",
+                    cfg->num_v_heads, cfg->num_qk_heads);
+    if (cfg->io_dtype != KDA_DTYPE_F32 && cfg->io_dtype != KDA_DTYPE_BF16)
+        return fail(KDA_ERR_ARG, "io_dtype must be KDA_DTYPE_F32 or KDA_DTYPE_BF16 (got %d)", cfg->io_dtype);
+    if (!kda::lin_supported(cfg->dk, cfg->dv))
+        return fail(KDA_ERR_UNSUPPORTED, "unsupported head dims dk=%d dv=%d", cfg->dk, cfg->dv);
+    if (cfg->num_v_heads > 65535)
+        return fail(KDA_ERR_UNSUPPORTED, "num_v_heads must be at most 65535 (got %d)", cfg->num_v_heads);
+    if (!std::isfinite(cfg->scale)) return fail(KDA_ERR_ARG, "scale must be finite");
+    return KDA_OK;
+}
+
+// Sizes that every launch of a call holds: 512 threads for each (sequence, head) pair and
+// for each 64 tokens of a head at most.
+int check_lin_sizes(const kda_lin_config *cfg, int32_t N, int64_t T) {
+    if (N < 0) return fail(KDA_ERR_ARG, "N must be >= 0 (got %d)", N);
+    if (T < 0) return fail(KDA_ERR_ARG, "T must be >= 0 (got %lld)", (long long)T);
+    if (T > (1 << 26) / cfg->num_v_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "T * num_v_heads must be at most 2^26 (got T = %lld)", (long long)T);
+    if (N > (1 << 20) / cfg->num_v_heads)
+        return fail(KDA_ERR_UNSUPPORTED, "N * num_v_heads must be at most 2^20 (got N = %d)", N);
+    if (T > 0 && N == 0) return fail(KDA_ERR_ARG, "T > 0 needs at least one sequence");
+    return KDA_OK;
+}
+
+// The distance between the tokens of a tensor of `width` elements a token.
+int check_distance(int32_t io_dtype, int64_t row, int64_t width, const char *name) {
+    if (row < width)
+        return fail(KDA_ERR_ARG, "%s must be at least %lld elements (got %lld)", name, (long long)width,
+                    (long long)row);
+    if (row * (io_dtype == KDA_DTYPE_BF16 ? 2 : 4) % 16 != 0)
+        return fail(KDA_ERR_ALIGN, "%s must be a multiple of 16 bytes (got %lld elements)", name, (long long)row);
+    return KDA_OK;
+}
+
+int check_lin_rows(const kda_lin_config *cfg, const void *q, int64_t q_row, const void *k, int64_t k_row,
+                   const void *v, int64_t v_row, const float *g, int64_t g_row, const void *o) {
+    KDA_TRY(check_distance(cfg->io_dtype, q_row, (int64_t)cfg->num_qk_heads * cfg->dk, "q_row"));
+    KDA_TRY(check_distance(cfg->io_dtype, k_row, (int64_t)cfg->num_qk_heads * cfg->dk, "k_row"));
+    KDA_TRY(check_distance(cfg->io_dtype, v_row, (int64_t)cfg->num_v_heads * cfg->dv, "v_row"));
+    if (g_row != 0 && g_row < cfg->num_v_heads)
+        return fail(KDA_ERR_ARG, "g_row must be 0 or at least %d (got %lld)", cfg->num_v_heads, (long long)g_row);
+    KDA_TRY(check_tensor(q, "q", true));
+    KDA_TRY(check_tensor(k, "k", true));
+    KDA_TRY(check_tensor(v, "v", true));
+    KDA_TRY(check_tensor(g, "g", true, 4));
+    KDA_TRY(check_tensor(o, "o", true));
+    if (o == q || o == k || o == v) return fail(KDA_ERR_ARG, "o must not alias q, k or v");
+    return KDA_OK;
+}
+
+int check_lin_pool(const kda_state_pool *pool, bool indices) {
+    if (pool->n_slots <= 0)
+        return fail(KDA_ERR_ARG, "pool->n_slots must be positive (got %lld)", (long long)pool->n_slots);
+    KDA_TRY(check_tensor(pool->states, "pool->states", true));
+    KDA_TRY(check_tensor(pool->read_idx, "pool->read_idx", indices, 4));
+    KDA_TRY(check_tensor(pool->write_idx, "pool->write_idx", indices, 4));
+    return KDA_OK;
+}
+
+kda::LinArgs lin_args(const kda_lin_config *cfg, const void *q, int64_t q_row, const void *k, int64_t k_row,
+                      const void *v, int64_t v_row, const float *g, int64_t g_row, int32_t N,
+                      const kda_state_pool *pool, void *o) {
+    kda::LinArgs a{};
+    a.q = q; a.k = k; a.v = v; a.q_row = q_row; a.k_row = k_row; a.v_row = v_row;
+    a.g = g; a.g_row = g_row; a.o = o; a.N = N;
+    a.Hk = cfg->num_qk_heads; a.Hv = cfg->num_v_heads; a.scale = cfg->scale;
+    if (pool) {
+        a.pool = pool->states; a.n_slots = pool->n_slots;
+        a.read_idx = pool->read_idx; a.write_idx = pool->write_idx;
+    }
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_lin_prefill_workspace(const kda_lin_config *cfg, int64_t T, int32_t N) {
+    if (check_lin_config(cfg) != KDA_OK || check_lin_sizes(cfg, N, T) != KDA_OK) return 0;
+    return 0;
+}
+
+int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, const void *k,
+                    int64_t k_row, const void *v, int64_t v_row, const float *g, int64_t g_row,
+                    const int64_t *cu_seqlens, int32_t N, int64_t T, const kda_state_pool *pool,
+                    void *o, const kda_ckpt *ckpt, void *ws, size_t ws_bytes, void *stream) {
+    (void)ws;
+    (void)ws_bytes;
+    KDA_TRY(check_lin_config(cfg));
+    KDA_TRY(check_lin_sizes(cfg, N, T));
+    if (pool) KDA_TRY(check_lin_pool(pool, false));
+    if (N == 0) return ok();
+    if (T > 0) KDA_TRY(check_lin_rows(cfg, q, q_row, k, k_row, v, v_row, g, g_row, o));
+    KDA_TRY(check_tensor(cu_seqlens, "cu_seqlens", true, 8));
+    if (ckpt) {
+        KDA_TRY(check_ckpt_interval(ckpt->interval));
+        KDA_TRY(check_tensor(ckpt->states, "ckpt->states", true));
+        KDA_TRY(check_tensor(ckpt->offsets, "ckpt->offsets", N > 1, 8));
+    }
+    kda::LinArgs a = lin_args(cfg, q, q_row, k, k_row, v, v_row, g, g_row, N, pool, o);
+    a.cu = cu_seqlens; a.T = T;
+    if (ckpt) {
+        a.interval = ckpt->interval; a.ckpt_off = ckpt->offsets; a.ckpt = ckpt->states;
+    }
+    return launched(kda::launch_lin(cfg->io_dtype == KDA_DTYPE_BF16, cfg->dk, cfg->dv, a, (hipStream_t)stream),
+                    "linear attention");
+}
+
+int kda_lin_decode(const kda_lin_config *cfg, int32_t N, const void *q, int64_t q_row,
+                   const void *k, int64_t k_row, const void *v, int64_t v_row, const float *g,
+                   int64_t g_row, const kda_state_pool *pool, void *o, void *stream) {
+    KDA_TRY(check_lin_config(cfg));
+    KDA_TRY(check_lin_sizes(cfg, N, 0));
+    if (!pool) return fail(KDA_ERR_ARG, "pool is NULL");
+    KDA_TRY(check_lin_pool(pool, N > 0));
+    if (N == 0) return ok();
+    KDA_TRY(check_lin_rows(cfg, q, q_row, k, k_row, v, v_row, g, g_row, o));
+    const kda::LinArgs a = lin_args(cfg, q, q_row, k, k_row, v, v_row, g, g_row, N, pool, o);
+    return launched(kda::launch_lin_step(cfg->io_dtype == KDA_DTYPE_BF16, cfg->dk, cfg->dv, a, (hipStream_t)stream),
+                    "linear attention step");
+}
+
+int kda_head_norm(int32_t io_dtype, int64_t T, int32_t H, int32_t D, const void *x, int64_t x_row,
+                  const void *gate, int64_t gate_row, const float *weight, const float *bias,
+                  int32_t per_head, float eps, int32_t center, int32_t act, void *y,
+                  int64_t y_row, void *stream) {
+    if (io_dtype != KDA_DTYPE_F32 && io_dtype != KDA_DTYPE_BF16)
+        return fail(KDA_ERR_ARG, "io_dtype must be KDA_DTYPE_F32 or KDA_DTYPE_BF16 (got %d)", io_dtype);
+    if (T < 0) return fail(KDA_ERR_ARG, "T must be >= 0 (got %lld)", (long long)T);
+    if (H <= 0) return fail(KDA_ERR_ARG, "H must be positive (got %d)", H);
+    if (D <= 0 || D % 8 != 0 || D > kda::kHeadNormMaxDim)
+        return fail(KDA_ERR_UNSUPPORTED, "D must be a multiple of 8, at most %d (got %d)", kda::kHeadNormMaxDim, D);
+    if (T > (1 << 26) / H)
+        return fail(KDA_ERR_UNSUPPORTED, "T * H must be at most 2^26 (got T = %lld)", (long long)T);
+    if (per_head != 0 && per_head != 1) return fail(KDA_ERR_ARG, "per_head must be 0 or 1 (got %d)", per_head);
+    if (center != 0 && center != 1) return fail(KDA_ERR_ARG, "center must be 0 or 1 (got %d)", center);
+    if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID)
+        return fail(KDA_ERR_ARG, "act must be KDA_ACT_NONE, KDA_ACT_SILU or KDA_ACT_SIGMOID (got %d)", act);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(KDA_ERR_ARG, "eps must be finite and >= 0");
+    KDA_TRY(check_distance(io_dtype, x_row, (int64_t)H * D, "x_row"));
+    if (gate) KDA_TRY(check_distance(io_dtype, gate_row, (int64_t)H * D, "gate_row"));
+    KDA_TRY(check_distance(io_dtype, y_row, (int64_t)H * D, "y_row"));
+    if (T == 0) return ok();
+    KDA_TRY(check_tensor(x, "x", true));
+    KDA_TRY(check_tensor(gate, "gate", false));
+    KDA_TRY(check_tensor(y, "y", true));
+    KDA_TRY(check_tensor(weight, "weight", false));
+    KDA_TRY(check_tensor(bias, "bias", false));
+    if ((y == x && y_row != x_row) || (y == gate && y_row != gate_row))
+        return fail(KDA_ERR_ARG, "an output in place of its input needs the same row distance");
+    kda::HeadNormArgs a{};
+    a.x = x; a.gate = gate; a.y = y; a.x_row = x_row; a.gate_row = gate_row; a.y_row = y_row;
+    a.weight = weight; a.bias = bias; a.T = T; a.H = H; a.D = D;
+    a.per_head = per_head; a.center = center; a.act = act; a.eps = eps;
+    return launched(kda::launch_head_norm(io_dtype == KDA_DTYPE_BF16, a, (hipStream_t)stream), "head norm");
 }
 
 }  // extern "C"

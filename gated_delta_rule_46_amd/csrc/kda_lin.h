@@ -1,0 +1,56 @@
+// kda_lin.h -- internal interfaces of the linear-attention layer (one decay per
+// head): prefill (kda_lin.hip), one-token step (kda_lin_step.hip) and the
+// norm of the heads (kda_headnorm.hip) with the C ABI (kda_api.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+struct LinArgs {
+    const void *q, *k, *v;       // rows of Hk heads of dk, Hk of dk, Hv of dv, io dtype
+    int64_t q_row, k_row, v_row; // distance between tokens, elements
+    const float *g;              // log decays: g[t * g_row + h] (g_row = 0: one per head)
+    int64_t g_row;
+    void *o;                     // [T,Hv,dv]
+    const int64_t *cu;           // [N+1]
+    int64_t T;
+    int32_t N, Hk, Hv;
+    float scale;
+    float *pool;                 // [n_slots,Hv,dk,dv] (nullable)
+    int64_t n_slots;
+    const int32_t *read_idx, *write_idx;   // [N] (nullable)
+    int32_t interval;            // checkpoint interval in tokens, 0 = none
+    const int64_t *ckpt_off;     // first rung row per sequence (nullable for N = 1)
+    float *ckpt;                 // rung rows
+};
+bool lin_supported(int dk, int dv);
+hipError_t launch_lin(bool bf16, int dk, int dv, const LinArgs &a, hipStream_t s);
+// one token per sequence: T and cu unused
+hipError_t launch_lin_step(bool bf16, int dk, int dv, const LinArgs &a, hipStream_t s);
+
+// Norm of every head with an activation.
+struct HeadNormArgs {
+    const void *x, *gate;        // rows of H heads of D, io dtype (gate nullable)
+    void *y;
+    int64_t x_row, gate_row, y_row;
+    const float *weight, *bias;  // [D], or [H,D] with per_head (nullable)
+    int64_t T;
+    int32_t H, D;
+    int32_t per_head, center, act;
+    float eps;
+};
+constexpr int kHeadNormMaxDim = 1024;
+hipError_t launch_head_norm(bool bf16, const HeadNormArgs &a, hipStream_t s);
+
+// Slot of the state pool that sequence n reads (writes); null if it has none.
+__device__ __forceinline__ float *slot_of(const LinArgs &a, const int32_t *idx, int n, int64_t state) {
+    if (!idx) return nullptr;
+    const int64_t i = idx[n];
+    return i >= 0 && i < a.n_slots ? a.pool + i * a.Hv * state : nullptr;
+}
+
+}  // namespace kda

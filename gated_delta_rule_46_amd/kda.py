@@ -26,11 +26,12 @@ EXPORTS = ("kda_prefill_workspace", "kda_prefill", "kda_prefill_noalloc", "kda_p
            "kda_output_fixup_ckpt", "kda_segment_package_fx", "kda_output_fixup_fx",
            "kda_checkpoint_write", "kda_decode", "kda_short_conv", "kda_conv_halo",
            "kda_qk_norm_rope", "kda_kv_write", "kda_kv_read", "kda_attn_workspace", "kda_attn",
+           "kda_lin_prefill_workspace", "kda_lin_prefill", "kda_lin_decode", "kda_head_norm",
            "kda_validate_inputs", "kda_status_string", "kda_last_error", "kda_version")
 # fields of kda_validate_inputs' report
 KDA_CHECK_FIELDS = 8
 CHECK_NAMES = ("bounds", "g_positive", "g_nonfinite", "g_block_floor", "beta_nonfinite")
-KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
+KDA_ACT_NONE, KDA_ACT_SILU, KDA_ACT_SIGMOID = 0, 1, 2
 KDA_ROPE_HALVES, KDA_ROPE_PAIRS = 0, 1
 
 
@@ -71,6 +72,11 @@ class kda_attn_config(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
 
 
+class kda_lin_config(ctypes.Structure):
+    _fields_ = [("num_qk_heads", ctypes.c_int32), ("num_v_heads", ctypes.c_int32), ("dk", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class kda_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page", ctypes.c_int32),
@@ -88,6 +94,7 @@ def _load():
     fxp = ctypes.POINTER(kda_fixop)
     convp = ctypes.POINTER(kda_conv_state)
     F32 = ctypes.c_float
+    lcfgp = ctypes.POINTER(kda_lin_config)
     acfgp, cachep = ctypes.POINTER(kda_attn_config), ctypes.POINTER(kda_kv_cache)
     sig = {
         "kda_prefill_workspace": (S, [cfgp, I64, I32]),
@@ -118,6 +125,12 @@ def _load():
         "kda_attn_workspace": (S, [acfgp, cachep, I32, I64, I32]),
         "kda_attn": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, I64, F32, I32, I32, P, P, P, S,
                                     P]),
+        "kda_lin_prefill_workspace": (S, [lcfgp, I64, I32]),
+        "kda_lin_prefill": (ctypes.c_int, [lcfgp, P, I64, P, I64, P, I64, P, I64, P, I32, I64, poolp, P,
+                                           ckp, P, S, P]),
+        "kda_lin_decode": (ctypes.c_int, [lcfgp, I32, P, I64, P, I64, P, I64, P, I64, poolp, P, P]),
+        "kda_head_norm": (ctypes.c_int, [I32, I64, I32, I32, P, I64, P, I64, P, P, I32, F32, I32, I32, P,
+                                         I64, P]),
         "kda_validate_inputs": (ctypes.c_int, [cfgp, I64, P, I32, I32, P, P, P, P]),
         "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "kda_last_error": (ctypes.c_char_p, []),
@@ -985,3 +998,187 @@ def kda_attn(q, cu_seqlens, kv_len, cache, *, scale=None, causal=True, window=0,
     if st:
         _check(st, "kda_attn")
     return (out, lse_out) if want_lse else out
+
+
+# ---------------------------------------------------------------------------
+# Linear-attention layers with one decay per head; the norm of the heads
+# (shapes are checked once for each combination, as above)
+# ---------------------------------------------------------------------------
+def _lin_inputs(q, k, v, g, scale):
+    """Checks the forms of a call's rows: (config, device, T, Hv, dk, dv, row distances)."""
+    dev = _on_device(q)
+    if len(q[0]) != 3 or len(v[0]) != 3:
+        raise ValueError("q and k are [T, Hk, dk], v is [T, Hv, dv]")
+    T, Hk, dk = q[0]
+    _, Hv, dv = v[0]
+    dtype = q[2]
+    rows = [_rows(q, "q", T, dk, dtype, dev), _rows(k, "k", T, dk, dtype, dev, Hk),
+            _rows(v, "v", T, dv, dtype, dev, Hv)]
+    if len(g[0]) == 1:
+        _dense(g, "g", (Hv,), torch.float32, dev)
+        rows.append(0)
+    else:
+        if g[0] != (T, Hv):
+            raise ValueError(f"g has shape {tuple(g[0])}, expected ({T}, {Hv}) or ({Hv},)")
+        if g[2] != torch.float32:
+            raise TypeError(f"g has dtype {g[2]}, expected {torch.float32}")
+        if g[3] != dev:
+            raise ValueError(f"g is on device {g[3]}, expected {dev}")
+        if g[1][1] != 1 and Hv > 1 and T > 0:
+            raise ValueError(f"g: the heads of a token must be contiguous (strides {g[1]})")
+        rows.append(g[1][0] if T > 1 else Hv)
+    cfg = ctypes.byref(kda_lin_config(Hk, Hv, dk, dv, _io_dtype(dtype), scale))
+    return cfg, dev, T, Hv, dk, dv, rows
+
+
+def _lin_pool(pool, read, write, N, Hv, dk, dv, dev):
+    """Checks the forms of a pool and its indices; returns the number of slots."""
+    if len(pool[0]) != 4:
+        raise ValueError("pool is [n_slots, Hv, dk, dv]")
+    _dense(pool, "pool", (pool[0][0], Hv, dk, dv), torch.float32, dev)
+    for f, name in ((read, "read_idx"), (write, "write_idx")):
+        if f is not None:
+            _dense(f, name, (N,), torch.int32, dev)
+    return pool[0][0]
+
+
+@functools.lru_cache(maxsize=1024)
+def _lin_prefill_plan(q, k, v, g, cu, pool, read, write, interval, offsets, ckpt, out, workspace, scale):
+    cfg, dev, T, Hv, dk, dv, rows = _lin_inputs(q, k, v, g, scale)
+    if len(cu[0]) != 1 or cu[0][0] < 1:
+        raise ValueError(f"cu_seqlens has shape {tuple(cu[0])}, expected (N + 1,)")
+    N = cu[0][0] - 1
+    _dense(cu, "cu_seqlens", (N + 1,), torch.int64, dev)
+    slots = 0
+    if pool is not None:
+        slots = _lin_pool(pool, read, write, N, Hv, dk, dv, dev)
+    elif read is not None or write is not None:
+        raise ValueError("read_idx / write_idx need a pool")
+    if interval:
+        if offsets is not None:
+            _dense(offsets, "ckpt_offsets", (N + 1,), torch.int64, dev)
+        elif N != 1:
+            raise ValueError("ckpt_offsets is required for more than one sequence")
+        if ckpt is not None:
+            _dense(ckpt, "ckpt_out", (ckpt[0][0], Hv, dk, dv), torch.float32, dev)
+    elif offsets is not None or ckpt is not None:
+        raise ValueError("ckpt_offsets / ckpt_out need ckpt_interval")
+    if out is not None:
+        _dense(out, "out", (T, Hv, dv), q[2], dev)
+    if workspace is not None:
+        _dense(workspace, "workspace", workspace[0], torch.uint8, dev)
+    wsb = LIB.kda_lin_prefill_workspace(cfg, T, N)
+    return cfg, dev, T, N, (Hv, dk, dv), rows, slots, wsb
+
+
+def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=None, *, ckpt_interval=0,
+                    ckpt_offsets=None, ckpt_out=None, scale=1.0, out=None, workspace=None, stream=None):
+    """Linear attention with one decay per head over packed sequences: q, k [T,Hk,dk], v [T,Hv,dv]
+    (bf16 or fp32; tokens may be apart), g fp32 log decays [T,Hv] (tokens may be apart) or [Hv] (for all
+    tokens), cu_seqlens int64 [N+1].  pool: fp32 [n_slots,Hv,dk,dv] states, read at read_idx and written
+    at write_idx (int32 [N]; None, or an index outside the pool: zeros, not stored).  Checkpoints as in
+    kda_prefill: ckpt_offsets int64 [N+1] (None for one sequence), ckpt_out the rungs' tensor (None: its
+    size is read from the last offset on the host).  workspace: a uint8 device tensor to use instead of one
+    of the queried size.  Returns (o [T,Hv,dv], checkpoint states or None).  stream: as
+    kda_qk_norm_rope."""
+    scale = float(scale)
+    cfg, dev, T, N, state, rows, slots, wsb = _lin_prefill_plan(
+        _form(q), _form(k), _form(v), _form(g), _form(cu_seqlens), _form(pool), _form(read_idx),
+        _form(write_idx), bool(ckpt_interval), _form(ckpt_offsets), _form(ckpt_out), _form(out),
+        _form(workspace), scale)
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_lin_prefill(q, k, v, g, cu_seqlens, pool, read_idx, write_idx,
+                                   ckpt_interval=ckpt_interval, ckpt_offsets=ckpt_offsets,
+                                   ckpt_out=ckpt_out, scale=scale, out=out, workspace=workspace)
+    if out is None:
+        out = q.new_empty((T, state[0], state[2]))
+    ck = None
+    if ckpt_interval:
+        if ckpt_out is None:
+            n = T // ckpt_interval if ckpt_offsets is None else int(ckpt_offsets[-1].item())
+            ckpt_out = q.new_empty((max(n, 0), *state), dtype=torch.float32)
+        if ckpt_out.shape[0]:
+            ck = ctypes.byref(kda_ckpt(ckpt_interval, _ptr(ckpt_offsets), ckpt_out.data_ptr()))
+    pl = None if pool is None else ctypes.byref(kda_state_pool(pool.data_ptr(), slots, _ptr(read_idx), _ptr(write_idx)))
+    if workspace is None:
+        workspace = q.new_empty(wsb, dtype=torch.uint8) if wsb else None
+    else:
+        wsb = workspace.numel()
+    st = LIB.kda_lin_prefill(cfg, q.data_ptr(), rows[0], k.data_ptr(), rows[1], v.data_ptr(), rows[2],
+                             g.data_ptr(), rows[3], cu_seqlens.data_ptr(), N, T, pl, out.data_ptr(), ck,
+                             _ptr(workspace), wsb, _current_stream(dev))
+    if st:
+        _check(st, "kda_lin_prefill")
+    return out, ckpt_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _lin_decode_plan(q, k, v, g, pool, read, write, out, scale):
+    cfg, dev, N, Hv, dk, dv, rows = _lin_inputs(q, k, v, g, scale)
+    for f, name in ((pool, "pool"), (read, "read_idx"), (write, "write_idx")):
+        if f is None:
+            raise ValueError(f"{name} is required")
+    slots = _lin_pool(pool, read, write, N, Hv, dk, dv, dev)
+    if out is not None:
+        _dense(out, "out", (N, Hv, dv), q[2], dev)
+    return cfg, dev, N, (N, Hv, dv), rows, slots
+
+
+def kda_lin_decode(q, k, v, g, pool, read_idx, write_idx, *, scale=1.0, out=None, stream=None):
+    """One token of each of N sequences (row n of q, k [N,Hk,dk], v [N,Hv,dv], g [N,Hv] or [Hv]) through
+    linear attention with one decay per head.  pool: fp32 [n_slots,Hv,dk,dv] states, updated in place at
+    write_idx; read_idx / write_idx: int32 [N] (outside the pool: zero state / not stored).  Returns o
+    [N,Hv,dv].  stream: as kda_qk_norm_rope."""
+    scale = float(scale)
+    cfg, dev, N, shape, rows, slots = _lin_decode_plan(_form(q), _form(k), _form(v), _form(g), _form(pool),
+                                                       _form(read_idx), _form(write_idx), _form(out), scale)
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_lin_decode(q, k, v, g, pool, read_idx, write_idx, scale=scale, out=out)
+    if out is None:
+        out = q.new_empty(shape)
+    pl = kda_state_pool(pool.data_ptr(), slots, read_idx.data_ptr(), write_idx.data_ptr())
+    st = LIB.kda_lin_decode(cfg, N, q.data_ptr(), rows[0], k.data_ptr(), rows[1], v.data_ptr(), rows[2],
+                            g.data_ptr(), rows[3], ctypes.byref(pl), out.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st, "kda_lin_decode")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _head_norm_plan(x, gate, weight, bias, out):
+    dev = _on_device(x)
+    if len(x[0]) != 3:
+        raise ValueError("x is [T, H, D]")
+    T, H, D = x[0]
+    rows = [_rows(x, "x", T, D, x[2], dev, H)]
+    rows.append(0 if gate is None else _rows(gate, "gate", T, D, x[2], dev, H))
+    rows.append(H * D if out is None else _rows(out, "out", T, D, x[2], dev, H))
+    per_head = any(w is not None and len(w[0]) == 2 for w in (weight, bias))
+    for w, name in ((weight, "weight"), (bias, "bias")):
+        if w is not None:
+            _dense(w, name, (H, D) if per_head else (D,), torch.float32, dev)
+    return _io_dtype(x[2]), dev, T, H, D, rows, int(per_head)
+
+
+def kda_head_norm(x, gate=None, *, weight=None, bias=None, eps=1e-6, center=False, activation=KDA_ACT_SILU,
+                  out=None, stream=None):
+    """Norm of every head of x [T,H,D] (bf16 or fp32; RMS, or of mean and variance with center) times weight
+    plus bias (fp32 [D], both [H,D], or None), then times activation(gate) with a gate [T,H,D], or
+    through the activation without one.  x, gate and out may have tokens apart; out may be x or gate.
+    Returns y [T,H,D].  stream: as kda_qk_norm_rope."""
+    io, dev, T, H, D, rows, per_head = _head_norm_plan(_form(x), _form(gate), _form(weight), _form(bias),
+                                                       _form(out))
+    if stream is not None or dev != _current_device():
+        with _placed(dev, stream):
+            return kda_head_norm(x, gate, weight=weight, bias=bias, eps=eps, center=center,
+                                 activation=activation, out=out)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    st = LIB.kda_head_norm(io, T, H, D, x.data_ptr(), rows[0], _ptr(gate), rows[1], _ptr(weight), _ptr(bias),
+                           per_head, eps, int(center), activation, out.data_ptr(), rows[2],
+                           _current_stream(dev))
+    if st:
+        _check(st, "kda_head_norm")
+    return out

@@ -430,8 +430,9 @@ int kda_decode(const kda_config *cfg, int32_t N, const void *q, const void *k, c
 /* Short causal convolution over tokens                                      */
 /* ------------------------------------------------------------------------ */
 
-#define KDA_ACT_NONE 0
-#define KDA_ACT_SILU 1
+#define KDA_ACT_NONE    0
+#define KDA_ACT_SILU    1
+#define KDA_ACT_SIGMOID 2   /* kda_head_norm only */
 
 /*
  * Window slots of the short convolution: states [n_slots, width-1, channels]
@@ -606,6 +607,93 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
              const int64_t *cu_seqlens, const int64_t *kv_len, const void *q, int64_t q_row,
              float scale, int32_t causal, int32_t window, void *o, float *lse, void *ws,
              size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Linear-attention layers with one decay per head; the norm of the heads    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The recurrence of kda_prefill without the delta rule's erase, and with one
+ * decay for all key channels of a head:
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t
+ * for prompts, chunks of prompts and drafted tokens (kda_lin_prefill) and for
+ * single tokens (kda_lin_decode), on the same packed rows and pool of states
+ * as the delta-rule layers.  q and k are used as they are (kda_qk_norm_rope
+ * normalises and rotates them).
+ *
+ * Rows.  q and k have num_qk_heads heads of dk values, v and o num_v_heads
+ * heads of dv, in io_dtype; value head h reads query/key head
+ * h / (num_v_heads / num_qk_heads).  The heads of a token are contiguous; *_row
+ * is the distance between tokens in elements (at least the row itself, a multiple
+ * of 16 bytes), so q, k and v may be views of one projection's rows.  o is
+ * contiguous and no input.  dk, dv in {64, 128}.
+ * g: fp32 log decays, g[t * g_row + h], 4-byte aligned; g_row is 0 (one decay
+ * per head for all tokens) or at least num_v_heads.  g <= 0, -infinity among it
+ * (the state is dropped); values below -10^4 count as that.
+ * T * num_v_heads is at most 2^26 and N * num_v_heads at most 2^20 (larger calls
+ * are split by the caller).
+ *
+ * All sums are accumulated in fp32.  With bf16 rows the weights of a chunk's
+ * tokens and the state are rounded to bf16 as operands of the outputs' products;
+ * the state itself is formed from operands that keep 24 bits.  With fp32 rows
+ * every operand keeps its 24 bits.  An output depends on no later token, nor on
+ * another sequence, infinities and NaN included.
+ */
+typedef struct {
+    int32_t num_qk_heads, num_v_heads, dk, dv;
+    int32_t io_dtype;    /* KDA_DTYPE_F32 or KDA_DTYPE_BF16 (q, k, v, o) */
+    float scale;
+} kda_lin_config;
+
+/*
+ * N sequences packed along T by cu_seqlens as in kda_prefill; rows from
+ * cu_seqlens[N] on are padding, their outputs left as they are.
+ *   pool: the states before and after each sequence's tokens, as described at
+ *       kda_state_pool; here read_idx may be NULL (all start from zeros) and
+ *       write_idx too (none stored); pool = NULL: both.  A sequence without
+ *       tokens carries its state over.
+ *   ckpt: NULL, or checkpoints as described at kda_ckpt (positions count from
+ *       the sequence's first token of this call).
+ *   ws / ws_bytes: at least kda_lin_prefill_workspace() bytes (it can be 0), not
+ *       shared by calls that overlap; nothing in it needs to start at zero and
+ *       nothing is kept in it between calls.
+ * N = 0 is a no-op.
+ */
+size_t kda_lin_prefill_workspace(const kda_lin_config *cfg, int64_t T, int32_t N);
+int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, const void *k,
+                    int64_t k_row, const void *v, int64_t v_row, const float *g, int64_t g_row,
+                    const int64_t *cu_seqlens, int32_t N, int64_t T, const kda_state_pool *pool,
+                    void *o, const kda_ckpt *ckpt, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * One token of each of N sequences: row n of q, k, v, g and o.  pool as in
+ * kda_decode.  N = 0 is a no-op.  No workspace.  One launch.
+ */
+int kda_lin_decode(const kda_lin_config *cfg, int32_t N, const void *q, int64_t q_row,
+                   const void *k, int64_t k_row, const void *v, int64_t v_row, const float *g,
+                   int64_t g_row, const kda_state_pool *pool, void *o, void *stream);
+
+/*
+ * Norm of every head (a group of D channels of a token, channels last) with an
+ * activation, the step that closes a linear or a delta-rule layer:
+ *     y = (x - mean) / sqrt(var + eps) * weight + bias
+ *     y <- y * act(gate),  or act(y) with gate = NULL
+ *   center 1: mean and var of the head's D values (group norm);
+ *          0: mean = 0, var = mean(x^2) (RMS norm);
+ *   x, gate, y: rows of H heads of D values in io_dtype, the heads of a token
+ *       contiguous, *_row elements between tokens (at least H * D, a multiple of 16
+ *       bytes); y may be x or gate itself with the same distance;
+ *   weight, bias: fp32 [D], or [H,D] with per_head = 1; NULL = ones, zeros;
+ *   eps >= 0;  act: KDA_ACT_NONE, KDA_ACT_SILU or KDA_ACT_SIGMOID;
+ *   D a multiple of 8, at most 1024; T * H at most 2^26.
+ * fp32 arithmetic, one rounding at the store; the squares of any finite head
+ * neither overflow nor vanish (it is scaled by a power of two where they
+ * would).  T = 0 is a no-op.  No workspace.  One launch.
+ */
+int kda_head_norm(int32_t io_dtype, int64_t T, int32_t H, int32_t D, const void *x, int64_t x_row,
+                  const void *gate, int64_t gate_row, const float *weight, const float *bias,
+                  int32_t per_head, float eps, int32_t center, int32_t act, void *y,
+                  int64_t y_row, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */

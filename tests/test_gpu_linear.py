@@ -1,0 +1,499 @@
+"""GPU tests of the linear-attention layer's operators against the fp64 oracle (oracle/linear.py).
+
+Tolerances follow from the arithmetic and are elementwise.  B is the same recurrence with every input's
+magnitude: what the terms of an element sum to without their signs.
+  * states: the operands keep 24 bits and sums are fp32: each of n tokens adds at most 6 roundings of 2^-24 (decay,
+    weight, product, three terms' sums), so n 6 2^-24 B at the very most; as the roundings have no common sign, all
+    elements together (rel-L2) stay within 2^-24 (8 + 4 sqrt(n));
+  * outputs: fp32 sums as above over n tokens and dk channels; with bf16 rows half a step (2^-8) of the output, and of B
+    each for the weights and for the state as operands;
+  * norm: fp32 arithmetic, (D / 2 + 24) 2^-24 of the largest value that is subtracted or added on the way, and half a
+    step of the output.
+"""
+import sys
+
+import numpy as np
+import pytest
+
+import oracle.linear as R
+from workloads.device import to_numpy_f64
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+U = 2.0 ** -24
+
+
+def say(msg):
+    print(f"[gpu-case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def K():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import gated_delta_rule_46_amd.kda as kda
+    return kda
+
+
+def dt(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def dev(x, dtype=None):
+    import torch
+    t = torch.as_tensor(np.asarray(x)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def i64(x):
+    return dev(np.asarray(x, np.int64))
+
+
+def i32(x):
+    return dev(np.asarray(x, np.int32))
+
+
+def f32(x):
+    return dev(np.asarray(x, np.float32))
+
+
+def within(name, got, ref, tol):
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(got - ref) <= tol)
+        bad &= ~((np.isnan(got) & np.isnan(ref)) | (np.isinf(ref) & (got == ref)))
+        part = np.where(tol > 0, np.abs(got - ref) / np.where(tol > 0, tol, 1), 0.0)
+    worst = float(np.nanmax(np.where(np.isfinite(part), part, 0.0))) if got.size else 0.0
+    say(f"{name}: worst error / tolerance {worst:.3f}")
+    assert not bad.any(), f"{name}: {bad.sum()} of {bad.size} outside, first at {np.argwhere(bad)[0]}: " \
+        f"{got[tuple(np.argwhere(bad)[0])]} against {ref[tuple(np.argwhere(bad)[0])]}"
+
+
+def rel_l2(got, ref):
+    return float(np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30))
+
+
+class Call:
+    """Inputs of a prefill: packed rows as views of one projection, a pool with spare slots."""
+
+    def __init__(self, dtype, lens, Hk, Hv, dk, dv, gate, seed, slots=(), pad=0, spread=1.0):
+        self.dtype, self.lens, self.dims = dtype, lens, (Hk, Hv, dk, dv)
+        rng = np.random.default_rng(seed)
+        T = sum(lens) + pad
+        self.cu = np.concatenate([[0], np.cumsum(lens)])
+        a, b = Hk * dk, 2 * Hk * dk
+        row = dev(rng.normal(size=(T, b + Hv * dv)) * spread, dt(dtype))
+        self.q, self.k = row[:, :a].view(T, Hk, dk), row[:, a:b].view(T, Hk, dk)
+        self.v = row[:, b:].view(T, Hv, dv)
+        base = -2.0 ** -np.linspace(0.5, 8, Hv)
+        if gate == "head":
+            self.g = f32(base)
+        elif gate == "token":
+            self.g = f32(base * np.exp(1.5 * rng.normal(size=(T, Hv))))
+        else:                                            # strong: mostly forgetting, with quiet stretches
+            self.g = f32(np.where(rng.random((T, Hv)) < 0.4, -60.0 * rng.random((T, Hv)), -0.01 * rng.random((T, Hv))))
+        N = len(lens)
+        self.pool = f32(rng.normal(size=(2 * N + 2, Hv, dk, dv)))
+        order = rng.permutation(2 * N + 2)
+        self.read, self.write = order[:N].copy(), order[N:2 * N].copy()
+        for n, r, w in slots:
+            self.read[n], self.write[n] = r, w
+
+    def oracle(self, interval=0, scale=1.0, size=False):
+        f = (lambda x: np.abs(to_numpy_f64(x))) if size else to_numpy_f64
+        return R.prefill(f(self.q), f(self.k), f(self.v), to_numpy_f64(self.g), self.cu, f(self.pool), self.read,
+                         self.write, interval, abs(scale) if size else scale)
+
+    def check(self, K, interval=0, scale=0.3, **kw):
+        import torch
+        Hk, Hv, dk, dv = self.dims
+        ref = self.oracle(interval, scale)
+        top = self.oracle(interval, scale, size=True)
+        T = self.q.shape[0]
+        out = torch.full((T, Hv, dv), 7.0, dtype=dt(self.dtype), device="cuda")
+        if interval:
+            off = np.concatenate([[0], np.cumsum([n // interval for n in self.lens])])
+            kw.update(ckpt_interval=interval, ckpt_offsets=i64(off),
+                      ckpt_out=torch.full((off[-1] + 1, Hv, dk, dv), 7.0, device="cuda"))
+        o, rungs = K.kda_lin_prefill(self.q, self.k, self.v, self.g, i64(self.cu), self.pool, i32(self.read),
+                                     i32(self.write), scale=scale, out=out, **kw)
+        torch.cuda.synchronize()
+        o, pool = to_numpy_f64(o), to_numpy_f64(self.pool)
+        live = self.cu[-1]
+        assert (o[live:] == 7.0).all(), "a padded row was written"
+        n = max(max(self.lens), 1)
+        half = HALF[self.dtype]
+        ops = 2 * half if self.dtype == "bf16" else 0.0
+        within("o", o[:live], ref[0][:live], half * np.abs(ref[0][:live]) + (ops + (6 * n + dk + 8) * U) * top[0][:live] + 1e-37)
+        if live and np.isfinite(ref[0][:live]).all():
+            e = rel_l2(o[:live], ref[0][:live])
+            say(f"o rel-L2 {e:.2e}")
+            assert e <= (half if self.dtype == "bf16" else U * (12 + 4 * n ** 0.5))
+        touched = np.zeros(len(pool), bool)
+        touched[[w for w in self.write if 0 <= w < len(pool)]] = True
+        assert np.array_equal(pool[~touched], ref[1][~touched]), "a slot that is not written changed"
+        self.states("pool", pool[touched], ref[1][touched], top[1][touched], n)
+        if interval:
+            rungs = to_numpy_f64(rungs)
+            assert (rungs[-1] == 7.0).all(), "a rung behind the last was written"
+            self.states("rungs", rungs[:-1], ref[2], top[2], n)
+        return o
+
+    @staticmethod
+    def states(name, got, ref, top, n):
+        within(name, got, ref, (6 * n + 8) * U * top + 1e-37)
+        if got.size and np.isfinite(ref).all():
+            e = rel_l2(got, ref)
+            say(f"{name} rel-L2 {e:.2e}")
+            assert e <= U * (8 + 4 * n ** 0.5)
+
+
+DIMS = [(128, 128), (128, 64), (64, 128), (64, 64)]
+
+
+@pytest.mark.parametrize("gate", ["head", "token", "strong"])
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill(K, dtype, dk, dv, gate):
+    Call(dtype, [70, 1, 0, 33, 200, 64], 2, 4, dk, dv, gate, 11, pad=3).check(K)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_lengths(K, dtype, n):
+    Call(dtype, [n], 1, 2, 128, 128, "token", n).check(K)
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 7), (3, 3), (5, 10)])
+def test_prefill_heads(K, Hk, Hv):
+    Call("bf16", [50, 90], Hk, Hv, 64, 64, "token", 3).check(K)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interval", [64, 128, 192])
+def test_prefill_rungs(K, dtype, interval):
+    Call(dtype, [200, 63, 64, 0, 257, 1], 1, 2, 64, 128, "head", 5).check(K, interval=interval)
+
+
+def test_prefill_slots(K):
+    """In place, forked from one prefix, from nothing, kept nowhere."""
+    c = Call("bf16", [20, 70, 3, 0, 5, 64, 0], 2, 2, 128, 64, "token", 6,
+             slots=[(0, 4, 4), (1, 9, 2), (2, 9, 3), (3, 9, 5), (4, -1, 6), (5, 10, -1), (6, 1 << 30, 11)])
+    c.check(K)
+
+
+def test_prefill_without_pool(K):
+    import torch
+    c = Call("bf16", [20, 70], 2, 2, 128, 64, "token", 7, slots=[(0, -1, -1), (1, -1, -1)])
+    a = c.check(K)
+    o, rungs = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), scale=0.3)
+    assert rungs is None and np.array_equal(to_numpy_f64(o), a)
+    o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, None, i32([0, 1]), scale=0.3)
+    assert np.array_equal(to_numpy_f64(o), a)
+    before = c.pool.clone()
+    o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32([-1, 99]), None, scale=0.3)
+    assert np.array_equal(to_numpy_f64(o), a) and torch.equal(before, c.pool)
+
+
+def test_prefill_empty_calls(K):
+    import torch
+    c = Call("bf16", [0, 0], 2, 2, 128, 64, "token", 8)
+    c.check(K)
+    o, rungs = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64([0]), c.pool, i32([]), i32([]))
+    assert o.shape == (0, 2, 64) and rungs is None
+    torch.cuda.synchronize()
+
+
+def test_prefill_decay_layouts(K):
+    """One decay per head as [Hv], as an expanded [T,Hv] and as a view of a wider tensor."""
+    import torch
+    c = Call("bf16", [70, 33], 2, 4, 64, 64, "head", 9)
+    a = c.check(K)
+    for g in (c.g.expand(103, 4), c.g.expand(103, 4).contiguous(), torch.cat([c.g, c.g]).repeat(103, 1)[:, 4:]):
+        o, _ = K.kda_lin_prefill(c.q, c.k, c.v, g, i64(c.cu), Call("bf16", [70, 33], 2, 4, 64, 64, "head", 9).pool,
+                                 i32(c.read), i32(c.write), scale=0.3)
+        assert np.array_equal(to_numpy_f64(o), a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_dropped_states(K, dtype):
+    """Decays of -inf and of any size; what follows them keeps its precision."""
+    c = Call(dtype, [130, 64, 40], 1, 2, 64, 64, "token", 10)
+    g = to_numpy_f64(c.g)
+    g[5], g[70], g[130], g[131], g[194 + 39] = -np.inf, -3e38, -np.inf, -2e4, -np.inf
+    g[20:40] = -150.0
+    c.g = f32(g)
+    c.check(K)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["q", "k", "v", "g"])
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_prefill_reaches_no_earlier_output(K, dtype, what, value):
+    """A value that is not finite changes no earlier output, no other head and no other sequence."""
+    import torch
+    if what == "g" and value == -np.inf:
+        pytest.skip("a dropped state, tested above")
+    a, b = (Call(dtype, [40, 100, 70], 2, 2, 64, 64, "token", 12) for _ in "ab")
+    t, h = 40 + 77, 1
+    x = getattr(b, what)
+    if what == "g":
+        x[t, h] = value
+    else:
+        x[t, h, 5] = value
+    outs = []
+    for c in (a, b):
+        o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write))
+        torch.cuda.synchronize()
+        outs.append((to_numpy_f64(o), to_numpy_f64(c.pool)))
+    (o, pool), (o2, pool2) = outs
+    same = np.ones(o.shape[:2], bool)
+    same[t:140, h] = False
+    assert np.array_equal(o[same], o2[same])
+    slot = int(a.write[1])
+    pool[slot, h] = pool2[slot, h] = 0
+    assert np.array_equal(pool, pool2)
+    assert not np.isfinite(o2[t, h]).all()
+    if what == "q":
+        assert np.array_equal(o[t + 1:, h], o2[t + 1:, h])
+    if what == "v":                                      # one column only
+        keep = np.arange(64) != 5
+        assert np.array_equal(o[:, :, keep], o2[:, :, keep])
+
+
+def test_prefill_infinite_values_stay_infinite(K):
+    """An infinite value enters the state as k times infinity (all of its terms)."""
+    import torch
+    c = Call("bf16", [70], 1, 1, 64, 64, "head", 13)
+    c.k.abs_().add_(0.1)
+    c.v[66, 0, 5] = np.inf
+    K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write))
+    torch.cuda.synchronize()
+    S = to_numpy_f64(c.pool)[int(c.write[0]), 0]
+    assert (S[:, 5] == np.inf).all() and np.isfinite(np.delete(S, 5, 1)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_resumed_equals_whole(K, dtype):
+    """A prompt in chunks of odd sizes, resumed through the pool, against the prompt at once."""
+    import torch
+    c = Call(dtype, [300], 2, 2, 128, 64, "token", 14, slots=[(0, -1, 0)])
+    whole = c.check(K)
+    S = to_numpy_f64(c.pool[0])
+    parts = []
+    for a, b in ((0, 1), (1, 64), (64, 190), (190, 300)):
+        o, _ = K.kda_lin_prefill(c.q[a:b], c.k[a:b], c.v[a:b], c.g[a:b], i64([0, b - a]), c.pool, i32([1 if a else -1]),
+                                 i32([1]), scale=0.3)
+        parts.append(to_numpy_f64(o))
+    torch.cuda.synchronize()
+    assert rel_l2(np.concatenate(parts), whole) <= 2 * HALF[dtype] * (1 if dtype == "bf16" else 80)
+    assert rel_l2(to_numpy_f64(c.pool[1]), S) <= U * 160
+
+
+@pytest.mark.parametrize("call", ["prefill", "decode", "norm"])
+def test_captured_calls_replay(K, call):
+    """Each replay of a captured call, between eager work, gives what the eager call gives on the same inputs."""
+    import torch
+    if call == "norm":
+        x, z = (dev(np.random.default_rng(s).normal(size=(40, 3, 64)), torch.bfloat16) for s in (1, 2))
+        ins, fn = [x, z], lambda: K.kda_head_norm(x, z)
+    else:
+        N = 3
+        c = Call("bf16", [90, 700, 5] if call == "prefill" else [1] * N, 2, 4, 128, 128, "token", 15)
+        ins, r, w, cu = [c.q, c.k, c.v, c.pool], i32(c.read), i32(c.write), i64(c.cu)
+        if call == "prefill":
+            fn = lambda: K.kda_lin_prefill(c.q, c.k, c.v, c.g, cu, c.pool, r, w)[0]
+        else:
+            fn = lambda: K.kda_lin_decode(c.q, c.k, c.v, c.g, c.pool, r, w)
+    fn()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fn()
+    for i in range(4):
+        for t in ins:
+            t.mul_(-0.7).add_(0.01 * i)
+        ref = fn().clone()
+        torch.cuda.synchronize()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), f"replay {i}"
+
+
+def test_calls_on_another_stream(K):
+    """stream=: the call runs, and allocates, on the stream given."""
+    import torch
+    c = Call("bf16", [90, 33], 2, 4, 128, 64, "token", 16)
+    a, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    b, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), stream=s)
+    y = K.kda_head_norm(b, stream=s)
+    s.synchronize()
+    assert torch.equal(a, b) and torch.equal(y, K.kda_head_norm(a))
+
+
+# ---------------------------------------------------------------------------
+# one token
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("gate", ["head", "token", "strong"])
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode(K, dtype, dk, dv, gate):
+    import torch
+    N, Hk, Hv = 7, 2, 6
+    c = Call(dtype, [1] * N, Hk, Hv, dk, dv, gate, 21,
+             slots=[(0, 3, 3), (1, 8, 2), (2, 8, 4), (3, -1, 5), (4, 9, -1), (5, 99, 6), (6, 10, 1 << 30)])
+    ref, top = c.oracle(scale=0.3), c.oracle(scale=0.3, size=True)
+    o = K.kda_lin_decode(c.q, c.k, c.v, c.g, c.pool, i32(c.read), i32(c.write), scale=0.3)
+    torch.cuda.synchronize()
+    within("o", to_numpy_f64(o), ref[0], HALF[dtype] * np.abs(ref[0]) + (dk + 12) * U * top[0])
+    within("pool", to_numpy_f64(c.pool), ref[1], 8 * U * top[1])
+
+
+def test_decode_no_sequences(K):
+    c = Call("bf16", [1], 2, 2, 64, 64, "head", 22)
+    z = c.q[:0]
+    assert K.kda_lin_decode(z, z, z, c.g, c.pool, i32([]), i32([])).shape == (0, 2, 64)
+
+
+# ---------------------------------------------------------------------------
+# norm of the heads
+# ---------------------------------------------------------------------------
+def norm_check(K, dtype, T, H, D, center, gate, act, per_head, seed, factor=1.0, eps=1e-6, shift=0.3, weights=True,
+               in_place=None):
+    import torch
+    rng = np.random.default_rng(seed)
+    row = dev((rng.normal(size=(T, H, D)) + shift) * factor, dt(dtype))
+    wide = dev(rng.normal(size=(T, 3 * H, D)) * 3, dt(dtype))
+    x = row
+    z = wide[:, H:2 * H] if gate else None
+    shape = (H, D) if per_head else (D,)
+    w = f32(1 + 0.3 * rng.normal(size=shape)) if weights else None
+    b = f32(0.5 * rng.normal(size=shape)) if weights and center else None
+    f = lambda t: None if t is None else to_numpy_f64(t)
+    ref, inner = R.head_norm(f(x), f(z), f(w), f(b), eps, center, act)
+    rest = wide.clone()
+    out = {None: torch.full_like(x, 7.0), "x": x, "gate": z}[in_place]
+    X = f(x)
+    y = K.kda_head_norm(x, z, weight=w, bias=b, eps=eps, center=center, activation=act, out=out)
+    torch.cuda.synchronize()
+    assert y is out
+    if in_place == "gate":
+        rest[:, H:2 * H] = wide[:, H:2 * H]
+    assert torch.equal(rest, wide)
+    # error before the activation: of the centered value (the mean's rounding is of the size of the largest x), the
+    # scale and the affine map; the activation's slope is at most 1.1, its own roundings 8 steps
+    sc = 1 / np.sqrt(((X - (X.mean(-1, keepdims=True) if center else 0)) ** 2).mean(-1, keepdims=True) + eps)
+    big = np.abs(X).max(-1, keepdims=True) * sc * (1 if w is None else np.abs(f(w)))
+    e = (D / 2 + 24) * U * (np.abs(inner) + (big if center else 0) + (0 if b is None else np.abs(f(b))))
+    if gate:
+        tol = e * np.abs(R.activation(f(z), act)) + 8 * U * np.abs(ref)
+    else:
+        tol = 1.1 * e + 8 * U * (np.abs(ref) + np.abs(inner))
+    within("y", f(y), ref, HALF[dtype] * np.abs(ref) + tol + 1e-37)
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 40, 64, 128, 200, 256, 264, 512, 520, 1016, 1024])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_widths(K, dtype, D):
+    norm_check(K, dtype, 37, 3, D, False, True, 1, False, D)
+    norm_check(K, dtype, 5, 2, D, True, False, 1, True, D + 1)
+
+
+@pytest.mark.parametrize("act", [0, 1, 2])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("center", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_forms(K, dtype, center, gate, act):
+    norm_check(K, dtype, 21, 5, 128, center, gate, act, gate != center, 31)
+    norm_check(K, dtype, 1, 1, 64, center, gate, act, False, 32, weights=False)
+
+
+@pytest.mark.parametrize("e", [-126, -100, -75, -60, -20, 20, 60, 63, 64, 90, 110, 120])
+@pytest.mark.parametrize("center", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_magnitudes(K, dtype, center, e):
+    """Heads whose squares or sums leave fp32's range, with an eps that vanishes or is their size."""
+    for eps in (0.0, min(2.0 ** (2 * e), 1e30) if e > -60 else 1e-30):
+        norm_check(K, dtype, 6, 2, 64, center, True, 1, False, 33, factor=2.0 ** e, eps=float(np.float32(eps)))
+
+
+def test_norm_far_mean(K):
+    """A mean far from zero: the variance comes from the centered values."""
+    norm_check(K, "f32", 9, 2, 128, True, False, 0, False, 34, shift=1000.0)
+
+
+@pytest.mark.parametrize("in_place", ["x", "gate"])
+def test_norm_in_place(K, in_place):
+    norm_check(K, "bf16", 40, 4, 128, False, True, 1, False, 35, in_place=in_place)
+
+
+def test_norm_extreme_gates(K):
+    """Sigmoid and SiLU far out, and at infinity."""
+    import torch
+    z = torch.tensor([0.0, -0.0, 88.0, 100.0, 3e38, np.inf, -88.0, -100.0], device="cuda").view(1, 1, 8)
+    x = torch.ones_like(z)
+    y = K.kda_head_norm(x, z, eps=0.0, activation=K.KDA_ACT_SIGMOID)
+    s = to_numpy_f64(y)[0, 0]
+    assert np.array_equal(s[:6], [0.5, 0.5, 1, 1, 1, 1]) and abs(s[6] / np.exp(-88.0) - 1) < 1e-5 and abs(s[7]) < 1e-37
+    y = to_numpy_f64(K.kda_head_norm(x, z, eps=0.0, activation=K.KDA_ACT_SILU))[0, 0]
+    assert np.array_equal(y[:6], [0, 0, 88, 100, np.float32(3e38), np.inf]) and abs(y[6] / (-88 * np.exp(-88.0)) - 1) < 1e-5
+
+
+def test_norm_not_finite_stays_in_its_head(K):
+    import torch
+    x = dev(np.random.default_rng(36).normal(size=(4, 3, 128)), torch.bfloat16)
+    a = K.kda_head_norm(x)
+    for value in (np.nan, np.inf):
+        y = x.clone()
+        y[2, 1, 7] = value
+        b = K.kda_head_norm(y)
+        keep = torch.ones(4, 3, dtype=torch.bool)
+        keep[2, 1] = False
+        assert torch.equal(a[keep], b[keep]) and torch.isnan(b[2, 1, 7])
+
+
+def test_norm_no_rows(K):
+    import torch
+    assert K.kda_head_norm(torch.empty((0, 3, 64), device="cuda")).shape == (0, 3, 64)
+
+
+# ---------------------------------------------------------------------------
+# the layer
+# ---------------------------------------------------------------------------
+def test_layer_prompts_then_tokens(K):
+    """Prompts, then tokens one by one, each with its gated norm, against the oracle over the whole sequences."""
+    import torch
+    lens, new, Hk, Hv, dk, dv = [130, 7, 64], 4, 2, 4, 128, 64
+    N = len(lens)
+    c = Call("bf16", [n + new for n in lens], Hk, Hv, dk, dv, "token", 41, slots=[(n, -1, n) for n in range(N)])
+    rng = np.random.default_rng(42)
+    z = dev(rng.normal(size=c.v.shape), torch.bfloat16)
+    w = f32(1 + 0.2 * rng.normal(size=dv))
+    ref = c.oracle(scale=dk ** -0.5)
+    top = c.oracle(scale=dk ** -0.5, size=True)
+    pick = [np.arange(a, a + n) for a, n in zip(c.cu, lens)]
+    at = i64(np.concatenate(pick))
+    slots = i32(range(N))
+    cu = i64(np.concatenate([[0], np.cumsum(lens)]))
+    got = torch.full(c.v.shape, np.nan, dtype=torch.float64, device="cuda")
+    y = got.clone()
+
+    def keep(o, at):
+        got[at] = o.double()
+        y[at] = K.kda_head_norm(o, z[at].contiguous(), weight=w, activation=K.KDA_ACT_SIGMOID).double()
+    o, _ = K.kda_lin_prefill(c.q[at], c.k[at], c.v[at], c.g[at], cu, c.pool, i32([-1] * N), slots, scale=dk ** -0.5)
+    keep(o, at)
+    for i in range(new):
+        at = i64([a + n + i for a, n in zip(c.cu, lens)])
+        keep(K.kda_lin_decode(c.q[at], c.k[at], c.v[at], c.g[at], c.pool, slots, slots, scale=dk ** -0.5), at)
+    torch.cuda.synchronize()
+    half = HALF["bf16"]
+    within("o", to_numpy_f64(got), ref[0], half * np.abs(ref[0]) + (2 * half + 1000 * U) * top[0])
+    assert rel_l2(to_numpy_f64(c.pool)[:N], ref[3]) <= U * 64
+    Y, _ = R.head_norm(to_numpy_f64(got), to_numpy_f64(z), to_numpy_f64(w), act=2)
+    within("y", to_numpy_f64(y), Y, half * np.abs(Y) + 200 * U * np.abs(Y) + 1e-37)
