@@ -1175,16 +1175,17 @@ kda::LinArgs lin_args(const kda_lin_config *cfg, const void *q, int64_t q_row, c
 extern "C" {
 
 size_t kda_lin_prefill_workspace(const kda_lin_config *cfg, int64_t T, int32_t N) {
-    if (check_lin_config(cfg) != KDA_OK || check_lin_sizes(cfg, N, T) != KDA_OK) return 0;
-    return 0;
+    if (check_lin_config(cfg) != KDA_OK || check_lin_sizes(cfg, N, T) != KDA_OK || N == 0) return 0;
+    kda::LinArgs a{};
+    a.N = N; a.T = T; a.Hv = cfg->num_v_heads;
+    kda::lin_plan(device_cus(), &a);
+    return round256(kda::lin_part_bytes(cfg->dk, cfg->dv, a));
 }
 
 int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, const void *k,
                     int64_t k_row, const void *v, int64_t v_row, const float *g, int64_t g_row,
                     const int64_t *cu_seqlens, int32_t N, int64_t T, const kda_state_pool *pool,
                     void *o, const kda_ckpt *ckpt, void *ws, size_t ws_bytes, void *stream) {
-    (void)ws;
-    (void)ws_bytes;
     KDA_TRY(check_lin_config(cfg));
     KDA_TRY(check_lin_sizes(cfg, N, T));
     if (pool) KDA_TRY(check_lin_pool(pool, false));
@@ -1200,6 +1201,15 @@ int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, con
     a.cu = cu_seqlens; a.T = T;
     if (ckpt) {
         a.interval = ckpt->interval; a.ckpt_off = ckpt->offsets; a.ckpt = ckpt->states;
+    }
+    kda::lin_plan(device_cus(), &a);
+    const size_t need = round256(kda::lin_part_bytes(cfg->dk, cfg->dv, a));
+    if (need) {
+        if (!ws || ws_bytes < need)
+            return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
+        KDA_TRY(check_tensor(ws, "ws", true));
+        a.part = (float *)ws;
+        a.kept = a.part + (size_t)a.slots * a.Hv * cfg->dk * cfg->dv;
     }
     return launched(kda::launch_lin(cfg->io_dtype == KDA_DTYPE_BF16, cfg->dk, cfg->dv, a, (hipStream_t)stream),
                     "linear attention");

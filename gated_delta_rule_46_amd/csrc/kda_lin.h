@@ -26,8 +26,17 @@ struct LinArgs {
     int32_t interval;            // checkpoint interval in tokens, 0 = none
     const int64_t *ckpt_off;     // first rung row per sequence (nullable for N = 1)
     float *ckpt;                 // rung rows
+    // Sequences longer than `seg` tokens in segments of so many (0: none is split).  Segment s of a
+    // sequence that starts at token c is unit n + c / seg + s, and finds its incoming state at slot
+    // 2 (c / seg) + s: no two units or split sequences meet, whatever the lengths are.
+    int32_t seg, units, slots;   // units: N + T / seg; slots: 2 (T / seg)
+    float *part;                 // [slots,Hv,dk,dv]
+    float *kept;                 // [slots,Hv] decay over the segment before
 };
 bool lin_supported(int dk, int dv);
+// The plan of a call on a device of `cus` compute units (seg, units, slots) and the bytes of part and kept.
+void lin_plan(int cus, LinArgs *a);
+size_t lin_part_bytes(int dk, int dv, const LinArgs &a);
 hipError_t launch_lin(bool bf16, int dk, int dv, const LinArgs &a, hipStream_t s);
 // one token per sequence: T and cu unused
 hipError_t launch_lin_step(bool bf16, int dk, int dv, const LinArgs &a, hipStream_t s);

@@ -11,15 +11,24 @@
 // overflows or needs a floor; G is summed in fp64 and kept as two floats, so that
 // a difference keeps its 24 bits behind a decay of any size.
 //
-// One workgroup takes a sequence and value head from its first chunk to its last;
-// a wave owns 16 of the value columns and keeps their part of S (dk x 16) in the
-// accumulators of the state product for the whole sequence.  As the rows of S that
-// a lane accumulates are chosen to be 8 consecutive ones of a 32-row block, the
-// registers are the operand of S^T q as they stand.  The tiles of P (C x C, its
-// lower triangle) are shared out over the waves and exchanged through LDS.
+// One workgroup takes a unit (a sequence, or a segment of a long one) and value head
+// from its first chunk to its last; a wave owns 16 of the value columns and keeps their
+// part of S (dk x 16) in the accumulators of the state product.  As the rows of S that a
+// lane accumulates are chosen to be 8 consecutive ones of a 32-row block, the registers are
+// the operand of S^T q as they stand.  The tiles of P (C x C, its lower triangle) are
+// shared out over the waves and exchanged through LDS.
 //
-// q, k and v of the next chunk but one are on their way from HBM into registers
-// while a chunk is computed, and the next chunk's lie in the other half of LDS.
+// Chunks are a pipeline with one barrier each.  Before it the waves form P of the chunk and
+// S^T q and put the next chunk's q, k, v (loaded into registers a chunk earlier) into
+// LDS; behind it they add P v and form the new state.  What is read on both sides
+// of the barrier (k, v, decays) has three buffers, q and P two.
+//
+// A long sequence is cut into segments where there are too few units for the card: a first
+// launch forms what each segment (but the last) adds to the state, from its end backwards
+// and only as far as its decays leave anything; a second one carries the states over the
+// segments; then all segments run as units of their own.
+
+#include <algorithm>
 
 #include "kda_attn.h"
 #include "kda_lin.h"
@@ -47,26 +56,33 @@ struct Shape {
     static constexpr int NW = DV / 16, THREADS = 64 * NW;
     static constexpr int NKB = DK / 32;
     static constexpr int TERMS = BF ? 3 : 1;        // operand terms that hold an fp32 value
-    static constexpr int SK = DK + O::PAD, SV = DV + O::PAD, SP = C + O::PAD;   // LDS rows
     static constexpr int E = 16 / sizeof(T);        // elements of a 16-byte piece
     static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
-    static constexpr int QB = C * SK * sizeof(T), VB = C * SV * sizeof(T), PB = C * SP * sizeof(T);
-    static constexpr int DECAYS = 4 * C + 4;        // floats: G high, G low, e^G, weights, e^G_C
-    static constexpr int STAGE = 2 * QB + VB + DECAYS * 4;
-    static constexpr int LDS = 2 * STAGE + PB;
+    static constexpr int KB = C * DK * sizeof(T), VB = C * DV * sizeof(T), PB = C * C * sizeof(T);
+    static constexpr int DB = (4 * C + 4) * sizeof(float);   // decays of a chunk
+    static constexpr int LDS = 5 * KB + 3 * VB + 2 * PB + 3 * DB;
+    static constexpr int LDS_STATES = 2 * (KB + VB + DB);    // of the launch that forms the segments' states
     static_assert(C * DK % (E * THREADS) == 0 && C * DV % (E * THREADS) == 0);
-    static_assert(LDS <= 160 * 1024 && QB % 16 == 0 && VB % 16 == 0 && STAGE % 16 == 0);
+    static_assert(LDS <= 160 * 1024);
 };
 
-// A chunk's tiles in LDS.
+// Element x of row r of an LDS tile of W columns.  Its 16-byte pieces are permuted by the row so
+// that neither 16 rows at one piece (operands along a row) nor 4 rows at 4 pieces (transposed
+// ones) meet in a bank.
+template <typename T, int W>
+__device__ __forceinline__ int at(int r, int x) {
+    constexpr int E = 16 / sizeof(T), PIECES = W / E;
+    const int f = PIECES == 8 ? ((r & 2) << 1 | ((r >> 2) & 3)) : sizeof(T) == 2 ? ((r & 3) << 2 | ((r >> 2) & 3)) : r & 15;
+    return r * W + ((x / E) ^ (PIECES == 4 ? f & 3 : f)) * E + x % E;
+}
+
+// A chunk's decays in LDS.
 template <class X>
-struct Stage {
-    typename X::T *q, *k, *v;
+struct Decays {
     float *hi, *lo, *out, *keep;      // G in log2 (two floats), scale e^G, e^{G_C - G}
     float *all;                       // e^{G_C}
-    __device__ explicit Stage(char *p)
-        : q((typename X::T *)p), k((typename X::T *)(p + X::QB)), v((typename X::T *)(p + 2 * X::QB)) {
-        hi = (float *)(p + 2 * X::QB + X::VB);
+    __device__ explicit Decays(char *p) {
+        hi = (float *)p;
         lo = hi + X::C;
         out = lo + X::C;
         keep = out + X::C;
@@ -74,23 +90,34 @@ struct Stage {
     }
 };
 
-// Transposed operand fragment from row-major LDS rows: lane (m, g) gets column col(m) of
-// rows 8g .. 8g+7.  bf16: p points at row 8g + (m / 4), 4 columns for m % 4 (a 16-lane group
-// loads 4 x 16 values and each lane gets one column of 4 rows); fp32: at row 8g, column col(m).
-template <class X>
-__device__ __forceinline__ typename X::O::F8 ld_t(const typename X::T *p, int stride) {
+// Transposed operand fragment from a row-major LDS tile of W columns: lane (m, g) gets
+// one column of rows r0 + 8 g .. + 7.  STEP 4: column x0 + m; STEP 8: column x0 + 8 (m / 4) + m % 4.
+// bf16: a 16-lane group loads 4 rows of 4 times 4 columns, and each lane gets one column of them.
+template <class X, int W, int STEP>
+__device__ __forceinline__ typename X::O::F8 ld_t(const typename X::T *tile, int r0, int x0) {
+    const int lane = threadIdx.x & 63, m = lane & 15, r = r0 + 8 * (lane >> 4);
     if constexpr (X::BF) {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s16x4 lds_t;
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)p);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)(p + 4 * stride));
+        const int x = x0 + STEP * (m & 3);
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)(tile + at<typename X::T, W>(r + (m >> 2), x)));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)(tile + at<typename X::T, W>(r + 4 + (m >> 2), x)));
         return X::O::cat(__builtin_bit_cast(bf16x4, a), __builtin_bit_cast(bf16x4, b));
     } else {
-        float x[8];
+        const int x = x0 + STEP * (m >> 2) + (m & 3);
+        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = p[e * stride];
-        return X::O::cvt8(x);
+        for (int e = 0; e < 8; ++e) y[e] = tile[at<typename X::T, W>(r + e, x)];
+        return X::O::cvt8(y);
     }
+}
+
+// Operand fragment along a row: elements x .. x + 7.
+template <class X, int W>
+__device__ __forceinline__ typename X::O::F8 ld_r(const typename X::T *tile, int r, int x) {
+    using T = typename X::T;
+    if constexpr (X::BF) return X::O::ld8(tile + at<T, W>(r, x));
+    else return X::O::ld44(tile + at<T, W>(r, x), tile + at<T, W>(r, x + 4));
 }
 
 template <class X> struct Terms { typename X::O::F8 t[X::TERMS]; };
@@ -135,17 +162,46 @@ __device__ __forceinline__ float exp2_of(double x) {
     return hi < -150.f ? 0.f : e + e * (lo * 0.6931471805599453f);
 }
 
-// The decays of a chunk from its log decays (lane = token; zero behind the end), by one wave.
+// Lane l - off of x in its row of 16 lanes, 0 before the row.
+template <int OFF>
+__device__ __forceinline__ double row_before(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, 0x110 | OFF, 0xF, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), 0x110 | OFF, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double x, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, l), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Log decays of a chunk's tokens (lane = token, zero behind the end) summed up to each, in log2.
 template <class X>
-__device__ __forceinline__ void write_decays(const Stage<X> &s, float g, float scale) {
+__device__ __forceinline__ double summed(float g, double *all) {
     const int lane = threadIdx.x & 63;
     double x = (double)(g < kLeastGate ? kLeastGate : g) * 1.4426950408889634;   // NaN stays
+    x += row_before<1>(x);
+    x += row_before<2>(x);
+    x += row_before<4>(x);
+    x += row_before<8>(x);
+    double sum = lane_of(x, 15);
 #pragma unroll
-    for (int off = 1; off < X::C; off <<= 1) {
-        const double y = __shfl_up(x, off);
-        if (lane >= off) x += y;
+    for (int row = 1; row < X::C / 16; ++row) {
+        if (lane >> 4 == row) x += sum;
+        sum = lane_of(x, 16 * row + 15);
     }
-    const double all = __shfl(x, X::C - 1);
+    *all = sum;
+    return x;
+}
+
+// The decays of a chunk, by one wave.
+template <class X>
+__device__ __forceinline__ void write_decays(char *p, float g, float scale) {
+    const int lane = threadIdx.x & 63;
+    const Decays<X> s(p);
+    double all;
+    const double x = summed<X>(g, &all);
     if (lane < X::C) {
         s.hi[lane] = (float)x;
         s.lo[lane] = (float)(x - (double)(float)x);
@@ -165,83 +221,154 @@ __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_
     return e + e * (((hi_i - (d - b)) + (-hi_j - b) + (lo_i - lo_j)) * 0.6931471805599453f);
 }
 
+// 16-byte pieces of a chunk's rows on their way from global memory to LDS; rows behind the
+// end are zeros.
+template <class X, int W>
+struct Rows {
+    using T = typename X::T;
+    static constexpr int PIECES = W / X::E, N = X::C * PIECES / X::THREADS;
+    u32x4 r[N];
+    __device__ __forceinline__ void fetch(const void *base, int64_t row, int64_t off, int valid) {   // base: first token
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = threadIdx.x + i * X::THREADS, t = p / PIECES, x = p % PIECES * X::E;
+            r[i] = u32x4{0, 0, 0, 0};
+            if (t < valid) r[i] = *(const u32x4 *)((const T *)base + t * row + off + x);
+        }
+    }
+    __device__ __forceinline__ void put(T *tile) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = threadIdx.x + i * X::THREADS;
+            *(u32x4 *)(tile + at<T, W>(p / PIECES, p % PIECES * X::E)) = r[i];
+        }
+    }
+};
+
+// A wave's 16 columns of the state: s[kb][hf][i] is row 32 kb + 8 gq + 4 hf + i of its lanes (m, gq).
+template <class X>
+struct State {
+    static constexpr int SIZE = X::DK * X::DV;
+    f32x4 s[X::NKB][2];
+    static __device__ __forceinline__ int first() {
+        const int lane = threadIdx.x & 63;
+        return 8 * (lane >> 4) * X::DV + 16 * (threadIdx.x >> 6) + (lane & 15);
+    }
+    __device__ __forceinline__ void load(const float *src) {   // null: zeros
+#pragma unroll
+        for (int kb = 0; kb < X::NKB; ++kb)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[kb][hf][i] = src ? src[first() + (32 * kb + 4 * hf + i) * X::DV] : 0.f;
+    }
+    __device__ __forceinline__ void store(float *dst) const {
+#pragma unroll
+        for (int kb = 0; kb < X::NKB; ++kb)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dst[first() + (32 * kb + 4 * hf + i) * X::DV] = s[kb][hf][i];
+    }
+    // s += k^T (weights v) for tokens 32 jb .. + 31; v as an operand, weights of the lane's tokens
+    __device__ __forceinline__ void add(const typename X::T *k, int jb, typename X::O::F8 v, const float *keep, int valid) {
+        const int gq = (threadIdx.x & 63) >> 4;
+        float x[8], wt[8];
+        X::O::unpack8(v, x);
+        mf::load8f(keep + 32 * jb + 8 * gq, wt);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 32 * jb + 8 * gq + e < valid ? x[e] * wt[e] : 0.f;
+        const Terms<X> wv = terms8<X>(x);
+#pragma unroll
+        for (int kb = 0; kb < X::NKB; ++kb)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const typename X::O::F8 kf = ld_t<X, X::DK, 8>(k, 32 * jb, 32 * kb + 4 * hf);
+#pragma unroll
+                for (int t = 0; t < X::TERMS; ++t) s[kb][hf] = X::O::mma32(s[kb][hf], kf, wv.t[t]);
+            }
+    }
+};
+
+// A sequence, and how it is cut.
+struct Seq {
+    int64_t c0;
+    int len, segs;
+    int first;        // c0 / seg
+    __device__ __forceinline__ Seq(const LinArgs &a, int n) {
+        c0 = min(max(a.cu[n], (int64_t)0), a.T);
+        const int64_t l = min(a.cu[n + 1], a.T) - c0;
+        len = l > 0 ? (int)l : 0;
+        segs = 1;
+        first = 0;
+        if (a.seg) {
+            first = (int)((uint32_t)c0 / (uint32_t)a.seg);
+            segs = max((int)(((uint32_t)len + a.seg - 1) / (uint32_t)a.seg), 1);
+        }
+    }
+};
+__device__ __forceinline__ int seg_of(const LinArgs &a, int n) {
+    return (int)((uint32_t)min(max(a.cu[n], (int64_t)0), a.T) / (uint32_t)a.seg);
+}
+
 template <int DK, int DV, bool BF>
 __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
     using O = typename X::O;
     using T = typename X::T;
     using F8 = typename O::F8;
-    constexpr int C = X::C, NT = X::NT, NJ = X::NJ, NKB = X::NKB, E = X::E;
+    constexpr int C = X::C, NT = X::NT, NJ = X::NJ, NKB = X::NKB;
     extern __shared__ __align__(16) char lds[];
-    T *const sp = (T *)(lds + 2 * X::STAGE);
+    T *const sq = (T *)lds, *const sk = (T *)(lds + 2 * X::KB), *const sv = (T *)(lds + 5 * X::KB);
+    T *const sp = (T *)(lds + 5 * X::KB + 3 * X::VB);
+    char *const sd = lds + 5 * X::KB + 3 * X::VB + 2 * X::PB;
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m = lane & 15, gq = lane >> 4;
-    const int n = blockIdx.x / a.Hv, h = blockIdx.x - n * a.Hv;
+    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
     const int hk = h / (a.Hv / a.Hk);
-    const int64_t c0 = max(a.cu[n], (int64_t)0);
-    const int64_t len64 = min(a.cu[n + 1], a.T) - c0;
-    const int len = len64 > 0 ? (int)len64 : 0;
-    constexpr int64_t state = (int64_t)DK * DV;
+    const int n = a.seg ? last_not_above(a.N, unit, [&](int i) { return (int64_t)i + seg_of(a, i); }) : unit;
+    const Seq seq(a, n);
+    const int seg = a.seg ? unit - n - seq.first : 0;
+    if (seg >= seq.segs) return;
+    const int skip = seg * a.seg;                        // tokens before the unit
+    const int len = seg + 1 < seq.segs ? a.seg : seq.len - skip;
+    const int64_t t0 = seq.c0 + skip;
 
-    // S[kb][half]: rows 32 kb + 8 gq + 4 half + i, column 16 w + m
-    const int s_at = 8 * gq * DV + 16 * w + m;
-    f32x4 S[NKB][2];
-    const float *src = slot_of(a, a.read_idx, n, state);
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[kb][hf][i] = src ? src[h * state + s_at + (32 * kb + 4 * hf + i) * DV] : 0.f;
+    State<X> S;
+    {
+        const float *src = seq.segs > 1 ? a.part + (int64_t)(2 * seq.first + seg) * a.Hv * S.SIZE
+                                        : slot_of(a, a.read_idx, n, S.SIZE);
+        S.load(src ? src + h * S.SIZE : nullptr);
+    }
 
-    u32x4 rq[X::NPK], rk[X::NPK], rv[X::NPV];
+    Rows<X, DK> rq, rk;
+    Rows<X, DV> rv;
     float rg = 0.f;
-    auto fetch = [&](int first) {                       // rows behind the end become zeros
+    auto fetch = [&](int first) {
         const int valid = min(C, len - first);
-        const int64_t t = c0 + first;
-        constexpr int PK = DK / E, PV = DV / E;
-#pragma unroll
-        for (int i = 0; i < X::NPK; ++i) {
-            const int p = tid + i * X::THREADS, row = p / PK, at = p % PK * E;
-            rq[i] = rk[i] = u32x4{0, 0, 0, 0};
-            if (row < valid) {
-                rq[i] = *(const u32x4 *)((const T *)a.q + (t + row) * a.q_row + hk * DK + at);
-                rk[i] = *(const u32x4 *)((const T *)a.k + (t + row) * a.k_row + hk * DK + at);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < X::NPV; ++i) {
-            const int p = tid + i * X::THREADS, row = p / PV, at = p % PV * E;
-            rv[i] = u32x4{0, 0, 0, 0};
-            if (row < valid) rv[i] = *(const u32x4 *)((const T *)a.v + (t + row) * a.v_row + (int64_t)h * DV + at);
-        }
+        const int64_t t = t0 + first;
+        rq.fetch((const T *)a.q + t * a.q_row, a.q_row, hk * DK, valid);
+        rk.fetch((const T *)a.k + t * a.k_row, a.k_row, hk * DK, valid);
+        rv.fetch((const T *)a.v + t * a.v_row, a.v_row, (int64_t)h * DV, valid);
         rg = 0.f;
-        if (w == X::NW - 1 && lane < valid) rg = a.g[(t + lane) * a.g_row + h];
+        if (first / C % X::NW == w && lane < valid) rg = a.g[(t + lane) * a.g_row + h];
     };
-    auto put = [&](const Stage<X> &s) {
-        constexpr int PK = DK / E, PV = DV / E;
-#pragma unroll
-        for (int i = 0; i < X::NPK; ++i) {
-            const int p = tid + i * X::THREADS, row = p / PK, at = p % PK * E;
-            *(u32x4 *)(s.q + row * X::SK + at) = rq[i];
-            *(u32x4 *)(s.k + row * X::SK + at) = rk[i];
-        }
-#pragma unroll
-        for (int i = 0; i < X::NPV; ++i) {
-            const int p = tid + i * X::THREADS, row = p / PV, at = p % PV * E;
-            *(u32x4 *)(s.v + row * X::SV + at) = rv[i];
-        }
-        if (w == X::NW - 1) write_decays<X>(s, rg, a.scale);
+    auto put = [&](int c) {
+        rq.put(sq + c % 2 * C * DK);
+        rk.put(sk + c % 3 * C * DK);
+        rv.put(sv + c % 3 * C * DV);
+        if (c % X::NW == w) write_decays<X>(sd + c % 3 * X::DB, rg, a.scale);
     };
 
     fetch(0);
-    put(Stage<X>(lds));
+    put(0);
     fetch(C);
     __syncthreads();
-    for (int first = 0, buf = 0; first < len; first += C, buf ^= 1) {
-        const Stage<X> s(lds + buf * X::STAGE);
+    for (int first = 0, c = 0; first < len; first += C, ++c) {
+        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 3 * C * DK, *const v = sv + c % 3 * C * DV;
+        T *const pt = sp + c % 2 * C * C;
+        const Decays<X> s(sd + c % 3 * X::DB);
         const int valid = min(C, len - first);
         const int nt = (valid + 15) >> 4;
 
@@ -249,8 +376,8 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         constexpr int TILES = NT * (NT + 1) / 2;
         for (int t = w; t < TILES + NJ; t += X::NW) {
             if (t >= TILES) {                           // the upper tile of a diagonal 32-block
-                const int it = 2 * (t - TILES);
-                O::st4(sp + (16 * it + m) * X::SP + 16 * it + 16 + 4 * gq, f32x4{0.f, 0.f, 0.f, 0.f});
+                const int i = 32 * (t - TILES) + m, j = 32 * (t - TILES) + 16 + 4 * gq;
+                O::st4(pt + at<T, C>(i, j), f32x4{0.f, 0.f, 0.f, 0.f});
                 continue;
             }
             const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jt = t - it * (it + 1) / 2;
@@ -259,14 +386,13 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb)
-                p = O::mma32(p, O::ld8(s.k + (16 * jt + m) * X::SK + 32 * kb + 8 * gq),
-                             O::ld8(s.q + i * X::SK + 32 * kb + 8 * gq));
+                p = O::mma32(p, ld_r<X, DK>(k, 16 * jt + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
             const f32x4 hj = *(const f32x4 *)(s.hi + j), lj = *(const f32x4 *)(s.lo + j);
             const float hi = s.hi[i], li = s.lo[i];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 p[r] = j + r <= i ? a.scale * decay_between<X>(hi, li, hj[r], lj[r]) * p[r] : 0.f;
-            O::st4(sp + i * X::SP + j, p);
+            O::st4(pt + at<T, C>(i, j), p);
         }
 
         // o^T = e^G S^T q^T: lane holds token 16 it + m, columns 16 w + 4 gq + r
@@ -275,10 +401,10 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         for (int it = 0; it < NT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
-            const F8 sf = O::cvt44(S[kb][0], S[kb][1]);
+            const F8 sf = O::cvt44(S.s[kb][0], S.s[kb][1]);
 #pragma unroll
             for (int it = 0; it < NT; ++it)
-                if (it < nt) acc[it] = O::mma32(acc[it], sf, O::ld8(s.q + (16 * it + m) * X::SK + 32 * kb + 8 * gq));
+                if (it < nt) acc[it] = O::mma32(acc[it], sf, ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq));
         }
 #pragma unroll
         for (int it = 0; it < NT; ++it) acc[it] *= s.out[16 * it + m];
@@ -288,14 +414,17 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         bool odd = false;
 #pragma unroll
         for (int jb = 0; jb < NJ; ++jb) {
-            if constexpr (BF) vf[jb] = ld_t<X>(s.v + (32 * jb + 8 * gq + (m >> 2)) * X::SV + 16 * w + 4 * (m & 3), X::SV);
-            else vf[jb] = ld_t<X>(s.v + (32 * jb + 8 * gq) * X::SV + 16 * w + m, X::SV);
+            vf[jb] = ld_t<X, DV, 4>(v, 32 * jb, 16 * w);
             float x[8];
             O::unpack8(vf[jb], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) odd |= not_finite(x[e]);
         }
-        __syncthreads();   // P is there
+        if (first + C < len) {
+            put(c + 1);
+            fetch(first + 2 * C);
+        }
+        __syncthreads();   // P and the next chunk are there
 
         // infinities and NaN must not meet the zeros of P above its diagonal: they are left out of
         // the products and added token by token
@@ -308,89 +437,177 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
             if (it < nt) {
 #pragma unroll
                 for (int jb = 0; jb < NJ; ++jb)
-                    if (2 * jb <= it) acc[it] = O::mma32(acc[it], vp[jb], O::ld8(sp + (16 * it + m) * X::SP + 32 * jb + 8 * gq));
+                    if (2 * jb <= it) acc[it] = O::mma32(acc[it], vp[jb], ld_r<X, C>(pt, 16 * it + m, 32 * jb + 8 * gq));
             }
         if (rare) {
             for (int j = 0; j < valid; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float x = (float)s.v[j * X::SV + 16 * w + 4 * gq + r];
+                    const float x = (float)v[at<T, DV>(j, 16 * w + 4 * gq + r)];
 #pragma unroll
                     for (int it = 0; it < NT; ++it)
-                        if (not_finite(x) && j <= 16 * it + m) acc[it][r] += (float)sp[(16 * it + m) * X::SP + j] * x;
+                        if (not_finite(x) && j <= 16 * it + m) acc[it][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
                 }
         }
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
             const int i = 16 * it + m;
-            if (i < valid)
-                O::st4((T *)a.o + ((c0 + first + i) * a.Hv + h) * DV + 16 * w + 4 * gq, acc[it]);
+            if (i < valid) O::st4((T *)a.o + ((t0 + first + i) * a.Hv + h) * DV + 16 * w + 4 * gq, acc[it]);
         }
 
         // S <- e^{G_C} S + k^T (weights v)
         const float all = *s.all;
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) { S[kb][0] *= all; S[kb][1] *= all; }
+        for (int kb = 0; kb < NKB; ++kb) { S.s[kb][0] *= all; S.s[kb][1] *= all; }
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) {
-            float x[8], wt[8];
-            O::unpack8(vf[jb], x);
-            mf::load8f(s.keep + 32 * jb + 8 * gq, wt);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 32 * jb + 8 * gq + e < valid ? x[e] * wt[e] : 0.f;
-            const Terms<X> wv = terms8<X>(x);
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    F8 kf;
-                    if constexpr (BF) kf = ld_t<X>(s.k + (32 * jb + 8 * gq + (m >> 2)) * X::SK + 32 * kb + 8 * (m & 3) + 4 * hf, X::SK);
-                    else kf = ld_t<X>(s.k + (32 * jb + 8 * gq) * X::SK + 32 * kb + 8 * (m >> 2) + (m & 3) + 4 * hf, X::SK);
-#pragma unroll
-                    for (int t = 0; t < X::TERMS; ++t) S[kb][hf] = O::mma32(S[kb][hf], kf, wv.t[t]);
-                }
-        }
+        for (int jb = 0; jb < NJ; ++jb) S.add(k, jb, vf[jb], s.keep, valid);
 
-        if (first + C < len) {
-            put(Stage<X>(lds + (buf ^ 1) * X::STAGE));
-            fetch(first + 2 * C);
-        }
         const int end = first + C;
-        if (a.interval && end <= len && end % a.interval == 0) {
-            float *dst = a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + end / a.interval - 1) * a.Hv + h) * state + s_at;
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dst[(32 * kb + 4 * hf + i) * DV] = S[kb][hf][i];
-        }
-        __syncthreads();
+        if (a.interval && end <= len && (skip + end) % a.interval == 0)
+            S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE);
     }
 
-    float *dst = slot_of(a, a.write_idx, n, state);
-    if (dst) {
-        dst += h * state + s_at;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dst[(32 * kb + 4 * hf + i) * DV] = S[kb][hf][i];
+    if (seg + 1 == seq.segs) {
+        float *dst = slot_of(a, a.write_idx, n, S.SIZE);
+        if (dst) S.store(dst + h * S.SIZE);
     }
+}
+
+// What a segment adds to the state, and its decay: at the slot of the segment behind it.
+// The weights count from the segment's end, so its chunks are walked backwards until
+// nothing is left of a token (weights below 2^-150 are zero).
+template <int DK, int DV, bool BF>
+__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_states_kernel(const LinArgs a) {
+    using X = Shape<DK, DV, BF>;
+    using T = typename X::T;
+    constexpr int C = X::C, NJ = X::NJ;
+    extern __shared__ __align__(16) char lds[];
+    __shared__ double s_rest[2];      // log2 decay behind the chunk
+    T *const sk = (T *)lds, *const sv = (T *)(lds + 2 * X::KB);
+    char *const sd = lds + 2 * (X::KB + X::VB);
+
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
+    const int hk = h / (a.Hv / a.Hk);
+    // only the last sequence that starts in or before the unit's stretch can have a segment here
+    const int n = last_not_above(a.N, unit, [&](int i) { return (int64_t)seg_of(a, i); });
+    const Seq seq(a, n);
+    const int seg = unit - seq.first;
+    if (seg < 0 || seg + 1 >= seq.segs) return;
+    const int64_t t0 = seq.c0 + (int64_t)seg * a.seg;
+
+    State<X> S;
+    S.load(nullptr);
+    Rows<X, DK> rk;
+    Rows<X, DV> rv;
+    float rg = 0.f;
+    const int chunks = a.seg / C;
+    auto fetch = [&](int c) {         // the c-th chunk from the end
+        if (c >= chunks) return;
+        const int64_t t = t0 + (int64_t)(chunks - 1 - c) * C;
+        rk.fetch((const T *)a.k + t * a.k_row, a.k_row, hk * DK, C);
+        rv.fetch((const T *)a.v + t * a.v_row, a.v_row, (int64_t)h * DV, C);
+        if (c % X::NW == w && lane < C) rg = a.g[(t + lane) * a.g_row + h];
+    };
+    auto put = [&](int c) {
+        rk.put(sk + c % 2 * C * DK);
+        rv.put(sv + c % 2 * C * DV);
+        if (c % X::NW == w) {
+            const Decays<X> s(sd + c % 2 * X::DB);
+            double all;
+            const double x = summed<X>(rg, &all);
+            const double rest = c ? s_rest[(c - 1) % 2] : 0.0;
+            if (lane < C) s.keep[lane] = exp2_of(rest + (all - x));
+            if (lane == 0) s_rest[c % 2] = rest + all;
+        }
+    };
+
+    fetch(0);
+    put(0);
+    fetch(1);
+    double rest = 0.0;
+    for (int c = 0; c < chunks; ++c) {
+        __syncthreads();
+        rest = s_rest[c % 2];
+        const bool more = c + 1 < chunks && !(rest < -150.0);
+        if (more) {
+            put(c + 1);
+            fetch(c + 2);
+        }
+        const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
+        const Decays<X> s(sd + c % 2 * X::DB);
+#pragma unroll
+        for (int jb = 0; jb < NJ; ++jb) S.add(k, jb, ld_t<X, DV, 4>(v, 32 * jb, 16 * w), s.keep, C);
+        if (!more) break;
+    }
+    const int64_t slot = (int64_t)(2 * seq.first + seg + 1) * a.Hv + h;
+    S.store(a.part + slot * S.SIZE);
+    if (threadIdx.x == 0) a.kept[slot] = exp2_of(rest);
+}
+
+// The incoming states of a split sequence's segments, in place of what each adds: four
+// elements a thread, one segment after the other.
+constexpr int kCarryThreads = 256;
+__global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs a, int size) {
+    const int blocks = size / (4 * kCarryThreads);
+    const int at = (blockIdx.x % blocks * kCarryThreads + threadIdx.x) * 4;
+    const int unit = blockIdx.x / blocks / a.Hv, h = blockIdx.x / blocks % a.Hv;
+    const int n = last_not_above(a.N, unit, [&](int i) { return (int64_t)seg_of(a, i); });
+    const Seq seq(a, n);
+    if (seq.first != unit || seq.segs < 2) return;
+    const float *src = slot_of(a, a.read_idx, n, size);
+    f32x4 S = {0.f, 0.f, 0.f, 0.f};
+    if (src) S = *(const f32x4 *)(src + (int64_t)h * size + at);
+    int64_t slot = (int64_t)2 * seq.first * a.Hv + h;
+    *(f32x4 *)(a.part + slot * size + at) = S;
+    for (int s = 1; s < seq.segs; ++s) {
+        slot += a.Hv;
+        f32x4 *p = (f32x4 *)(a.part + slot * size + at);
+        S = S * a.kept[slot] + *p;
+        *p = S;
+    }
+}
+
+template <typename K>
+hipError_t start(K *kernel, int64_t grid, int threads, int lds, const LinArgs &a, hipStream_t s) {
+    const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, s, a);
+    return hipGetLastError();
 }
 
 template <int DK, int DV, bool BF>
 hipError_t launch(const LinArgs &a, hipStream_t s) {
     using X = Shape<DK, DV, BF>;
-    const hipError_t e = hipFuncSetAttribute((const void *)lin_kernel<DK, DV, BF>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, X::LDS);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((lin_kernel<DK, DV, BF>), dim3((unsigned)(a.N * a.Hv)), dim3(X::THREADS), X::LDS, s, a);
-    return hipGetLastError();
+    if (a.seg) {
+        const int64_t stretches = a.T / a.seg;
+        hipError_t e = start(lin_states_kernel<DK, DV, BF>, stretches * a.Hv, X::THREADS, X::LDS_STATES, a, s);
+        if (e != hipSuccess) return e;
+        const int64_t grid = stretches * a.Hv * (DK * DV / (4 * kCarryThreads));
+        hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)grid), dim3(kCarryThreads), 0, s, a, DK * DV);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return start(lin_kernel<DK, DV, BF>, (int64_t)a.units * a.Hv, X::THREADS, X::LDS, a, s);
 }
 
+constexpr int kLeastSegment = 512;
+
 }  // namespace
+
+void lin_plan(int cus, LinArgs *a) {
+    a->seg = a->slots = 0;
+    a->units = a->N;
+    const int64_t per_head = std::max(cus / a->Hv, 1);
+    const int64_t seg = std::max<int64_t>(((a->T + per_head - 1) / per_head + 63) / 64 * 64, kLeastSegment);
+    if (a->T <= seg) return;          // no sequence can be longer
+    a->seg = (int32_t)seg;
+    a->units = (int32_t)(a->N + a->T / seg);
+    a->slots = (int32_t)(2 * (a->T / seg));
+}
+
+size_t lin_part_bytes(int dk, int dv, const LinArgs &a) {
+    return (size_t)a.slots * a.Hv * ((size_t)dk * dv + 1) * sizeof(float);
+}
 
 bool lin_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 

@@ -497,3 +497,72 @@ def test_layer_prompts_then_tokens(K):
     assert rel_l2(to_numpy_f64(c.pool)[:N], ref[3]) <= U * 64
     Y, _ = R.head_norm(to_numpy_f64(got), to_numpy_f64(z), to_numpy_f64(w), act=2)
     within("y", to_numpy_f64(y), Y, half * np.abs(Y) + 200 * U * np.abs(Y) + 1e-37)
+
+
+# ---------------------------------------------------------------------------
+# long sequences, cut into segments
+# ---------------------------------------------------------------------------
+def split_plan(Hv, T, N, dk=64, dv=64, Hk=1):
+    """Workspace bytes: more than none where sequences are cut."""
+    import ctypes
+    import gated_delta_rule_46_amd.kda as K
+    c = K.kda_lin_config(Hk, Hv, dk, dv, 1, 1.0)
+    return K.LIB.kda_lin_prefill_workspace(ctypes.byref(c), T, N)
+
+
+@pytest.mark.parametrize("gate", ["head", "token", "strong"])
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("bf16", 64, 64), ("f32", 64, 128), ("f32", 128, 64)])
+def test_split_prompt(K, dtype, dk, dv, gate):
+    """One prompt in several segments, the last one ragged; in place in its slot, with rungs on and off the cuts."""
+    assert split_plan(1, 1800, 1, dk, dv)
+    Call(dtype, [1800], 1, 1, dk, dv, gate, 51, slots=[(0, 2, 2)]).check(K, interval=320)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_split_among_short(K, dtype):
+    """Long and short sequences, empty ones and padding in one call, forked and in place."""
+    lens = [3, 700, 0, 512, 513, 0, 1, 1100, 64, 1024, 0]
+    assert split_plan(2, sum(lens) + 5, len(lens))
+    Call(dtype, lens, 1, 2, 64, 64, "token", 52, pad=5,
+         slots=[(1, 4, 4), (3, 9, 9), (4, 9, 10), (7, -1, 7), (9, 8, -1)]).check(K, interval=256)
+
+
+def test_split_heads(K):
+    Call("bf16", [1500, 20], 3, 6, 64, 128, "token", 53).check(K)
+
+
+def test_split_dropped_states(K):
+    """Decays that leave nothing of a segment's start: what is behind its last drop alone counts."""
+    c = Call("bf16", [2100], 1, 2, 64, 64, "head", 54)
+    g = np.broadcast_to(to_numpy_f64(c.g), (2100, 2)).copy()
+    g[900, 0], g[511, 1], g[512, 1], g[1023, 0], g[1300:1400, 1] = -np.inf, -np.inf, -1e30, -np.inf, -3.0
+    c.g = f32(g)
+    c.check(K)
+
+
+def test_split_workspace(K):
+    """A smaller workspace is refused; its content on entry does not matter; the cut does not change the result."""
+    import torch
+    need = split_plan(2, 1500, 1)
+    c = Call("bf16", [1500], 1, 2, 64, 64, "token", 55, slots=[(0, 0, 1)])
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    c.check(K, workspace=ws)
+    with pytest.raises(K.KdaError):
+        K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), workspace=ws[:need - 256])
+    whole = to_numpy_f64(c.pool[1])
+    for a, b in ((0, 500), (500, 1000), (1000, 1500)):
+        K.kda_lin_prefill(c.q[a:b], c.k[a:b], c.v[a:b], c.g[a:b], i64([0, b - a]), c.pool, i32([0 if a == 0 else 2]),
+                          i32([2]), scale=0.3)
+    torch.cuda.synchronize()
+    assert rel_l2(to_numpy_f64(c.pool[2]), whole) <= U * 160
+
+
+def test_split_not_finite(K):
+    """Values that are not finite in one segment leave the outputs of the earlier ones alone."""
+    import torch
+    a, b = (Call("bf16", [1500], 1, 2, 64, 64, "head", 56) for _ in "ab")
+    b.v[700, 1, 3] = np.nan
+    o, o2 = (to_numpy_f64(K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu))[0]) for c in (a, b))
+    torch.cuda.synchronize()
+    assert np.array_equal(o[:700], o2[:700]) and np.array_equal(o[:, 0], o2[:, 0])
+    assert np.isnan(o2[700:, 1, 3]).all() and np.array_equal(np.delete(o, 3, 2), np.delete(o2, 3, 2))
