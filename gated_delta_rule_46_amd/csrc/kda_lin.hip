@@ -120,29 +120,62 @@ __device__ __forceinline__ typename X::O::F8 ld_r(const typename X::T *tile, int
     else return X::O::ld44(tile + at<T, W>(r, x), tile + at<T, W>(r, x + 4));
 }
 
+__device__ __forceinline__ bool not_finite(float x) { return (f32_bits(x) & 0x7f800000u) == 0x7f800000u; }
+
+// Whether any of an operand's values is an infinity or a NaN.
+template <class X>
+__device__ __forceinline__ bool any_not_finite(const typename X::O::F8 *f, int n) {
+    if constexpr (X::BF) {
+        uint32_t r = 0;                // an exponent of all ones carries into the sign's place
+        for (int i = 0; i < n; ++i) {
+            const u32x4 u = __builtin_bit_cast(u32x4, f[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r |= (u[j] & 0x7f807f80u) + 0x00800080u;
+        }
+        return r & 0x80008000u;
+    } else {
+        bool r = false;
+        for (int i = 0; i < n; ++i) {
+            float x[8];
+            X::O::unpack8(f[i], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r |= not_finite(x[e]);
+        }
+        return r;
+    }
+}
+
 template <class X> struct Terms { typename X::O::F8 t[X::TERMS]; };
 
-// fp32 values as operand terms (an infinity is its first term alone).
+// fp32 values as operand terms.  bf16: three times the upper half of what is left, which holds all
+// 24 bits; an infinity would leave a NaN behind its first term (`rare`: it leaves nothing).
 template <class X>
-__device__ __forceinline__ Terms<X> terms8(const float *x) {
+__device__ __forceinline__ Terms<X> terms8(const float *x, bool rare) {
     Terms<X> r;
-    float y[8];
+    if constexpr (X::BF) {
+        float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = x[j];
+        for (int j = 0; j < 8; ++j) y[j] = x[j];
 #pragma unroll
-    for (int t = 0; t < X::TERMS; ++t) {
-        r.t[t] = X::O::cvt8(y);
-        if (t + 1 < X::TERMS) {
-            float z[8];
-            X::O::unpack8(r.t[t], z);
+        for (int t = 0; t < X::TERMS; ++t) {
+            u32x4 u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = (f32_bits(z[j]) & 0x7fffffffu) == 0x7f800000u ? 0.f : y[j] - z[j];
+            for (int j = 0; j < 4; ++j) u[j] = __builtin_amdgcn_perm(f32_bits(y[2 * j + 1]), f32_bits(y[2 * j]), 0x07060302u);
+            r.t[t] = __builtin_bit_cast(bf16x8, u);
+            if (t + 1 < X::TERMS) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] -= bits_f32(f32_bits(y[j]) & 0xffff0000u);
+                if (rare) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = t == 0 && not_finite(x[j]) ? 0.f : y[j];
+                }
+            }
         }
+    } else {
+        r.t[0] = X::O::cvt8(x);
     }
     return r;
 }
-
-__device__ __forceinline__ bool not_finite(float x) { return (f32_bits(x) & 0x7f800000u) == 0x7f800000u; }
 
 // The operand with zeros in place of infinities and NaN.
 template <class X>
@@ -221,26 +254,39 @@ __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_
     return e + e * (((hi_i - (d - b)) + (-hi_j - b) + (lo_i - lo_j)) * 0.6931471805599453f);
 }
 
-// 16-byte pieces of a chunk's rows on their way from global memory to LDS; rows behind the
-// end are zeros.
+// 16-byte pieces of a chunk's rows on their way from global memory to LDS.  A thread keeps its
+// first piece's address and moves it from chunk to chunk.
 template <class X, int W>
 struct Rows {
     using T = typename X::T;
-    static constexpr int PIECES = W / X::E, N = X::C * PIECES / X::THREADS;
+    static constexpr int PIECES = W / X::E, N = X::C * PIECES / X::THREADS, STEP = X::THREADS / PIECES;
+    static_assert(X::THREADS % PIECES == 0);
+    const T *p;
+    int64_t row;
     u32x4 r[N];
-    __device__ __forceinline__ void fetch(const void *base, int64_t row, int64_t off, int valid) {   // base: first token
+    __device__ __forceinline__ void start(const void *base, int64_t t, int64_t distance, int64_t off) {
+        row = distance;
+        p = (const T *)base + (t + threadIdx.x / PIECES) * row + off + threadIdx.x % PIECES * X::E;
+    }
+    // the chunk's first `valid` rows, zeros behind them; then on by `chunks` chunks
+    __device__ __forceinline__ void fetch(int valid, int chunks) {
+        if (valid >= X::C) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int p = threadIdx.x + i * X::THREADS, t = p / PIECES, x = p % PIECES * X::E;
-            r[i] = u32x4{0, 0, 0, 0};
-            if (t < valid) r[i] = *(const u32x4 *)((const T *)base + t * row + off + x);
+            for (int i = 0; i < N; ++i) r[i] = *(const u32x4 *)(p + i * STEP * row);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                r[i] = u32x4{0, 0, 0, 0};
+                if ((int)threadIdx.x / PIECES + i * STEP < valid) r[i] = *(const u32x4 *)(p + i * STEP * row);
+            }
         }
+        p += chunks * X::C * row;
     }
     __device__ __forceinline__ void put(T *tile) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int p = threadIdx.x + i * X::THREADS;
-            *(u32x4 *)(tile + at<T, W>(p / PIECES, p % PIECES * X::E)) = r[i];
+            const int q = threadIdx.x + i * X::THREADS;
+            *(u32x4 *)(tile + at<T, W>(q / PIECES, q % PIECES * X::E)) = r[i];
         }
     }
 };
@@ -271,14 +317,14 @@ struct State {
                 for (int i = 0; i < 4; ++i) dst[first() + (32 * kb + 4 * hf + i) * X::DV] = s[kb][hf][i];
     }
     // s += k^T (weights v) for tokens 32 jb .. + 31; v as an operand, weights of the lane's tokens
-    __device__ __forceinline__ void add(const typename X::T *k, int jb, typename X::O::F8 v, const float *keep, int valid) {
+    __device__ __forceinline__ void add(const typename X::T *k, int jb, typename X::O::F8 v, const float *keep, bool rare) {
         const int gq = (threadIdx.x & 63) >> 4;
         float x[8], wt[8];
         X::O::unpack8(v, x);
         mf::load8f(keep + 32 * jb + 8 * gq, wt);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 32 * jb + 8 * gq + e < valid ? x[e] * wt[e] : 0.f;
-        const Terms<X> wv = terms8<X>(x);
+        for (int e = 0; e < 8; ++e) x[e] *= wt[e];
+        const Terms<X> wv = terms8<X>(x, rare);
 #pragma unroll
         for (int kb = 0; kb < X::NKB; ++kb)
 #pragma unroll
@@ -344,15 +390,17 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
 
     Rows<X, DK> rq, rk;
     Rows<X, DV> rv;
+    rq.start(a.q, t0, a.q_row, hk * DK);
+    rk.start(a.k, t0, a.k_row, hk * DK);
+    rv.start(a.v, t0, a.v_row, (int64_t)h * DV);
     float rg = 0.f;
     auto fetch = [&](int first) {
-        const int valid = min(C, len - first);
-        const int64_t t = t0 + first;
-        rq.fetch((const T *)a.q + t * a.q_row, a.q_row, hk * DK, valid);
-        rk.fetch((const T *)a.k + t * a.k_row, a.k_row, hk * DK, valid);
-        rv.fetch((const T *)a.v + t * a.v_row, a.v_row, (int64_t)h * DV, valid);
+        const int valid = len - first;
+        rq.fetch(valid, 1);
+        rk.fetch(valid, 1);
+        rv.fetch(valid, 1);
         rg = 0.f;
-        if (first / C % X::NW == w && lane < valid) rg = a.g[(t + lane) * a.g_row + h];
+        if (first / C % X::NW == w && lane < min(valid, C)) rg = a.g[(t0 + first + lane) * a.g_row + h];
     };
     auto put = [&](int c) {
         rq.put(sq + c % 2 * C * DK);
@@ -361,6 +409,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         if (c % X::NW == w) write_decays<X>(sd + c % 3 * X::DB, rg, a.scale);
     };
 
+    T *out = (T *)a.o + ((t0 + m) * a.Hv + h) * DV + 16 * w + 4 * gq;
     fetch(0);
     put(0);
     fetch(C);
@@ -370,7 +419,6 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         T *const pt = sp + c % 2 * C * C;
         const Decays<X> s(sd + c % 3 * X::DB);
         const int valid = min(C, len - first);
-        const int nt = (valid + 15) >> 4;
 
         // P^T tiles (rows j, columns i): lane holds 4 consecutive j of its i
         constexpr int TILES = NT * (NT + 1) / 2;
@@ -381,7 +429,6 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
                 continue;
             }
             const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jt = t - it * (it + 1) / 2;
-            if (it >= nt) continue;
             const int i = 16 * it + m, j = 16 * jt + 4 * gq;
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -404,22 +451,16 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
             const F8 sf = O::cvt44(S.s[kb][0], S.s[kb][1]);
 #pragma unroll
             for (int it = 0; it < NT; ++it)
-                if (it < nt) acc[it] = O::mma32(acc[it], sf, ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq));
+                acc[it] = O::mma32(acc[it], sf, ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq));
         }
 #pragma unroll
         for (int it = 0; it < NT; ++it) acc[it] *= s.out[16 * it + m];
 
         // v^T of this wave's columns
         F8 vf[NJ];
-        bool odd = false;
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) {
-            vf[jb] = ld_t<X, DV, 4>(v, 32 * jb, 16 * w);
-            float x[8];
-            O::unpack8(vf[jb], x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd |= not_finite(x[e]);
-        }
+        for (int jb = 0; jb < NJ; ++jb) vf[jb] = ld_t<X, DV, 4>(v, 32 * jb, 16 * w);
+        const bool rare = __any(any_not_finite<X>(vf, NJ));
         if (first + C < len) {
             put(c + 1);
             fetch(first + 2 * C);
@@ -428,17 +469,18 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
 
         // infinities and NaN must not meet the zeros of P above its diagonal: they are left out of
         // the products and added token by token
-        const bool rare = __any(odd);
         F8 vp[NJ];
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) vp[jb] = rare ? finite_part<X>(vf[jb]) : vf[jb];
+        for (int jb = 0; jb < NJ; ++jb) vp[jb] = vf[jb];
+        if (rare) {
+#pragma unroll
+            for (int jb = 0; jb < NJ; ++jb) vp[jb] = finite_part<X>(vf[jb]);
+        }
 #pragma unroll
         for (int it = 0; it < NT; ++it)
-            if (it < nt) {
 #pragma unroll
-                for (int jb = 0; jb < NJ; ++jb)
-                    if (2 * jb <= it) acc[it] = O::mma32(acc[it], vp[jb], ld_r<X, C>(pt, 16 * it + m, 32 * jb + 8 * gq));
-            }
+            for (int jb = 0; jb < NJ; ++jb)
+                if (2 * jb <= it) acc[it] = O::mma32(acc[it], vp[jb], ld_r<X, C>(pt, 16 * it + m, 32 * jb + 8 * gq));
         if (rare) {
             for (int j = 0; j < valid; ++j)
 #pragma unroll
@@ -452,15 +494,16 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
             const int i = 16 * it + m;
-            if (i < valid) O::st4((T *)a.o + ((t0 + first + i) * a.Hv + h) * DV + 16 * w + 4 * gq, acc[it]);
+            if (i < valid) O::st4(out + 16 * it * a.Hv * DV, acc[it]);
         }
+        out += (int64_t)C * a.Hv * DV;
 
         // S <- e^{G_C} S + k^T (weights v)
         const float all = *s.all;
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) { S.s[kb][0] *= all; S.s[kb][1] *= all; }
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) S.add(k, jb, vf[jb], s.keep, valid);
+        for (int jb = 0; jb < NJ; ++jb) S.add(k, jb, vf[jb], s.keep, rare);
 
         const int end = first + C;
         if (a.interval && end <= len && (skip + end) % a.interval == 0)
@@ -498,16 +541,17 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_states_kerne
 
     State<X> S;
     S.load(nullptr);
+    const int chunks = a.seg / C;
     Rows<X, DK> rk;
     Rows<X, DV> rv;
+    rk.start(a.k, t0 + (int64_t)(chunks - 1) * C, a.k_row, hk * DK);
+    rv.start(a.v, t0 + (int64_t)(chunks - 1) * C, a.v_row, (int64_t)h * DV);
     float rg = 0.f;
-    const int chunks = a.seg / C;
     auto fetch = [&](int c) {         // the c-th chunk from the end
         if (c >= chunks) return;
-        const int64_t t = t0 + (int64_t)(chunks - 1 - c) * C;
-        rk.fetch((const T *)a.k + t * a.k_row, a.k_row, hk * DK, C);
-        rv.fetch((const T *)a.v + t * a.v_row, a.v_row, (int64_t)h * DV, C);
-        if (c % X::NW == w && lane < C) rg = a.g[(t + lane) * a.g_row + h];
+        rk.fetch(C, -1);
+        rv.fetch(C, -1);
+        if (c % X::NW == w && lane < C) rg = a.g[(t0 + (int64_t)(chunks - 1 - c) * C + lane) * a.g_row + h];
     };
     auto put = [&](int c) {
         rk.put(sk + c % 2 * C * DK);
@@ -537,7 +581,10 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_states_kerne
         const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
         const Decays<X> s(sd + c % 2 * X::DB);
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) S.add(k, jb, ld_t<X, DV, 4>(v, 32 * jb, 16 * w), s.keep, C);
+        for (int jb = 0; jb < NJ; ++jb) {
+            const typename X::O::F8 vf = ld_t<X, DV, 4>(v, 32 * jb, 16 * w);
+            S.add(k, jb, vf, s.keep, __any(any_not_finite<X>(&vf, 1)));
+        }
         if (!more) break;
     }
     const int64_t slot = (int64_t)(2 * seq.first + seg + 1) * a.Hv + h;
