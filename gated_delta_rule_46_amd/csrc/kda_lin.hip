@@ -51,9 +51,10 @@ struct Shape {
     static constexpr bool BF = BF_;
     using O = mf::Ops<BF>;
     using T = typename O::T;
-    static constexpr int C = BF ? 64 : 32;          // tokens per chunk
-    static constexpr int NT = C / 16, NJ = C / 32;  // tiles of 16 and blocks of 32 tokens
-    static constexpr int NW = DV / 16, THREADS = 64 * NW;
+    static constexpr int C = 32, NT = C / 16;       // tokens per chunk, tiles of 16
+    static constexpr int NW = BF ? 4 : DV / 16, THREADS = 64 * NW;
+    static constexpr int NB = DV / 16 / NW;         // column tiles of a wave
+    static_assert(NB == 1 || NB == 2);
     static constexpr int NKB = DK / 32;
     static constexpr int TERMS = BF ? 3 : 1;        // operand terms that hold an fp32 value
     static constexpr int E = 16 / sizeof(T);        // elements of a 16-byte piece
@@ -291,47 +292,68 @@ struct Rows {
     }
 };
 
-// A wave's 16 columns of the state: s[kb][hf][i] is row 32 kb + 8 gq + 4 hf + i of its lanes (m, gq).
+// A wave's columns of the state: s[b][kb][hf][i] is row 32 kb + 8 gq + 4 hf + i, column col(b), of
+// lane (m, gq).
 template <class X>
 struct State {
     static constexpr int SIZE = X::DK * X::DV;
-    f32x4 s[X::NKB][2];
+    // With two tiles a wave's columns alternate by 4, so that a lane of the transposed outputs
+    // holds 8 in a row.
+    static constexpr int STEP = 4 * X::NB;
+    f32x4 s[X::NB][X::NKB][2];
     static __device__ __forceinline__ int first() {
-        const int lane = threadIdx.x & 63;
-        return 8 * (lane >> 4) * X::DV + 16 * (threadIdx.x >> 6) + (lane & 15);
+        const int lane = threadIdx.x & 63, m = lane & 15;
+        return 8 * (lane >> 4) * X::DV + 16 * X::NB * (threadIdx.x >> 6) + STEP * (m >> 2) + (m & 3);
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {
+        const int at = first();
+#pragma unroll
+        for (int b = 0; b < X::NB; ++b)
+#pragma unroll
+            for (int kb = 0; kb < X::NKB; ++kb)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) f(s[b][kb][hf], at + (32 * kb + 4 * hf) * X::DV + 4 * b);
     }
     __device__ __forceinline__ void load(const float *src) {   // null: zeros
+        each([&](f32x4 &x, int at) {
 #pragma unroll
-        for (int kb = 0; kb < X::NKB; ++kb)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[kb][hf][i] = src ? src[first() + (32 * kb + 4 * hf + i) * X::DV] : 0.f;
+            for (int i = 0; i < 4; ++i) x[i] = src ? src[at + i * X::DV] : 0.f;
+        });
     }
-    __device__ __forceinline__ void store(float *dst) const {
+    __device__ __forceinline__ void store(float *dst) {
+        each([&](f32x4 &x, int at) {
 #pragma unroll
-        for (int kb = 0; kb < X::NKB; ++kb)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dst[first() + (32 * kb + 4 * hf + i) * X::DV] = s[kb][hf][i];
+            for (int i = 0; i < 4; ++i) dst[at + i * X::DV] = x[i];
+        });
     }
-    // s += k^T (weights v) for tokens 32 jb .. + 31; v as an operand, weights of the lane's tokens
-    __device__ __forceinline__ void add(const typename X::T *k, int jb, typename X::O::F8 v, const float *keep, bool rare) {
-        const int gq = (threadIdx.x & 63) >> 4;
-        float x[8], wt[8];
-        X::O::unpack8(v, x);
-        mf::load8f(keep + 32 * jb + 8 * gq, wt);
+    // v^T of the wave's columns
+    __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= wt[e];
-        const Terms<X> wv = terms8<X>(x, rare);
+        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
+    }
+    // s += k^T (weights v)
+    __device__ __forceinline__ void add(const typename X::T *k, const typename X::O::F8 *v, const float *keep, bool rare) {
+        float wt[8];
+        mf::load8f(keep + 8 * ((threadIdx.x & 63) >> 4), wt);
+        Terms<X> wv[X::NB];
+#pragma unroll
+        for (int b = 0; b < X::NB; ++b) {
+            float x[8];
+            X::O::unpack8(v[b], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= wt[e];
+            wv[b] = terms8<X>(x, rare);
+        }
 #pragma unroll
         for (int kb = 0; kb < X::NKB; ++kb)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const typename X::O::F8 kf = ld_t<X, X::DK, 8>(k, 32 * jb, 32 * kb + 4 * hf);
+                const typename X::O::F8 kf = ld_t<X, X::DK, 8>(k, 0, 32 * kb + 4 * hf);
 #pragma unroll
-                for (int t = 0; t < X::TERMS; ++t) s[kb][hf] = X::O::mma32(s[kb][hf], kf, wv.t[t]);
+                for (int t = 0; t < X::TERMS; ++t)
+#pragma unroll
+                    for (int b = 0; b < X::NB; ++b) s[b][kb][hf] = X::O::mma32(s[b][kb][hf], kf, wv[b].t[t]);
             }
     }
 };
@@ -358,12 +380,12 @@ __device__ __forceinline__ int seg_of(const LinArgs &a, int n) {
 }
 
 template <int DK, int DV, bool BF>
-__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const LinArgs a) {
+__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
     using O = typename X::O;
     using T = typename X::T;
     using F8 = typename O::F8;
-    constexpr int C = X::C, NT = X::NT, NJ = X::NJ, NKB = X::NKB;
+    constexpr int C = X::C, NT = X::NT, NB = X::NB, NKB = X::NKB;
     extern __shared__ __align__(16) char lds[];
     T *const sq = (T *)lds, *const sk = (T *)(lds + 2 * X::KB), *const sv = (T *)(lds + 5 * X::KB);
     T *const sp = (T *)(lds + 5 * X::KB + 3 * X::VB);
@@ -409,7 +431,8 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         if (c % X::NW == w) write_decays<X>(sd + c % 3 * X::DB, rg, a.scale);
     };
 
-    T *out = (T *)a.o + ((t0 + m) * a.Hv + h) * DV + 16 * w + 4 * gq;
+    const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
+    T *out = (T *)a.o + ((t0 + m) * a.Hv + h) * DV + col;
     fetch(0);
     put(0);
     fetch(C);
@@ -421,19 +444,16 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
         const int valid = min(C, len - first);
 
         // P^T tiles (rows j, columns i): lane holds 4 consecutive j of its i
-        constexpr int TILES = NT * (NT + 1) / 2;
-        for (int t = w; t < TILES + NJ; t += X::NW) {
-            if (t >= TILES) {                           // the upper tile of a diagonal 32-block
-                const int i = 32 * (t - TILES) + m, j = 32 * (t - TILES) + 16 + 4 * gq;
-                O::st4(pt + at<T, C>(i, j), f32x4{0.f, 0.f, 0.f, 0.f});
-                continue;
+        for (int t = w; t < 4; t += X::NW) {
+            const int i = 16 * (t > 0) + m, j = 16 * (t > 1) + 4 * gq;
+            if (t == 3) {                               // the upper one
+                O::st4(pt + at<T, C>(m, 16 + 4 * gq), f32x4{0.f, 0.f, 0.f, 0.f});
+                break;
             }
-            const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jt = t - it * (it + 1) / 2;
-            const int i = 16 * it + m, j = 16 * jt + 4 * gq;
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb)
-                p = O::mma32(p, ld_r<X, DK>(k, 16 * jt + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
+                p = O::mma32(p, ld_r<X, DK>(k, 16 * (t > 1) + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
             const f32x4 hj = *(const f32x4 *)(s.hi + j), lj = *(const f32x4 *)(s.lo + j);
             const float hi = s.hi[i], li = s.lo[i];
 #pragma unroll
@@ -442,25 +462,32 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
             O::st4(pt + at<T, C>(i, j), p);
         }
 
-        // o^T = e^G S^T q^T: lane holds token 16 it + m, columns 16 w + 4 gq + r
-        f32x4 acc[NT];
+        // o^T = e^G S^T q^T: lane holds token 16 it + m, four columns of each tile
+        f32x4 acc[NT][NB];
 #pragma unroll
-        for (int it = 0; it < NT; ++it) acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int it = 0; it < NT; ++it)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[it][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
-            const F8 sf = O::cvt44(S.s[kb][0], S.s[kb][1]);
+            F8 sf[NB];
 #pragma unroll
-            for (int it = 0; it < NT; ++it)
-                acc[it] = O::mma32(acc[it], sf, ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq));
+            for (int b = 0; b < NB; ++b) sf[b] = O::cvt44(S.s[b][kb][0], S.s[b][kb][1]);
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+                const F8 qf = ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], sf[b], qf);
+            }
         }
 #pragma unroll
-        for (int it = 0; it < NT; ++it) acc[it] *= s.out[16 * it + m];
-
-        // v^T of this wave's columns
-        F8 vf[NJ];
+        for (int it = 0; it < NT; ++it)
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) vf[jb] = ld_t<X, DV, 4>(v, 32 * jb, 16 * w);
-        const bool rare = __any(any_not_finite<X>(vf, NJ));
+            for (int b = 0; b < NB; ++b) acc[it][b] *= s.out[16 * it + m];
+
+        F8 vf[NB];
+        S.values(v, vf);
+        const bool rare = __any(any_not_finite<X>(vf, NB));
         if (first + C < len) {
             put(c + 1);
             fetch(first + 2 * C);
@@ -469,41 +496,44 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
 
         // infinities and NaN must not meet the zeros of P above its diagonal: they are left out of
         // the products and added token by token
-        F8 vp[NJ];
+        F8 vp[NB];
 #pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) vp[jb] = vf[jb];
+        for (int b = 0; b < NB; ++b) vp[b] = vf[b];
         if (rare) {
 #pragma unroll
-            for (int jb = 0; jb < NJ; ++jb) vp[jb] = finite_part<X>(vf[jb]);
-        }
-#pragma unroll
-        for (int it = 0; it < NT; ++it)
-#pragma unroll
-            for (int jb = 0; jb < NJ; ++jb)
-                if (2 * jb <= it) acc[it] = O::mma32(acc[it], vp[jb], ld_r<X, C>(pt, 16 * it + m, 32 * jb + 8 * gq));
-        if (rare) {
-            for (int j = 0; j < valid; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float x = (float)v[at<T, DV>(j, 16 * w + 4 * gq + r)];
-#pragma unroll
-                    for (int it = 0; it < NT; ++it)
-                        if (not_finite(x) && j <= 16 * it + m) acc[it][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
-                }
+            for (int b = 0; b < NB; ++b) vp[b] = finite_part<X>(vf[b]);
         }
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
-            const int i = 16 * it + m;
-            if (i < valid) O::st4(out + 16 * it * a.Hv * DV, acc[it]);
+            const F8 pf = ld_r<X, C>(pt, 16 * it + m, 8 * gq);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vp[b], pf);
         }
+        if (rare) {
+            for (int j = 0; j < valid; ++j)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = (float)v[at<T, DV>(j, col + 4 * b + r)];
+#pragma unroll
+                        for (int it = 0; it < NT; ++it)
+                            if (not_finite(x) && j <= 16 * it + m) acc[it][b][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
+                    }
+        }
+#pragma unroll
+        for (int it = 0; it < NT; ++it)
+            if (16 * it + m < valid) {
+                T *const dst = out + 16 * it * a.Hv * DV;
+                if constexpr (NB == 2) O::stf(dst, O::cvt44(acc[it][0], acc[it][1]));
+                else O::st4(dst, acc[it][0]);
+            }
         out += (int64_t)C * a.Hv * DV;
 
         // S <- e^{G_C} S + k^T (weights v)
         const float all = *s.all;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) { S.s[kb][0] *= all; S.s[kb][1] *= all; }
-#pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) S.add(k, jb, vf[jb], s.keep, rare);
+        S.each([&](f32x4 &x, int) { x *= all; });
+        S.add(k, vf, s.keep, rare);
 
         const int end = first + C;
         if (a.interval && end <= len && (skip + end) % a.interval == 0)
@@ -520,10 +550,10 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_kernel(const
 // The weights count from the segment's end, so its chunks are walked backwards until
 // nothing is left of a token (weights below 2^-150 are zero).
 template <int DK, int DV, bool BF>
-__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_states_kernel(const LinArgs a) {
+__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
     using T = typename X::T;
-    constexpr int C = X::C, NJ = X::NJ;
+    constexpr int C = X::C;
     extern __shared__ __align__(16) char lds[];
     __shared__ double s_rest[2];      // log2 decay behind the chunk
     T *const sk = (T *)lds, *const sv = (T *)(lds + 2 * X::KB);
@@ -580,11 +610,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS)) void lin_states_kerne
         }
         const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
         const Decays<X> s(sd + c % 2 * X::DB);
-#pragma unroll
-        for (int jb = 0; jb < NJ; ++jb) {
-            const typename X::O::F8 vf = ld_t<X, DV, 4>(v, 32 * jb, 16 * w);
-            S.add(k, jb, vf, s.keep, __any(any_not_finite<X>(&vf, 1)));
-        }
+        typename X::O::F8 vf[X::NB];
+        S.values(v, vf);
+        S.add(k, vf, s.keep, __any(any_not_finite<X>(vf, X::NB)));
         if (!more) break;
     }
     const int64_t slot = (int64_t)(2 * seq.first + seg + 1) * a.Hv + h;
@@ -644,7 +672,7 @@ constexpr int kLeastSegment = 512;
 void lin_plan(int cus, LinArgs *a) {
     a->seg = a->slots = 0;
     a->units = a->N;
-    const int64_t per_head = std::max(cus / a->Hv, 1);
+    const int64_t per_head = std::max(2 * cus / a->Hv, 1);
     const int64_t seg = std::max<int64_t>(((a->T + per_head - 1) / per_head + 63) / 64 * 64, kLeastSegment);
     if (a->T <= seg) return;          // no sequence can be longer
     a->seg = (int32_t)seg;
