@@ -210,11 +210,15 @@ __device__ __forceinline__ double lane_of(double x, int l) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+__device__ __forceinline__ double log2_decay(float g) {
+    return (double)(g < kLeastGate ? kLeastGate : g) * 1.4426950408889634;   // NaN stays
+}
+
 // Log decays of a chunk's tokens (lane = token, zero behind the end) summed up to each, in log2.
 template <class X>
 __device__ __forceinline__ double summed(float g, double *all) {
     const int lane = threadIdx.x & 63;
-    double x = (double)(g < kLeastGate ? kLeastGate : g) * 1.4426950408889634;   // NaN stays
+    double x = log2_decay(g);
     x += row_before<1>(x);
     x += row_before<2>(x);
     x += row_before<4>(x);
@@ -405,7 +409,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 
     State<X> S;
     {
-        const float *src = seq.segs > 1 ? a.part + (int64_t)(2 * seq.first + seg) * a.Hv * S.SIZE
+        const float *src = seq.segs > 1 ? a.carry + (int64_t)(2 * seq.first + seg) * a.Hv * S.SIZE
                                         : slot_of(a, a.read_idx, n, S.SIZE);
         S.load(src ? src + h * S.SIZE : nullptr);
     }
@@ -546,9 +550,43 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     }
 }
 
-// What a segment adds to the state, and its decay: at the slot of the segment behind it.
-// The weights count from the segment's end, so its chunks are walked backwards until
-// nothing is left of a token (weights below 2^-150 are zero).
+// Log2 decays of every 64 tokens of the segments that are formed in pieces.  One workgroup a
+// block of tokens; a row of lanes takes a token's heads.
+constexpr int kSum = 64, kSumThreads = 256;
+__global__ __launch_bounds__(kSumThreads) void lin_sums_kernel(const LinArgs a) {
+    __shared__ double s_sum[kSumThreads];
+    const int blocks = a.seg / kSum;
+    const int stretch = blockIdx.x / blocks, block = blockIdx.x - stretch * blocks;
+    const int n = last_not_above(a.N, stretch, [&](int i) { return (int64_t)seg_of(a, i); });
+    const Seq seq(a, n);
+    const int seg = stretch - seq.first;
+    if (seg < 0 || seg + 1 >= seq.segs) return;
+    const int64_t t0 = seq.c0 + (int64_t)seg * a.seg + block * kSum;
+    int row = 64;                     // lanes of a token: the smallest power of two that holds its heads
+    while (row > 1 && row / 2 >= a.Hv) row /= 2;
+    const int rows = kSumThreads / row, r = threadIdx.x / row;
+    for (int h0 = 0; h0 < a.Hv; h0 += row) {
+        const int h = h0 + threadIdx.x % row;
+        double sum = 0.0;
+        if (h < a.Hv) {
+#pragma unroll 8
+            for (int t = r; t < kSum; t += rows) sum += log2_decay(a.g[(t0 + t) * a.g_row + h]);
+        }
+        s_sum[threadIdx.x] = sum;
+        __syncthreads();
+        if (r == 0 && h < a.Hv) {
+            for (int i = 1; i < rows; ++i) sum += s_sum[threadIdx.x + i * row];
+            a.sums[(int64_t)blockIdx.x * a.Hv + h] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+// What a piece of a segment adds to the state at the segment's end, and the segment's decay.
+// The weights count from that end, so the piece's chunks are walked backwards until nothing
+// is left of a token (weights below 2^-150 are zero), and a piece of which nothing is left ends at once.
+constexpr double kGone = -150.0;
+
 template <int DK, int DV, bool BF>
 __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
@@ -556,32 +594,58 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     constexpr int C = X::C;
     extern __shared__ __align__(16) char lds[];
     __shared__ double s_rest[2];      // log2 decay behind the chunk
+    __shared__ double s_sum[X::NW];
     T *const sk = (T *)lds, *const sv = (T *)(lds + 2 * X::KB);
     char *const sd = lds + 2 * (X::KB + X::VB);
 
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
+    const int stretch = unit / a.pieces, piece = unit - stretch * a.pieces;
     const int hk = h / (a.Hv / a.Hk);
-    // only the last sequence that starts in or before the unit's stretch can have a segment here
-    const int n = last_not_above(a.N, unit, [&](int i) { return (int64_t)seg_of(a, i); });
+    // only the last sequence that starts in or before a stretch can have a segment here
+    const int n = last_not_above(a.N, stretch, [&](int i) { return (int64_t)seg_of(a, i); });
     const Seq seq(a, n);
-    const int seg = unit - seq.first;
+    const int seg = stretch - seq.first;
     if (seg < 0 || seg + 1 >= seq.segs) return;
-    const int64_t t0 = seq.c0 + (int64_t)seg * a.seg;
+    const int64_t t1 = seq.c0 + (int64_t)(seg + 1) * a.seg;   // the segment's end
+    const int64_t t0 = t1 - a.seg + (int64_t)piece * a.piece;
+    const int len = min(a.piece, (int)(t1 - t0));             // a multiple of 64
+
+    // decay of the tokens behind the piece
+    double rest = 0.0;
+    if (piece + 1 < a.pieces) {
+        const double *sums = a.sums + (int64_t)stretch * (a.seg / kSum) * a.Hv + h;
+        for (int i = (piece + 1) * (a.piece / kSum) + threadIdx.x; i < a.seg / kSum; i += X::THREADS) rest += sums[(int64_t)i * a.Hv];
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) rest += __shfl_xor(rest, off);
+        if (lane == 0) s_sum[w] = rest;
+        __syncthreads();
+        rest = 0.0;
+#pragma unroll
+        for (int i = 0; i < X::NW; ++i) rest += s_sum[i];
+    }
+    const int64_t kept = (int64_t)stretch * a.Hv + h, slot = (int64_t)unit * a.Hv + h;
+    const bool gone = rest < kGone;
+    if (threadIdx.x == 0) a.live[slot] = !gone;
+    if (gone) {
+        if (threadIdx.x == 0 && piece == 0) a.kept[kept] = 0.f;
+        return;
+    }
+    const double behind = rest;
 
     State<X> S;
     S.load(nullptr);
-    const int chunks = a.seg / C;
+    const int chunks = len / C;
     Rows<X, DK> rk;
     Rows<X, DV> rv;
-    rk.start(a.k, t0 + (int64_t)(chunks - 1) * C, a.k_row, hk * DK);
-    rv.start(a.v, t0 + (int64_t)(chunks - 1) * C, a.v_row, (int64_t)h * DV);
+    rk.start(a.k, t0 + len - C, a.k_row, hk * DK);
+    rv.start(a.v, t0 + len - C, a.v_row, (int64_t)h * DV);
     float rg = 0.f;
     auto fetch = [&](int c) {         // the c-th chunk from the end
         if (c >= chunks) return;
         rk.fetch(C, -1);
         rv.fetch(C, -1);
-        if (c % X::NW == w && lane < C) rg = a.g[(t0 + (int64_t)(chunks - 1 - c) * C + lane) * a.g_row + h];
+        if (c % X::NW == w && lane < C) rg = a.g[(t0 + len - (int64_t)(c + 1) * C + lane) * a.g_row + h];
     };
     auto put = [&](int c) {
         rk.put(sk + c % 2 * C * DK);
@@ -590,20 +654,19 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
             const Decays<X> s(sd + c % 2 * X::DB);
             double all;
             const double x = summed<X>(rg, &all);
-            const double rest = c ? s_rest[(c - 1) % 2] : 0.0;
-            if (lane < C) s.keep[lane] = exp2_of(rest + (all - x));
-            if (lane == 0) s_rest[c % 2] = rest + all;
+            const double after = c ? s_rest[(c - 1) % 2] : behind;
+            if (lane < C) s.keep[lane] = exp2_of(after + (all - x));
+            if (lane == 0) s_rest[c % 2] = after + all;
         }
     };
 
     fetch(0);
     put(0);
     fetch(1);
-    double rest = 0.0;
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
         rest = s_rest[c % 2];
-        const bool more = c + 1 < chunks && !(rest < -150.0);
+        const bool more = c + 1 < chunks && !(rest < kGone);
         if (more) {
             put(c + 1);
             fetch(c + 2);
@@ -615,31 +678,33 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
         S.add(k, vf, s.keep, __any(any_not_finite<X>(vf, X::NB)));
         if (!more) break;
     }
-    const int64_t slot = (int64_t)(2 * seq.first + seg + 1) * a.Hv + h;
     S.store(a.part + slot * S.SIZE);
-    if (threadIdx.x == 0) a.kept[slot] = exp2_of(rest);
+    if (threadIdx.x == 0 && piece == 0) a.kept[kept] = exp2_of(rest);
 }
 
-// The incoming states of a split sequence's segments, in place of what each adds: four
-// elements a thread, one segment after the other.
+// The incoming states of a split sequence's segments: four elements a thread, one segment
+// after the other.
 constexpr int kCarryThreads = 256;
 __global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs a, int size) {
     const int blocks = size / (4 * kCarryThreads);
     const int at = (blockIdx.x % blocks * kCarryThreads + threadIdx.x) * 4;
-    const int unit = blockIdx.x / blocks / a.Hv, h = blockIdx.x / blocks % a.Hv;
-    const int n = last_not_above(a.N, unit, [&](int i) { return (int64_t)seg_of(a, i); });
+    const int stretch = blockIdx.x / blocks / a.Hv, h = blockIdx.x / blocks % a.Hv;
+    const int n = last_not_above(a.N, stretch, [&](int i) { return (int64_t)seg_of(a, i); });
     const Seq seq(a, n);
-    if (seq.first != unit || seq.segs < 2) return;
+    if (seq.first != stretch || seq.segs < 2) return;
     const float *src = slot_of(a, a.read_idx, n, size);
     f32x4 S = {0.f, 0.f, 0.f, 0.f};
     if (src) S = *(const f32x4 *)(src + (int64_t)h * size + at);
-    int64_t slot = (int64_t)2 * seq.first * a.Hv + h;
-    *(f32x4 *)(a.part + slot * size + at) = S;
-    for (int s = 1; s < seq.segs; ++s) {
-        slot += a.Hv;
-        f32x4 *p = (f32x4 *)(a.part + slot * size + at);
-        S = S * a.kept[slot] + *p;
-        *p = S;
+    float *dst = a.carry + ((int64_t)2 * stretch * a.Hv + h) * size + at;
+    *(f32x4 *)dst = S;
+    for (int s = 0; s + 1 < seq.segs; ++s) {
+        S *= a.kept[(int64_t)(stretch + s) * a.Hv + h];
+        for (int p = 0; p < a.pieces; ++p) {
+            const int64_t slot = ((int64_t)(stretch + s) * a.pieces + p) * a.Hv + h;
+            if (a.live[slot]) S += *(const f32x4 *)(a.part + slot * size + at);
+        }
+        dst += (int64_t)a.Hv * size;
+        *(f32x4 *)dst = S;
     }
 }
 
@@ -655,10 +720,15 @@ template <int DK, int DV, bool BF>
 hipError_t launch(const LinArgs &a, hipStream_t s) {
     using X = Shape<DK, DV, BF>;
     if (a.seg) {
-        const int64_t stretches = a.T / a.seg;
-        hipError_t e = start(lin_states_kernel<DK, DV, BF>, stretches * a.Hv, X::THREADS, X::LDS_STATES, a, s);
+        hipError_t e = hipSuccess;
+        if (a.pieces > 1) {
+            const int64_t blocks = (int64_t)a.stretches * (a.seg / kSum);
+            hipLaunchKernelGGL(lin_sums_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, s, a);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        e = start(lin_states_kernel<DK, DV, BF>, (int64_t)a.stretches * a.pieces * a.Hv, X::THREADS, X::LDS_STATES, a, s);
         if (e != hipSuccess) return e;
-        const int64_t grid = stretches * a.Hv * (DK * DV / (4 * kCarryThreads));
+        const int64_t grid = (int64_t)a.stretches * a.Hv * (DK * DV / (4 * kCarryThreads));
         hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)grid), dim3(kCarryThreads), 0, s, a, DK * DV);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -666,22 +736,38 @@ hipError_t launch(const LinArgs &a, hipStream_t s) {
 }
 
 constexpr int kLeastSegment = 512;
+constexpr int kPiece = 2048;
 
 }  // namespace
 
 void lin_plan(int cus, LinArgs *a) {
-    a->seg = a->slots = 0;
+    a->seg = a->slots = a->stretches = a->piece = a->pieces = 0;
     a->units = a->N;
     const int64_t per_head = std::max(2 * cus / a->Hv, 1);
     const int64_t seg = std::max<int64_t>(((a->T + per_head - 1) / per_head + 63) / 64 * 64, kLeastSegment);
     if (a->T <= seg) return;          // no sequence can be longer
     a->seg = (int32_t)seg;
-    a->units = (int32_t)(a->N + a->T / seg);
-    a->slots = (int32_t)(2 * (a->T / seg));
+    a->stretches = (int32_t)(a->T / seg);
+    a->units = a->N + a->stretches;
+    a->slots = 2 * a->stretches;
+    const int32_t pieces = (int32_t)((seg + kPiece - 1) / kPiece);
+    a->piece = ((a->seg + pieces - 1) / pieces + 63) / 64 * 64;
+    a->pieces = (a->seg + a->piece - 1) / a->piece;
 }
 
-size_t lin_part_bytes(int dk, int dv, const LinArgs &a) {
-    return (size_t)a.slots * a.Hv * ((size_t)dk * dv + 1) * sizeof(float);
+size_t lin_bytes(int dk, int dv, const LinArgs &a) {
+    const size_t size = (size_t)dk * dv, pieces = (size_t)a.stretches * a.pieces;
+    const size_t sums = a.pieces > 1 ? (size_t)a.stretches * (a.seg / kSum) * sizeof(double) : 0;
+    return a.Hv * ((((size_t)a.slots + pieces) * size + a.stretches + pieces) * sizeof(float) + sums);
+}
+
+void lin_buffers(int dk, int dv, void *ws, LinArgs *a) {
+    const size_t size = (size_t)dk * dv, pieces = (size_t)a->stretches * a->pieces;
+    a->carry = (float *)ws;
+    a->part = a->carry + a->slots * a->Hv * size;
+    a->sums = (double *)(a->part + pieces * a->Hv * size);
+    a->kept = (float *)(a->sums + (a->pieces > 1 ? (size_t)a->stretches * (a->seg / kSum) * a->Hv : 0));
+    a->live = (int32_t *)(a->kept + (size_t)a->stretches * a->Hv);
 }
 
 bool lin_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }

@@ -566,3 +566,22 @@ def test_split_not_finite(K):
     torch.cuda.synchronize()
     assert np.array_equal(o[:700], o2[:700]) and np.array_equal(o[:, 0], o2[:, 0])
     assert np.isnan(o2[700:, 1, 3]).all() and np.array_equal(np.delete(o, 3, 2), np.delete(o2, 3, 2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["head", "strong"])
+def test_split_in_pieces(K, dtype, gate):
+    """Segments long enough to be formed in pieces, some of which nothing is left of."""
+    Hv, T = 256, 4500
+    c = Call(dtype, [T, 100], 256, Hv, 64, 64, gate, 57, slots=[(0, 1, 1)])
+    import torch
+    pick = [0, 120, 255]                                  # the oracle takes some heads
+    first = c.pool.clone()
+    o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write), scale=0.3)
+    torch.cuda.synchronize()
+    f = to_numpy_f64
+    g = R.decays(f(c.g), T + 100, Hv)[:, pick]
+    ref = R.prefill(f(c.q[:, pick]), f(c.k[:, pick]), f(c.v[:, pick]), g, c.cu, f(first[:, pick]), c.read, c.write, scale=0.3)
+    assert rel_l2(f(o[:, pick]), ref[0]) <= (HALF["bf16"] if dtype == "bf16" else U * 600)
+    w = int(c.write[0])
+    assert rel_l2(f(c.pool[w][pick]), ref[3][0]) <= U * 600
