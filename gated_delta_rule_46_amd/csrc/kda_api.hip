@@ -1138,6 +1138,9 @@ int check_lin_rows(const kda_lin_config *cfg, const void *q, int64_t q_row, cons
     KDA_TRY(check_distance(cfg->io_dtype, v_row, (int64_t)cfg->num_v_heads * cfg->dv, "v_row"));
     if (g_row != 0 && g_row < cfg->num_v_heads)
         return fail(KDA_ERR_ARG, "g_row must be 0 or at least %d (got %lld)", cfg->num_v_heads, (long long)g_row);
+    // 32 rows lie within the 31 bits of a bounded load
+    if (std::max(std::max(q_row, k_row), std::max(v_row, g_row)) > 1 << 24)
+        return fail(KDA_ERR_UNSUPPORTED, "q_row, k_row, v_row and g_row must be at most 2^24 elements");
     KDA_TRY(check_tensor(q, "q", true));
     KDA_TRY(check_tensor(k, "k", true));
     KDA_TRY(check_tensor(v, "v", true));

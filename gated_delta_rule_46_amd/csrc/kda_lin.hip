@@ -41,6 +41,7 @@ using mf::bf16_t;
 using mf::bf16x4;
 using mf::bf16x8;
 using mf::f32x4;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLeastGate = -1e4f;   // e^-10000 is zero; sums of it stay exact to 2^-30 in fp64
@@ -52,18 +53,21 @@ struct Shape {
     using O = mf::Ops<BF>;
     using T = typename O::T;
     static constexpr int C = 32, NT = C / 16;       // tokens per chunk, tiles of 16
+    static constexpr int CW = DV, NCB = DV / CW;   // value columns of a workgroup
     static constexpr int NW = BF ? 4 : DV / 16, THREADS = 64 * NW;
-    static constexpr int NB = DV / 16 / NW;         // column tiles of a wave
+    static constexpr int NB = CW / 16 / NW;         // column tiles of a wave
     static_assert(NB == 1 || NB == 2);
     static constexpr int NKB = DK / 32;
+    static constexpr int DEPTH = 1;                 // chunks on their way in registers
+    static constexpr int DEPTH_STATES = 1;          // and in the launch that forms the segments' states
     static constexpr int TERMS = BF ? 3 : 1;        // operand terms that hold an fp32 value
     static constexpr int E = 16 / sizeof(T);        // elements of a 16-byte piece
-    static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
-    static constexpr int KB = C * DK * sizeof(T), VB = C * DV * sizeof(T), PB = C * C * sizeof(T);
+    static constexpr int NPK = C * DK / E / THREADS, NPV = C * CW / E / THREADS;
+    static constexpr int KB = C * DK * sizeof(T), VB = C * CW * sizeof(T), PB = C * C * sizeof(T);
     static constexpr int DB = (4 * C + 4) * sizeof(float);   // decays of a chunk
     static constexpr int LDS = 5 * KB + 3 * VB + 2 * PB + 3 * DB;
     static constexpr int LDS_STATES = 2 * (KB + VB + DB);    // of the launch that forms the segments' states
-    static_assert(C * DK % (E * THREADS) == 0 && C * DV % (E * THREADS) == 0);
+    static_assert(C * DK % (E * THREADS) == 0 && C * CW % (E * THREADS) == 0);
     static_assert(LDS <= 160 * 1024);
 };
 
@@ -259,39 +263,49 @@ __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_
     return e + e * (((hi_i - (d - b)) + (-hi_j - b) + (lo_i - lo_j)) * 0.6931471805599453f);
 }
 
-// 16-byte pieces of a chunk's rows on their way from global memory to LDS.  A thread keeps its
-// first piece's address and moves it from chunk to chunk.
+// Global memory from a uniform address on, `bytes` of it: loads behind them give zeros, stores are
+// dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const char *p, int bytes) {
+    const uint64_t u = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)hi << 32 | lo), 0, __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
+}
+// `rows` rows of `width` bytes, `distance` apart (31 bits in all)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const char *p, int rows, int distance, int width) {
+    return window(p, rows > 0 ? (rows - 1) * distance + width : 0);
+}
+
+// A tensor's rows of a unit, W columns of them, chunk after chunk.
 template <class X, int W>
-struct Rows {
+struct Source {
     using T = typename X::T;
     static constexpr int PIECES = W / X::E, N = X::C * PIECES / X::THREADS, STEP = X::THREADS / PIECES;
     static_assert(X::THREADS % PIECES == 0);
-    const T *p;
-    int64_t row;
-    u32x4 r[N];
-    __device__ __forceinline__ void start(const void *base, int64_t t, int64_t distance, int64_t off) {
-        row = distance;
-        p = (const T *)base + (t + threadIdx.x / PIECES) * row + off + threadIdx.x % PIECES * X::E;
+    const char *p;                    // the chunk's first row
+    int row;                          // bytes between rows
+    int offset;                       // of the thread's first piece
+    __device__ __forceinline__ Source(const void *base, int64_t t, int64_t distance, int64_t off)
+        : p((const char *)((const T *)base + t * distance + off)), row((int)distance * (int)sizeof(T)),
+          offset(threadIdx.x / PIECES * row + threadIdx.x % PIECES * 16) {}
+    __device__ __forceinline__ void step(int chunks) { p += (int64_t)row * (chunks * X::C); }
+};
+
+// A chunk's 16-byte pieces on their way from global memory to LDS.
+template <class X, int W>
+struct Rows {
+    using S = Source<X, W>;
+    u32x4 r[S::N];
+    // `valid` rows (all of the chunk's at most), zeros behind them
+    __device__ __forceinline__ void fetch(const S &s, int valid) {
+        const auto w = window(s.p, valid, s.row, W * (int)sizeof(typename X::T));
+#pragma unroll
+        for (int i = 0; i < S::N; ++i) r[i] = __builtin_amdgcn_raw_buffer_load_b128(w, s.offset, i * S::STEP * s.row, 0);
     }
-    // the chunk's first `valid` rows, zeros behind them; then on by `chunks` chunks
-    __device__ __forceinline__ void fetch(int valid, int chunks) {
-        if (valid >= X::C) {
+    __device__ __forceinline__ void put(typename X::T *tile) const {
 #pragma unroll
-            for (int i = 0; i < N; ++i) r[i] = *(const u32x4 *)(p + i * STEP * row);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                r[i] = u32x4{0, 0, 0, 0};
-                if ((int)threadIdx.x / PIECES + i * STEP < valid) r[i] = *(const u32x4 *)(p + i * STEP * row);
-            }
-        }
-        p += chunks * X::C * row;
-    }
-    __device__ __forceinline__ void put(T *tile) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < S::N; ++i) {
             const int q = threadIdx.x + i * X::THREADS;
-            *(u32x4 *)(tile + at<T, W>(q / PIECES, q % PIECES * X::E)) = r[i];
+            *(u32x4 *)(tile + at<typename X::T, W>(q / S::PIECES, q % S::PIECES * X::E)) = r[i];
         }
     }
 };
@@ -320,10 +334,12 @@ struct State {
                 for (int hf = 0; hf < 2; ++hf) f(s[b][kb][hf], at + (32 * kb + 4 * hf) * X::DV + 4 * b);
     }
     __device__ __forceinline__ void load(const float *src) {   // null: zeros
-        each([&](f32x4 &x, int at) {
+        each([&](f32x4 &x, int) { x = f32x4{0.f, 0.f, 0.f, 0.f}; });
+        if (src)
+            each([&](f32x4 &x, int at) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = src ? src[at + i * X::DV] : 0.f;
-        });
+                for (int i = 0; i < 4; ++i) x[i] = src[at + i * X::DV];
+            });
     }
     __device__ __forceinline__ void store(float *dst) {
         each([&](f32x4 &x, int at) {
@@ -334,7 +350,7 @@ struct State {
     // v^T of the wave's columns
     __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
-        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
+        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::CW, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
     }
     // s += k^T (weights v)
     __device__ __forceinline__ void add(const typename X::T *k, const typename X::O::F8 *v, const float *keep, bool rare) {
@@ -368,9 +384,9 @@ struct Seq {
     int len, segs;
     int first;        // c0 / seg
     __device__ __forceinline__ Seq(const LinArgs &a, int n) {
-        c0 = min(max(a.cu[n], (int64_t)0), a.T);
-        const int64_t l = min(a.cu[n + 1], a.T) - c0;
-        len = l > 0 ? (int)l : 0;
+        const int begin = (int)min(max(a.cu[n], (int64_t)0), a.T), end = (int)min(max(a.cu[n + 1], (int64_t)0), a.T);
+        c0 = __builtin_amdgcn_readfirstlane(begin);
+        len = __builtin_amdgcn_readfirstlane(max(end - begin, 0));
         segs = 1;
         first = 0;
         if (a.seg) {
@@ -383,13 +399,25 @@ __device__ __forceinline__ int seg_of(const LinArgs &a, int n) {
     return (int)((uint32_t)min(max(a.cu[n], (int64_t)0), a.T) / (uint32_t)a.seg);
 }
 
+// Unit, head and column block of a workgroup.  The column blocks of a head read the same q and k:
+// they stand 8 workgroups apart, which puts them on one XCD, behind one L2, at the same time.
+struct Block { int unit, h, cb; };
+template <class X>
+__device__ __forceinline__ Block block_of(const LinArgs &a) {
+    const int lane = blockIdx.x % 8, rest = blockIdx.x / 8;
+    const int item = rest / X::NCB * 8 + lane;
+    return {item / a.Hv, item % a.Hv, rest % X::NCB};
+}
+template <class X>
+int64_t blocks_of(int64_t units, int Hv) { return (units * Hv + 7) / 8 * 8 * X::NCB; }
+
 template <int DK, int DV, bool BF>
 __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
     using O = typename X::O;
     using T = typename X::T;
     using F8 = typename O::F8;
-    constexpr int C = X::C, NT = X::NT, NB = X::NB, NKB = X::NKB;
+    constexpr int C = X::C, NT = X::NT, NB = X::NB, NKB = X::NKB, DEPTH = X::DEPTH;
     extern __shared__ __align__(16) char lds[];
     T *const sq = (T *)lds, *const sk = (T *)(lds + 2 * X::KB), *const sv = (T *)(lds + 5 * X::KB);
     T *const sp = (T *)(lds + 5 * X::KB + 3 * X::VB);
@@ -397,7 +425,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m = lane & 15, gq = lane >> 4;
-    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
+    const Block blk = block_of<X>(a);
+    const int unit = blk.unit, h = blk.h, x0 = blk.cb * X::CW;
+    if (unit >= a.units) return;
     const int hk = h / (a.Hv / a.Hk);
     const int n = a.seg ? last_not_above(a.N, unit, [&](int i) { return (int64_t)i + seg_of(a, i); }) : unit;
     const Seq seq(a, n);
@@ -411,41 +441,44 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     {
         const float *src = seq.segs > 1 ? a.carry + (int64_t)(2 * seq.first + seg) * a.Hv * S.SIZE
                                         : slot_of(a, a.read_idx, n, S.SIZE);
-        S.load(src ? src + h * S.SIZE : nullptr);
+        S.load(src ? src + h * S.SIZE + x0 : nullptr);
     }
 
-    Rows<X, DK> rq, rk;
-    Rows<X, DV> rv;
-    rq.start(a.q, t0, a.q_row, hk * DK);
-    rk.start(a.k, t0, a.k_row, hk * DK);
-    rv.start(a.v, t0, a.v_row, (int64_t)h * DV);
-    float rg = 0.f;
-    auto fetch = [&](int first) {
-        const int valid = len - first;
-        rq.fetch(valid, 1);
-        rk.fetch(valid, 1);
-        rv.fetch(valid, 1);
-        rg = 0.f;
-        if (first / C % X::NW == w && lane < min(valid, C)) rg = a.g[(t0 + first + lane) * a.g_row + h];
+    Source<X, DK> fq(a.q, t0, a.q_row, hk * DK), fk(a.k, t0, a.k_row, hk * DK);
+    Source<X, X::CW> fv(a.v, t0, a.v_row, (int64_t)h * DV + x0);
+    const char *fg = (const char *)(a.g + t0 * a.g_row + h);
+    const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
+    struct Chunk { Rows<X, DK> q, k; Rows<X, X::CW> v; float g; };
+    // the next chunk that has not been fetched; always as many loads, so that waiting for them waits for
+    // nothing else
+    auto fetch = [&](Chunk &r, int c) {
+        const int valid = min(len - c * C, C);
+        r.q.fetch(fq, valid);
+        r.k.fetch(fk, valid);
+        r.v.fetch(fv, valid);
+        r.g = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(window(fg, valid, g_row, 4), g_at, 0, 0));
+        fq.step(1);
+        fk.step(1);
+        fv.step(1);
+        fg += (int64_t)g_row * C;
     };
-    auto put = [&](int c) {
-        rq.put(sq + c % 2 * C * DK);
-        rk.put(sk + c % 3 * C * DK);
-        rv.put(sv + c % 3 * C * DV);
-        if (c % X::NW == w) write_decays<X>(sd + c % 3 * X::DB, rg, a.scale);
+    auto put = [&](const Chunk &r, int c) {
+        r.q.put(sq + c % 2 * C * DK);
+        r.k.put(sk + c % 3 * C * DK);
+        r.v.put(sv + c % 3 * C * X::CW);
+        if (c % X::NW == w) write_decays<X>(sd + c % 3 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
     };
 
     const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
-    T *out = (T *)a.o + ((t0 + m) * a.Hv + h) * DV + col;
-    fetch(0);
-    put(0);
-    fetch(C);
-    __syncthreads();
-    for (int first = 0, c = 0; first < len; first += C, ++c) {
-        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 3 * C * DK, *const v = sv + c % 3 * C * DV;
+    const int o_row = a.Hv * DV * (int)sizeof(T), o_at = m * o_row + col * (int)sizeof(T);
+    const char *out = (const char *)((T *)a.o + (t0 * a.Hv + h) * DV + x0);
+    // chunk c, whose rows are in LDS; `next` holds those of the one behind it, and takes those of the one DEPTH
+    // further
+    auto chunk = [&](int c, Chunk &next) {
+        const int valid = min(len - c * C, C);
+        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 3 * C * DK, *const v = sv + c % 3 * C * X::CW;
         T *const pt = sp + c % 2 * C * C;
         const Decays<X> s(sd + c % 3 * X::DB);
-        const int valid = min(C, len - first);
 
         // P^T tiles (rows j, columns i): lane holds 4 consecutive j of its i
         for (int t = w; t < 4; t += X::NW) {
@@ -492,10 +525,8 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
         F8 vf[NB];
         S.values(v, vf);
         const bool rare = __any(any_not_finite<X>(vf, NB));
-        if (first + C < len) {
-            put(c + 1);
-            fetch(first + 2 * C);
-        }
+        put(next, c + 1);
+        fetch(next, c + 1 + DEPTH);
         __syncthreads();   // P and the next chunk are there
 
         // infinities and NaN must not meet the zeros of P above its diagonal: they are left out of
@@ -519,34 +550,53 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float x = (float)v[at<T, DV>(j, col + 4 * b + r)];
+                        const float x = (float)v[at<T, X::CW>(j, col + 4 * b + r)];
 #pragma unroll
                         for (int it = 0; it < NT; ++it)
                             if (not_finite(x) && j <= 16 * it + m) acc[it][b][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
                     }
         }
+        const auto ow = window(out, valid, o_row, X::CW * (int)sizeof(T));
+        out += (int64_t)o_row * C;
 #pragma unroll
-        for (int it = 0; it < NT; ++it)
-            if (16 * it + m < valid) {
-                T *const dst = out + 16 * it * a.Hv * DV;
-                if constexpr (NB == 2) O::stf(dst, O::cvt44(acc[it][0], acc[it][1]));
-                else O::st4(dst, acc[it][0]);
+        for (int it = 0; it < NT; ++it) {
+            if constexpr (!BF) {
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it][0]), ow, o_at, 16 * it * o_row, 0);
+            } else if constexpr (NB == 2) {
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O::cvt44(acc[it][0], acc[it][1])), ow, o_at,
+                                                       16 * it * o_row, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, O::cvt4(acc[it][0])), ow, o_at, 16 * it * o_row, 0);
             }
-        out += (int64_t)C * a.Hv * DV;
+        }
 
         // S <- e^{G_C} S + k^T (weights v)
         const float all = *s.all;
         S.each([&](f32x4 &x, int) { x *= all; });
         S.add(k, vf, s.keep, rare);
 
-        const int end = first + C;
-        if (a.interval && end <= len && (skip + end) % a.interval == 0)
-            S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE);
+        const int end = (c + 1) * C;
+        if (valid == C && a.interval && (skip + end) % a.interval == 0)
+            S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE + x0);
+    };
+
+    if (len > 0) {
+        Chunk r[DEPTH];
+        fetch(r[0], 0);
+        put(r[0], 0);
+#pragma unroll
+        for (int i = 1; i <= DEPTH; ++i) fetch(r[i % DEPTH], i);
+        __syncthreads();
+        for (int c = 0; c * C < len; c += DEPTH) {
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i)
+                if (i == 0 || (c + i) * C < len) chunk(c + i, r[(i + 1) % DEPTH]);
+        }
     }
 
     if (seg + 1 == seq.segs) {
         float *dst = slot_of(a, a.write_idx, n, S.SIZE);
-        if (dst) S.store(dst + h * S.SIZE);
+        if (dst) S.store(dst + h * S.SIZE + x0);
     }
 }
 
@@ -599,7 +649,11 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     char *const sd = lds + 2 * (X::KB + X::VB);
 
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
+    const Block blk = block_of<X>(a);
+    // heads that remember longest take most of the time: they come at another place in each unit's row, as
+    // workgroups are dealt out to the compute units in turn
+    const int unit = blk.unit, h = (blk.h + unit) % a.Hv, x0 = blk.cb * X::CW;
+    if (unit >= a.stretches * a.pieces) return;
     const int stretch = unit / a.pieces, piece = unit - stretch * a.pieces;
     const int hk = h / (a.Hv / a.Hk);
     // only the last sequence that starts in or before a stretch can have a segment here
@@ -636,55 +690,63 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     State<X> S;
     S.load(nullptr);
     const int chunks = len / C;
-    Rows<X, DK> rk;
-    Rows<X, DV> rv;
-    rk.start(a.k, t0 + len - C, a.k_row, hk * DK);
-    rv.start(a.v, t0 + len - C, a.v_row, (int64_t)h * DV);
-    float rg = 0.f;
-    auto fetch = [&](int c) {         // the c-th chunk from the end
-        if (c >= chunks) return;
-        rk.fetch(C, -1);
-        rv.fetch(C, -1);
-        if (c % X::NW == w && lane < C) rg = a.g[(t0 + len - (int64_t)(c + 1) * C + lane) * a.g_row + h];
+    Source<X, DK> fk(a.k, t0 + len - C, a.k_row, hk * DK);
+    Source<X, X::CW> fv(a.v, t0 + len - C, a.v_row, (int64_t)h * DV + x0);
+    const char *fg = (const char *)(a.g + (t0 + len - C) * a.g_row + h);
+    const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
+    struct Chunk { Rows<X, DK> k; Rows<X, X::CW> v; float g; };
+    auto fetch = [&](Chunk &r, int c) {         // the c-th chunk from the end
+        const int valid = c < chunks ? C : 0;
+        r.k.fetch(fk, valid);
+        r.v.fetch(fv, valid);
+        r.g = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(window(fg, valid, g_row, 4), g_at, 0, 0));
+        fk.step(-1);
+        fv.step(-1);
+        fg -= (int64_t)g_row * C;
     };
-    auto put = [&](int c) {
-        rk.put(sk + c % 2 * C * DK);
-        rv.put(sv + c % 2 * C * DV);
+    auto put = [&](const Chunk &r, int c) {
+        r.k.put(sk + c % 2 * C * DK);
+        r.v.put(sv + c % 2 * C * X::CW);
         if (c % X::NW == w) {
             const Decays<X> s(sd + c % 2 * X::DB);
             double all;
-            const double x = summed<X>(rg, &all);
+            const double x = summed<X>(r.g, &all);
             const double after = c ? s_rest[(c - 1) % 2] : behind;
             if (lane < C) s.keep[lane] = exp2_of(after + (all - x));
             if (lane == 0) s_rest[c % 2] = after + all;
         }
     };
 
-    fetch(0);
-    put(0);
-    fetch(1);
-    for (int c = 0; c < chunks; ++c) {
-        __syncthreads();
-        rest = s_rest[c % 2];
-        const bool more = c + 1 < chunks && !(rest < kGone);
-        if (more) {
-            put(c + 1);
-            fetch(c + 2);
+    constexpr int DEPTH = X::DEPTH_STATES;
+    Chunk r[DEPTH];
+    fetch(r[0], 0);
+    put(r[0], 0);
+#pragma unroll
+    for (int i = 1; i <= DEPTH; ++i) fetch(r[i % DEPTH], i);
+    bool more = true;
+    for (int c = 0; more; c += DEPTH) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            if (!more) break;
+            __syncthreads();
+            rest = s_rest[(c + i) % 2];
+            more = c + i + 1 < chunks && !(rest < kGone);
+            if (more) put(r[(i + 1) % DEPTH], c + i + 1);
+            fetch(r[(i + 1) % DEPTH], c + i + 1 + DEPTH);
+            const T *const k = sk + (c + i) % 2 * C * DK, *const v = sv + (c + i) % 2 * C * X::CW;
+            const Decays<X> s(sd + (c + i) % 2 * X::DB);
+            typename X::O::F8 vf[X::NB];
+            S.values(v, vf);
+            S.add(k, vf, s.keep, __any(any_not_finite<X>(vf, X::NB)));
         }
-        const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
-        const Decays<X> s(sd + c % 2 * X::DB);
-        typename X::O::F8 vf[X::NB];
-        S.values(v, vf);
-        S.add(k, vf, s.keep, __any(any_not_finite<X>(vf, X::NB)));
-        if (!more) break;
     }
-    S.store(a.part + slot * S.SIZE);
+    S.store(a.part + slot * S.SIZE + x0);
     if (threadIdx.x == 0 && piece == 0) a.kept[kept] = exp2_of(rest);
 }
 
 // The incoming states of a split sequence's segments: four elements a thread, one segment
 // after the other.
-constexpr int kCarryThreads = 256;
+constexpr int kCarryThreads = 256, kMaxPieces = 4;
 __global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs a, int size) {
     const int blocks = size / (4 * kCarryThreads);
     const int at = (blockIdx.x % blocks * kCarryThreads + threadIdx.x) * 4;
@@ -697,14 +759,37 @@ __global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs 
     if (src) S = *(const f32x4 *)(src + (int64_t)h * size + at);
     float *dst = a.carry + ((int64_t)2 * stretch * a.Hv + h) * size + at;
     *(f32x4 *)dst = S;
-    for (int s = 0; s + 1 < seq.segs; ++s) {
-        S *= a.kept[(int64_t)(stretch + s) * a.Hv + h];
-        for (int p = 0; p < a.pieces; ++p) {
-            const int64_t slot = ((int64_t)(stretch + s) * a.pieces + p) * a.Hv + h;
-            if (a.live[slot]) S += *(const f32x4 *)(a.part + slot * size + at);
+    constexpr int G = 4;              // segments whose parts are on their way at once
+    for (int s0 = 0; s0 + 1 < seq.segs; s0 += G) {
+        float kept[G];
+        bool live[G][kMaxPieces];
+        f32x4 part[G][kMaxPieces];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const int s = min(s0 + i, seq.segs - 2);
+            kept[i] = a.kept[(int64_t)(stretch + s) * a.Hv + h];
+#pragma unroll
+            for (int p = 0; p < kMaxPieces; ++p)
+                live[i][p] = p < a.pieces && a.live[((int64_t)(stretch + s) * a.pieces + p) * a.Hv + h];
         }
-        dst += (int64_t)a.Hv * size;
-        *(f32x4 *)dst = S;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const int64_t s = stretch + min(s0 + i, seq.segs - 2);
+#pragma unroll
+            for (int p = 0; p < kMaxPieces; ++p) {
+                part[i][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (live[i][p]) part[i][p] = *(const f32x4 *)(a.part + ((s * a.pieces + p) * a.Hv + h) * size + at);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            S *= kept[i];
+#pragma unroll
+            for (int p = 0; p < kMaxPieces; ++p)
+                if (live[i][p]) S += part[i][p];
+            dst += (int64_t)a.Hv * size;
+            if (s0 + i + 1 < seq.segs) *(f32x4 *)dst = S;
+        }
     }
 }
 
@@ -726,17 +811,17 @@ hipError_t launch(const LinArgs &a, hipStream_t s) {
             hipLaunchKernelGGL(lin_sums_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, s, a);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        e = start(lin_states_kernel<DK, DV, BF>, (int64_t)a.stretches * a.pieces * a.Hv, X::THREADS, X::LDS_STATES, a, s);
+        e = start(lin_states_kernel<DK, DV, BF>, blocks_of<X>((int64_t)a.stretches * a.pieces, a.Hv), X::THREADS, X::LDS_STATES, a, s);
         if (e != hipSuccess) return e;
         const int64_t grid = (int64_t)a.stretches * a.Hv * (DK * DV / (4 * kCarryThreads));
         hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)grid), dim3(kCarryThreads), 0, s, a, DK * DV);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    return start(lin_kernel<DK, DV, BF>, (int64_t)a.units * a.Hv, X::THREADS, X::LDS, a, s);
+    return start(lin_kernel<DK, DV, BF>, blocks_of<X>(a.units, a.Hv), X::THREADS, X::LDS, a, s);
 }
 
 constexpr int kLeastSegment = 512;
-constexpr int kPiece = 2048;
+constexpr int kLeastPiece = 1024;
 
 }  // namespace
 
@@ -750,7 +835,7 @@ void lin_plan(int cus, LinArgs *a) {
     a->stretches = (int32_t)(a->T / seg);
     a->units = a->N + a->stretches;
     a->slots = 2 * a->stretches;
-    const int32_t pieces = (int32_t)((seg + kPiece - 1) / kPiece);
+    const int32_t pieces = (int32_t)std::max<int64_t>(std::min<int64_t>(kMaxPieces, seg / kLeastPiece), 1);
     a->piece = ((a->seg + pieces - 1) / pieces + 63) / 64 * 64;
     a->pieces = (a->seg + a->piece - 1) / a->piece;
 }

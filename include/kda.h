@@ -624,11 +624,11 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
  * Rows.  q and k have num_qk_heads heads of dk values, v and o num_v_heads
  * heads of dv, in io_dtype; value head h reads query/key head
  * h / (num_v_heads / num_qk_heads).  The heads of a token are contiguous; *_row
- * is the distance between tokens in elements (at least the row itself, a multiple
- * of 16 bytes), so q, k and v may be views of one projection's rows.  o is
+ * is the distance between tokens in elements (at least the row itself, at most 2^24,
+ * a multiple of 16 bytes), so q, k and v may be views of one projection's rows.  o is
  * contiguous and no input.  dk, dv in {64, 128}.
  * g: fp32 log decays, g[t * g_row + h], 4-byte aligned; g_row is 0 (one decay
- * per head for all tokens) or at least num_v_heads.  g <= 0, -infinity among it
+ * per head for all tokens) or num_v_heads .. 2^24.  g <= 0, -infinity among it
  * (the state is dropped); values below -10^4 count as that.
  * T * num_v_heads is at most 2^26 and N * num_v_heads at most 2^20 (larger calls
  * are split by the caller).

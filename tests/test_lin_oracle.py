@@ -135,8 +135,10 @@ def test_rows_and_config_are_checked(call):
     for name in ("q_row", "k_row", "v_row"):
         assert call(**{name: 255}) == E and name in err()
         assert call(**{name: 257}) == A and name in err()
+        assert call(**{name: (1 << 24) + 8}) == U and name in err()
     assert call(g_row=3) == E and "g_row" in err()
     assert call(g_row=-4) == E
+    assert call(g_row=(1 << 24) + 1) == U
     for name in ("q", "k", "v"):
         assert call(o=3 * FAKE, **{name: 3 * FAKE}) == E and "alias" in err()
     assert call(pool=K.kda_state_pool(FAKE, 0, FAKE, FAKE)) == E
