@@ -1243,6 +1243,8 @@ int kda_head_norm(int32_t io_dtype, int64_t T, int32_t H, int32_t D, const void 
         return fail(KDA_ERR_UNSUPPORTED, "D must be a multiple of 8, at most %d (got %d)", kda::kHeadNormMaxDim, D);
     if (T > (1 << 26) / H)
         return fail(KDA_ERR_UNSUPPORTED, "T * H must be at most 2^26 (got T = %lld)", (long long)T);
+    if ((int64_t)H * D > 1 << 30)
+        return fail(KDA_ERR_UNSUPPORTED, "H * D must be at most 2^30 (got H = %d)", H);
     if (per_head != 0 && per_head != 1) return fail(KDA_ERR_ARG, "per_head must be 0 or 1 (got %d)", per_head);
     if (center != 0 && center != 1) return fail(KDA_ERR_ARG, "center must be 0 or 1 (got %d)", center);
     if (act != KDA_ACT_NONE && act != KDA_ACT_SILU && act != KDA_ACT_SIGMOID)

@@ -46,9 +46,21 @@ __device__ __forceinline__ float sum_of(float x) {
     return x;
 }
 
+// e^-|x| neither overflows nor needs a special case.  bf16 outputs take the hardware's exponential and
+// reciprocal (an ulp of fp32 each, and |x| 2^-24 from the exponent's scaling).
+template <bool BF>
 __device__ __forceinline__ float activation(float x, int act) {
     if (act == KDA_ACT_NONE) return x;
-    return (act == KDA_ACT_SILU ? x : 1.f) / (1.f + expf(-x));
+    float s;
+    if (BF) {
+        const float e = mf::ex2(-fabsf(x) * mf::kLog2e), r = __builtin_amdgcn_rcpf(1.f + e);
+        s = x < 0.f ? e * r : r;
+    } else {
+        const float e = expf(-fabsf(x));
+        s = (x < 0.f ? e : 1.f) / (1.f + e);
+    }
+    s = x != x ? x : s;
+    return act == KDA_ACT_SILU ? x * s : s;
 }
 
 // V pieces of E values in each of L lanes; pieces behind the head's end hold zeros.
@@ -71,80 +83,113 @@ struct Head {
         for (int j = 0; j < NX; ++j) ss += x[j] * x[j];
         return sum_of<L>(ss) * inv;
     }
+    __device__ __forceinline__ void take(const u32x4 *r) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) unpack<BF>(r[i], x + i * E);
+    }
 };
 
-template <int L, int V, bool BF>
+// R heads a lane, whose loads are on their way together.
+template <int L, int V, int R, bool BF>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(const HeadNormArgs a) {
-    constexpr int E = BF ? 8 : 4, NX = V * E;
+    constexpr int E = BF ? 8 : 4, NX = V * E, PER = kNormThreads / L;
     using T = typename mf::Ops<BF>::T;
     const int l = threadIdx.x % L;
-    const int64_t head = (int64_t)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
-    const bool live = head < a.T * a.H;
-    const int64_t t = live ? head / a.H : 0;
-    const int h = live ? (int)(head - t * a.H) : 0;
+    const uint32_t heads = (uint32_t)(a.T * a.H), first = blockIdx.x * (uint32_t)(PER * R) + threadIdx.x / L;
     const float inv = 1.f / (float)a.D;
 
-    u32x4 rx[V], rz[V];
-    Head<L, V, BF> y;
+    int64_t t[R];
+    int at[R];                        // the lane's first element in its token's row
+    u32x4 rx[R][V], rz[R][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int d = (l + L * i) * E;
-        rx[i] = rz[i] = u32x4{0, 0, 0, 0};
-        if (live && d < a.D) {
-            rx[i] = *(const u32x4 *)((const T *)a.x + t * a.x_row + (int64_t)h * a.D + d);
-            if (a.gate) rz[i] = *(const u32x4 *)((const T *)a.gate + t * a.gate_row + (int64_t)h * a.D + d);
+    for (int r = 0; r < R; ++r) {
+        const uint32_t head = min(first + r * PER, heads - 1);
+        t[r] = head / (uint32_t)a.H;
+        at[r] = (int)(head - (uint32_t)t[r] * a.H) * a.D + l * E;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            rx[r][i] = rz[r][i] = u32x4{0, 0, 0, 0};
+            if ((l + L * i) * E < a.D) {
+                rx[r][i] = __builtin_nontemporal_load((const u32x4 *)((const T *)a.x + t[r] * a.x_row + at[r] + L * i * E));
+                if (a.gate)
+                    rz[r][i] = __builtin_nontemporal_load((const u32x4 *)((const T *)a.gate + t[r] * a.gate_row + at[r] + L * i * E));
+            }
         }
-        unpack<BF>(rx[i], y.x + i * E);
     }
-    const float ms = y.squares(a, l, inv) + a.eps;
-    float r = rsqrtf(ms);
-    if (!(ms >= kLeastSquare && ms < __builtin_inff())) {   // the same in a head's lanes
-        // x and sqrt(eps) as multiples of 2^k, the larger of them within [1/2, 1);
-        // infinities and NaN stay as they are
-        float top = sqrtf(a.eps);
+    float w[NX], b[NX];
+    auto affine = [&](int from) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) unpack<BF>(rx[i], y.x + i * E);
+        for (int j = 0; j < NX; j += 4) {
+            const bool in = (l + L * (j / E)) * E < a.D;
+            const int d = from + L * (j / E) * E + j % E;
+            const mf::f32x4 one = {1.f, 1.f, 1.f, 1.f}, zero = {0.f, 0.f, 0.f, 0.f};
+            const mf::f32x4 x = a.weight && in ? *(const mf::f32x4 *)(a.weight + d) : one;
+            const mf::f32x4 y = a.bias && in ? *(const mf::f32x4 *)(a.bias + d) : zero;
 #pragma unroll
-        for (int j = 0; j < NX; ++j) top = fmaxf(top, fabsf(y.x[j]));
-#pragma unroll
-        for (int off = 1; off < L; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-        const int k = top > 0.f && top < __builtin_inff() ? __builtin_amdgcn_frexp_expf(top) : 0;
-#pragma unroll
-        for (int j = 0; j < NX; ++j) y.x[j] = ldexpf(y.x[j], -k);
-        r = rsqrtf(y.squares(a, l, inv) + ldexpf(a.eps, -2 * k));
-    }
-    if (!live) return;
-    const int64_t w0 = a.per_head ? (int64_t)h * a.D : 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int d = (l + L * i) * E;
-        if (d >= a.D) break;
-        float z[E];
-        unpack<BF>(rz[i], z);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            float x = y.x[i * E + j] * r;
-            if (a.weight) x *= a.weight[w0 + d + j];
-            if (a.bias) x += a.bias[w0 + d + j];
-            y.x[i * E + j] = a.gate ? x * activation(z[j], a.act) : activation(x, a.act);
+            for (int i = 0; i < 4; ++i) { w[j + i] = x[i]; b[j + i] = y[i]; }
         }
-        T *const out = (T *)a.y + t * a.y_row + (int64_t)h * a.D + d;
-        if constexpr (BF) mf::Ops<BF>::st8(out, y.x + i * E);
-        else *(mf::f32x4 *)out = mf::f32x4{y.x[i * E], y.x[i * E + 1], y.x[i * E + 2], y.x[i * E + 3]};
+    };
+    if (!a.per_head) affine(l * E);
+
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        Head<L, V, BF> y;
+        y.take(rx[r]);
+        const float ms = y.squares(a, l, inv) + a.eps;
+        float scale = rsqrtf(ms);
+        if (!(ms >= kLeastSquare && ms < __builtin_inff())) {   // the same in a head's lanes
+            // x and sqrt(eps) as multiples of 2^k, the larger of them within [1/2, 1);
+            // infinities and NaN stay as they are
+            float top = sqrtf(a.eps);
+            y.take(rx[r]);
+#pragma unroll
+            for (int j = 0; j < NX; ++j) top = fmaxf(top, fabsf(y.x[j]));
+#pragma unroll
+            for (int off = 1; off < L; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
+            const int k = top > 0.f && top < __builtin_inff() ? __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+            for (int j = 0; j < NX; ++j) y.x[j] = ldexpf(y.x[j], -k);
+            scale = rsqrtf(y.squares(a, l, inv) + ldexpf(a.eps, -2 * k));
+        }
+        if (a.per_head) affine(at[r]);
+        const bool live = first + r * PER < heads;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float z[E], out[E];
+            unpack<BF>(rz[r][i], z);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const float x = y.x[i * E + j] * scale * w[i * E + j] + b[i * E + j];
+                out[j] = a.gate ? x * activation<BF>(z[j], a.act) : activation<BF>(x, a.act);
+            }
+            T *const dst = (T *)a.y + t[r] * a.y_row + at[r] + L * i * E;
+            if (live && (l + L * i) * E < a.D) {
+                if constexpr (BF) mf::Ops<BF>::st8(dst, out);
+                else *(mf::f32x4 *)dst = mf::f32x4{out[0], out[1], out[2], out[3]};
+            }
+        }
     }
 }
 
+template <int L, int V, int R, bool BF>
+hipError_t launch(const HeadNormArgs &a, hipStream_t s) {
+    constexpr int per = kNormThreads / L * R;
+    const dim3 grid((unsigned)((a.T * a.H + per - 1) / per));
+    hipLaunchKernelGGL((norm_kernel<L, V, R, BF>), grid, dim3(kNormThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// One head a lane where there are too few of them to give each compute unit some workgroups.
 template <int L, int V, bool BF>
 hipError_t launch(const HeadNormArgs &a, hipStream_t s) {
-    constexpr int per = kNormThreads / L;
-    const dim3 grid((unsigned)((a.T * a.H + per - 1) / per));
-    hipLaunchKernelGGL((norm_kernel<L, V, BF>), grid, dim3(kNormThreads), 0, s, a);
-    return hipGetLastError();
+    constexpr int R = V == 1 ? 4 : V == 2 ? 2 : 1;
+    if (a.T * a.H < (int64_t)kNormThreads / L * R * 1024) return launch<L, V, 1, BF>(a, s);
+    return launch<L, V, R, BF>(a, s);
 }
 
 template <bool BF>
 hipError_t pick(const HeadNormArgs &a, hipStream_t s) {
-    const int pieces = (a.D + (BF ? 7 : 3)) / (BF ? 8 : 4);
+    const int pieces = a.D / (BF ? 8 : 4);
     if (pieces <= 1) return launch<1, 1, BF>(a, s);
     if (pieces <= 2) return launch<2, 1, BF>(a, s);
     if (pieces <= 4) return launch<4, 1, BF>(a, s);

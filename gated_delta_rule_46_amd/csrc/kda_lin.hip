@@ -18,10 +18,10 @@
 // the operand of S^T q as they stand.  The tiles of P (C x C, its lower triangle) are
 // shared out over the waves and exchanged through LDS.
 //
-// Chunks are a pipeline with one barrier each.  Before it the waves form P of the chunk and
-// S^T q and put the next chunk's q, k, v (loaded into registers a chunk earlier) into
-// LDS; behind it they add P v and form the new state.  What is read on both sides
-// of the barrier (k, v, decays) has three buffers, q and P two.
+// Chunks are a pipeline with one barrier each.  Before it the waves form P of the chunk, S^T q and the new
+// state, and put the next chunk's q, k, v (loaded into registers a chunk earlier) into the other half of
+// LDS; behind it they add P v (v is an operand in registers by then).  So a wave can be a whole chunk behind
+// another one, and two buffers of everything are enough.
 //
 // A long sequence is cut into segments where there are too few units for the card: a first
 // launch forms what each segment (but the last) adds to the state, from its end backwards
@@ -65,7 +65,7 @@ struct Shape {
     static constexpr int NPK = C * DK / E / THREADS, NPV = C * CW / E / THREADS;
     static constexpr int KB = C * DK * sizeof(T), VB = C * CW * sizeof(T), PB = C * C * sizeof(T);
     static constexpr int DB = (4 * C + 4) * sizeof(float);   // decays of a chunk
-    static constexpr int LDS = 5 * KB + 3 * VB + 2 * PB + 3 * DB;
+    static constexpr int LDS = 4 * KB + 2 * VB + 2 * PB + 2 * DB;
     static constexpr int LDS_STATES = 2 * (KB + VB + DB);    // of the launch that forms the segments' states
     static_assert(C * DK % (E * THREADS) == 0 && C * CW % (E * THREADS) == 0);
     static_assert(LDS <= 160 * 1024);
@@ -419,9 +419,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     using F8 = typename O::F8;
     constexpr int C = X::C, NT = X::NT, NB = X::NB, NKB = X::NKB, DEPTH = X::DEPTH;
     extern __shared__ __align__(16) char lds[];
-    T *const sq = (T *)lds, *const sk = (T *)(lds + 2 * X::KB), *const sv = (T *)(lds + 5 * X::KB);
-    T *const sp = (T *)(lds + 5 * X::KB + 3 * X::VB);
-    char *const sd = lds + 5 * X::KB + 3 * X::VB + 2 * X::PB;
+    T *const sq = (T *)lds, *const sk = (T *)(lds + 2 * X::KB), *const sv = (T *)(lds + 4 * X::KB);
+    T *const sp = (T *)(lds + 4 * X::KB + 2 * X::VB);
+    char *const sd = lds + 4 * X::KB + 2 * X::VB + 2 * X::PB;
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m = lane & 15, gq = lane >> 4;
@@ -464,9 +464,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     };
     auto put = [&](const Chunk &r, int c) {
         r.q.put(sq + c % 2 * C * DK);
-        r.k.put(sk + c % 3 * C * DK);
-        r.v.put(sv + c % 3 * C * X::CW);
-        if (c % X::NW == w) write_decays<X>(sd + c % 3 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
+        r.k.put(sk + c % 2 * C * DK);
+        r.v.put(sv + c % 2 * C * X::CW);
+        if (c % X::NW == w) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
     };
 
     const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
@@ -476,9 +476,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     // further
     auto chunk = [&](int c, Chunk &next) {
         const int valid = min(len - c * C, C);
-        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 3 * C * DK, *const v = sv + c % 3 * C * X::CW;
+        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * X::CW;
         T *const pt = sp + c % 2 * C * C;
-        const Decays<X> s(sd + c % 3 * X::DB);
+        const Decays<X> s(sd + c % 2 * X::DB);
 
         // P^T tiles (rows j, columns i): lane holds 4 consecutive j of its i
         for (int t = w; t < 4; t += X::NW) {
@@ -525,6 +525,11 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
         F8 vf[NB];
         S.values(v, vf);
         const bool rare = __any(any_not_finite<X>(vf, NB));
+        // S <- e^{G_C} S + k^T (weights v)
+        const float all = *s.all;
+        S.each([&](f32x4 &x, int) { x *= all; });
+        S.add(k, vf, s.keep, rare);
+
         put(next, c + 1);
         fetch(next, c + 1 + DEPTH);
         __syncthreads();   // P and the next chunk are there
@@ -545,12 +550,13 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
             for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vp[b], pf);
         }
         if (rare) {
+            const T *const v0 = (const T *)a.v + (t0 + c * C) * a.v_row + (int64_t)h * DV + x0 + col;
             for (int j = 0; j < valid; ++j)
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float x = (float)v[at<T, X::CW>(j, col + 4 * b + r)];
+                        const float x = (float)v0[j * a.v_row + 4 * b + r];
 #pragma unroll
                         for (int it = 0; it < NT; ++it)
                             if (not_finite(x) && j <= 16 * it + m) acc[it][b][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
@@ -569,11 +575,6 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
                 __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, O::cvt4(acc[it][0])), ow, o_at, 16 * it * o_row, 0);
             }
         }
-
-        // S <- e^{G_C} S + k^T (weights v)
-        const float all = *s.all;
-        S.each([&](f32x4 &x, int) { x *= all; });
-        S.add(k, vf, s.keep, rare);
 
         const int end = (c + 1) * C;
         if (valid == C && a.interval && (skip + end) % a.interval == 0)

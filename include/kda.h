@@ -685,7 +685,7 @@ int kda_lin_decode(const kda_lin_config *cfg, int32_t N, const void *q, int64_t 
  *       bytes); y may be x or gate itself with the same distance;
  *   weight, bias: fp32 [D], or [H,D] with per_head = 1; NULL = ones, zeros;
  *   eps >= 0;  act: KDA_ACT_NONE, KDA_ACT_SILU or KDA_ACT_SIGMOID;
- *   D a multiple of 8, at most 1024; T * H at most 2^26.
+ *   D a multiple of 8, at most 1024; T * H at most 2^26, H * D at most 2^30.
  * fp32 arithmetic, one rounding at the store; the squares of any finite head
  * neither overflow nor vanish (it is scaled by a power of two where they
  * would).  T = 0 is a no-op.  No workspace.  One launch.

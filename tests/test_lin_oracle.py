@@ -181,6 +181,7 @@ def test_head_norm_is_checked():
     for D in (0, -8, 12, 1032):
         assert norm(D=D, x_row=8192, gate_row=8192, y_row=8192) == U
     assert norm(T=(1 << 24) + 1) == U
+    assert norm(H=(1 << 24) + 1, D=64, T=1, x_row=1 << 31, gate_row=1 << 31, y_row=1 << 31) == U
     assert norm(per_head=2) == E and norm(center=-1) == E and norm(act=3) == E
     for eps in (-1e-6, float("inf"), float("nan")):
         assert norm(eps=eps) == E
