@@ -1182,7 +1182,7 @@ size_t kda_lin_prefill_workspace(const kda_lin_config *cfg, int64_t T, int32_t N
     kda::LinArgs a{};
     a.N = N; a.T = T; a.Hv = cfg->num_v_heads;
     kda::lin_plan(device_cus(), &a);
-    return round256(kda::lin_bytes(cfg->dk, cfg->dv, a));
+    return round256(kda::lin_buffers(cfg->dk, cfg->dv, nullptr, &a));
 }
 
 int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, const void *k,
@@ -1206,12 +1206,11 @@ int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, con
         a.interval = ckpt->interval; a.ckpt_off = ckpt->offsets; a.ckpt = ckpt->states;
     }
     kda::lin_plan(device_cus(), &a);
-    const size_t need = round256(kda::lin_bytes(cfg->dk, cfg->dv, a));
+    const size_t need = round256(kda::lin_buffers(cfg->dk, cfg->dv, (char *)ws, &a));
     if (need) {
         if (!ws || ws_bytes < need)
             return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws_bytes);
         KDA_TRY(check_tensor(ws, "ws", true));
-        kda::lin_buffers(cfg->dk, cfg->dv, ws, &a);
     }
     return launched(kda::launch_lin(cfg->io_dtype == KDA_DTYPE_BF16, cfg->dk, cfg->dv, a, (hipStream_t)stream),
                     "linear attention");

@@ -27,22 +27,23 @@ struct LinArgs {
     const int64_t *ckpt_off;     // first rung row per sequence (nullable for N = 1)
     float *ckpt;                 // rung rows
     // Sequences longer than `seg` tokens in segments of so many (0: none is split).  Segment s of a
-    // sequence that starts at token c is unit n + c / seg + s and stretch c / seg + s, and finds its
-    // incoming state at slot 2 (c / seg) + s: no two units, segments with another behind them, or split
-    // sequences meet, whatever the lengths are.  What a segment adds to the state is formed in
-    // `pieces` pieces of `piece` tokens.
-    int32_t seg, units, slots, stretches;   // units: N + T / seg; slots: 2 (T / seg); stretches: T / seg
+    // sequence that starts at token c lies in stretch c / seg + s: no two segments with another behind
+    // them share one, whatever the lengths are.  A unit is such a stretch, or the last segment of a sequence.
+    // A split sequence's segment finds its incoming state at slot 2 (c / seg) + s.  What a segment adds to the
+    // state is formed in `pieces` pieces of `piece` tokens.
+    int32_t seg, slots, stretches;          // slots: 2 (T / seg); stretches: T / seg
     int32_t piece, pieces;
+    bool ordered;                // whether there is an order
+    int32_t *order;              // [N] sequences by the length of their last segment (null: as they come)
     float *carry;                // [slots,Hv,dk,dv]
     float *part;                 // [stretches,pieces,Hv,dk,dv]
     float *kept;                 // [stretches,Hv] decay over a segment
     int32_t *live;               // [stretches,pieces,Hv] whether the piece adds anything
     double *sums;                // [stretches,seg/64,Hv] log2 decays of 64 tokens (with more than one piece)
 };
-// The plan of a call on a device of `cus` compute units, the bytes of its buffers, and the buffers.
+// The plan of a call on a device of `cus` compute units; its buffers at ws, and their bytes.
 void lin_plan(int cus, LinArgs *a);
-size_t lin_bytes(int dk, int dv, const LinArgs &a);
-void lin_buffers(int dk, int dv, void *ws, LinArgs *a);
+size_t lin_buffers(int dk, int dv, char *ws, LinArgs *a);
 bool lin_supported(int dk, int dv);
 hipError_t launch_lin(bool bf16, int dk, int dv, const LinArgs &a, hipStream_t s);
 // one token per sequence: T and cu unused

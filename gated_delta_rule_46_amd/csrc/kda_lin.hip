@@ -53,21 +53,20 @@ struct Shape {
     using O = mf::Ops<BF>;
     using T = typename O::T;
     static constexpr int C = 32, NT = C / 16;       // tokens per chunk, tiles of 16
-    static constexpr int CW = DV, NCB = DV / CW;   // value columns of a workgroup
     static constexpr int NW = BF ? 4 : DV / 16, THREADS = 64 * NW;
-    static constexpr int NB = CW / 16 / NW;         // column tiles of a wave
+    static constexpr int NB = DV / 16 / NW;         // column tiles of a wave
     static_assert(NB == 1 || NB == 2);
     static constexpr int NKB = DK / 32;
     static constexpr int DEPTH = 1;                 // chunks on their way in registers
     static constexpr int DEPTH_STATES = 1;          // and in the launch that forms the segments' states
     static constexpr int TERMS = BF ? 3 : 1;        // operand terms that hold an fp32 value
     static constexpr int E = 16 / sizeof(T);        // elements of a 16-byte piece
-    static constexpr int NPK = C * DK / E / THREADS, NPV = C * CW / E / THREADS;
-    static constexpr int KB = C * DK * sizeof(T), VB = C * CW * sizeof(T), PB = C * C * sizeof(T);
+    static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
+    static constexpr int KB = C * DK * sizeof(T), VB = C * DV * sizeof(T), PB = C * C * sizeof(T);
     static constexpr int DB = (4 * C + 4) * sizeof(float);   // decays of a chunk
     static constexpr int LDS = 4 * KB + 2 * VB + 2 * PB + 2 * DB;
     static constexpr int LDS_STATES = 2 * (KB + VB + DB);    // of the launch that forms the segments' states
-    static_assert(C * DK % (E * THREADS) == 0 && C * CW % (E * THREADS) == 0);
+    static_assert(C * DK % (E * THREADS) == 0 && C * DV % (E * THREADS) == 0);
     static_assert(LDS <= 160 * 1024);
 };
 
@@ -350,7 +349,7 @@ struct State {
     // v^T of the wave's columns
     __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
-        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::CW, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
+        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
     }
     // s += k^T (weights v)
     __device__ __forceinline__ void add(const typename X::T *k, const typename X::O::F8 *v, const float *keep, bool rare) {
@@ -399,18 +398,6 @@ __device__ __forceinline__ int seg_of(const LinArgs &a, int n) {
     return (int)((uint32_t)min(max(a.cu[n], (int64_t)0), a.T) / (uint32_t)a.seg);
 }
 
-// Unit, head and column block of a workgroup.  The column blocks of a head read the same q and k:
-// they stand 8 workgroups apart, which puts them on one XCD, behind one L2, at the same time.
-struct Block { int unit, h, cb; };
-template <class X>
-__device__ __forceinline__ Block block_of(const LinArgs &a) {
-    const int lane = blockIdx.x % 8, rest = blockIdx.x / 8;
-    const int item = rest / X::NCB * 8 + lane;
-    return {item / a.Hv, item % a.Hv, rest % X::NCB};
-}
-template <class X>
-int64_t blocks_of(int64_t units, int Hv) { return (units * Hv + 7) / 8 * 8 * X::NCB; }
-
 template <int DK, int DV, bool BF>
 __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
@@ -425,30 +412,31 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m = lane & 15, gq = lane >> 4;
-    const Block blk = block_of<X>(a);
-    const int unit = blk.unit, h = blk.h, x0 = blk.cb * X::CW;
-    if (unit >= a.units) return;
+    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
     const int hk = h / (a.Hv / a.Hk);
-    const int n = a.seg ? last_not_above(a.N, unit, [&](int i) { return (int64_t)i + seg_of(a, i); }) : unit;
+    const bool last = unit >= a.stretches;
+    int n = unit - a.stretches;
+    if (!last) n = last_not_above(a.N, unit, [&](int i) { return (int64_t)seg_of(a, i); });
+    else if (a.order) n = a.order[n];
     const Seq seq(a, n);
-    const int seg = a.seg ? unit - n - seq.first : 0;
-    if (seg >= seq.segs) return;
+    const int seg = last ? seq.segs - 1 : unit - seq.first;
+    if (!last && (seg < 0 || seg + 1 >= seq.segs)) return;
     const int skip = seg * a.seg;                        // tokens before the unit
-    const int len = seg + 1 < seq.segs ? a.seg : seq.len - skip;
+    const int len = last ? seq.len - skip : a.seg;
     const int64_t t0 = seq.c0 + skip;
 
     State<X> S;
     {
         const float *src = seq.segs > 1 ? a.carry + (int64_t)(2 * seq.first + seg) * a.Hv * S.SIZE
                                         : slot_of(a, a.read_idx, n, S.SIZE);
-        S.load(src ? src + h * S.SIZE + x0 : nullptr);
+        S.load(src ? src + h * S.SIZE : nullptr);
     }
 
     Source<X, DK> fq(a.q, t0, a.q_row, hk * DK), fk(a.k, t0, a.k_row, hk * DK);
-    Source<X, X::CW> fv(a.v, t0, a.v_row, (int64_t)h * DV + x0);
+    Source<X, DV> fv(a.v, t0, a.v_row, (int64_t)h * DV);
     const char *fg = (const char *)(a.g + t0 * a.g_row + h);
     const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
-    struct Chunk { Rows<X, DK> q, k; Rows<X, X::CW> v; float g; };
+    struct Chunk { Rows<X, DK> q, k; Rows<X, DV> v; float g; };
     // the next chunk that has not been fetched; always as many loads, so that waiting for them waits for
     // nothing else
     auto fetch = [&](Chunk &r, int c) {
@@ -465,18 +453,18 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     auto put = [&](const Chunk &r, int c) {
         r.q.put(sq + c % 2 * C * DK);
         r.k.put(sk + c % 2 * C * DK);
-        r.v.put(sv + c % 2 * C * X::CW);
+        r.v.put(sv + c % 2 * C * DV);
         if (c % X::NW == w) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
     };
 
     const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
     const int o_row = a.Hv * DV * (int)sizeof(T), o_at = m * o_row + col * (int)sizeof(T);
-    const char *out = (const char *)((T *)a.o + (t0 * a.Hv + h) * DV + x0);
+    const char *out = (const char *)((T *)a.o + (t0 * a.Hv + h) * DV);
     // chunk c, whose rows are in LDS; `next` holds those of the one behind it, and takes those of the one DEPTH
     // further
     auto chunk = [&](int c, Chunk &next) {
         const int valid = min(len - c * C, C);
-        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * X::CW;
+        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
         T *const pt = sp + c % 2 * C * C;
         const Decays<X> s(sd + c % 2 * X::DB);
 
@@ -550,7 +538,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
             for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vp[b], pf);
         }
         if (rare) {
-            const T *const v0 = (const T *)a.v + (t0 + c * C) * a.v_row + (int64_t)h * DV + x0 + col;
+            const T *const v0 = (const T *)a.v + (t0 + c * C) * a.v_row + (int64_t)h * DV + col;
             for (int j = 0; j < valid; ++j)
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
@@ -562,7 +550,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
                             if (not_finite(x) && j <= 16 * it + m) acc[it][b][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
                     }
         }
-        const auto ow = window(out, valid, o_row, X::CW * (int)sizeof(T));
+        const auto ow = window(out, valid, o_row, DV * (int)sizeof(T));
         out += (int64_t)o_row * C;
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
@@ -578,7 +566,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 
         const int end = (c + 1) * C;
         if (valid == C && a.interval && (skip + end) % a.interval == 0)
-            S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE + x0);
+            S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE);
     };
 
     if (len > 0) {
@@ -595,9 +583,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
         }
     }
 
-    if (seg + 1 == seq.segs) {
+    if (last) {
         float *dst = slot_of(a, a.write_idx, n, S.SIZE);
-        if (dst) S.store(dst + h * S.SIZE + x0);
+        if (dst) S.store(dst + h * S.SIZE);
     }
 }
 
@@ -650,11 +638,9 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     char *const sd = lds + 2 * (X::KB + X::VB);
 
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const Block blk = block_of<X>(a);
     // heads that remember longest take most of the time: they come at another place in each unit's row, as
     // workgroups are dealt out to the compute units in turn
-    const int unit = blk.unit, h = (blk.h + unit) % a.Hv, x0 = blk.cb * X::CW;
-    if (unit >= a.stretches * a.pieces) return;
+    const int unit = blockIdx.x / a.Hv, h = (blockIdx.x - unit * a.Hv + unit) % a.Hv;
     const int stretch = unit / a.pieces, piece = unit - stretch * a.pieces;
     const int hk = h / (a.Hv / a.Hk);
     // only the last sequence that starts in or before a stretch can have a segment here
@@ -692,10 +678,10 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     S.load(nullptr);
     const int chunks = len / C;
     Source<X, DK> fk(a.k, t0 + len - C, a.k_row, hk * DK);
-    Source<X, X::CW> fv(a.v, t0 + len - C, a.v_row, (int64_t)h * DV + x0);
+    Source<X, DV> fv(a.v, t0 + len - C, a.v_row, (int64_t)h * DV);
     const char *fg = (const char *)(a.g + (t0 + len - C) * a.g_row + h);
     const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
-    struct Chunk { Rows<X, DK> k; Rows<X, X::CW> v; float g; };
+    struct Chunk { Rows<X, DK> k; Rows<X, DV> v; float g; };
     auto fetch = [&](Chunk &r, int c) {         // the c-th chunk from the end
         const int valid = c < chunks ? C : 0;
         r.k.fetch(fk, valid);
@@ -707,7 +693,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     };
     auto put = [&](const Chunk &r, int c) {
         r.k.put(sk + c % 2 * C * DK);
-        r.v.put(sv + c % 2 * C * X::CW);
+        r.v.put(sv + c % 2 * C * DV);
         if (c % X::NW == w) {
             const Decays<X> s(sd + c % 2 * X::DB);
             double all;
@@ -734,14 +720,14 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
             more = c + i + 1 < chunks && !(rest < kGone);
             if (more) put(r[(i + 1) % DEPTH], c + i + 1);
             fetch(r[(i + 1) % DEPTH], c + i + 1 + DEPTH);
-            const T *const k = sk + (c + i) % 2 * C * DK, *const v = sv + (c + i) % 2 * C * X::CW;
+            const T *const k = sk + (c + i) % 2 * C * DK, *const v = sv + (c + i) % 2 * C * DV;
             const Decays<X> s(sd + (c + i) % 2 * X::DB);
             typename X::O::F8 vf[X::NB];
             S.values(v, vf);
             S.add(k, vf, s.keep, __any(any_not_finite<X>(vf, X::NB)));
         }
     }
-    S.store(a.part + slot * S.SIZE + x0);
+    S.store(a.part + slot * S.SIZE);
     if (threadIdx.x == 0 && piece == 0) a.kept[kept] = exp2_of(rest);
 }
 
@@ -802,9 +788,34 @@ hipError_t start(K *kernel, int64_t grid, int threads, int lds, const LinArgs &a
     return hipGetLastError();
 }
 
+// Sequences by the length of their last segment, the longest first: workgroups start in this
+// order, and the short ones fill up what the long ones leave.
+constexpr int kOrderThreads = 1024;
+__global__ __launch_bounds__(kOrderThreads) void lin_order_kernel(const LinArgs a) {
+    __shared__ int s_len[kOrderThreads];
+    const int n = threadIdx.x;
+    int len = 0;
+    if (n < a.N) {
+        const int begin = (int)min(max(a.cu[n], (int64_t)0), a.T), end = (int)min(max(a.cu[n + 1], (int64_t)0), a.T);
+        len = max(end - begin, 0);
+        if (a.seg && len > a.seg) len -= (len - 1) / a.seg * a.seg;
+    }
+    s_len[n] = len;
+    __syncthreads();
+    if (n >= a.N) return;
+    int rank = 0;
+    for (int i = 0; i < a.N; ++i) rank += s_len[i] > len || (s_len[i] == len && i < n);
+    a.order[rank] = n;
+}
+
 template <int DK, int DV, bool BF>
 hipError_t launch(const LinArgs &a, hipStream_t s) {
     using X = Shape<DK, DV, BF>;
+    if (a.order) {
+        hipLaunchKernelGGL(lin_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (a.seg) {
         hipError_t e = hipSuccess;
         if (a.pieces > 1) {
@@ -812,48 +823,53 @@ hipError_t launch(const LinArgs &a, hipStream_t s) {
             hipLaunchKernelGGL(lin_sums_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, s, a);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        e = start(lin_states_kernel<DK, DV, BF>, blocks_of<X>((int64_t)a.stretches * a.pieces, a.Hv), X::THREADS, X::LDS_STATES, a, s);
+        e = start(lin_states_kernel<DK, DV, BF>, (int64_t)a.stretches * a.pieces * a.Hv, X::THREADS, X::LDS_STATES, a, s);
         if (e != hipSuccess) return e;
         const int64_t grid = (int64_t)a.stretches * a.Hv * (DK * DV / (4 * kCarryThreads));
         hipLaunchKernelGGL(lin_carry_kernel, dim3((unsigned)grid), dim3(kCarryThreads), 0, s, a, DK * DV);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    return start(lin_kernel<DK, DV, BF>, blocks_of<X>(a.units, a.Hv), X::THREADS, X::LDS, a, s);
+    return start(lin_kernel<DK, DV, BF>, ((int64_t)a.stretches + a.N) * a.Hv, X::THREADS, X::LDS, a, s);
 }
 
 constexpr int kLeastSegment = 512;
 constexpr int kLeastPiece = 1024;
+constexpr int kLeastOrdered = 128;   // tokens of a sequence on average
 
 }  // namespace
 
 void lin_plan(int cus, LinArgs *a) {
     a->seg = a->slots = a->stretches = a->piece = a->pieces = 0;
-    a->units = a->N;
+    a->order = nullptr;
+    a->ordered = a->N > 1 && a->N <= kOrderThreads && (int64_t)a->N * a->Hv > 2 * cus && a->T / a->N >= kLeastOrdered;
     const int64_t per_head = std::max(2 * cus / a->Hv, 1);
     const int64_t seg = std::max<int64_t>(((a->T + per_head - 1) / per_head + 63) / 64 * 64, kLeastSegment);
     if (a->T <= seg) return;          // no sequence can be longer
     a->seg = (int32_t)seg;
     a->stretches = (int32_t)(a->T / seg);
-    a->units = a->N + a->stretches;
     a->slots = 2 * a->stretches;
     const int32_t pieces = (int32_t)std::max<int64_t>(std::min<int64_t>(kMaxPieces, seg / kLeastPiece), 1);
     a->piece = ((a->seg + pieces - 1) / pieces + 63) / 64 * 64;
     a->pieces = (a->seg + a->piece - 1) / a->piece;
 }
 
-size_t lin_bytes(int dk, int dv, const LinArgs &a) {
-    const size_t size = (size_t)dk * dv, pieces = (size_t)a.stretches * a.pieces;
-    const size_t sums = a.pieces > 1 ? (size_t)a.stretches * (a.seg / kSum) * sizeof(double) : 0;
-    return a.Hv * ((((size_t)a.slots + pieces) * size + a.stretches + pieces) * sizeof(float) + sums);
-}
-
-void lin_buffers(int dk, int dv, void *ws, LinArgs *a) {
-    const size_t size = (size_t)dk * dv, pieces = (size_t)a->stretches * a->pieces;
-    a->carry = (float *)ws;
-    a->part = a->carry + a->slots * a->Hv * size;
-    a->sums = (double *)(a->part + pieces * a->Hv * size);
-    a->kept = (float *)(a->sums + (a->pieces > 1 ? (size_t)a->stretches * (a->seg / kSum) * a->Hv : 0));
-    a->live = (int32_t *)(a->kept + (size_t)a->stretches * a->Hv);
+// The buffers, from the largest alignment to the smallest.
+size_t lin_buffers(int dk, int dv, char *ws, LinArgs *a) {
+    const size_t state = (size_t)dk * dv * sizeof(float) * a->Hv, pieces = (size_t)a->stretches * a->pieces;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char *const p = ws + at;
+        at += bytes;
+        return p;
+    };
+    a->carry = (float *)take(a->slots * state);
+    a->part = (float *)take(pieces * state);
+    a->sums = (double *)take(a->pieces > 1 ? (size_t)a->stretches * (a->seg / kSum) * a->Hv * sizeof(double) : 0);
+    a->kept = (float *)take((size_t)a->stretches * a->Hv * sizeof(float));
+    a->live = (int32_t *)take(pieces * a->Hv * sizeof(int32_t));
+    char *const order = take(a->ordered ? a->N * sizeof(int32_t) : 0);
+    if (a->ordered) a->order = (int32_t *)order;
+    return at;
 }
 
 bool lin_supported(int dk, int dv) { return (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
