@@ -57,8 +57,6 @@ struct Shape {
     static constexpr int NB = DV / 16 / NW;         // column tiles of a wave
     static_assert(NB == 1 || NB == 2);
     static constexpr int NKB = DK / 32;
-    static constexpr int DEPTH = 1;                 // chunks on their way in registers
-    static constexpr int DEPTH_STATES = 1;          // and in the launch that forms the segments' states
     static constexpr int TERMS = BF ? 3 : 1;        // operand terms that hold an fp32 value
     static constexpr int E = 16 / sizeof(T);        // elements of a 16-byte piece
     static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
@@ -151,10 +149,10 @@ __device__ __forceinline__ bool any_not_finite(const typename X::O::F8 *f, int n
 
 template <class X> struct Terms { typename X::O::F8 t[X::TERMS]; };
 
-// fp32 values as operand terms.  bf16: three times the upper half of what is left, which holds all
-// 24 bits; an infinity would leave a NaN behind its first term (`rare`: it leaves nothing).
+// Finite fp32 values as operand terms.  bf16: three times the upper half of what is left, which holds all
+// 24 bits.
 template <class X>
-__device__ __forceinline__ Terms<X> terms8(const float *x, bool rare) {
+__device__ __forceinline__ Terms<X> terms8(const float *x) {
     Terms<X> r;
     if constexpr (X::BF) {
         float y[8];
@@ -169,10 +167,6 @@ __device__ __forceinline__ Terms<X> terms8(const float *x, bool rare) {
             if (t + 1 < X::TERMS) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] -= bits_f32(f32_bits(y[j]) & 0xffff0000u);
-                if (rare) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = t == 0 && not_finite(x[j]) ? 0.f : y[j];
-                }
             }
         }
     } else {
@@ -346,13 +340,37 @@ struct State {
             for (int i = 0; i < 4; ++i) dst[at + i * X::DV] = x[i];
         });
     }
-    // v^T of the wave's columns
-    __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
+    // v^T of the wave's columns with zeros in place of infinities and NaN; returns whether there are any
+    __device__ __forceinline__ static bool values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
         for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
+        const bool rare = __any(any_not_finite<X>(vf, X::NB));
+        if (rare) {
+#pragma unroll
+            for (int b = 0; b < X::NB; ++b) vf[b] = finite_part<X>(vf[b]);
+        }
+        return rare;
+    }
+    // s += k^T (weights v) for the infinities and NaN that values() left out, token by token
+    __device__ __forceinline__ void add_rare(const typename X::T *k, const typename X::T *v, const float *keep) {
+        using T = typename X::T;
+        const int lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4;
+        for (int j = 0; j < X::C; ++j)
+#pragma unroll
+            for (int b = 0; b < X::NB; ++b) {
+                const float x = (float)v[at<T, X::DV>(j, 16 * X::NB * (threadIdx.x >> 6) + STEP * (m >> 2) + (m & 3) + 4 * b)];
+                if (!not_finite(x)) continue;
+#pragma unroll
+                for (int kb = 0; kb < X::NKB; ++kb)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[b][kb][hf][i] += (float)k[at<T, X::DK>(j, 32 * kb + 8 * gq + 4 * hf + i)] * (x * keep[j]);
+            }
     }
     // s += k^T (weights v)
-    __device__ __forceinline__ void add(const typename X::T *k, const typename X::O::F8 *v, const float *keep, bool rare) {
+    __device__ __forceinline__ void add(const typename X::T *k, const typename X::O::F8 *v, const float *keep) {
         float wt[8];
         mf::load8f(keep + 8 * ((threadIdx.x & 63) >> 4), wt);
         Terms<X> wv[X::NB];
@@ -362,7 +380,7 @@ struct State {
             X::O::unpack8(v[b], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= wt[e];
-            wv[b] = terms8<X>(x, rare);
+            wv[b] = terms8<X>(x);
         }
 #pragma unroll
         for (int kb = 0; kb < X::NKB; ++kb)
@@ -398,13 +416,17 @@ __device__ __forceinline__ int seg_of(const LinArgs &a, int n) {
     return (int)((uint32_t)min(max(a.cu[n], (int64_t)0), a.T) / (uint32_t)a.seg);
 }
 
+// Head of the b-th workgroup of a unit.  Neighbouring heads, which may share q and k, stand 8 workgroups
+// apart: on one XCD, behind one L2.
+__device__ __forceinline__ int head_of(const LinArgs &a, int b) { return a.Hv % 8 ? b : b % 8 * (a.Hv / 8) + b / 8; }
+
 template <int DK, int DV, bool BF>
 __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
     using O = typename X::O;
     using T = typename X::T;
     using F8 = typename O::F8;
-    constexpr int C = X::C, NT = X::NT, NB = X::NB, NKB = X::NKB, DEPTH = X::DEPTH;
+    constexpr int C = X::C, NT = X::NT, NB = X::NB, NKB = X::NKB;
     extern __shared__ __align__(16) char lds[];
     T *const sq = (T *)lds, *const sk = (T *)(lds + 2 * X::KB), *const sv = (T *)(lds + 4 * X::KB);
     T *const sp = (T *)(lds + 4 * X::KB + 2 * X::VB);
@@ -412,7 +434,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m = lane & 15, gq = lane >> 4;
-    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
+    const int unit = blockIdx.x / a.Hv, h = head_of(a, blockIdx.x - unit * a.Hv);
     const int hk = h / (a.Hv / a.Hk);
     const bool last = unit >= a.stretches;
     int n = unit - a.stretches;
@@ -460,25 +482,24 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
     const int o_row = a.Hv * DV * (int)sizeof(T), o_at = m * o_row + col * (int)sizeof(T);
     const char *out = (const char *)((T *)a.o + (t0 * a.Hv + h) * DV);
-    // chunk c, whose rows are in LDS; `next` holds those of the one behind it, and takes those of the one DEPTH
-    // further
+    // chunk c, whose rows are in LDS; `next` holds those of the one behind it, and takes those of the one further
     auto chunk = [&](int c, Chunk &next) {
         const int valid = min(len - c * C, C);
         const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
         T *const pt = sp + c % 2 * C * C;
         const Decays<X> s(sd + c % 2 * X::DB);
 
-        // P^T tiles (rows j, columns i): lane holds 4 consecutive j of its i
-        for (int t = w; t < 4; t += X::NW) {
-            const int i = 16 * (t > 0) + m, j = 16 * (t > 1) + 4 * gq;
-            if (t == 3) {                               // the upper one
-                O::st4(pt + at<T, C>(m, 16 + 4 * gq), f32x4{0.f, 0.f, 0.f, 0.f});
-                break;
-            }
+        F8 vf[NB];
+        const bool rare = S.values(v, vf);
+
+        // P^T tiles (rows j, columns i), one a wave, zeros above the diagonal: lane holds 4 consecutive j of its i
+        if (X::NW == 4 || w < 4) {
+            const int it = w == 1 || w == 2, jt = w >= 2;
+            const int i = 16 * it + m, j = 16 * jt + 4 * gq;
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb)
-                p = O::mma32(p, ld_r<X, DK>(k, 16 * (t > 1) + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
+                p = O::mma32(p, ld_r<X, DK>(k, 16 * jt + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
             const f32x4 hj = *(const f32x4 *)(s.hi + j), lj = *(const f32x4 *)(s.lo + j);
             const float hi = s.hi[i], li = s.lo[i];
 #pragma unroll
@@ -510,34 +531,23 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 #pragma unroll
             for (int b = 0; b < NB; ++b) acc[it][b] *= s.out[16 * it + m];
 
-        F8 vf[NB];
-        S.values(v, vf);
-        const bool rare = __any(any_not_finite<X>(vf, NB));
         // S <- e^{G_C} S + k^T (weights v)
         const float all = *s.all;
         S.each([&](f32x4 &x, int) { x *= all; });
-        S.add(k, vf, s.keep, rare);
+        S.add(k, vf, s.keep);
+        if (rare) S.add_rare(k, v, s.keep);
 
         put(next, c + 1);
-        fetch(next, c + 1 + DEPTH);
+        fetch(next, c + 2);
         __syncthreads();   // P and the next chunk are there
 
-        // infinities and NaN must not meet the zeros of P above its diagonal: they are left out of
-        // the products and added token by token
-        F8 vp[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) vp[b] = vf[b];
-        if (rare) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) vp[b] = finite_part<X>(vf[b]);
-        }
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
             const F8 pf = ld_r<X, C>(pt, 16 * it + m, 8 * gq);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vp[b], pf);
+            for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vf[b], pf);
         }
-        if (rare) {
+        if (rare) {   // infinities and NaN must not meet the zeros of P above its diagonal: token by token
             const T *const v0 = (const T *)a.v + (t0 + c * C) * a.v_row + (int64_t)h * DV + col;
             for (int j = 0; j < valid; ++j)
 #pragma unroll
@@ -570,17 +580,12 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
     };
 
     if (len > 0) {
-        Chunk r[DEPTH];
-        fetch(r[0], 0);
-        put(r[0], 0);
-#pragma unroll
-        for (int i = 1; i <= DEPTH; ++i) fetch(r[i % DEPTH], i);
+        Chunk next;
+        fetch(next, 0);
+        put(next, 0);
+        fetch(next, 1);
         __syncthreads();
-        for (int c = 0; c * C < len; c += DEPTH) {
-#pragma unroll
-            for (int i = 0; i < DEPTH; ++i)
-                if (i == 0 || (c + i) * C < len) chunk(c + i, r[(i + 1) % DEPTH]);
-        }
+        for (int c = 0; c * C < len; ++c) chunk(c, next);
     }
 
     if (last) {
@@ -639,8 +644,8 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
 
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     // heads that remember longest take most of the time: they come at another place in each unit's row, as
-    // workgroups are dealt out to the compute units in turn
-    const int unit = blockIdx.x / a.Hv, h = (blockIdx.x - unit * a.Hv + unit) % a.Hv;
+    // workgroups are dealt out to the XCDs and their compute units in turn
+    const int unit = blockIdx.x / a.Hv, h = head_of(a, (blockIdx.x - unit * a.Hv + unit + unit / 8) % a.Hv);
     const int stretch = unit / a.pieces, piece = unit - stretch * a.pieces;
     const int hk = h / (a.Hv / a.Hk);
     // only the last sequence that starts in or before a stretch can have a segment here
@@ -704,28 +709,23 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
         }
     };
 
-    constexpr int DEPTH = X::DEPTH_STATES;
-    Chunk r[DEPTH];
-    fetch(r[0], 0);
-    put(r[0], 0);
-#pragma unroll
-    for (int i = 1; i <= DEPTH; ++i) fetch(r[i % DEPTH], i);
+    Chunk next;
+    fetch(next, 0);
+    put(next, 0);
+    fetch(next, 1);
     bool more = true;
-    for (int c = 0; more; c += DEPTH) {
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-            if (!more) break;
-            __syncthreads();
-            rest = s_rest[(c + i) % 2];
-            more = c + i + 1 < chunks && !(rest < kGone);
-            if (more) put(r[(i + 1) % DEPTH], c + i + 1);
-            fetch(r[(i + 1) % DEPTH], c + i + 1 + DEPTH);
-            const T *const k = sk + (c + i) % 2 * C * DK, *const v = sv + (c + i) % 2 * C * DV;
-            const Decays<X> s(sd + (c + i) % 2 * X::DB);
-            typename X::O::F8 vf[X::NB];
-            S.values(v, vf);
-            S.add(k, vf, s.keep, __any(any_not_finite<X>(vf, X::NB)));
-        }
+    for (int c = 0; more; ++c) {
+        __syncthreads();
+        rest = s_rest[c % 2];
+        more = c + 1 < chunks && !(rest < kGone);
+        if (more) put(next, c + 1);
+        fetch(next, c + 2);
+        const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
+        const Decays<X> s(sd + c % 2 * X::DB);
+        typename X::O::F8 vf[X::NB];
+        const bool rare = S.values(v, vf);
+        S.add(k, vf, s.keep);
+        if (rare) S.add_rare(k, v, s.keep);
     }
     S.store(a.part + slot * S.SIZE);
     if (threadIdx.x == 0 && piece == 0) a.kept[kept] = exp2_of(rest);
@@ -747,33 +747,38 @@ __global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs 
     float *dst = a.carry + ((int64_t)2 * stretch * a.Hv + h) * size + at;
     *(f32x4 *)dst = S;
     constexpr int G = 4;              // segments whose parts are on their way at once
+    float kept[G];
+    int live[G][kMaxPieces];
+    auto look = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const int s = stretch + min(s0 + i, seq.segs - 2);
+            kept[i] = a.kept[(int64_t)s * a.Hv + h];
+#pragma unroll
+            for (int p = 0; p < kMaxPieces; ++p)
+                live[i][p] = p < a.pieces ? a.live[((int64_t)s * a.pieces + p) * a.Hv + h] : 0;
+        }
+    };
+    look(0);
     for (int s0 = 0; s0 + 1 < seq.segs; s0 += G) {
-        float kept[G];
-        bool live[G][kMaxPieces];
+        float keep[G];
         f32x4 part[G][kMaxPieces];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            const int s = min(s0 + i, seq.segs - 2);
-            kept[i] = a.kept[(int64_t)(stretch + s) * a.Hv + h];
-#pragma unroll
-            for (int p = 0; p < kMaxPieces; ++p)
-                live[i][p] = p < a.pieces && a.live[((int64_t)(stretch + s) * a.pieces + p) * a.Hv + h];
-        }
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
             const int64_t s = stretch + min(s0 + i, seq.segs - 2);
+            keep[i] = kept[i];
 #pragma unroll
             for (int p = 0; p < kMaxPieces; ++p) {
                 part[i][p] = f32x4{0.f, 0.f, 0.f, 0.f};
                 if (live[i][p]) part[i][p] = *(const f32x4 *)(a.part + ((s * a.pieces + p) * a.Hv + h) * size + at);
             }
         }
+        look(s0 + G);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            S *= kept[i];
+            S *= keep[i];
 #pragma unroll
-            for (int p = 0; p < kMaxPieces; ++p)
-                if (live[i][p]) S += part[i][p];
+            for (int p = 0; p < kMaxPieces; ++p) S += part[i][p];
             dst += (int64_t)a.Hv * size;
             if (s0 + i + 1 < seq.segs) *(f32x4 *)dst = S;
         }

@@ -96,10 +96,14 @@ class Call:
             self.g = f32(np.where(rng.random((T, Hv)) < 0.4, -60.0 * rng.random((T, Hv)), -0.01 * rng.random((T, Hv))))
         N = len(lens)
         self.pool = f32(rng.normal(size=(2 * N + 2, Hv, dk, dv)))
-        order = rng.permutation(2 * N + 2)
-        self.read, self.write = order[:N].copy(), order[N:2 * N].copy()
+        # slots of their own for all that are not given: a write slot is no other sequence's read or write slot
+        given = {x for _, r, w in slots for x in (r, w)}
+        rest = [x for x in rng.permutation(2 * N + 2) if x not in given]
+        self.read, self.write = np.full(N, -1), np.full(N, -1)
         for n, r, w in slots:
             self.read[n], self.write[n] = r, w
+        for n in set(range(N)) - {n for n, _, _ in slots}:
+            self.read[n], self.write[n] = rest.pop(), rest.pop()
 
     def oracle(self, interval=0, scale=1.0, size=False):
         f = (lambda x: np.abs(to_numpy_f64(x))) if size else to_numpy_f64
