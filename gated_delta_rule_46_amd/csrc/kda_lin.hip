@@ -62,7 +62,9 @@ struct Shape {
     static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
     static constexpr int KB = C * DK * sizeof(T), VB = C * DV * sizeof(T), PB = C * C * sizeof(T);
     static constexpr int DB = (4 * C + 4) * sizeof(float);   // decays of a chunk
-    static constexpr int LDS = 4 * KB + 2 * VB + 2 * PB + 2 * DB;
+    // Two workgroups a compute unit, which is what the calls are cut for: where three or four fit they are
+    // dealt out unevenly (16 sequences of 8,192 tokens at 32 heads of 64: 574 us with two, 651 with three).
+    static constexpr int LDS = std::max(4 * KB + 2 * VB + 2 * PB + 2 * DB, 56 * 1024);
     static constexpr int LDS_STATES = 2 * (KB + VB + DB);    // of the launch that forms the segments' states
     static_assert(C * DK % (E * THREADS) == 0 && C * DV % (E * THREADS) == 0);
     static_assert(LDS <= 160 * 1024);
@@ -416,10 +418,6 @@ __device__ __forceinline__ int seg_of(const LinArgs &a, int n) {
     return (int)((uint32_t)min(max(a.cu[n], (int64_t)0), a.T) / (uint32_t)a.seg);
 }
 
-// Head of the b-th workgroup of a unit.  Neighbouring heads, which may share q and k, stand 8 workgroups
-// apart: on one XCD, behind one L2.
-__device__ __forceinline__ int head_of(const LinArgs &a, int b) { return a.Hv % 8 ? b : b % 8 * (a.Hv / 8) + b / 8; }
-
 template <int DK, int DV, bool BF>
 __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
@@ -434,7 +432,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_kernel(co
 
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m = lane & 15, gq = lane >> 4;
-    const int unit = blockIdx.x / a.Hv, h = head_of(a, blockIdx.x - unit * a.Hv);
+    const int unit = blockIdx.x / a.Hv, h = blockIdx.x - unit * a.Hv;
     const int hk = h / (a.Hv / a.Hk);
     const bool last = unit >= a.stretches;
     int n = unit - a.stretches;
@@ -644,8 +642,8 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
 
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     // heads that remember longest take most of the time: they come at another place in each unit's row, as
-    // workgroups are dealt out to the XCDs and their compute units in turn
-    const int unit = blockIdx.x / a.Hv, h = head_of(a, (blockIdx.x - unit * a.Hv + unit + unit / 8) % a.Hv);
+    // workgroups are dealt out to the compute units in turn
+    const int unit = blockIdx.x / a.Hv, h = (blockIdx.x - unit * a.Hv + unit) % a.Hv;
     const int stretch = unit / a.pieces, piece = unit - stretch * a.pieces;
     const int hk = h / (a.Hv / a.Hk);
     // only the last sequence that starts in or before a stretch can have a segment here

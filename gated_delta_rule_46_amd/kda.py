@@ -1055,6 +1055,8 @@ def _lin_prefill_plan(q, k, v, g, cu, pool, read, write, interval, offsets, ckpt
     elif read is not None or write is not None:
         raise ValueError("read_idx / write_idx need a pool")
     if interval:
+        if interval < 0 or interval % CHUNK:
+            raise ValueError(f"ckpt_interval must be a multiple of {CHUNK} (got {interval})")
         if offsets is not None:
             _dense(offsets, "ckpt_offsets", (N + 1,), torch.int64, dev)
         elif N != 1:
@@ -1067,8 +1069,7 @@ def _lin_prefill_plan(q, k, v, g, cu, pool, read, write, interval, offsets, ckpt
         _dense(out, "out", (T, Hv, dv), q[2], dev)
     if workspace is not None:
         _dense(workspace, "workspace", workspace[0], torch.uint8, dev)
-    wsb = LIB.kda_lin_prefill_workspace(cfg, T, N)
-    return cfg, dev, T, N, (Hv, dk, dv), rows, slots, wsb
+    return cfg, dev, T, N, (Hv, dk, dv), rows, slots
 
 
 def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=None, *, ckpt_interval=0,
@@ -1082,9 +1083,9 @@ def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=
     of the queried size.  Returns (o [T,Hv,dv], checkpoint states or None).  stream: as
     kda_qk_norm_rope."""
     scale = float(scale)
-    cfg, dev, T, N, state, rows, slots, wsb = _lin_prefill_plan(
+    cfg, dev, T, N, state, rows, slots = _lin_prefill_plan(
         _form(q), _form(k), _form(v), _form(g), _form(cu_seqlens), _form(pool), _form(read_idx),
-        _form(write_idx), bool(ckpt_interval), _form(ckpt_offsets), _form(ckpt_out), _form(out),
+        _form(write_idx), ckpt_interval, _form(ckpt_offsets), _form(ckpt_out), _form(out),
         _form(workspace), scale)
     if stream is not None or dev != _current_device():
         with _placed(dev, stream):
@@ -1102,6 +1103,7 @@ def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=
             ck = ctypes.byref(kda_ckpt(ckpt_interval, _ptr(ckpt_offsets), ckpt_out.data_ptr()))
     pl = None if pool is None else ctypes.byref(kda_state_pool(pool.data_ptr(), slots, _ptr(read_idx), _ptr(write_idx)))
     if workspace is None:
+        wsb = LIB.kda_lin_prefill_workspace(cfg, T, N)
         workspace = q.new_empty(wsb, dtype=torch.uint8) if wsb else None
     else:
         wsb = workspace.numel()

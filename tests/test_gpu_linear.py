@@ -589,3 +589,90 @@ def test_split_in_pieces(K, dtype, gate):
     assert rel_l2(f(o[:, pick]), ref[0]) <= (HALF["bf16"] if dtype == "bf16" else U * 600)
     w = int(c.write[0])
     assert rel_l2(f(c.pool[w][pick]), ref[3][0]) <= U * 600
+
+
+# ---------------------------------------------------------------------------
+# far addresses
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("call", ["prefill", "decode", "norm"])
+def test_rows_far_apart(K, call):
+    """Tokens 2^24 elements apart: offsets beyond 2^32 bytes and 2^31 elements."""
+    import torch
+    T, far = 150, 1 << 24
+    buf = torch.empty(T * far, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(61)
+
+    def spread(x, at):
+        t = torch.as_strided(buf, x.shape, (far, x.shape[2], 1), at)
+        t.copy_(dev(x))
+        return t
+    q, k = (spread(rng.normal(size=(T, 1, 64)), at) for at in (0, 64))
+    v = spread(rng.normal(size=(T, 2, 64)), 128)
+    near = [x.contiguous() for x in (q, k, v)]
+    assert q.stride(0) == far
+    if call == "norm":
+        z = spread(rng.normal(size=(T, 2, 64)), 256)
+        assert torch.equal(K.kda_head_norm(v, z), K.kda_head_norm(near[2], z.contiguous()))
+        y = spread(np.zeros((T, 2, 64)), 384)
+        assert torch.equal(K.kda_head_norm(v, z, out=y), K.kda_head_norm(near[2], z.contiguous()))
+        return
+    g = f32(-rng.random((T, 2)))
+    pools = [f32(rng.normal(size=(T + 1, 2, 64, 64))) for _ in "ab"]
+    pools[1].copy_(pools[0])
+    outs = []
+    for p, (a, b, c) in zip(pools, ((q, k, v), near)):
+        if call == "prefill":
+            o, _ = K.kda_lin_prefill(a, b, c, g, i64([0, T]), p, i32([3]), i32([4]))
+        else:
+            o = K.kda_lin_decode(a, b, c, g, p, i32(range(T)), i32(range(T)))
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs) and torch.equal(*pools)
+
+
+def test_far_slots_and_rungs(K):
+    """Slots and rungs beyond 2^32 bytes of their tensors."""
+    import torch
+    H, dk, dv, far = 2, 128, 128, 40000
+    c = Call("bf16", [200], H, H, dk, dv, "token", 62, slots=[(0, 1, 2)])
+    o = c.check(K, interval=64)
+    near = c.pool
+    pool = torch.empty((far + 1, H, dk, dv), device="cuda")
+    d = Call("bf16", [200], H, H, dk, dv, "token", 62, slots=[(0, 1, 2)])
+    pool[far - 1] = d.pool[1]
+    rungs = torch.empty((far + 1, H, dk, dv), device="cuda")
+    o2, _ = K.kda_lin_prefill(d.q, d.k, d.v, d.g, i64([0, 200]), pool, i32([far - 1]), i32([far]), scale=0.3,
+                              ckpt_interval=64, ckpt_offsets=i64([far - 3, far]), ckpt_out=rungs)
+    torch.cuda.synchronize()
+    assert np.array_equal(o, to_numpy_f64(o2)) and torch.equal(pool[far], near[2])
+    ref = d.oracle(64, 0.3)[2]
+    assert rel_l2(to_numpy_f64(rungs[far - 3:far]), ref) <= U * 64
+
+
+@pytest.mark.parametrize("N,Hv", [(1500, 1), (700, 2)])
+def test_many_sequences(K, N, Hv):
+    """More sequences than the order by length takes, and just below; ragged, some empty."""
+    rng = np.random.default_rng(63)
+    lens = rng.integers(0, 5, N)
+    lens[::97] = 300
+    Call("bf16", lens.tolist(), 1, Hv, 64, 64, "token", 64).check(K)
+
+
+def test_ordered_ragged(K):
+    """Enough (sequence, head) pairs of ragged lengths to be taken longest first, some of them cut."""
+    rng = np.random.default_rng(65)
+    lens = np.exp(rng.uniform(np.log(20), np.log(900), 40)).astype(int).tolist() + [0, 1, 2600]
+    c = Call("bf16", lens, 16, 16, 64, 64, "token", 66)
+    import torch
+    pick, first = [0, 7, 15], c.pool.clone()
+    off = np.concatenate([[0], np.cumsum([n // 256 for n in lens])])
+    o, rungs = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write), scale=0.3,
+                                 ckpt_interval=256, ckpt_offsets=i64(off))
+    torch.cuda.synchronize()
+    f = to_numpy_f64
+    ref = R.prefill(f(c.q[:, pick]), f(c.k[:, pick]), f(c.v[:, pick]), f(c.g[:, pick]), c.cu, f(first[:, pick]), c.read,
+                    c.write, 256, scale=0.3)
+    assert rel_l2(f(o[:, pick]), ref[0]) <= HALF["bf16"]
+    assert rel_l2(f(c.pool[:, pick]), ref[1]) <= U * 200 and rel_l2(f(rungs[:, pick]), ref[2]) <= U * 200
+    rest = np.setdiff1d(np.arange(len(first)), c.write)
+    assert torch.equal(first[rest], c.pool[rest])

@@ -205,7 +205,7 @@ def form(shape, dtype=torch.bfloat16, strides=None, dev=0):
 
 F32, I32, I64 = torch.float32, torch.int32, torch.int64
 GOOD = dict(q=form((9, 2, 64)), k=form((9, 2, 64)), v=form((9, 4, 128)), g=form((9, 4), F32), cu=form((3,), I64),
-            pool=form((5, 4, 64, 128), F32), read=form((2,), I32), write=form((2,), I32), interval=False, offsets=None,
+            pool=form((5, 4, 64, 128), F32), read=form((2,), I32), write=form((2,), I32), interval=0, offsets=None,
             ckpt=None, out=None, workspace=None, scale=1.0)
 
 
@@ -220,7 +220,7 @@ def test_prefill_forms():
     assert plan(q=form((9, 2, 64), strides=(640, 64, 1)), g=form((9, 4), F32, (12, 1)))[5] == [640, 128, 512, 12]
     one = dict(q=form((1, 2, 64)), k=form((1, 2, 64)), v=form((1, 4, 128)), cu=form((2,), I64), read=None, write=None)
     assert plan(**one, g=form((1, 4), F32, (0, 1)))[5] == [128, 128, 512, 4]
-    plan(interval=True, offsets=form((3,), I64), ckpt=form((7, 4, 64, 128), F32))
+    plan(interval=128, offsets=form((3,), I64), ckpt=form((7, 4, 64, 128), F32))
 
 
 @pytest.mark.parametrize("kw,kind", [
@@ -232,9 +232,10 @@ def test_prefill_forms():
     (dict(g=form((3,), F32)), ValueError), (dict(cu=form((3,), I32)), TypeError), (dict(cu=form((0,), I64)), ValueError),
     (dict(pool=form((5, 4, 128, 64), F32)), ValueError), (dict(pool=form((5, 4, 64, 128))), TypeError),
     (dict(read=form((3,), I32)), ValueError), (dict(write=form((2,), I64)), TypeError), (dict(pool=None), ValueError),
-    (dict(interval=True), ValueError), (dict(offsets=form((3,), I64)), ValueError),
+    (dict(interval=64), ValueError), (dict(offsets=form((3,), I64)), ValueError),
     (dict(ckpt=form((7, 4, 64, 128), F32)), ValueError), (dict(out=form((9, 4, 64))), ValueError),
-    (dict(interval=True, offsets=form((2,), I64)), ValueError),
+    (dict(interval=64, offsets=form((2,), I64)), ValueError),
+    (dict(interval=96, offsets=form((3,), I64)), ValueError), (dict(interval=-64, offsets=form((3,), I64)), ValueError),
 ])
 def test_prefill_refuses_forms(kw, kind):
     with pytest.raises(kind):
