@@ -29,6 +29,7 @@
 // segments; then all segments run as units of their own.
 
 #include <algorithm>
+#include <cmath>
 
 #include "kda_attn.h"
 #include "kda_lin.h"
@@ -835,7 +836,6 @@ hipError_t launch(const LinArgs &a, hipStream_t s) {
     return start(lin_kernel<DK, DV, BF>, ((int64_t)a.stretches + a.N) * a.Hv, X::THREADS, X::LDS, a, s);
 }
 
-constexpr int kLeastSegment = 512;
 constexpr int kLeastPiece = 1024;
 constexpr int kLeastOrdered = 128;   // tokens of a sequence on average
 
@@ -845,9 +845,20 @@ void lin_plan(int cus, LinArgs *a) {
     a->seg = a->slots = a->stretches = a->piece = a->pieces = 0;
     a->order = nullptr;
     a->ordered = a->N > 1 && a->N <= kOrderThreads && (int64_t)a->N * a->Hv > 2 * cus && a->T / a->N >= kLeastOrdered;
+    // Where it pays to cut, the segments give every compute unit its two workgroups, but:
+    //  - at least 2 sqrt(T) tokens: a segment takes about 4 us per 32 tokens in its two launches, and each
+    //    one lengthens the carry by about 0.5 us (one head, 4,096 tokens: 41 us with segments of 64, 34 of 128,
+    //    41 of 256; 16,384: 114, 71, 59);
+    //  - at least 4 tokens a head: a segment's state is written and read twice (32 heads, 1,024 tokens: 44 us with
+    //    segments of 64, 39 of 128);
+    //  - four of the shortest ones at least, or the additional launches cost what they save (32 heads, 257 tokens:
+    //    21 us in one, 26 in segments of 128; 64 heads, 512 tokens: 34 us in one, 41 in segments of 256), and three
+    //    of any (256 heads leave each compute unit one workgroup in one piece, and halves take as long);
+    //  - none where the sequences are so short on average that few can be longer than one.
     const int64_t per_head = std::max(2 * cus / a->Hv, 1);
-    const int64_t seg = std::max<int64_t>(((a->T + per_head - 1) / per_head + 63) / 64 * 64, kLeastSegment);
-    if (a->T <= seg) return;          // no sequence can be longer
+    const int64_t least = std::max((int64_t)4 * a->Hv, (int64_t)std::ceil(2.0 * std::sqrt((double)a->T)));
+    const int64_t seg = (std::max((a->T + per_head - 1) / per_head, least) + 63) / 64 * 64;
+    if (a->T < 4 * ((least + 63) / 64 * 64) || a->T < 3 * seg || a->T / a->N < seg / 4) return;
     a->seg = (int32_t)seg;
     a->stretches = (int32_t)(a->T / seg);
     a->slots = 2 * a->stretches;
