@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -126,9 +127,9 @@ def _load():
         "kda_attn": (ctypes.c_int, [acfgp, cachep, I32, I64, P, P, P, I64, F32, I32, I32, P, P, P, S,
                                     P]),
         "kda_lin_prefill_workspace": (S, [lcfgp, I64, I32]),
-        "kda_lin_prefill": (ctypes.c_int, [lcfgp, P, I64, P, I64, P, I64, P, I64, P, I32, I64, poolp, P,
+        "kda_lin_prefill": (ctypes.c_int, [lcfgp, P, I64, P, I64, P, I64, P, I64, P, I32, I64, P, P,
                                            ckp, P, S, P]),
-        "kda_lin_decode": (ctypes.c_int, [lcfgp, I32, P, I64, P, I64, P, I64, P, I64, poolp, P, P]),
+        "kda_lin_decode": (ctypes.c_int, [lcfgp, I32, P, I64, P, I64, P, I64, P, I64, P, P, P]),
         "kda_head_norm": (ctypes.c_int, [I32, I64, I32, I32, P, I64, P, I64, P, P, I32, F32, I32, I32, P,
                                          I64, P]),
         "kda_validate_inputs": (ctypes.c_int, [cfgp, I64, P, I32, I32, P, P, P, P]),
@@ -1042,6 +1043,9 @@ def _lin_pool(pool, read, write, N, Hv, dk, dv, dev):
     return pool[0][0]
 
 
+_pool_bytes = struct.Struct("@PqPP").pack               # a kda_state_pool, in a third of a ctypes object's time
+
+
 @functools.lru_cache(maxsize=1024)
 def _lin_prefill_plan(q, k, v, g, cu, pool, read, write, interval, offsets, ckpt, out, workspace, scale):
     cfg, dev, T, Hv, dk, dv, rows = _lin_inputs(q, k, v, g, scale)
@@ -1093,7 +1097,7 @@ def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=
                                    ckpt_interval=ckpt_interval, ckpt_offsets=ckpt_offsets,
                                    ckpt_out=ckpt_out, scale=scale, out=out, workspace=workspace)
     if out is None:
-        out = q.new_empty((T, state[0], state[2]))
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
     ck = None
     if ckpt_interval:
         if ckpt_out is None:
@@ -1101,7 +1105,7 @@ def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=
             ckpt_out = q.new_empty((max(n, 0), *state), dtype=torch.float32)
         if ckpt_out.shape[0]:
             ck = ctypes.byref(kda_ckpt(ckpt_interval, _ptr(ckpt_offsets), ckpt_out.data_ptr()))
-    pl = None if pool is None else ctypes.byref(kda_state_pool(pool.data_ptr(), slots, _ptr(read_idx), _ptr(write_idx)))
+    pl = None if pool is None else _pool_bytes(pool.data_ptr(), slots, _ptr(read_idx) or 0, _ptr(write_idx) or 0)
     if workspace is None:
         wsb = LIB.kda_lin_prefill_workspace(cfg, T, N)
         workspace = q.new_empty(wsb, dtype=torch.uint8) if wsb else None
@@ -1124,7 +1128,7 @@ def _lin_decode_plan(q, k, v, g, pool, read, write, out, scale):
     slots = _lin_pool(pool, read, write, N, Hv, dk, dv, dev)
     if out is not None:
         _dense(out, "out", (N, Hv, dv), q[2], dev)
-    return cfg, dev, N, (N, Hv, dv), rows, slots
+    return cfg, dev, N, rows, slots
 
 
 def kda_lin_decode(q, k, v, g, pool, read_idx, write_idx, *, scale=1.0, out=None, stream=None):
@@ -1133,16 +1137,16 @@ def kda_lin_decode(q, k, v, g, pool, read_idx, write_idx, *, scale=1.0, out=None
     write_idx; read_idx / write_idx: int32 [N] (outside the pool: zero state / not stored).  Returns o
     [N,Hv,dv].  stream: as kda_qk_norm_rope."""
     scale = float(scale)
-    cfg, dev, N, shape, rows, slots = _lin_decode_plan(_form(q), _form(k), _form(v), _form(g), _form(pool),
-                                                       _form(read_idx), _form(write_idx), _form(out), scale)
+    cfg, dev, N, rows, slots = _lin_decode_plan(_form(q), _form(k), _form(v), _form(g), _form(pool),
+                                                _form(read_idx), _form(write_idx), _form(out), scale)
     if stream is not None or dev != _current_device():
         with _placed(dev, stream):
             return kda_lin_decode(q, k, v, g, pool, read_idx, write_idx, scale=scale, out=out)
     if out is None:
-        out = q.new_empty(shape)
-    pl = kda_state_pool(pool.data_ptr(), slots, read_idx.data_ptr(), write_idx.data_ptr())
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
+    pl = _pool_bytes(pool.data_ptr(), slots, read_idx.data_ptr(), write_idx.data_ptr())
     st = LIB.kda_lin_decode(cfg, N, q.data_ptr(), rows[0], k.data_ptr(), rows[1], v.data_ptr(), rows[2],
-                            g.data_ptr(), rows[3], ctypes.byref(pl), out.data_ptr(), _current_stream(dev))
+                            g.data_ptr(), rows[3], pl, out.data_ptr(), _current_stream(dev))
     if st:
         _check(st, "kda_lin_decode")
     return out

@@ -114,6 +114,8 @@ def norm(dtype=1, T=8, H=4, D=64, x=FAKE, x_row=256, gate=FAKE, gate_row=256, we
 
 
 def test_struct_layout():
+    pool = K.kda_state_pool.from_buffer_copy(K._pool_bytes(1 << 40, -3, 0, 5))
+    assert (pool.states, pool.n_slots, pool.read_idx, pool.write_idx) == (1 << 40, -3, None, 5)
     assert ctypes.sizeof(K.kda_lin_config) == 24 and K.kda_lin_config.scale.offset == 20
 
 
@@ -245,7 +247,7 @@ def test_prefill_refuses_forms(kw, kind):
 def test_decode_and_norm_refuse_forms():
     d = dict(q=form((3, 2, 64)), k=form((3, 2, 64)), v=form((3, 4, 128)), g=form((4,), F32), pool=form((5, 4, 64, 128), F32),
              read=form((3,), I32), write=form((3,), I32), out=None, scale=1.0)
-    assert K._lin_decode_plan(*d.values())[4] == [128, 128, 512, 0]
+    assert K._lin_decode_plan(*d.values())[3] == [128, 128, 512, 0]
     for kw in (dict(pool=None), dict(read=None), dict(write=None), dict(read=form((2,), I32)), dict(out=form((3, 2, 128)))):
         with pytest.raises(ValueError):
             K._lin_decode_plan(*{**d, **kw}.values())
