@@ -34,6 +34,7 @@ struct LinArgs {
     int32_t seg, slots, stretches;          // slots: 2 (T / seg); stretches: T / seg
     int32_t piece, pieces;
     bool ordered;                // whether there is an order
+    bool narrow;                 // whether a head's columns are shared out over two workgroups
     int32_t *order;              // [N] sequences by the length of their last segment (null: as they come)
     float *carry;                // [slots,Hv,dk,dv]
     float *part;                 // [stretches,pieces,Hv,dk,dv]

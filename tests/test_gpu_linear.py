@@ -170,9 +170,11 @@ def test_prefill_lengths(K, dtype, n):
     Call(dtype, [n], 1, 2, 128, 128, "token", n).check(K)
 
 
-@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 7), (3, 3), (5, 10)])
-def test_prefill_heads(K, Hk, Hv):
-    Call("bf16", [50, 90], Hk, Hv, 64, 64, "token", 3).check(K)
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 7), (3, 3), (5, 10), (64, 64), (65, 65), (30, 150)])
+def test_prefill_heads(K, Hk, Hv, dv):
+    """Grouped heads; few enough for two workgroups a head, and more."""
+    Call("bf16", [50, 90], Hk, Hv, 64, dv, "token", 3).check(K, interval=64)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -676,3 +678,51 @@ def test_ordered_ragged(K):
     assert rel_l2(f(c.pool[:, pick]), ref[1]) <= U * 200 and rel_l2(f(rungs[:, pick]), ref[2]) <= U * 200
     rest = np.setdiff1d(np.arange(len(first)), c.write)
     assert torch.equal(first[rest], c.pool[rest])
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("gate", ["head", "token", "strong"])
+def test_grouped_heads_ragged(K, dk, gate):
+    """Many value heads that share q and k; ragged sequences, taken longest first, some cut, with rungs."""
+    import torch
+    lens = [1, 33, 0, 64, 200, 31, 1100, 7, 90, 257, 65, 12]
+    Hk, Hv = 12, 48
+    c = Call("bf16", lens, Hk, Hv, dk, 64, gate, 71, pad=2)
+    pick, first = [0, 1, 6, 7, 47], c.pool.clone()
+    qk = [h // 4 for h in pick]
+    off = np.concatenate([[0], np.cumsum([n // 64 for n in lens])])
+    f = to_numpy_f64
+    out = torch.full(c.v.shape, 7.0, dtype=c.v.dtype, device="cuda")
+    o, rungs = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write), scale=0.3,
+                                 ckpt_interval=64, ckpt_offsets=i64(off), out=out)
+    torch.cuda.synchronize()
+    assert (f(o)[c.cu[-1]:] == 7.0).all()
+    args = (f(c.q[:, qk]), f(c.k[:, qk]), f(c.v[:, pick]), R.decays(f(c.g), sum(lens) + 2, Hv)[:, pick], c.cu,
+            f(first[:, pick]), c.read, c.write, 64)
+    ref = R.prefill(*args, scale=0.3)
+    top = R.prefill(*(np.abs(x) if i in (0, 1, 2, 5) else x for i, x in enumerate(args)), scale=0.3)
+    live = c.cu[-1]
+    half = HALF["bf16"]
+    within("o", f(o[:live, pick]), ref[0][:live], half * np.abs(ref[0][:live]) + (2 * half + 7000 * U) * top[0][:live] + 1e-37)
+    Call.states("pool", f(c.pool[:, pick])[c.write], ref[1][c.write], top[1][c.write], 1100)
+    Call.states("rungs", f(rungs[:, pick]), ref[2], top[2], 1100)
+    rest = np.setdiff1d(np.arange(len(first)), c.write)
+    assert torch.equal(first[rest], c.pool[rest])
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_grouped_heads_keep_values_apart(K, value):
+    """A value that is not finite in one of two heads that share q and k changes nothing in the other, nor before it."""
+    a, b = (Call("bf16", [40, 100], 128, 256, 64, 64, "token", 72) for _ in "ab")
+    b.v[117, 5, 9] = value
+    outs = []
+    for c in (a, b):
+        o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write))
+        outs.append((to_numpy_f64(o), to_numpy_f64(c.pool)))
+    (o, pool), (o2, pool2) = outs
+    touched = np.zeros(o.shape, bool)
+    touched[117:, 5, 9] = True
+    assert np.array_equal(o[~touched], o2[~touched]) and not np.isfinite(o2[117, 5, 9])
+    w = int(a.write[1])
+    pool[w, 5, :, 9] = pool2[w, 5, :, 9] = 0
+    assert np.array_equal(pool, pool2)
