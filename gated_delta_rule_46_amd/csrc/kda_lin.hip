@@ -128,13 +128,16 @@ __device__ __forceinline__ typename X::O::F8 ld_r(const typename X::T *tile, int
 
 __device__ __forceinline__ bool not_finite(float x) { return (f32_bits(x) & 0x7f800000u) == 0x7f800000u; }
 
+template <typename V>
+__device__ __forceinline__ u32x4 words(V v) { return __builtin_bit_cast(u32x4, v); }
+
 // Whether any of an operand's values is an infinity or a NaN.
 template <class X>
 __device__ __forceinline__ bool any_not_finite(const typename X::O::F8 *f, int n) {
     if constexpr (X::BF) {
         uint32_t r = 0;                // an exponent of all ones carries into the sign's place
         for (int i = 0; i < n; ++i) {
-            const u32x4 u = __builtin_bit_cast(u32x4, f[i]);
+            const u32x4 u = words(f[i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r |= (u[j] & 0x7f807f80u) + 0x00800080u;
         }
@@ -566,7 +569,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
 #pragma unroll
         for (int it = 0; it < NT; ++it) {
             if constexpr (!BF) {
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[it][0]), ow, o_at, 16 * it * o_row, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(words(acc[it][0]), ow, o_at, 16 * it * o_row, 0);
             } else if constexpr (NB == 2) {
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O::cvt44(acc[it][0], acc[it][1])), ow, o_at,
                                                        16 * it * o_row, 0);
