@@ -354,10 +354,13 @@ struct State {
             for (int i = 0; i < 4; ++i) dst[at + i * X::HV] = x[i];
         });
     }
-    // v^T of the wave's columns with zeros in place of infinities and NaN; returns whether there are any
-    __device__ __forceinline__ static bool values(const typename X::T *v, typename X::O::F8 *vf) {
+    // v^T of the wave's columns
+    __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
         for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
+    }
+    // Puts zeros in place of infinities and NaN; returns whether there were any.
+    __device__ __forceinline__ static bool clean(typename X::O::F8 *vf) {
         const bool rare = __any(any_not_finite<X>(vf, X::NB));
         if (rare) {
 #pragma unroll
@@ -365,7 +368,7 @@ struct State {
         }
         return rare;
     }
-    // s += k^T (weights v) for the infinities and NaN that values() left out, token by token
+    // s += k^T (weights v) for the infinities and NaN that clean() took out, token by token
     __device__ __forceinline__ void add_rare(const typename X::T *k, const typename X::T *v, const float *keep) {
         using T = typename X::T;
         const int lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4;
@@ -487,7 +490,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
         r.q.put(sq + c % 2 * C * DK);
         r.k.put(sk + c % 2 * C * DK);
         r.v.put(sv + c % 2 * C * DV);
-        if (c % X::NW == w) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
+        if (w == X::NW - 1) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
     };
 
     const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
@@ -501,11 +504,12 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
         const Decays<X> s(sd + c % 2 * X::DB);
 
         F8 vf[NB];
-        const bool rare = S.values(v, vf);
+        S.values(v, vf);
 
-        // P^T tiles (rows j, columns i), one a wave, zeros above the diagonal: lane holds 4 consecutive j of its i
-        if (X::NW == 4 || w < 4) {
-            const int it = w == 1 || w == 2, jt = w >= 2;
+        // P^T tiles (rows j, columns i) of the first three waves (the last one has the decays of the next chunk to
+        // form): lane holds 4 consecutive j of its i
+        if (w < 3) {
+            const int it = w > 0, jt = w > 1;
             const int i = 16 * it + m, j = 16 * jt + 4 * gq;
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -542,6 +546,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
 #pragma unroll
             for (int b = 0; b < NB; ++b) acc[it][b] *= s.out[16 * it + m];
 
+        const bool rare = S.clean(vf);
         // S <- e^{G_C} S + k^T (weights v)
         const float all = *s.all;
         S.each([&](f32x4 &x, int) { x *= all; });
@@ -590,6 +595,10 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
             S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE + x0);
     };
 
+    if (w == 3) {                                        // P's upper tile, of both buffers
+#pragma unroll
+        for (int i = 0; i < 2; ++i) O::st4(sp + i * C * C + at<T, C>(m, 16 + 4 * gq), f32x4{0.f, 0.f, 0.f, 0.f});
+    }
     if (len > 0) {
         Chunk next;
         fetch(next, 0);
@@ -734,7 +743,8 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
         const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
         const Decays<X> s(sd + c % 2 * X::DB);
         typename X::O::F8 vf[X::NB];
-        const bool rare = S.values(v, vf);
+        S.values(v, vf);
+        const bool rare = S.clean(vf);
         S.add(k, vf, s.keep);
         if (rare) S.add_rare(k, v, s.keep);
     }
