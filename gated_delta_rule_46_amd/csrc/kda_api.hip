@@ -1181,7 +1181,7 @@ size_t kda_lin_prefill_workspace(const kda_lin_config *cfg, int64_t T, int32_t N
     if (check_lin_config(cfg) != KDA_OK || check_lin_sizes(cfg, N, T) != KDA_OK || N == 0) return 0;
     kda::LinArgs a{};
     a.N = N; a.T = T; a.Hv = cfg->num_v_heads;
-    kda::lin_plan(device_cus(), &a);
+    kda::lin_plan(device_cus(), cfg->io_dtype == KDA_DTYPE_BF16, cfg->dv, &a);
     return round256(kda::lin_buffers(cfg->dk, cfg->dv, nullptr, &a));
 }
 
@@ -1205,7 +1205,7 @@ int kda_lin_prefill(const kda_lin_config *cfg, const void *q, int64_t q_row, con
     if (ckpt) {
         a.interval = ckpt->interval; a.ckpt_off = ckpt->offsets; a.ckpt = ckpt->states;
     }
-    kda::lin_plan(device_cus(), &a);
+    kda::lin_plan(device_cus(), cfg->io_dtype == KDA_DTYPE_BF16, cfg->dv, &a);
     const size_t need = round256(kda::lin_buffers(cfg->dk, cfg->dv, (char *)ws, &a));
     if (need) {
         if (!ws || ws_bytes < need)

@@ -43,7 +43,7 @@ struct LinArgs {
     double *sums;                // [stretches,seg/64,Hv] log2 decays of 64 tokens (with more than one piece)
 };
 // The plan of a call on a device of `cus` compute units; its buffers at ws, and their bytes.
-void lin_plan(int cus, LinArgs *a);
+void lin_plan(int cus, bool bf16, int dv, LinArgs *a);
 size_t lin_buffers(int dk, int dv, char *ws, LinArgs *a);
 bool lin_supported(int dk, int dv);
 hipError_t launch_lin(bool bf16, int dk, int dv, const LinArgs &a, hipStream_t s);

@@ -870,7 +870,7 @@ constexpr int kLeastOrdered = 128;   // tokens of a sequence on average
 }  // namespace
 
 namespace {
-void cut(int cus, LinArgs *a) {
+void cut(int cus, bool bf16, int dv, LinArgs *a) {
     a->seg = a->slots = a->stretches = a->piece = a->pieces = 0;
     a->order = nullptr;
     a->ordered = a->N > 1 && a->N <= kOrderThreads && (int64_t)a->N * a->Hv > 2 * cus && a->T / a->N >= kLeastOrdered;
@@ -880,14 +880,19 @@ void cut(int cus, LinArgs *a) {
     //    41 of 256; 16,384: 114, 71, 59);
     //  - at least 4 tokens a head: a segment's state is written and read twice (32 heads, 1,024 tokens: 44 us with
     //    segments of 64, 39 of 128);
-    //  - four of the shortest ones at least, or the additional launches cost what they save (32 heads, 257 tokens:
-    //    21 us in one, 26 in segments of 128; 64 heads, 512 tokens: 34 us in one, 41 in segments of 256), and three
-    //    of any (256 heads leave each compute unit one workgroup in one piece, and halves take as long);
+    //  - six of the shortest ones at least for bf16 heads of 128 columns, or the additional launches cost what they
+    //    save (in one / cut: 32 heads, 512 tokens 25 / 31 us, 768 35 / 35, 1,024 47 / 42; one head, 384 19 / 20, 512
+    //    24 / 20), four for the others, whose states are smaller or chunks slower (32 heads of 64 x 64, 512 tokens:
+    //    20 / 20; fp32 heads of 128 x 128: 100 / 56), and three of any (256 heads leave each compute unit one
+    //    workgroup in one piece, and halves take as long);
+    //  - among several sequences the longest one may have from T / N to T tokens: half as many again of those halfway
+    //    (32 heads, 2 x 512 tokens 26 / 43 us, but 47 / 42 if one has all; 8 x 512 42 / 81, but 163 / 75);
     //  - none where the sequences are so short on average that few can be longer than one.
     const int64_t per_head = std::max(2 * cus / a->Hv, 1);
     const int64_t least = std::max((int64_t)4 * a->Hv, (int64_t)std::ceil(2.0 * std::sqrt((double)a->T)));
     const int64_t seg = (std::max((a->T + per_head - 1) / per_head, least) + 63) / 64 * 64;
-    if (a->T < 4 * ((least + 63) / 64 * 64) || a->T < 3 * seg || a->T / a->N < seg / 4) return;
+    const int64_t longest = (a->T + a->T / a->N) / 2, fewest = (bf16 && dv == 128 ? 6 : 4) * (a->N > 1 ? 3 : 2);
+    if (2 * longest < fewest * ((least + 63) / 64 * 64) || a->T < 3 * seg || a->T / a->N < seg / 4) return;
     a->seg = (int32_t)seg;
     a->stretches = (int32_t)(a->T / seg);
     a->slots = 2 * a->stretches;
@@ -898,10 +903,10 @@ void cut(int cus, LinArgs *a) {
 
 }  // namespace
 
-void lin_plan(int cus, LinArgs *a) {
-    cut(cus, a);
-    // A workgroup alone on its compute unit takes 20% less time for half of the columns (32 heads, 257 tokens: 21 ->
-    // 18 us); where there are enough, q and k would be read and multiplied twice for nothing.
+void lin_plan(int cus, bool bf16, int dv, LinArgs *a) {
+    cut(cus, bf16, dv, a);
+    // A workgroup alone on its compute unit takes 28% less time for half of the columns (32 heads, 257 tokens: 22.6 ->
+    // 16.3 us); where there are enough, q and k would be read and multiplied twice for nothing.
     a->narrow = (int64_t)(a->stretches + a->N) * a->Hv * 2 <= cus;
 }
 

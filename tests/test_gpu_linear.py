@@ -591,6 +591,45 @@ def test_split_in_pieces(K, dtype, gate):
     assert rel_l2(f(c.pool[w][pick]), ref[3][0]) <= U * 600
 
 
+@pytest.mark.parametrize("dk", [64, 128])
+def test_split_wide_heads(K, dk):
+    """Grouped heads of 128 columns in several sequences, of which those behind the first one start inside a segment."""
+    lens = [1900, 20, 0, 900]
+    assert split_plan(6, sum(lens) + 3, len(lens), dk, 128, Hk=3)
+    Call("bf16", lens, 3, 6, dk, 128, "token", 58, pad=3, slots=[(0, 1, 1), (3, -1, 5)]).check(K, interval=448)
+
+
+def pieces_of(Hv, T, N, dk, dv, seg):
+    """Pieces of a plan with segments of `seg` tokens, from its workspace: states at both ends of a stretch and one a
+    piece, two words a head and piece or stretch, and with pieces the sums of 64 tokens."""
+    need, stretches = split_plan(Hv, T, N, dk, dv, Hk=Hv), T // seg
+    for pieces in range(1, 5):
+        words = (2 + pieces) * dk * dv + 1 + pieces + (2 * seg // 64 if pieces > 1 else 0)
+        if need == -(-stretches * Hv * words * 4 // 256) * 256:
+            return pieces
+    return 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["head", "strong"])
+def test_split_many_heads_in_pieces(K, dtype, gate):
+    """Segments of 2,112 tokens in two pieces each, some of which nothing is left of.  A state takes 8,300 / 32 = 260
+    updates, each one rounding of the sum, one of the decay and two of the product's terms."""
+    import torch
+    lens, H = [8300, 148], 128
+    assert pieces_of(H, sum(lens), 2, 64, 64, 2112) == 2
+    c = Call(dtype, lens, H, H, 64, 64, gate, 59, slots=[(0, 1, 1)])
+    pick, f = [0, 77, 127], to_numpy_f64                  # the oracle takes some heads
+    first = c.pool.clone()
+    o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write), scale=0.3)
+    torch.cuda.synchronize()
+    g = R.decays(f(c.g), sum(lens), H)[:, pick]
+    ref = R.prefill(f(c.q[:, pick]), f(c.k[:, pick]), f(c.v[:, pick]), g, c.cu, f(first[:, pick]), c.read, c.write, scale=0.3)
+    assert rel_l2(f(o[:, pick]), ref[0]) <= (HALF["bf16"] if dtype == "bf16" else U * 1040)
+    w = int(c.write[0])
+    assert rel_l2(f(c.pool[w][pick]), ref[3][0]) <= U * 1040
+
+
 # ---------------------------------------------------------------------------
 # far addresses
 # ---------------------------------------------------------------------------

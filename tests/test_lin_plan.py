@@ -79,3 +79,13 @@ def test_workspace_is_bounded(Hv):
         for N in (1, 2, 17, 1024):
             if N * Hv <= 1 << 20:
                 assert workspace(T, N, Hv) <= 512 * 8 * 128 * 128 * 4 + (1 << 24)
+
+
+def test_where_cutting_begins():
+    """Six of the shortest segments for bf16 heads of 128 columns, four for others; half as many again, of the length
+    halfway between the mean and all tokens, where there are several sequences."""
+    for dk, dv, dtype, fewest in ((128, 128, 1, 6), (64, 128, 1, 6), (128, 64, 1, 4), (64, 64, 1, 4), (128, 128, 0, 4)):
+        T = fewest * 128                                              # 32 heads: segments of 4 x 32 tokens at least
+        assert workspace(T - 1, 1, 32, dk, dv, dtype) == 0 < workspace(T, 1, 32, dk, dv, dtype)
+        assert workspace(2 * T - 1, 2, 32, dk, dv, dtype) == 0 < workspace(2 * T, 2, 32, dk, dv, dtype)
+        assert workspace(0, 1, 32, dk, dv, dtype) == 0 == workspace(1, 1, 32, dk, dv, dtype)
