@@ -29,10 +29,10 @@
 // segments; then all segments run as units of their own.
 //
 // Bound by HBM with 4 waves of 32 columns and two workgroups a compute unit: 64 x 2,048 tokens at 32
-// heads of 128 x 128, bf16, 970 us (4.3 GB, 4.4 TB/s; a large copy 5.15, and 757 us with the loads left
+// heads of 128 x 128, bf16, 965 us (4.3 GB, 4.4 TB/s; a large copy 5.15, and 757 us with the loads left
 // out).  Chunks of 64 tokens on 8 waves of 16 columns took 25% longer: q and k^T are
 // read from LDS by every wave, and one barrier keeps all waves of a compute unit in step.  131,072 tokens of
-// one sequence 1,152 us: 930 for the segments, 200 for what they add (a head that remembers is read
+// one sequence 1,155 us: 930 for the segments, 200 for what they add (a head that remembers is read
 // twice), 30 for the rest.
 
 #include <algorithm>
