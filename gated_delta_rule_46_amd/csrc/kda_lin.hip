@@ -70,7 +70,7 @@ struct Shape {
     static constexpr int E = 16 / sizeof(T);        // elements of a 16-byte piece
     static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
     static constexpr int KB = C * DK * sizeof(T), VB = C * DV * sizeof(T), PB = C * C * sizeof(T);
-    static constexpr int DB = (4 * C + 4) * sizeof(float);   // decays of a chunk
+    static constexpr int DB = (4 * C + 4 + 2 * NW) * sizeof(float);   // decays of a chunk, and its rows that are not finite
     // Two workgroups a compute unit, which is what the calls are cut for: where three or four fit they are
     // dealt out unevenly (16 sequences of 8,192 tokens at 32 heads of 64: 574 us with two, 651 with three).
     static constexpr int LDS = std::max(4 * KB + 2 * VB + 2 * PB + 2 * DB, 56 * 1024);
@@ -94,12 +94,22 @@ template <class X>
 struct Decays {
     float *hi, *lo, *out, *keep;      // G in log2 (two floats), scale e^G, e^{G_C - G}
     float *all;                       // e^{G_C}
+    uint32_t *odd_k, *odd_v;          // per wave: which rows of k and v that it put there hold infinities or NaN
     __device__ explicit Decays(char *p) {
         hi = (float *)p;
         lo = hi + X::C;
         out = lo + X::C;
         keep = out + X::C;
         all = keep + X::C;
+        odd_k = (uint32_t *)(all + 4);
+        odd_v = odd_k + X::NW;
+    }
+    // what any wave has set, the same for every thread
+    static __device__ __forceinline__ uint32_t any(const uint32_t *waves) {
+        uint32_t r = 0;
+#pragma unroll
+        for (int i = 0; i < X::NW; ++i) r |= waves[i];
+        return __builtin_amdgcn_readfirstlane((int)r);
     }
 };
 
@@ -138,29 +148,6 @@ __device__ __forceinline__ bool not_finite(float x) { return (f32_bits(x) & 0x7f
 template <typename V>
 __device__ __forceinline__ u32x4 words(V v) { return __builtin_bit_cast(u32x4, v); }
 
-// Whether any of an operand's values is an infinity or a NaN.
-template <class X>
-__device__ __forceinline__ bool any_not_finite(const typename X::O::F8 *f, int n) {
-    if constexpr (X::BF) {
-        uint32_t r = 0;                // an exponent of all ones carries into the sign's place
-        for (int i = 0; i < n; ++i) {
-            const u32x4 u = words(f[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r |= (u[j] & 0x7f807f80u) + 0x00800080u;
-        }
-        return r & 0x80008000u;
-    } else {
-        bool r = false;
-        for (int i = 0; i < n; ++i) {
-            float x[8];
-            X::O::unpack8(f[i], x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r |= not_finite(x[e]);
-        }
-        return r;
-    }
-}
-
 template <class X> struct Terms { typename X::O::F8 t[X::TERMS]; };
 
 // Finite fp32 values as operand terms.  bf16: three times the upper half of what is left, which holds all
@@ -189,14 +176,14 @@ __device__ __forceinline__ Terms<X> terms8(const float *x) {
     return r;
 }
 
-// The operand with zeros in place of infinities and NaN.
+// Puts zeros in place of infinities and NaN.
 template <class X>
-__device__ __forceinline__ typename X::O::F8 finite_part(typename X::O::F8 f) {
+__device__ __forceinline__ void clean(typename X::O::F8 *f) {
     float x[8];
-    X::O::unpack8(f, x);
+    X::O::unpack8(*f, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = not_finite(x[e]) ? 0.f : x[e];
-    return X::O::cvt8(x);
+    *f = X::O::cvt8(x);
 }
 
 // 2^x of an fp64 x <= 0 or so, to about an ulp of fp32.
@@ -297,6 +284,10 @@ struct Source {
     __device__ __forceinline__ void step(int chunks) { p += (int64_t)row * (chunks * X::C); }
 };
 
+// Nothing that loads or stores global memory is moved across, so that the loads of all chunks leave in one order (where
+// those before a loop had another one, waiting for a load in the loop waited for outputs too).
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0x78f); }
+
 // A chunk's 16-byte pieces on their way from global memory to LDS.
 template <class X, int W>
 struct Rows {
@@ -307,6 +298,7 @@ struct Rows {
         const auto w = window(s.p, valid, s.row, W * (int)sizeof(typename X::T));
 #pragma unroll
         for (int i = 0; i < S::N; ++i) r[i] = __builtin_amdgcn_raw_buffer_load_b128(w, s.offset, i * S::STEP * s.row, 0);
+        in_order();
     }
     __device__ __forceinline__ void put(typename X::T *tile) const {
 #pragma unroll
@@ -315,7 +307,34 @@ struct Rows {
             *(u32x4 *)(tile + at<typename X::T, W>(q / S::PIECES, q % S::PIECES * X::E)) = r[i];
         }
     }
+    // Sets the wave's word to the rows of its pieces that hold infinities or NaN (which leave a NaN times zero).
+    __device__ __forceinline__ void mark(uint32_t *waves) const {
+        constexpr int ROWS = 64 / S::PIECES;                  // of a wave
+        uint32_t rows = 0;
+#pragma unroll
+        for (int i = 0; i < S::N; ++i) {
+            float x = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u = r[i][j];
+                x = fmaf(bits_f32(X::BF ? u & 0xffff0000u : u), 0.f, x);
+                if (X::BF) x = fmaf(bits_f32(u << 16), 0.f, x);
+            }
+            const uint64_t lanes = __ballot(x != x);
+#pragma unroll
+            for (int l = 0; l < ROWS; ++l)
+                if (lanes >> (l * S::PIECES) & ((1ull << S::PIECES) - 1)) rows |= 1u << (i * S::STEP + (threadIdx.x >> 6) * ROWS + l);
+        }
+        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = rows;
+    }
 };
+
+// x, for the compiler another one in each turn of a loop: what follows from it is formed there and takes no registers
+// elsewhere.
+__device__ __forceinline__ int in_loop(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 // A wave's columns of the state: s[b][kb][hf][i] is row 32 kb + 8 gq + 4 hf + i, column col(b), of
 // lane (m, gq).
@@ -354,39 +373,62 @@ struct State {
             for (int i = 0; i < 4; ++i) dst[at + i * X::HV] = x[i];
         });
     }
+    // Whether k or v may have had an infinity or a NaN, the same for every thread: one of k leaves none of its row's
+    // values finite and one of v none of its column's, and neither ever leaves the state again.
+    __device__ __forceinline__ bool odd(uint32_t *waves) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = i < X::NB ? s[i][0][0][0] * 0.f : 0.f;
+#pragma unroll
+        for (int kb = 0; kb < X::NKB; ++kb)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = fmaf(s[0][kb][hf][i], 0.f, x[i]);
+        const float sum = (x[0] + x[1]) + (x[2] + x[3]);
+        const bool mine = __any(sum != sum);
+        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = mine;
+        __syncthreads();
+        return Decays<X>::any(waves);
+    }
     // v^T of the wave's columns
     __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
         for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
     }
-    // Puts zeros in place of infinities and NaN; returns whether there were any.
-    __device__ __forceinline__ static bool clean(typename X::O::F8 *vf) {
-        const bool rare = __any(any_not_finite<X>(vf, X::NB));
-        if (rare) {
-#pragma unroll
-            for (int b = 0; b < X::NB; ++b) vf[b] = finite_part<X>(vf[b]);
-        }
-        return rare;
-    }
-    // s += k^T (weights v) for the infinities and NaN that clean() took out, token by token
-    __device__ __forceinline__ void add_rare(const typename X::T *k, const typename X::T *v, const float *keep) {
-        using T = typename X::T;
-        const int lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4;
-        for (int j = 0; j < X::C; ++j)
+    // s += k^T (weights v) token by token: all of a token whose k has an infinity or a NaN (bits of odd_k), and columns of
+    // one whose v has.
+    __device__ __forceinline__ void add_rare(const typename X::T *k, const typename X::T *v, const float *keep, uint32_t odd_k,
+                                             uint32_t odd_v) {
+        const int lane = threadIdx.x & 63, m = lane & 15;
+        for (uint32_t left = odd_k | odd_v; left; left &= left - 1) {
+            const int j = __builtin_ctz(left), gq = in_loop(lane >> 4);
+            const bool whole = odd_k >> j & 1;
+            float x[X::NB];
+            bool there[X::NB];
 #pragma unroll
             for (int b = 0; b < X::NB; ++b) {
-                const float x = (float)v[at<T, X::DV>(j, 16 * X::NB * (threadIdx.x >> 6) + STEP * (m >> 2) + (m & 3) + 4 * b)];
-                if (!not_finite(x)) continue;
-#pragma unroll
-                for (int kb = 0; kb < X::NKB; ++kb)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[b][kb][hf][i] += (float)k[at<T, X::DK>(j, 32 * kb + 8 * gq + 4 * hf + i)] * (x * keep[j]);
+                x[b] = (float)v[at<typename X::T, X::DV>(j, 16 * X::NB * (threadIdx.x >> 6) + STEP * (m >> 2) + (m & 3) + 4 * b)];
+                there[b] = whole || not_finite(x[b]);
+                x[b] *= keep[j];
             }
+#pragma unroll
+            for (int kb = 0; kb < X::NKB; ++kb) {
+                float y[8];
+                X::O::unpack8(ld_r<X, X::DK>(k, j, 32 * kb + 8 * gq), y);
+#pragma unroll
+                for (int b = 0; b < X::NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f32x4 &z = s[b][kb][e / 4];
+                        const float t = z[e % 4] + y[e] * x[b];
+                        z[e % 4] = there[b] ? t : z[e % 4];
+                    }
+            }
+        }
     }
-    // s += k^T (weights v)
+    // s += k^T (weights v), both finite: an infinite k that meets a term of v that is zero, or the zero that stands in for
+    // an infinite v, would leave a NaN where k v is an infinity
     __device__ __forceinline__ void add(const typename X::T *k, const typename X::O::F8 *v, const float *keep) {
         float wt[8];
         mf::load8f(keep + 8 * ((threadIdx.x & 63) >> 4), wt);
@@ -461,151 +503,191 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
     const int len = last ? seq.len - skip : a.seg;
     const int64_t t0 = seq.c0 + skip;
 
+    const float *src = seq.segs > 1 ? a.carry + (int64_t)(2 * seq.first + seg) * a.Hv * State<X>::SIZE
+                                    : slot_of(a, a.read_idx, n, State<X>::SIZE);
+    if (src) src += h * State<X>::SIZE + x0;
     State<X> S;
-    {
-        const float *src = seq.segs > 1 ? a.carry + (int64_t)(2 * seq.first + seg) * a.Hv * S.SIZE
-                                        : slot_of(a, a.read_idx, n, S.SIZE);
-        S.load(src ? src + h * S.SIZE + x0 : nullptr);
-    }
 
-    Source<X, DK> fq(a.q, t0, a.q_row, hk * DK), fk(a.k, t0, a.k_row, hk * DK);
-    Source<X, DV> fv(a.v, t0, a.v_row, (int64_t)h * HV + x0);
-    const char *fg = (const char *)(a.g + t0 * a.g_row + h);
-    const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
-    struct Chunk { Rows<X, DK> q, k; Rows<X, DV> v; float g; };
-    // the next chunk that has not been fetched; always as many loads, so that waiting for them waits for
-    // nothing else
-    auto fetch = [&](Chunk &r, int c) {
-        const int valid = min(len - c * C, C);
-        r.q.fetch(fq, valid);
-        r.k.fetch(fk, valid);
-        r.v.fetch(fv, valid);
-        r.g = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(window(fg, valid, g_row, 4), g_at, 0, 0));
-        fq.step(1);
-        fk.step(1);
-        fv.step(1);
-        fg += (int64_t)g_row * C;
-    };
-    auto put = [&](const Chunk &r, int c) {
-        r.q.put(sq + c % 2 * C * DK);
-        r.k.put(sk + c % 2 * C * DK);
-        r.v.put(sv + c % 2 * C * DV);
-        if (w == X::NW - 1) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
-    };
+    // The unit from its first chunk to its last.  careful: infinities and NaN of k and v are added token by token.
+    // A unit whose state ends with any is run once more so, from the same state and over the same outputs: a look at
+    // k and v of every chunk took 5 to 12% of short prompts.
+    auto pass = [&](auto careful) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+        S.load(src);
+        Source<X, DK> fq(a.q, t0, a.q_row, hk * DK), fk(a.k, t0, a.k_row, hk * DK);
+        Source<X, DV> fv(a.v, t0, a.v_row, (int64_t)h * HV + x0);
+        const char *fg = (const char *)(a.g + t0 * a.g_row + h);
+        const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
+        struct Chunk { Rows<X, DK> q, k; Rows<X, DV> v; float g; };
+        // the next chunk that has not been fetched; always as many loads, so that waiting for them waits for
+        // nothing else
+        auto fetch = [&](Chunk &r, int c) {
+            const int valid = min(len - c * C, C);
+            r.q.fetch(fq, valid);
+            r.k.fetch(fk, valid);
+            r.v.fetch(fv, valid);
+            r.g = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(window(fg, valid, g_row, 4), g_at, 0, 0));
+            fq.step(1);
+            fk.step(1);
+            fv.step(1);
+            fg += (int64_t)g_row * C;
+        };
+        auto put = [&](const Chunk &r, int c) {
+            r.q.put(sq + c % 2 * C * DK);
+            r.k.put(sk + c % 2 * C * DK);
+            r.v.put(sv + c % 2 * C * DV);
+            if constexpr (CAREFUL) {
+                const Decays<X> s(sd + c % 2 * X::DB);
+                r.k.mark(s.odd_k);
+                r.v.mark(s.odd_v);
+            }
+            if (w == X::NW - 1) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
+        };
 
-    const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
-    const int o_row = a.Hv * HV * (int)sizeof(T), o_at = m * o_row + col * (int)sizeof(T);
-    const char *out = (const char *)((T *)a.o + (t0 * a.Hv + h) * HV + x0);
-    // chunk c, whose rows are in LDS; `next` holds those of the one behind it, and takes those of the one further
-    auto chunk = [&](int c, Chunk &next) {
-        const int valid = min(len - c * C, C);
-        const T *const q = sq + c % 2 * C * DK, *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
-        T *const pt = sp + c % 2 * C * C;
-        const Decays<X> s(sd + c % 2 * X::DB);
+        const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
+        const int o_row = a.Hv * HV * (int)sizeof(T), o_at = m * o_row + col * (int)sizeof(T);
+        const char *out = (const char *)((T *)a.o + (t0 * a.Hv + h) * HV + x0);
+        // chunk c, whose rows are in LDS; `next` holds those of the one behind it, and takes those of the one further
+        auto chunk = [&](int c, Chunk &next) {
+            const int valid = min(len - c * C, C);
+            const T *const q = sq + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
+            T *const k = sk + c % 2 * C * DK, *const pt = sp + c % 2 * C * C;
+            const Decays<X> s(sd + c % 2 * X::DB);
 
-        F8 vf[NB];
-        S.values(v, vf);
+            F8 vf[NB];
+            S.values(v, vf);
 
-        // P^T tiles (rows j, columns i) of the first three waves (the last one has the decays of the next chunk to
-        // form): lane holds 4 consecutive j of its i
-        if (w < 3) {
-            const int it = w > 0, jt = w > 1;
-            const int i = 16 * it + m, j = 16 * jt + 4 * gq;
-            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+            // P^T tiles (rows j, columns i) of the first three waves (the last one has the decays of the next chunk to
+            // form): lane holds 4 consecutive j of its i
+            if (w < 3) {
+                const int it = w > 0, jt = w > 1;
+                const int i = 16 * it + m, j = 16 * jt + 4 * gq;
+                f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb)
-                p = O::mma32(p, ld_r<X, DK>(k, 16 * jt + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
-            const f32x4 hj = *(const f32x4 *)(s.hi + j), lj = *(const f32x4 *)(s.lo + j);
-            const float hi = s.hi[i], li = s.lo[i];
+                for (int kb = 0; kb < NKB; ++kb)
+                    p = O::mma32(p, ld_r<X, DK>(k, 16 * jt + m, 32 * kb + 8 * gq), ld_r<X, DK>(q, i, 32 * kb + 8 * gq));
+                const f32x4 hj = *(const f32x4 *)(s.hi + j), lj = *(const f32x4 *)(s.lo + j);
+                const float hi = s.hi[i], li = s.lo[i];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                p[r] = j + r <= i ? a.scale * decay_between<X>(hi, li, hj[r], lj[r]) * p[r] : 0.f;
-            O::st4(pt + at<T, C>(i, j), p);
-        }
+                for (int r = 0; r < 4; ++r)
+                    p[r] = j + r <= i ? a.scale * decay_between<X>(hi, li, hj[r], lj[r]) * p[r] : 0.f;
+                O::st4(pt + at<T, C>(i, j), p);
+            }
 
-        // o^T = e^G S^T q^T: lane holds token 16 it + m, four columns of each tile
-        f32x4 acc[NT][NB];
+            // o^T = e^G S^T q^T: lane holds token 16 it + m, four columns of each tile
+            f32x4 acc[NT][NB];
 #pragma unroll
-        for (int it = 0; it < NT; ++it)
+            for (int it = 0; it < NT; ++it)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[it][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int b = 0; b < NB; ++b) acc[it][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            F8 sf[NB];
+            for (int kb = 0; kb < NKB; ++kb) {
+                F8 sf[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) sf[b] = O::cvt44(S.s[b][kb][0], S.s[b][kb][1]);
+                for (int b = 0; b < NB; ++b) sf[b] = O::cvt44(S.s[b][kb][0], S.s[b][kb][1]);
+#pragma unroll
+                for (int it = 0; it < NT; ++it) {
+                    const F8 qf = ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], sf[b], qf);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < NT; ++it)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) acc[it][b] *= s.out[16 * it + m];
+
+            // S <- e^{G_C} S + k^T (weights v)
+            const float all = *s.all;
+            S.each([&](f32x4 &x, int) { x *= all; });
+            uint32_t odd_k = 0, odd_v = 0;
+            if constexpr (CAREFUL) {
+                odd_k = s.any(s.odd_k);
+                odd_v = s.any(s.odd_v);
+            }
+            if (odd_k | odd_v) {
+                // They are added token by token, then zeros stand in for them: infinite values must not meet the zeros of P
+                // above its diagonal, nor infinite keys the zero terms of a value.
+                __syncthreads();
+                for (uint32_t left = odd_k | odd_v; left; left &= left - 1) {
+                    const int j = __builtin_ctz(left), i = in_loop(m);
+                    const bool whole = odd_k >> j & 1;
+                    float y[NT];
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) y[it] = (float)pt[at<T, C>(16 * it + i, j)];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float x = (float)v[at<T, DV>(j, col + 4 * b + r)];
+                            const bool there = whole || not_finite(x);
+#pragma unroll
+                            for (int it = 0; it < NT; ++it) {
+                                f32x4 &z = acc[it][b];
+                                const float t = z[r] + y[it] * x;
+                                z[r] = there && j <= 16 * it + i ? t : z[r];
+                            }
+                        }
+                }
+                S.add_rare(k, v, s.keep, odd_k, odd_v);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) clean<X>(&vf[b]);
+                __syncthreads();
+                for (uint32_t left = odd_k; left; left &= left - 1) {
+                    const int j = __builtin_ctz(left);
+                    if (tid < DK) k[at<T, DK>(j, tid)] = (T)0.f;
+                    if (tid < C) pt[at<T, C>(tid, j)] = (T)0.f;
+                }
+                __syncthreads();
+            }
+            S.add(k, vf, s.keep);
+
+            put(next, c + 1);
+            fetch(next, c + 2);
+            __syncthreads();   // P and the next chunk are there
+
 #pragma unroll
             for (int it = 0; it < NT; ++it) {
-                const F8 qf = ld_r<X, DK>(q, 16 * it + m, 32 * kb + 8 * gq);
+                const F8 pf = ld_r<X, C>(pt, 16 * it + m, 8 * gq);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], sf[b], qf);
+                for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vf[b], pf);
             }
-        }
+            const auto ow = window(out, valid, o_row, DV * (int)sizeof(T));
+            out += (int64_t)o_row * C;
 #pragma unroll
-        for (int it = 0; it < NT; ++it)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc[it][b] *= s.out[16 * it + m];
-
-        const bool rare = S.clean(vf);
-        // S <- e^{G_C} S + k^T (weights v)
-        const float all = *s.all;
-        S.each([&](f32x4 &x, int) { x *= all; });
-        S.add(k, vf, s.keep);
-        if (rare) S.add_rare(k, v, s.keep);
-
-        put(next, c + 1);
-        fetch(next, c + 2);
-        __syncthreads();   // P and the next chunk are there
-
-#pragma unroll
-        for (int it = 0; it < NT; ++it) {
-            const F8 pf = ld_r<X, C>(pt, 16 * it + m, 8 * gq);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc[it][b] = O::mma32(acc[it][b], vf[b], pf);
-        }
-        if (rare) {   // infinities and NaN must not meet the zeros of P above its diagonal: token by token
-            const T *const v0 = (const T *)a.v + (t0 + c * C) * a.v_row + (int64_t)h * HV + x0 + col;
-            for (int j = 0; j < valid; ++j)
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = (float)v0[j * a.v_row + 4 * b + r];
-#pragma unroll
-                        for (int it = 0; it < NT; ++it)
-                            if (not_finite(x) && j <= 16 * it + m) acc[it][b][r] += (float)pt[at<T, C>(16 * it + m, j)] * x;
-                    }
-        }
-        const auto ow = window(out, valid, o_row, DV * (int)sizeof(T));
-        out += (int64_t)o_row * C;
-#pragma unroll
-        for (int it = 0; it < NT; ++it) {
-            if constexpr (!BF) {
-                __builtin_amdgcn_raw_buffer_store_b128(words(acc[it][0]), ow, o_at, 16 * it * o_row, 0);
-            } else if constexpr (NB == 2) {
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O::cvt44(acc[it][0], acc[it][1])), ow, o_at,
-                                                       16 * it * o_row, 0);
-            } else {
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, O::cvt4(acc[it][0])), ow, o_at, 16 * it * o_row, 0);
+            for (int it = 0; it < NT; ++it) {
+                if constexpr (!BF) {
+                    __builtin_amdgcn_raw_buffer_store_b128(words(acc[it][0]), ow, o_at, 16 * it * o_row, 0);
+                } else if constexpr (NB == 2) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O::cvt44(acc[it][0], acc[it][1])), ow, o_at,
+                                                           16 * it * o_row, 0);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, O::cvt4(acc[it][0])), ow, o_at, 16 * it * o_row, 0);
+                }
             }
-        }
 
-        const int end = (c + 1) * C;
-        if (valid == C && a.interval && (skip + end) % a.interval == 0)
-            S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE + x0);
+            const int end = (c + 1) * C;
+            if (valid == C && a.interval && (skip + end) % a.interval == 0)
+                S.store(a.ckpt + (((a.ckpt_off ? a.ckpt_off[n] : 0) + (skip + end) / a.interval - 1) * a.Hv + h) * S.SIZE + x0);
+        };
+
+        if (w == 3) {                                        // P's upper tile, of both buffers
+#pragma unroll
+            for (int i = 0; i < 2; ++i) O::st4(sp + i * C * C + at<T, C>(m, 16 + 4 * gq), f32x4{0.f, 0.f, 0.f, 0.f});
+        }
+        if (len > 0) {
+            Chunk next;
+            fetch(next, 0);
+            put(next, 0);
+            fetch(next, 1);
+            __syncthreads();
+            for (int c = 0; c * C < len; ++c) chunk(c, next);
+        }
     };
-
-    if (w == 3) {                                        // P's upper tile, of both buffers
-#pragma unroll
-        for (int i = 0; i < 2; ++i) O::st4(sp + i * C * C + at<T, C>(m, 16 + 4 * gq), f32x4{0.f, 0.f, 0.f, 0.f});
-    }
-    if (len > 0) {
-        Chunk next;
-        fetch(next, 0);
-        put(next, 0);
-        fetch(next, 1);
-        __syncthreads();
-        for (int c = 0; c * C < len; ++c) chunk(c, next);
+    pass(std::false_type());
+    if (S.odd(Decays<X>(sd).odd_k)) {
+        __syncthreads();                                 // all have read it
+        pass(std::true_type());
     }
 
     if (last) {
@@ -652,7 +734,7 @@ __global__ __launch_bounds__(kSumThreads) void lin_sums_kernel(const LinArgs a) 
 constexpr double kGone = -150.0;
 
 template <int DK, int DV, bool BF>
-__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_kernel(const LinArgs a) {
+__global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), BF ? 3 : 2) void lin_states_kernel(const LinArgs a) {
     using X = Shape<DK, DV, BF>;
     using T = typename X::T;
     constexpr int C = X::C;
@@ -700,53 +782,83 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), 2) void lin_states_ke
     const double behind = rest;
 
     State<X> S;
-    S.load(nullptr);
-    const int chunks = len / C;
-    Source<X, DK> fk(a.k, t0 + len - C, a.k_row, hk * DK);
-    Source<X, DV> fv(a.v, t0 + len - C, a.v_row, (int64_t)h * DV);
-    const char *fg = (const char *)(a.g + (t0 + len - C) * a.g_row + h);
-    const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
-    struct Chunk { Rows<X, DK> k; Rows<X, DV> v; float g; };
-    auto fetch = [&](Chunk &r, int c) {         // the c-th chunk from the end
-        const int valid = c < chunks ? C : 0;
-        r.k.fetch(fk, valid);
-        r.v.fetch(fv, valid);
-        r.g = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(window(fg, valid, g_row, 4), g_at, 0, 0));
-        fk.step(-1);
-        fv.step(-1);
-        fg -= (int64_t)g_row * C;
-    };
-    auto put = [&](const Chunk &r, int c) {
-        r.k.put(sk + c % 2 * C * DK);
-        r.v.put(sv + c % 2 * C * DV);
-        if (c % X::NW == w) {
+    // As in lin_kernel, but one body: the registers of two would leave room for two workgroups a compute unit, not three.
+    bool careful = false;
+    auto pass = [&]() {
+        S.load(nullptr);
+        rest = behind;
+        const int chunks = len / C;
+        Source<X, DK> fk(a.k, t0 + len - C, a.k_row, hk * DK);
+        Source<X, DV> fv(a.v, t0 + len - C, a.v_row, (int64_t)h * DV);
+        const char *fg = (const char *)(a.g + (t0 + len - C) * a.g_row + h);
+        const int g_row = (int)a.g_row * 4, g_at = lane % C * g_row;
+        struct Chunk { Rows<X, DK> k; Rows<X, DV> v; float g; };
+        auto fetch = [&](Chunk &r, int c) {         // the c-th chunk from the end
+            const int valid = c < chunks ? C : 0;
+            r.k.fetch(fk, valid);
+            r.v.fetch(fv, valid);
+            r.g = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(window(fg, valid, g_row, 4), g_at, 0, 0));
+            fk.step(-1);
+            fv.step(-1);
+            fg -= (int64_t)g_row * C;
+        };
+        auto put = [&](const Chunk &r, int c) {
+            r.k.put(sk + c % 2 * C * DK);
+            r.v.put(sv + c % 2 * C * DV);
+            if (careful) {
+                const Decays<X> s(sd + c % 2 * X::DB);
+                r.k.mark(s.odd_k);
+                r.v.mark(s.odd_v);
+            }
+            if (c % X::NW == w) {
+                const Decays<X> s(sd + c % 2 * X::DB);
+                double all;
+                const double x = summed<X>(r.g, &all);
+                const double after = c ? s_rest[(c - 1) % 2] : behind;
+                if (lane < C) s.keep[lane] = exp2_of(after + (all - x));
+                if (lane == 0) s_rest[c % 2] = after + all;
+            }
+        };
+
+        Chunk next;
+        fetch(next, 0);
+        put(next, 0);
+        fetch(next, 1);
+        bool more = true;
+        for (int c = 0; more; ++c) {
+            __syncthreads();
+            rest = s_rest[c % 2];
+            more = c + 1 < chunks && !(rest < kGone);
+            if (more) put(next, c + 1);
+            fetch(next, c + 2);
+            __builtin_amdgcn_sched_barrier(0);   // the loads leave before the products, which take long
+            T *const k = sk + c % 2 * C * DK;
+            const T *const v = sv + c % 2 * C * DV;
             const Decays<X> s(sd + c % 2 * X::DB);
-            double all;
-            const double x = summed<X>(r.g, &all);
-            const double after = c ? s_rest[(c - 1) % 2] : behind;
-            if (lane < C) s.keep[lane] = exp2_of(after + (all - x));
-            if (lane == 0) s_rest[c % 2] = after + all;
+            typename X::O::F8 vf[X::NB];
+            S.values(v, vf);
+            uint32_t odd_k = 0, odd_v = 0;
+            if (careful) {
+                odd_k = s.any(s.odd_k);
+                odd_v = s.any(s.odd_v);
+            }
+            if (odd_k | odd_v) {
+                S.add_rare(k, v, s.keep, odd_k, odd_v);
+#pragma unroll
+                for (int b = 0; b < X::NB; ++b) clean<X>(&vf[b]);
+                __syncthreads();
+                for (uint32_t left = odd_k; left; left &= left - 1)
+                    if (threadIdx.x < DK) k[at<T, DK>(__builtin_ctz(left), threadIdx.x)] = (T)0.f;
+                __syncthreads();
+            }
+            S.add(k, vf, s.keep);
         }
     };
-
-    Chunk next;
-    fetch(next, 0);
-    put(next, 0);
-    fetch(next, 1);
-    bool more = true;
-    for (int c = 0; more; ++c) {
+    for (;;) {
+        pass();
+        if (careful || !S.odd(Decays<X>(sd).odd_k)) break;
+        careful = true;
         __syncthreads();
-        rest = s_rest[c % 2];
-        more = c + 1 < chunks && !(rest < kGone);
-        if (more) put(next, c + 1);
-        fetch(next, c + 2);
-        const T *const k = sk + c % 2 * C * DK, *const v = sv + c % 2 * C * DV;
-        const Decays<X> s(sd + c % 2 * X::DB);
-        typename X::O::F8 vf[X::NB];
-        S.values(v, vf);
-        const bool rare = S.clean(vf);
-        S.add(k, vf, s.keep);
-        if (rare) S.add_rare(k, v, s.keep);
     }
     S.store(a.part + slot * S.SIZE);
     if (threadIdx.x == 0 && piece == 0) a.kept[kept] = exp2_of(rest);

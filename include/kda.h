@@ -639,7 +639,9 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
  * tokens and the state are rounded to bf16 as operands of the outputs' products;
  * the state itself is formed from operands that keep 24 bits.  With fp32 rows
  * every operand keeps its 24 bits.  An output depends on no later token, nor on
- * another sequence, infinities and NaN included.
+ * another sequence, infinities and NaN included.  Infinities and NaN of k and v
+ * enter the state as the formula says; outputs sum them as q^T (k v^T) or as
+ * (q.k) v, so that infinities of both signs may leave an infinity or a NaN.
  */
 typedef struct {
     int32_t num_qk_heads, num_v_heads, dk, dv;

@@ -1,0 +1,92 @@
+"""GPU tests of the linear-attention layer's operators at the ends of their number range and in every launch plan,
+against the fp64 oracle (oracle/linear.py).  Tolerances as in test_gpu_linear.py unless a test derives its own."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import test_gpu_linear as G
+from test_gpu_linear import HALF, U, Call, f32, i32, i64, within
+from workloads.device import to_numpy_f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def K():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import gated_delta_rule_46_amd.kda as kda
+    return kda
+
+
+def workspace(K, dtype, T, N, Hk, Hv, dk, dv):
+    c = K.kda_lin_config(Hk, Hv, dk, dv, {"bf16": 1, "f32": 0}[dtype], 1.0)
+    return K.LIB.kda_lin_prefill_workspace(ctypes.byref(c), T, N)
+
+
+def is_cut(K, c):
+    """Whether a call's long sequences run in segments: its workspace holds more than an order of the sequences."""
+    return workspace(K, c.dtype, c.q.shape[0], len(c.lens), *c.dims) > -(-4 * len(c.lens) // 256) * 256
+
+
+def run(K, c, scale=0.3, **kw):
+    """Outputs of the sequences' rows and the pool, in fp64."""
+    import torch
+    o, _ = K.kda_lin_prefill(c.q, c.k, c.v, c.g, i64(c.cu), c.pool, i32(c.read), i32(c.write), scale=scale, **kw)
+    torch.cuda.synchronize()
+    return to_numpy_f64(o)[:c.cu[-1]], to_numpy_f64(c.pool)
+
+
+def same_or_within(name, got, ref, tol):
+    """Infinities and NaN where the reference has them, the rest within tol."""
+    odd = ~np.isfinite(ref)
+    assert np.array_equal(got[odd], ref[odd], equal_nan=True), \
+        f"{name}: {(~((got == ref) | (np.isnan(got) & np.isnan(ref))) & odd).sum()} of {odd.sum()} values that are not finite differ"
+    within(name, got[~odd], ref[~odd], tol[~odd])
+
+
+def close(c, o, pool, ref, top, n):
+    """The tolerances of Call.check, elementwise."""
+    live = c.cu[-1]
+    half = HALF[c.dtype]
+    ops = 2 * half if c.dtype == "bf16" else 0.0
+    dk = c.dims[2]
+    same_or_within("o", o, ref[0][:live], half * np.abs(ref[0][:live]) + (ops + (6 * n + dk + 8) * U) * top[0][:live] + 1e-37)
+    same_or_within("pool", pool, ref[1], (6 * n + 8) * U * top[1] + 1e-37)
+
+
+# ---------------------------------------------------------------------------
+# infinities and NaN
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("lens", [[70], [33, 1, 64], [700, 1500]])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_keys(K, dtype, dk, dv, lens):
+    """An infinite key enters the state as infinity times v, whose sign is v's, a NaN where v is zero; beside
+    infinite values too, at a call's last token (weight 1) and in the middle of it, in one piece and in segments."""
+    c = Call(dtype, lens, 1, 2, dk, dv, "token", 81)
+    assert is_cut(K, c) == (len(lens) == 2)
+    T = sum(lens)
+    c.g = f32(-0.01 * np.random.default_rng(82).random((T, 2)))
+    for n, end in enumerate(c.cu[1:]):
+        begin = c.cu[n]
+        if end - begin < 33:
+            continue
+        c.v[end - 1, 0, 3] = 0.0                           # infinity times zero
+        c.v[end - 1, 0, 5] = np.inf                        # beside an infinite value
+        c.k[end - 1, 0, 7] = np.inf
+        c.k[end - 2, 0, dk - 1] = -np.inf
+        c.k[begin + 20, 0, 9] = np.nan if n == 1 else np.inf
+        c.v[begin + 20, 1, 6] = -np.inf
+    with np.errstate(all="ignore"):
+        ref, top = c.oracle(scale=0.3), c.oracle(scale=0.3, size=True)
+        assert np.isinf(ref[1]).any() and np.isnan(ref[1]).any()
+        o, pool = run(K, c)
+        # with an infinite value an output sums infinities of both signs, q_d k_d v over the channels d: (q.k) v is one
+        # infinity where q^T (k v) is a NaN, and both are the formula
+        for h, x in ((0, 5), (1, 6)):
+            odd = ~np.isfinite(ref[0][:, h, x])
+            assert not np.isfinite(o[odd, h, x]).any()
+            o[odd, h, x] = ref[0][odd, h, x]
+        close(c, o, pool, ref, top, max(lens))
