@@ -8,7 +8,8 @@ off (-packed-fp32-ops): the kernels rely on plain fp32 arithmetic only.
 
 The device assembly of every source is emitted alongside (_build/*.s) and
 checked by isa_check: the build fails if any MFMA accumulates onto the fresh
-result of an MFMA of another shape (see isa_check for why).
+result of an MFMA of another shape, or if a register is copied where half of
+the lanes miss the copy (see isa_check for why).
 """
 from __future__ import annotations
 
@@ -51,10 +52,15 @@ def _assemble_listing(src: str) -> str:
 
 
 def check_listings(paths) -> None:
-    from .isa_check import check_file
+    from .isa_check import check_file, masked_copies
     bad = []
     for p in paths:
         bad += [(os.path.basename(p),) + h for h in check_file(p)]
+        with open(p) as f:
+            lost = masked_copies(f.read())
+        if lost:
+            raise RuntimeError(f"{os.path.basename(p)}: {len(lost)} vector write(s) that a branch's other lanes miss:\n" +
+                               "\n".join(f"  {ln} ({fn[:60]}): {t}" for fn, ln, t in lost[:20]))
     if bad:
         lines = "\n".join(f"  {f}:{ln} ({fn[:60]}): {a}  ->  {b}  [{d} wait states]"
                            for (f, fn, ln, a, b, d) in bad[:20])

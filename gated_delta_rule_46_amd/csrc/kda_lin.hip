@@ -79,6 +79,9 @@ struct Shape {
     static_assert(LDS <= 160 * 1024);
 };
 
+// The wave's number, in a scalar register: branches on it change no lane masks.
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
 // Element x of row r of an LDS tile of W columns.  Its 16-byte pieces are permuted by the row so
 // that neither 16 rows at one piece (operands along a row) nor 4 rows at 4 pieces (transposed
 // ones) meet in a bank.
@@ -323,9 +326,9 @@ struct Rows {
             const uint64_t lanes = __ballot(x != x);
 #pragma unroll
             for (int l = 0; l < ROWS; ++l)
-                if (lanes >> (l * S::PIECES) & ((1ull << S::PIECES) - 1)) rows |= 1u << (i * S::STEP + (threadIdx.x >> 6) * ROWS + l);
+                if (lanes >> (l * S::PIECES) & ((1ull << S::PIECES) - 1)) rows |= 1u << (i * S::STEP + wave_of() * ROWS + l);
         }
-        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = rows;
+        if ((threadIdx.x & 63) == 0) waves[wave_of()] = rows;
     }
 };
 
@@ -347,7 +350,7 @@ struct State {
     f32x4 s[X::NB][X::NKB][2];
     static __device__ __forceinline__ int first() {
         const int lane = threadIdx.x & 63, m = lane & 15;
-        return 8 * (lane >> 4) * X::HV + 16 * X::NB * (threadIdx.x >> 6) + STEP * (m >> 2) + (m & 3);
+        return 8 * (lane >> 4) * X::HV + 16 * X::NB * wave_of() + STEP * (m >> 2) + (m & 3);
     }
     template <typename F>
     __device__ __forceinline__ void each(F f) {
@@ -387,28 +390,27 @@ struct State {
                 for (int i = 0; i < 4; ++i) x[i] = fmaf(s[0][kb][hf][i], 0.f, x[i]);
         const float sum = (x[0] + x[1]) + (x[2] + x[3]);
         const bool mine = __any(sum != sum);
-        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = mine;
+        if ((threadIdx.x & 63) == 0) waves[wave_of()] = mine;
         __syncthreads();
         return Decays<X>::any(waves);
     }
     // v^T of the wave's columns
     __device__ __forceinline__ static void values(const typename X::T *v, typename X::O::F8 *vf) {
 #pragma unroll
-        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * (threadIdx.x >> 6) + 4 * b);
+        for (int b = 0; b < X::NB; ++b) vf[b] = ld_t<X, X::DV, STEP>(v, 0, 16 * X::NB * wave_of() + 4 * b);
     }
     // s += k^T (weights v) token by token: all of a token whose k has an infinity or a NaN (bits of odd_k), and columns of
     // one whose v has.
     __device__ __forceinline__ void add_rare(const typename X::T *k, const typename X::T *v, const float *keep, uint32_t odd_k,
                                              uint32_t odd_v) {
-        const int lane = threadIdx.x & 63, m = lane & 15;
         for (uint32_t left = odd_k | odd_v; left; left &= left - 1) {
-            const int j = __builtin_ctz(left), gq = in_loop(lane >> 4);
+            const int j = __builtin_ctz(left), lane = in_loop(threadIdx.x & 63), m = lane & 15, gq = lane >> 4;
             const bool whole = odd_k >> j & 1;
             float x[X::NB];
             bool there[X::NB];
 #pragma unroll
             for (int b = 0; b < X::NB; ++b) {
-                x[b] = (float)v[at<typename X::T, X::DV>(j, 16 * X::NB * (threadIdx.x >> 6) + STEP * (m >> 2) + (m & 3) + 4 * b)];
+                x[b] = (float)v[at<typename X::T, X::DV>(j, 16 * X::NB * wave_of() + STEP * (m >> 2) + (m & 3) + 4 * b)];
                 there[b] = whole || not_finite(x[b]);
                 x[b] *= keep[j];
             }
@@ -487,7 +489,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
     T *const sp = (T *)(lds + 4 * X::KB + 2 * X::VB);
     char *const sd = lds + 4 * X::KB + 2 * X::VB + 2 * X::PB;
 
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_of();
     const int m = lane & 15, gq = lane >> 4;
     const int x0 = blockIdx.x % (HV / DV) * DV;          // first of the workgroup's columns
     const int item = blockIdx.x / (HV / DV), unit = item / a.Hv, h = item - unit * a.Hv;
@@ -610,7 +612,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
                 // above its diagonal, nor infinite keys the zero terms of a value.
                 __syncthreads();
                 for (uint32_t left = odd_k | odd_v; left; left &= left - 1) {
-                    const int j = __builtin_ctz(left), i = in_loop(m);
+                    const int j = __builtin_ctz(left), i = in_loop(m), x0 = in_loop(col);
                     const bool whole = odd_k >> j & 1;
                     float y[NT];
 #pragma unroll
@@ -619,7 +621,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float x = (float)v[at<T, DV>(j, col + 4 * b + r)];
+                            const float x = (float)v[at<T, DV>(j, x0 + 4 * b + r)];
                             const bool there = whole || not_finite(x);
 #pragma unroll
                             for (int it = 0; it < NT; ++it) {
@@ -642,8 +644,9 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
             }
             S.add(k, vf, s.keep);
 
+            if constexpr (CAREFUL) fetch(next, c + 1);   // no sooner: its registers are needed above
             put(next, c + 1);
-            fetch(next, c + 2);
+            if constexpr (!CAREFUL) fetch(next, c + 2);
             __syncthreads();   // P and the next chunk are there
 
 #pragma unroll
@@ -679,7 +682,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
             Chunk next;
             fetch(next, 0);
             put(next, 0);
-            fetch(next, 1);
+            if constexpr (!CAREFUL) fetch(next, 1);
             __syncthreads();
             for (int c = 0; c * C < len; ++c) chunk(c, next);
         }
@@ -744,7 +747,7 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), BF ? 3 : 2) void lin_
     T *const sk = (T *)lds, *const sv = (T *)(lds + 2 * X::KB);
     char *const sd = lds + 2 * (X::KB + X::VB);
 
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = wave_of();
     // heads that remember longest take most of the time: they come at another place in each unit's row, as
     // workgroups are dealt out to the compute units in turn
     const int unit = blockIdx.x / a.Hv, h = (blockIdx.x - unit * a.Hv + unit) % a.Hv;

@@ -7,6 +7,13 @@ separates the two, and the compiler inserts no wait states for that case.
 The kernels therefore never chain accumulators across MFMA shapes; this check
 scans the emitted assembly and reports every place where such a chain appears
 within `window` wait states, so the build fails instead of the numerics.
+
+The compiler may also place a copy of a vector register, made where registers
+run short, between the masked half of a lane-dependent branch and the
+instruction that turns to the other lanes.  Lanes of the other half then miss
+the copy and read what was in the register before.  No vector register is
+written at that place in a right program of these kernels, so the check
+reports every one that is.
 """
 from __future__ import annotations
 
@@ -75,6 +82,29 @@ def mixed_mfma_chains(asm: str, window: int = 32):
             if w:
                 recent = [(r[0], r[1], r[2] - w, r[3], r[4]) for r in recent if r[2] - w]
         ws += 1
+    return hits
+
+
+_BLOCK = re.compile(r"^(\.LBB\d+_\d+:|; %bb\.\d+:)")
+
+
+def masked_copies(asm: str):
+    """Vector registers written in a block before the s_andn2_saveexec or s_or_saveexec that turns to a branch's other
+    lanes: [(function, line_no, text)].  Writes of single lanes take no notice of the mask and pass."""
+    hits, func, block = [], "?", []
+    for no, raw in enumerate(asm.split("\n"), 1):
+        t = raw.strip()
+        fm = _FUNC.match(t)
+        if fm and not t.startswith((".L", "$")):
+            func, block = fm.group(1), []
+        elif _BLOCK.match(t):
+            block = []
+        elif t.startswith(("s_andn2_saveexec", "s_or_saveexec")):
+            hits += block
+            block = []
+        elif t.startswith(("v_", "ds_read", "scratch_load", "global_load", "buffer_load")) and \
+                not t.startswith(("v_writelane", "v_readlane", "v_readfirstlane", "v_cmp")):
+            block.append((func, no, t))
     return hits
 
 
