@@ -95,7 +95,7 @@ __device__ __forceinline__ int at(int r, int x) {
 // A chunk's decays in LDS.
 template <class X>
 struct Decays {
-    float *hi, *lo, *out, *keep;      // G in log2 (two floats), scale e^G, e^{G_C - G}
+    float *hi, *lo, *out, *keep;      // G / 2 in log2 (two floats), scale e^G, e^{G_C - G}
     float *all;                       // e^{G_C}
     uint32_t *odd_k, *odd_v;          // per wave: which rows of k and v that it put there hold infinities or NaN
     __device__ explicit Decays(char *p) {
@@ -189,12 +189,14 @@ __device__ __forceinline__ void clean(typename X::O::F8 *f) {
     *f = X::O::cvt8(x);
 }
 
-// 2^x of an fp64 x <= 0 or so, to about an ulp of fp32.
+// 2^x of an fp64 x <= 0 or so, to about an ulp of fp32.  (The exponential instruction gives zeros below 2^-126.)
 __device__ __forceinline__ float exp2_of(double x) {
     const float hi = (float)x;
     const float lo = (float)(x - (double)hi);
-    const float e = mf::ex2(hi);
-    return hi < -150.f ? 0.f : e + e * (lo * 0.6931471805599453f);
+    const bool small = hi < -126.f;
+    const float e = mf::ex2(small ? hi + 64.f : hi);
+    const float r = e + e * (lo * 0.6931471805599453f);
+    return hi < -150.f ? 0.f : small ? r * 0x1p-64f : r;
 }
 
 // Lane l - off of x in its row of 16 lanes, 0 before the row.
@@ -242,15 +244,16 @@ __device__ __forceinline__ void write_decays(char *p, float g, float scale) {
     double all;
     const double x = summed<X>(g, &all);
     if (lane < X::C) {
-        s.hi[lane] = (float)x;
-        s.lo[lane] = (float)(x - (double)(float)x);
+        const double half = 0.5 * x;
+        s.hi[lane] = (float)half;
+        s.lo[lane] = (float)(half - (double)(float)half);
         s.out[lane] = scale * exp2_of(x);
         s.keep[lane] = exp2_of(all - x);
         if (lane == 0) *s.all = exp2_of(all);
     }
 }
 
-// 2^(G_i - G_j)
+// 2^((G_i - G_j) / 2) of halves of G: its square reaches below the smallest normal number
 template <class X>
 __device__ __forceinline__ float decay_between(float hi_i, float lo_i, float hi_j, float lo_j) {
     const float d = hi_i - hi_j;
@@ -571,8 +574,10 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
                 const f32x4 hj = *(const f32x4 *)(s.hi + j), lj = *(const f32x4 *)(s.lo + j);
                 const float hi = s.hi[i], li = s.lo[i];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    p[r] = j + r <= i ? a.scale * decay_between<X>(hi, li, hj[r], lj[r]) * p[r] : 0.f;
+                for (int r = 0; r < 4; ++r) {
+                    const float e = decay_between<X>(hi, li, hj[r], lj[r]);
+                    p[r] = j + r <= i ? a.scale * (p[r] * e * e) : 0.f;
+                }
                 O::st4(pt + at<T, C>(i, j), p);
             }
 

@@ -630,8 +630,9 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
  * g: fp32 log decays, g[t * g_row + h], 4-byte aligned; g_row is 0 (one decay
  * per head for all tokens) or num_v_heads .. 2^24.  g <= 0, -infinity among it
  * (the state is dropped); values below -10^4 count as that.  What the decays have
- * brought below 2^-150 of itself counts as nothing (an infinity or a NaN that they
- * have brought there may still leave a NaN).
+ * brought below 2^-150 of itself may count as nothing (an infinity or a NaN that
+ * they have brought there may still leave a NaN); below 2^-126 of itself it has an
+ * error of 2^-149 of what it was.
  * T * num_v_heads is at most 2^26 and N * num_v_heads at most 2^20 (larger calls
  * are split by the caller).
  *

@@ -90,3 +90,66 @@ def test_infinite_keys(K, dtype, dk, dv, lens):
             assert not np.isfinite(o[odd, h, x]).any()
             o[odd, h, x] = ref[0][odd, h, x]
         close(c, o, pool, ref, top, max(lens))
+
+
+# ---------------------------------------------------------------------------
+# decays below the smallest normal number
+# ---------------------------------------------------------------------------
+def small_decays(dtype, lens, seed, at):
+    """States of 2^100 and decays of e^-95 = 2^-137 at tokens `at` of every sequence; k and v of about 2^-18, so that
+    what they add is of the size of what the state leaves."""
+    c = Call(dtype, lens, 1, 2, 64, 64, "head", seed)
+    rng = np.random.default_rng(seed + 1)
+    g = -1e-4 * rng.random((sum(lens), 2))
+    for begin, n in zip(c.cu, lens):
+        for t in at:
+            g[begin + t if t >= 0 else begin + n + t] = -95.0
+    c.g = f32(g)
+    c.k.mul_(2.0 ** -18)
+    c.v.mul_(2.0 ** -18)
+    c.pool.mul_(2.0 ** 100)
+    return c
+
+
+def check_small(K, c, size, out=None):
+    """As Call.check, and for each factor between 2^-126 and 2^-149 an error of 2^-149 (one step there) of what it
+    multiplies, which is at most `size` times what is there after it."""
+    ref, top = c.oracle(scale=0.3), c.oracle(scale=0.3, size=True)
+    o, pool = run(K, c) if out is None else out
+    n, half = max(c.lens), HALF[c.dtype]
+    ops = 2 * half if c.dtype == "bf16" else 0.0
+    rel = 2.0 ** -149 * size
+    within("o", o, ref[0], half * np.abs(ref[0]) + (ops + (6 * n + c.dims[2] + 8) * U + rel) * top[0] + 1e-37)
+    within("pool", pool, ref[1], ((6 * n + 8) * U + rel) * top[1] + 1e-37)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[1], [1, 40, 3], [100, 33]])
+def test_states_behind_small_decays(K, dtype, lens):
+    check_small(K, small_decays(dtype, lens, 83, [0]), 2.0 ** 138)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_behind_small_decays_in_segments(K, dtype):
+    c = small_decays(dtype, [2000], 84, [300])
+    assert is_cut(K, c)
+    check_small(K, c, 2.0 ** 138)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tokens_behind_small_decays(K, dtype):
+    """Within one chunk: what tokens of 2^50 and 2^50 leave behind a decay of 2^-137."""
+    c = small_decays(dtype, [30], 85, [11])
+    c.k[:11].mul_(2.0 ** 68)
+    c.v[:11].mul_(2.0 ** 68)
+    c.pool.mul_(0.0)
+    check_small(K, c, 2.0 ** 138)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_of_small_decays(K, dtype):
+    import torch
+    c = small_decays(dtype, [1, 1, 1], 86, [0])
+    o = K.kda_lin_decode(c.q, c.k, c.v, c.g, c.pool, i32(c.read), i32(c.write), scale=0.3)
+    torch.cuda.synchronize()
+    check_small(K, small_decays(dtype, [1, 1, 1], 86, [0]), 2.0 ** 138, (to_numpy_f64(o), to_numpy_f64(c.pool)))
