@@ -38,7 +38,7 @@ struct LinArgs {
     int32_t *order;              // [N] sequences by the length of their last segment (null: as they come)
     float *carry;                // [slots,Hv,dk,dv]
     float *part;                 // [stretches,pieces,Hv,dk,dv]
-    float *kept;                 // [stretches,Hv] decay over a segment
+    float *kept;                 // [stretches,Hv] decay over a segment: e^G, or e^G - 1 with its sign where G is near 0
     int32_t *live;               // [stretches,pieces,Hv] whether the piece adds anything
     double *sums;                // [stretches,seg/64,Hv] log2 decays of 64 tokens (with more than one piece)
 };
@@ -69,6 +69,13 @@ __device__ __forceinline__ float *slot_of(const LinArgs &a, const int32_t *idx, 
     if (!idx) return nullptr;
     const int64_t i = idx[n];
     return i >= 0 && i < a.n_slots ? a.pool + i * a.Hv * state : nullptr;
+}
+
+// e^t - 1 for t within 1/8 of zero: the terms left out are below 2^-30 of it.  (e^t as a float keeps few bits of it where
+// t is near zero, and one decay for all tokens would add up the same error with every one of them.)
+constexpr float kSlow = -0.125f;
+__device__ __forceinline__ float expm1_small(float t) {
+    return t + t * t * (1.f / 2 + t * (1.f / 6 + t * (1.f / 24 + t * (1.f / 120 + t * (1.f / 720)))));
 }
 
 }  // namespace kda

@@ -236,9 +236,23 @@ __device__ __forceinline__ double summed(float g, double *all) {
     return x;
 }
 
+// The factor 2^x of a state.  A head with one decay for all tokens would have the same factor in every chunk, and its
+// rounding would add up over some 1 / (1 - factor) of them (16,384 tokens at a decay of e^-0.00003: 10^-5).  So what the
+// rounding of a factor near one left out goes into the next one.
+__device__ __forceinline__ float state_factor(double x, float *left_out) {
+    const float t = (float)(x * 0.6931471805599453) + *left_out;
+    if (t > kSlow && t < 0x1p-20f) {
+        const float m = expm1_small(t), f = 1.f + m;
+        *left_out = m - (f - 1.f);
+        return f;
+    }
+    *left_out = 0.f;
+    return exp2_of(x);
+}
+
 // The decays of a chunk, by one wave.
 template <class X>
-__device__ __forceinline__ void write_decays(char *p, float g, float scale) {
+__device__ __forceinline__ void write_decays(char *p, float g, float scale, float *left_out) {
     const int lane = threadIdx.x & 63;
     const Decays<X> s(p);
     double all;
@@ -249,8 +263,9 @@ __device__ __forceinline__ void write_decays(char *p, float g, float scale) {
         s.lo[lane] = (float)(half - (double)(float)half);
         s.out[lane] = scale * exp2_of(x);
         s.keep[lane] = exp2_of(all - x);
-        if (lane == 0) *s.all = exp2_of(all);
     }
+    const float f = state_factor(all, left_out);
+    if (lane == 0) *s.all = f;
 }
 
 // 2^((G_i - G_j) / 2) of halves of G: its square reaches below the smallest normal number
@@ -537,6 +552,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
             fv.step(1);
             fg += (int64_t)g_row * C;
         };
+        float left_out = 0.f;
         auto put = [&](const Chunk &r, int c) {
             r.q.put(sq + c % 2 * C * DK);
             r.k.put(sk + c % 2 * C * DK);
@@ -546,7 +562,7 @@ __global__ __launch_bounds__((Shape<DK, HV, BF, DV>::THREADS), 2) void lin_kerne
                 r.k.mark(s.odd_k);
                 r.v.mark(s.odd_v);
             }
-            if (w == X::NW - 1) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale);
+            if (w == X::NW - 1) write_decays<X>(sd + c % 2 * X::DB, lane % C < len - c * C ? r.g : 0.f, a.scale, &left_out);
         };
 
         const int col = 16 * NB * w + S.STEP * gq;           // first of the columns that the lane stores
@@ -869,7 +885,10 @@ __global__ __launch_bounds__((Shape<DK, DV, BF>::THREADS), BF ? 3 : 2) void lin_
         __syncthreads();
     }
     S.store(a.part + slot * S.SIZE);
-    if (threadIdx.x == 0 && piece == 0) a.kept[kept] = exp2_of(rest);
+    if (threadIdx.x == 0 && piece == 0) {
+        const float t = (float)(rest * 0.6931471805599453);
+        a.kept[kept] = t > kSlow && t <= 0.f ? -fabsf(expm1_small(t)) : exp2_of(rest);
+    }
 }
 
 // The incoming states of a split sequence's segments: four elements a thread, one segment
@@ -917,7 +936,8 @@ __global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs 
         look(s0 + G);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            S *= keep[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[j] = fmaf(S[j], keep[i], f32_bits(keep[i]) >> 31 ? S[j] : 0.f);
 #pragma unroll
             for (int p = 0; p < kMaxPieces; ++p) S += part[i][p];
             dst += (int64_t)a.Hv * size;

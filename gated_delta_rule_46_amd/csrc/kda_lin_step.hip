@@ -63,7 +63,9 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const LinArgs a) {
     const int64_t t = n;
     const int hk = h / (a.Hv / a.Hk);
     const f32x4 v = load4<BF>(a.v, t * a.v_row + (int64_t)h * DV + col);
-    const float keep = expf(a.g[t * a.g_row + h]);
+    const float g = a.g[t * a.g_row + h];
+    const bool slow = g > kSlow && g <= 0.f;                  // S + S (e^g - 1)
+    const float keep = slow ? expm1_small(g) : expf(g);
     if (tid < DK) {
         s_q[tid] = a.scale * load1<BF>(a.q, t * a.q_row + hk * DK + tid);
         s_k[tid] = load1<BF>(a.k, t * a.k_row + hk * DK + tid);
@@ -74,7 +76,9 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const LinArgs a) {
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
         const int row = 16 * j + 4 * w + ro;
-        S[j] = keep * S[j] + s_k[row] * v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[j][c] = fmaf(S[j][c], keep, slow ? S[j][c] : 0.f);
+        S[j] += s_k[row] * v;
         o += s_q[row] * S[j];
     }
     if (dst) {

@@ -153,3 +153,72 @@ def test_decode_of_small_decays(K, dtype):
     o = K.kda_lin_decode(c.q, c.k, c.v, c.g, c.pool, i32(c.read), i32(c.write), scale=0.3)
     torch.cuda.synchronize()
     check_small(K, small_decays(dtype, [1, 1, 1], 86, [0]), 2.0 ** 138, (to_numpy_f64(o), to_numpy_f64(c.pool)))
+
+
+# ---------------------------------------------------------------------------
+# one decay for all tokens, near one
+# ---------------------------------------------------------------------------
+def slow_heads(rng, H, lo, hi):
+    """Decays that no two heads share, between e^-lo and e^-hi a token."""
+    return -np.exp(rng.uniform(np.log(lo), np.log(hi), H)).astype(np.float32)
+
+
+def test_constant_decays_do_not_drift(K):
+    """An uncut sequence of 512 chunks whose values are zeros: each chunk rounds an element of the state once, by at most
+    2^-24 and with no common sign, so all together stay within 2^-24 (8 + sqrt(512)).  One factor rounded the same in
+    every chunk would put a head off by up to 512 2^-25, 2^-24 150 on average."""
+    import torch
+    H, T, dk, dv = 256, 16384, 64, 64
+    rng = np.random.default_rng(91)
+    assert workspace(K, "bf16", T, 1, 1, H, dk, dv) == 0
+    q = torch.ones((T, 1, dk), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros((T, H, dv), dtype=torch.bfloat16, device="cuda")
+    g = slow_heads(rng, H, 1e-6, 1e-4)
+    S = rng.normal(size=(H, dk, dv)).astype(np.float32)
+    pool = f32(np.stack([S, np.zeros_like(S)]))
+    K.kda_lin_prefill(q, q, v, f32(g), i64([0, T]), pool, i32([0]), i32([1]), scale=0.1)
+    torch.cuda.synchronize()
+    ref = S.astype(np.float64) * np.exp(T * g.astype(np.float64))[:, None, None]
+    e = G.rel_l2(to_numpy_f64(pool[1]), ref)
+    G.say(f"drift over 512 chunks {e / U:.1f} of 2^-24")
+    assert e <= U * (8 + 512 ** 0.5)
+
+
+def test_constant_decays_do_not_drift_in_segments(K):
+    """As above over 16 and more segments, whose states are carried with one rounding each."""
+    import torch
+    T, dk, dv = 8192, 64, 64
+    rng = np.random.default_rng(92)
+    assert workspace(K, "f32", T, 1, 1, 4, dk, dv) > 0
+    q = torch.ones((T, 1, dk), device="cuda")
+    v = torch.zeros((T, 4, dv), device="cuda")
+    g = slow_heads(rng, 4, 1e-7, 1e-5)
+    S = rng.normal(size=(4, dk, dv)).astype(np.float32)
+    pool = f32(np.stack([S, np.zeros_like(S)]))
+    K.kda_lin_prefill(q, q, v, f32(g), i64([0, T]), pool, i32([0]), i32([1]), scale=0.1)
+    torch.cuda.synchronize()
+    ref = S.astype(np.float64) * np.exp(T * g.astype(np.float64))[:, None, None]
+    for h in range(4):
+        e = G.rel_l2(to_numpy_f64(pool[1, h]), ref[h])
+        G.say(f"head {h}: {e / U:.1f} of 2^-24")
+        assert e <= U * (8 + (T // 64) ** 0.5)
+
+
+def test_decode_with_constant_decays_does_not_drift(K):
+    """2,048 steps: an element is rounded once in each, so within 2^-24 (8 + sqrt(2,048)) together; a factor rounded the
+    same in every step would put a head off by up to 2^-25 2,048."""
+    import torch
+    H, n, dk, dv = 64, 2048, 64, 64
+    rng = np.random.default_rng(93)
+    q = torch.ones((1, 1, dk), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros((1, H, dv), dtype=torch.bfloat16, device="cuda")
+    g = slow_heads(rng, H, 1e-5, 1e-3)
+    S = rng.normal(size=(H, dk, dv)).astype(np.float32)
+    pool, slot, gd = f32(S[None]), i32([0]), f32(g)
+    for _ in range(n):
+        K.kda_lin_decode(q, q, v, gd, pool, slot, slot, scale=0.1)
+    torch.cuda.synchronize()
+    ref = S.astype(np.float64) * np.exp(n * g.astype(np.float64))[:, None, None]
+    e = G.rel_l2(to_numpy_f64(pool[0]), ref)
+    G.say(f"drift over 2,048 steps {e / U:.1f} of 2^-24")
+    assert e <= U * (8 + n ** 0.5)
