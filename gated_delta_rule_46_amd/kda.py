@@ -1067,6 +1067,8 @@ def _lin_prefill_plan(q, k, v, g, cu, pool, read, write, interval, offsets, ckpt
             raise ValueError("ckpt_offsets is required for more than one sequence")
         if ckpt is not None:
             _dense(ckpt, "ckpt_out", (ckpt[0][0], Hv, dk, dv), torch.float32, dev)
+            if offsets is None and ckpt[0][0] < T // interval:
+                raise ValueError(f"ckpt_out has {ckpt[0][0]} rows, the sequence may have {T // interval} rungs")
     elif offsets is not None or ckpt is not None:
         raise ValueError("ckpt_offsets / ckpt_out need ckpt_interval")
     if out is not None:
@@ -1083,7 +1085,7 @@ def kda_lin_prefill(q, k, v, g, cu_seqlens, pool=None, read_idx=None, write_idx=
     tokens), cu_seqlens int64 [N+1].  pool: fp32 [n_slots,Hv,dk,dv] states, read at read_idx and written
     at write_idx (int32 [N]; None, or an index outside the pool: zeros, not stored).  Checkpoints as in
     kda_prefill: ckpt_offsets int64 [N+1] (None for one sequence), ckpt_out the rungs' tensor (None: its
-    size is read from the last offset on the host).  workspace: a uint8 device tensor to use instead of one
+    size is read from the last offset on the host; without offsets T // ckpt_interval rows at least).  workspace: a uint8 device tensor to use instead of one
     of the queried size.  Returns (o [T,Hv,dv], checkpoint states or None).  stream: as
     kda_qk_norm_rope."""
     scale = float(scale)
