@@ -92,6 +92,36 @@ def test_infinite_keys(K, dtype, dk, dv, lens):
         close(c, o, pool, ref, top, max(lens))
 
 
+@pytest.mark.parametrize("what", ["k", "v", "both"])
+@pytest.mark.parametrize("Hk,Hv,dk,lens", [(65, 130, 128, [70, 33]), (65, 130, 64, [40]), (8, 16, 128, [2600]), (8, 16, 64, [2600, 3])])
+def test_infinities_where_a_workgroup_has_all_columns(K, Hk, Hv, dk, lens, what):
+    """Heads of 128 columns in one workgroup each (more than 256 halves of them), whole and in segments: infinities of one
+    head in the middle of the call, and no other head's bits change."""
+    T = sum(lens)
+    a, b = (Call("bf16", lens, Hk, Hv, dk, 128, "token", 83) for _ in "ab")
+    assert is_cut(K, a) == (T > 2000) and (len(lens) * Hv * 2 > 256 or T > 2000)
+    for c in (a, b):
+        c.g = f32(-0.01 * np.random.default_rng(84).random((T, Hv)))
+    t, hk = lens[0] // 2, 3
+    if what != "v":
+        b.k[t, hk, 7] = np.inf
+        b.k[t - 9, hk, dk - 1] = -np.inf
+    if what != "k":
+        b.v[t, 6, 100] = -np.inf
+    with np.errstate(all="ignore"):
+        ref, top = b.oracle(scale=0.3), b.oracle(scale=0.3, size=True)
+        o1, pool1 = run(K, a)
+        o2, pool2 = run(K, b)
+        rest = [h for h in range(Hv) if h // 2 != hk]
+        assert np.array_equal(o1[:, rest], o2[:, rest]) and np.array_equal(pool1[:, rest], pool2[:, rest])
+        assert np.array_equal(o1[:t - 9], o2[:t - 9])
+        odd = ~np.isfinite(ref[0][:, 6, 100])              # as above
+        assert what == "k" or not np.isfinite(o2[odd, 6, 100]).any()
+        if what != "k":
+            o2[odd, 6, 100] = ref[0][odd, 6, 100]
+        close(b, o2, pool2, ref, top, max(lens))
+
+
 # ---------------------------------------------------------------------------
 # decays below the smallest normal number
 # ---------------------------------------------------------------------------
