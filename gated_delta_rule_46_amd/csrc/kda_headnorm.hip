@@ -10,7 +10,7 @@
 // at the store.  A head whose mean square leaves fp32's range is scaled by a power of
 // two first.
 //
-// A lane has the pieces of four heads on their way before it waits for the first, and weights that all
+// A lane of bf16 heads has the pieces of four on their way before it waits for the first, and weights that all
 // heads share are loaded once: 16,384 tokens of 32 heads of 128 with a gate, bf16, 159 us with one head a
 // lane and the weights read for each, 64.5 so (403 MB, 6.2 TB/s; a large copy 5.15).  With the library's
 // exponential and a division for the bf16 gates too it takes 80.6.  64 tokens: 4 us, the launch.
@@ -184,12 +184,17 @@ hipError_t launch(const HeadNormArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// One head a lane where there are too few of them to give each compute unit four workgroups.
+// One head a lane where there are too few of them to give each of 256 compute units four workgroups (32 heads of 128 with
+// a gate, bf16: 1,500 tokens 8.0 us with one, 8.9 with four; 2,048 10.8 / 10.9; 8,192 39.0 / 34.6; two wide ones, 16 of
+// 520, fp32: 16,384 tokens 374 / 317), and for fp32 heads of one piece a lane at any number (32 of 128, 16,384 tokens 120
+// with one, 134 with four, 119 with two; 32 of 256 261 / 285 / 275).
 template <int L, int V, bool BF>
 hipError_t launch(const HeadNormArgs &a, hipStream_t s) {
-    constexpr int R = V == 1 ? 4 : 2;
-    if (a.T * a.H < (int64_t)kNormThreads / L * R * 1024) return launch<L, V, 1, BF>(a, s);
-    return launch<L, V, R, BF>(a, s);
+    if constexpr (BF || V > 1) {
+        constexpr int R = V == 1 ? 4 : 2;
+        if (a.T * a.H >= (int64_t)kNormThreads / L * R * 1024) return launch<L, V, R, BF>(a, s);
+    }
+    return launch<L, V, 1, BF>(a, s);
 }
 
 template <bool BF>

@@ -6,7 +6,7 @@ from test_gpu_linear_edges import K  # noqa: F401 (the fixture)
 
 pytestmark = pytest.mark.gpu
 
-NORMS = [  # heads from which a lane takes several: 1,024 workgroups of them
+NORMS = [  # D, heads and lanes of a head where 1,024 workgroups are full (fp32 heads of 128: one head a lane at any number)
     ("bf16", 128, 4, 16), ("f32", 128, 4, 32), ("bf16", 8, 4, 1), ("bf16", 264, 4, 64), ("f32", 264, 2, 64),
     ("bf16", 1024, 2, 64), ("f32", 520, 2, 64), ("f32", 1024, 2, 64),
 ]
