@@ -12,11 +12,15 @@
 // a difference keeps its 24 bits behind a decay of any size.
 //
 // One workgroup takes a unit (a sequence, or a segment of a long one) and value head
-// from its first chunk to its last; a wave owns 16 of the value columns and keeps their
-// part of S (dk x 16) in the accumulators of the state product.  As the rows of S that a
+// from its first chunk to its last; a wave owns 16 of the value columns (32 of bf16 heads of 128 in one
+// workgroup) and keeps their part of S in the accumulators of the state product.  As the rows of S that a
 // lane accumulates are chosen to be 8 consecutive ones of a 32-row block, the registers are
-// the operand of S^T q as they stand.  The tiles of P (C x C, its lower triangle) are
-// shared out over the waves and exchanged through LDS.
+// the operand of S^T q as they stand.  The three tiles of P (C x C, its lower triangle) are formed by the
+// first three waves and exchanged through LDS.
+//
+// With bf16 rows P and the state as an operand of S^T q are rounded to bf16, one half step (2^-9 of a
+// value) each: a second term of the state alone would be 16 more products on the 72 of a chunk.  The
+// product that forms the state takes its weighted values in three terms, which hold 24 bits.
 //
 // Chunks are a pipeline with one barrier each.  Before it the waves form P of the chunk, S^T q and the new
 // state, and put the next chunk's q, k, v (loaded into registers a chunk earlier) into the other half of
@@ -29,11 +33,11 @@
 // segments; then all segments run as units of their own.
 //
 // Bound by HBM with 4 waves of 32 columns and two workgroups a compute unit: 64 x 2,048 tokens at 32
-// heads of 128 x 128, bf16, 965 us (4.3 GB, 4.4 TB/s; a large copy 5.15, and 757 us with the loads left
-// out).  Chunks of 64 tokens on 8 waves of 16 columns took 25% longer: q and k^T are
+// heads of 128 x 128, bf16, 946 us (4.3 GB, 4.5 TB/s; a large copy 5.15).  Chunks of 64 tokens on 8 waves of 16
+// columns took 25% longer: q and k^T are
 // read from LDS by every wave, and one barrier keeps all waves of a compute unit in step.  131,072 tokens of
-// one sequence 1,155 us: 930 for the segments, 200 for what they add (a head that remembers is read
-// twice), 30 for the rest.
+// one sequence 1,130 to 1,176 us: 930 for the segments, 196 for what they add (a head that remembers is read
+// twice: 1,390 us in all if no head forgets), 30 for the rest.
 
 #include <algorithm>
 #include <cmath>
@@ -71,8 +75,10 @@ struct Shape {
     static constexpr int NPK = C * DK / E / THREADS, NPV = C * DV / E / THREADS;
     static constexpr int KB = C * DK * sizeof(T), VB = C * DV * sizeof(T), PB = C * C * sizeof(T);
     static constexpr int DB = (4 * C + 4 + 2 * NW) * sizeof(float);   // decays of a chunk, and its rows that are not finite
-    // Two workgroups a compute unit, which is what the calls are cut for: where three or four fit they are
-    // dealt out unevenly (16 sequences of 8,192 tokens at 32 heads of 64: 574 us with two, 651 with three).
+    // At most two workgroups a compute unit, which is what the calls are cut for: where three or four fit they are dealt
+    // out unevenly among few units (heads of 64, two / three: 32 of 8 x 2,048 tokens 101 / 120 us; 128 x 64, 8 / 32 of 64
+    // ragged sequences to 8,000 tokens 475 / 517, but 32 of 200 x 700 64 x 64 612 / 597).  Of fp32 heads with dk 128
+    // one fits (91 and 108 KB).
     static constexpr int LDS = std::max(4 * KB + 2 * VB + 2 * PB + 2 * DB, 56 * 1024);
     static constexpr int LDS_STATES = 2 * (KB + VB + DB);    // of the launch that forms the segments' states
     static_assert(C * DK % (E * THREADS) == 0 && C * DV % (E * THREADS) == 0);
@@ -1004,8 +1010,13 @@ hipError_t launch(const LinArgs &a, hipStream_t s) {
     return start(lin_kernel<DK, DV, BF, DV>, heads, X::THREADS, X::LDS, a, s);
 }
 
+// Pieces of fewer tokens cost more than they save: 32 heads, segments of 1,024 tokens in one piece / two 198 / 212 us (16,384
+// tokens).  Of longer ones they cost where heads remember and save where they forget: one / two to four, 65,536 tokens
+// 695 / 754 and 653 / 633 us, 131,072 1,367 / 1,414 and 1,276 / 1,168.
 constexpr int kLeastPiece = 1024;
-constexpr int kLeastOrdered = 128;   // tokens of a sequence on average
+// Tokens of a sequence on average from which the order pays for its launch: 200 ragged sequences of 100 to 3,000 tokens at
+// 32 heads 1,238 us as they come, 1,158 in order; 64 of 64 to 512 125.5 / 124.2; 64 of 60 61 / 65.
+constexpr int kLeastOrdered = 128;
 
 }  // namespace
 
@@ -1027,7 +1038,11 @@ void cut(int cus, bool bf16, int dv, LinArgs *a) {
     //    workgroup in one piece, and halves take as long);
     //  - among several sequences the longest one may have from T / N to T tokens: half as many again of those halfway
     //    (32 heads, 2 x 512 tokens 26 / 43 us, but 47 / 42 if one has all; 8 x 512 42 / 81, but 163 / 75);
-    //  - none where the sequences are so short on average that few can be longer than one.
+    //  - none where the sequences are shorter than a quarter of one on average, so that few can be longer than one (32
+    //    heads, 64 x 60 tokens 61 us whole, 73 cut); those between pay for one that may be long (8 heads, 64 x 60 18.6 /
+    //    25.7, but 234 / 54 if one has 3,777 of the tokens).
+    // Fp32 heads with dk 128, one workgroup a compute unit, are cut for two as well (for two / one, dv 128: 8 heads of
+    // 8,192 tokens 149 / 154 us, 32 of 2,048 118 / 98).
     const int64_t per_head = std::max(2 * cus / a->Hv, 1);
     const int64_t least = std::max((int64_t)4 * a->Hv, (int64_t)std::ceil(2.0 * std::sqrt((double)a->T)));
     const int64_t seg = (std::max((a->T + per_head - 1) / per_head, least) + 63) / 64 * 64;

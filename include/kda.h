@@ -634,7 +634,8 @@ int kda_attn(const kda_attn_config *cfg, const kda_kv_cache *cache, int32_t N, i
  * they have brought there may still leave a NaN); below 2^-126 of itself it has an
  * error of 2^-149 of what it was.
  * T * num_v_heads is at most 2^26 and N * num_v_heads at most 2^20 (larger calls
- * are split by the caller).
+ * are split by the caller).  kda_validate_inputs does not know these calls: what
+ * they take on trust (cu_seqlens in order, g <= 0, the rungs' rows) has no check.
  *
  * All sums are accumulated in fp32.  With bf16 rows the weights of a chunk's
  * tokens and the state are rounded to bf16 as operands of the outputs' products;
