@@ -78,4 +78,10 @@ __device__ __forceinline__ float expm1_small(float t) {
     return t + t * t * (1.f / 2 + t * (1.f / 6 + t * (1.f / 24 + t * (1.f / 120 + t * (1.f / 720)))));
 }
 
+// A state's value behind a decay: keep is e^g, or e^g - 1 where slow (an infinity stays one).
+__device__ __forceinline__ float decayed(float s, float keep, bool slow) {
+    const float r = fmaf(s, keep, slow ? s : 0.f);
+    return slow && fabsf(s) == __builtin_inff() ? s : r;
+}
+
 }  // namespace kda

@@ -943,7 +943,7 @@ __global__ __launch_bounds__(kCarryThreads) void lin_carry_kernel(const LinArgs 
 #pragma unroll
         for (int i = 0; i < G; ++i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[j] = fmaf(S[j], keep[i], f32_bits(keep[i]) >> 31 ? S[j] : 0.f);
+            for (int j = 0; j < 4; ++j) S[j] = decayed(S[j], keep[i], f32_bits(keep[i]) >> 31);
 #pragma unroll
             for (int p = 0; p < kMaxPieces; ++p) S += part[i][p];
             dst += (int64_t)a.Hv * size;

@@ -64,13 +64,27 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const LinArgs a) {
     const int hk = h / (a.Hv / a.Hk);
     const f32x4 v = load4<BF>(a.v, t * a.v_row + (int64_t)h * DV + col);
     const float g = a.g[t * a.g_row + h];
-    const bool slow = g > kSlow && g <= 0.f;                  // S + S (e^g - 1)
-    const float keep = slow ? expm1_small(g) : expf(g);
+    bool slow = g > kSlow && g <= 0.f;                   // S + S (e^g - 1), but for infinities
+    float keep = slow ? expm1_small(g) : expf(g);
     if (tid < DK) {
         s_q[tid] = a.scale * load1<BF>(a.q, t * a.q_row + hk * DK + tid);
         s_k[tid] = load1<BF>(a.k, t * a.k_row + hk * DK + tid);
     }
     __syncthreads();
+
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top = fmaxf(top, fabsf(S[j][c]));
+    if (slow && __any(top == __builtin_inff())) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) S[j][c] = decayed(S[j][c], keep, slow);
+        keep = 1.f;
+        slow = false;
+    }
 
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -252,3 +252,36 @@ def test_decode_with_constant_decays_does_not_drift(K):
     e = G.rel_l2(to_numpy_f64(pool[0]), ref)
     G.say(f"drift over 2,048 steps {e / U:.1f} of 2^-24")
     assert e <= U * (8 + n ** 0.5)
+
+
+@pytest.mark.parametrize("g", [0.0, -0.0, -1e-6, -0.01, -0.1249, -0.2, -3.0])
+def test_infinite_states_stay_infinite(K, g):
+    """Infinities of a state keep their sign at any decay, in one-token steps, in prompts and over segments."""
+    import torch
+    H, dk, dv, T = 2, 64, 64, 1800
+    rng = np.random.default_rng(94)
+    assert workspace(K, "bf16", T, 1, 1, H, dk, dv) > 0 == workspace(K, "bf16", 40, 1, 1, H, dk, dv)
+    S = rng.normal(size=(H, dk, dv)).astype(np.float32)
+    S[0, 3, 5], S[1, 60, 63] = np.inf, -np.inf
+    q, k, v = (torch.ones((T, h, d), dtype=torch.bfloat16, device="cuda") for h, d in ((1, dk), (1, dk), (H, dv)))
+    gd = f32([g, g / T])                                          # over all tokens of the second head the same
+    for call in ("decode", "chunks", "segments"):
+        pool = f32(np.stack([S, np.zeros_like(S)]))
+        n = {"decode": 1, "chunks": 40, "segments": T}[call]
+        if call == "decode":
+            K.kda_lin_decode(q[:1], k[:1], v[:1], gd, pool, i32([0]), i32([1]))
+        else:
+            K.kda_lin_prefill(q[:n], k[:n], v[:n], gd, i64([0, n]), pool, i32([0]), i32([1]))
+        torch.cuda.synchronize()
+        got = to_numpy_f64(pool[1])
+        for h, at, value in ((0, (3, 5), np.inf), (1, (60, 63), -np.inf)):
+            a = np.float64(gd[h].item())
+            if a * n < -100:                                      # below 2^-150 of itself: a NaN is allowed there
+                assert not np.isfinite(got[h][at])
+                continue
+            assert got[h][at] == value, f"{call}: {got[h][at]}"
+            ref = S[h].astype(np.float64) * np.exp(a * n) + np.exp(a * np.arange(n)).sum()
+            fine = np.isfinite(ref)
+            assert fine.sum() == dk * dv - 1
+            tol = (6 * n + 8) * U * (np.abs(S[h]) * np.exp(a * n) + np.exp(a * np.arange(n)).sum())
+            within(f"{call} head {h}", got[h][fine], ref[fine], tol[fine])
