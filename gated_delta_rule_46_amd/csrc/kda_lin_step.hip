@@ -7,8 +7,8 @@
 // of a (sequence, head): lane (cq, ro) of wave w owns columns 4 cq .. 4 cq + 3 and rows
 // 16 j + 4 w + ro, in registers from the read to the write, so that a wave's load covers
 // four 256-byte row segments.  The rows are asked for before anything else; q and k go
-// through LDS, as each lane needs them at its rows.  64 sequences at 32 heads of 128 x 128: 53 us
-// (270 MB, 5.1 TB/s; a large copy 5.15); one sequence 4 us, the launch.
+// through LDS, as each lane needs them at its rows.  64 sequences at 32 heads of 128 x 128: 54 us
+// (270 MB, 5.0 TB/s; a large copy 5.15); one sequence 4 us, the launch.
 
 #include "kda_lin.h"
 #include "kda_mfma.h"

@@ -38,11 +38,15 @@ def plan_of(K, dtype, T, N, Hk, Hv, dk, dv):
 # ---------------------------------------------------------------------------
 # pieces
 # ---------------------------------------------------------------------------
-def heads_on_device(dtype, T, Hk, Hv, dk, dv, seed):
+def normal(seed, *shapes):
     import torch
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
-    return [torch.randn((T, h, d), generator=g, device="cuda").to(dt(dtype)) for h, d in ((Hk, dk), (Hk, dk), (Hv, dv))]
+    return [torch.randn(s, generator=g, device="cuda") for s in shapes]
+
+
+def heads_on_device(dtype, T, Hk, Hv, dk, dv, seed):
+    return [x.to(dt(dtype)) for x in normal(seed, (T, Hk, dk), (T, Hk, dk), (T, Hv, dv))]
 
 
 def decays(kind, T, H, seed):
@@ -70,7 +74,7 @@ def test_pieces(K, dtype, dk, dv, T, pieces, kind):
     assert p == pieces and T // seg >= 3
     q, k, v = heads_on_device(dtype, T, Hk, Hv, dk, dv, 101)
     g = decays(kind, T, Hv, 102)
-    pool = torch.randn((4, Hv, dk, dv), device="cuda")
+    pool, = normal(103, (4, Hv, dk, dv))
     pick = [0, 31, 64, 100, 127]
     first = to_numpy_f64(pool[:, pick])
     read, write = [1, -1], [1, 3]
@@ -167,7 +171,7 @@ def test_captured_segments_replay(K, dtype, Hk, Hv, dk, dv, lens):
     g = decays("mixed", T, Hv, 132)
     N = len(lens)
     cu, slots = i64(np.concatenate([[0], np.cumsum(lens)])), i32(range(N))
-    start = torch.randn((N, Hv, dk, dv), device="cuda")
+    start, = normal(133, (N, Hv, dk, dv))
     pool = start.clone()
     rungs = torch.zeros((sum(n // 64 for n in lens), Hv, dk, dv), device="cuda")
     off = i64(np.concatenate([[0], np.cumsum([n // 64 for n in lens])]))
